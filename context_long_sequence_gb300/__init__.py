@@ -46,6 +46,9 @@ CP_OP_BWD_RANK_STATS = 2
 
 
 CP_RESHARD_MAX_JOBS = 8
+CP_PAGED_VERSION = 1
+CP_DTYPE_BF16 = 0
+CP_DTYPE_FP16 = 1
 
 
 class cp_reshard_job_t(ctypes.Structure):
@@ -78,6 +81,44 @@ class cp_plan_desc_t(ctypes.Structure):
         ("out_fp32", ctypes.c_int32),
         ("chunks_per_rank", ctypes.c_int32),
         ("kv_exchange", ctypes.c_int32),
+    ]
+
+
+class cp_paged_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "dtype", "Hq", "Hkv", "d", "page_size", "max_seqs", "max_tokens", "max_new", "max_pages",
+        "max_prefixes", "max_prefix_pages", "causal", "out_fp32")] + [
+        ("softmax_scale", ctypes.c_float),
+        ("rope_dim", ctypes.c_int32),
+        ("rope_interleaved", ctypes.c_int32),
+        ("rope_base", ctypes.c_double),
+        ("rope_freqs", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
+class cp_paged_cache_t(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class cp_paged_batch_t(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32),
+        ("n_tokens", ctypes.c_int32),
+        ("q_start", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("n_prefixes", ctypes.c_int32),
+        ("prefix_first", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p),
+        ("prefix_table", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
     ]
 
 
@@ -117,6 +158,12 @@ def _L():
     lib.cp_get_status_detail.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32)]
     lib.cp_tile_classes.argtypes = [_vp, ctypes.POINTER(ctypes.c_int32), ctypes.c_int64,
                                     ctypes.POINTER(ctypes.c_int64), _vp]
+    lib.cp_paged_create.argtypes = [ctypes.POINTER(cp_paged_desc_t), ctypes.POINTER(_vp)]
+    lib.cp_paged_destroy.argtypes = [_vp]
+    lib.cp_paged_destroy.restype = None
+    lib.cp_paged_workspace_size.argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.cp_cache_append.argtypes = [_vp, _vp, _vp] + [_vp, ctypes.c_int64] * 4 + [_vp]
+    lib.cp_attn_paged.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.cp_debug_build.argtypes = []
     lib.cp_measure_rates.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
     lib.cp_measure_barrier_check.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
@@ -130,6 +177,7 @@ EXPORTED = ["cp_plan_create", "cp_plan_destroy", "cp_index_map", "cp_workspace_s
             "ulysses_reshard_batch",
             "cp_attn_fwd", "cp_attn_fwd_local", "cp_attn_fwd_rank", "cp_attn_fwd_noalloc", "cp_attn_bwd",
             "cp_attn_fwd_step", "cp_attn_bwd_delta", "cp_attn_bwd_step",
+            "cp_paged_create", "cp_paged_destroy", "cp_paged_workspace_size", "cp_cache_append", "cp_attn_paged",
             "cp_merge_lse", "cp_get_status", "cp_get_status_detail", "cp_debug_build", "cp_strerror",
             "cp_selftest_wait_timeout", "cp_selftest_bounds", "cp_tile_classes", "cp_measure_rates", "cp_measure_barrier_check"]
 
@@ -367,4 +415,179 @@ def alloc_workspace(plan: Plan, op=CP_OP_FWD, device="cuda"):
     """A device byte buffer of cp_workspace_size() bytes (None when zero)."""
     import torch
     n = plan.workspace_size(op)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _refuse(where: str, why: str):
+    e = CPError(CP_ERR_INVALID_ARG, where)
+    e.args = (f"{e.args[0]}: {why}",)
+    raise e
+
+
+class PagedPlan:
+    """Owns a cp_paged_t (cp_paged_create / cp_paged_destroy): the shapes and
+    bounds of serving steps over a paged cache.  ``dtype`` is torch.bfloat16
+    or torch.float16; ``rope_freqs`` (rope_dim/2 numbers) replaces
+    ``rope_base``."""
+
+    def __init__(self, Hq, Hkv, d, page_size, dtype, max_seqs, max_tokens, max_new, max_pages, max_prefixes=0,
+                 max_prefix_pages=0, causal=True, out_fp32=False, softmax_scale=0.0, rope_dim=0, rope_interleaved=False,
+                 rope_base=10000.0, rope_freqs=None):
+        import torch
+        self._h = None
+        codes = {torch.bfloat16: CP_DTYPE_BF16, torch.float16: CP_DTYPE_FP16}
+        if dtype not in codes:
+            _refuse("cp_paged_create", f"dtype {dtype} is neither bfloat16 nor float16")
+        desc = cp_paged_desc_t(CP_PAGED_VERSION, codes[dtype], int(Hq), int(Hkv), int(d), int(page_size), int(max_seqs),
+                               int(max_tokens), int(max_new), int(max_pages), int(max_prefixes), int(max_prefix_pages),
+                               1 if causal else 0, 1 if out_fp32 else 0, float(softmax_scale), int(rope_dim),
+                               1 if rope_interleaved else 0, float(rope_base), None)
+        if rope_freqs is not None:
+            if len(rope_freqs) != int(rope_dim) // 2:
+                _refuse("cp_paged_create", f"{len(rope_freqs)} rope_freqs for rope_dim {rope_dim}")
+            freqs = (ctypes.c_double * max(1, len(rope_freqs)))(*[float(x) for x in rope_freqs])
+            desc.rope_freqs = ctypes.cast(freqs, ctypes.POINTER(ctypes.c_double))
+        h = _vp()
+        _check(_L().cp_paged_create(ctypes.byref(desc), ctypes.byref(h)), "cp_paged_create")
+        self._h = h
+        self.Hq, self.Hkv, self.d, self.page_size, self.dtype = desc.Hq, desc.Hkv, desc.d, desc.page_size, dtype
+        self.max_seqs, self.max_tokens, self.max_new = desc.max_seqs, desc.max_tokens, desc.max_new
+        self.max_pages, self.max_prefixes, self.max_prefix_pages = desc.max_pages, desc.max_prefixes, desc.max_prefix_pages
+        self.out_fp32 = bool(out_fp32)
+        self.o_dtype = torch.float32 if out_fp32 else dtype
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h is not None:
+            _L().cp_paged_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def workspace_size(self) -> int:
+        n = ctypes.c_size_t()
+        _check(_L().cp_paged_workspace_size(self._h, ctypes.byref(n)), "cp_paged_workspace_size")
+        return n.value
+
+
+class PagedCache:
+    """The cache's tensors, as cp_paged_cache_t: ``k`` and ``v`` are
+    [pages][page_size][Hkv][d] views of equal strides (a cache stored
+    [pages][Hkv][page_size][d] is passed transposed)."""
+
+    def __init__(self, k, v):
+        strides = []
+        for x in (k, v):  # the stride of a dimension of one element says nothing
+            strides.append([st if n > 1 else x.shape[-1] for n, st in zip(x.shape, x.stride())] if x.dim() == 4 else None)
+        if k.dim() != 4 or k.shape != v.shape or strides[0] != strides[1] or k.dtype != v.dtype or k.device != v.device \
+                or k.stride(3) != 1:
+            _refuse("PagedCache", "k and v are [pages][page_size][Hkv][d] tensors alike, the last dimension contiguous")
+        self.k, self.v = k, v
+        self.c = cp_paged_cache_t(k.data_ptr(), v.data_ptr(), k.shape[0], *strides[0][:3])
+        self.ref = ctypes.addressof(self.c)
+
+
+class PagedBatch:
+    """A step's batch, as cp_paged_batch_t: int32 tensors on the cache's
+    device, kept alive here and read by the kernels when they run."""
+
+    def __init__(self, q_start, kv_len, page_table, n_tokens, prefix_first=None, prefix_len=None, prefix_table=None,
+                 positions=None):
+        import torch
+        self.n_seqs, self.n_tokens = kv_len.shape[0], int(n_tokens)
+        self.n_prefixes = 0 if prefix_len is None else prefix_len.shape[0]
+        self.device = q_start.device
+        self.max_pages = page_table.shape[1] if page_table.dim() == 2 else -1
+        self.max_prefix_pages = prefix_table.shape[1] if prefix_table is not None and prefix_table.dim() == 2 else 0
+        want = [(q_start, (self.n_seqs + 1,)), (kv_len, (self.n_seqs,)), (page_table, (self.n_seqs, self.max_pages)),
+                (positions, (self.n_tokens,))]
+        given = [x is not None for x in (prefix_first, prefix_len, prefix_table)]
+        if any(given) and not all(given):
+            _refuse("PagedBatch", "prefix_first, prefix_len and prefix_table come together")
+        want += [(prefix_first, (self.n_prefixes + 1,)), (prefix_len, (self.n_prefixes,)),
+                 (prefix_table, (self.n_prefixes, self.max_prefix_pages))]
+        for x, shape in want:
+            if x is not None and (x.dtype != torch.int32 or tuple(x.shape) != shape or not x.is_contiguous()
+                                  or x.device != self.device):
+                _refuse("PagedBatch", f"a contiguous int32 tensor of shape {shape} on {self.device} is wanted, got "
+                                      f"{x.dtype} {tuple(x.shape)} on {x.device}")
+        self._keep = (q_start, kv_len, page_table, prefix_first, prefix_len, prefix_table, positions)
+        self.c = cp_paged_batch_t(self.n_seqs, self.n_tokens, _ptr(q_start), _ptr(kv_len), _ptr(page_table),
+                                  self.n_prefixes, _ptr(prefix_first), _ptr(prefix_len), _ptr(prefix_table),
+                                  _ptr(positions))
+        self.ref = ctypes.addressof(self.c)
+
+
+def _paged_stream(where, plan, cache, batch, stream):
+    """The checks that need the tensors' shapes, types and devices (the
+    library sees addresses); the stream the call goes to."""
+    import torch
+    k = cache.k
+    if k.shape[1] != plan.page_size or k.shape[2] != plan.Hkv or k.shape[3] != plan.d or k.dtype != plan.dtype:
+        _refuse(where, f"the cache is {k.dtype} {tuple(k.shape)}, the plan's pages are {plan.dtype} "
+                       f"[{plan.page_size}][{plan.Hkv}][{plan.d}]")
+    if batch.max_pages != plan.max_pages or (batch.n_prefixes and batch.max_prefix_pages != plan.max_prefix_pages):
+        _refuse(where, "the page tables' columns differ from the plan's")
+    if batch.device != k.device:
+        _refuse(where, f"the batch is on {batch.device}, the cache on {k.device}")
+    if k.device.type != "cuda" or k.device.index != torch.cuda.current_device():
+        _refuse(where, f"the tensors are on {k.device}, which is not the current device")
+    return _stream(stream)
+
+
+def _tokens(where, name, x, batch, heads, d, dtype, device):
+    """Address and token stride of a [n_tokens][heads][d] tensor."""
+    s = x.stride()
+    if x.dim() != 3 or x.shape[0] != batch.n_tokens or x.shape[1] != heads or x.shape[2] != d or x.dtype != dtype \
+            or s[2] != 1 or (heads > 1 and s[1] != d) or x.device != device:
+        _refuse(where, f"{name} is [{batch.n_tokens}][{heads}][{d}] {dtype} with contiguous heads on {device}, got "
+                       f"{x.dtype} {tuple(x.shape)} with strides {s} on {x.device}")
+    return x.data_ptr(), s[0] if x.shape[0] > 1 else heads * d
+
+
+def cp_cache_append(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, k, v, q_out=None, stream=None):
+    where = "cp_cache_append"
+    st = _paged_stream(where, plan, cache, batch, stream)
+    dev = cache.k.device
+    if q is not None and q_out is None:
+        _refuse(where, "q needs q_out")
+    qa = _tokens(where, "q", q, batch, plan.Hq, plan.d, plan.dtype, dev) if q is not None else (None, 0)
+    ka = _tokens(where, "k", k, batch, plan.Hkv, plan.d, plan.dtype, dev)
+    va = _tokens(where, "v", v, batch, plan.Hkv, plan.d, plan.dtype, dev)
+    oa = _tokens(where, "q_out", q_out, batch, plan.Hq, plan.d, plan.dtype, dev) if q is not None else (None, 0)
+    rc = _L().cp_cache_append(plan._h, cache.ref, batch.ref, *qa, *ka, *va, *oa, st)
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def cp_attn_paged(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, o, lse, workspace=None, stream=None):
+    where = "cp_attn_paged"
+    st = _paged_stream(where, plan, cache, batch, stream)
+    dev = cache.k.device
+    qa = _tokens(where, "q", q, batch, plan.Hq, plan.d, plan.dtype, dev)
+    if tuple(o.shape) != (batch.n_tokens, plan.Hq, plan.d) or o.dtype != plan.o_dtype or not o.is_contiguous() \
+            or o.device != dev:
+        _refuse(where, f"o is a contiguous [{batch.n_tokens}][{plan.Hq}][{plan.d}] {plan.o_dtype} on {dev}")
+    if tuple(lse.shape) != (plan.Hq, batch.n_tokens) or lse.element_size() != 4 or not lse.is_floating_point() \
+            or not lse.is_contiguous() or lse.device != dev:
+        _refuse(where, f"lse is a contiguous [{plan.Hq}][{batch.n_tokens}] float32 on {dev}")
+    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if n and workspace.device != dev:
+        _refuse(where, f"the workspace is on {workspace.device}")
+    rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), _ptr(workspace), n, st)
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def alloc_paged_workspace(plan: PagedPlan, device="cuda"):
+    """A device byte buffer of cp_paged_workspace_size() bytes (None when zero)."""
+    import torch
+    n = plan.workspace_size()
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None

@@ -17,6 +17,7 @@
 #include "cp_attn.h"
 #include "debug.cuh"
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 
 using cpattn::AttnGeom;
@@ -374,6 +375,8 @@ BwdWorkspace bwd_workspace(const cp_plan* p) {
 }
 
 }  // namespace
+
+int32_t* cpattn::device_status_ptr() { return status_ptr(); }
 
 extern "C" {
 

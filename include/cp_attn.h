@@ -67,7 +67,7 @@ extern "C" {
 #define CP_ERR_ALIGNMENT      -3  /* a device pointer is not 16-byte aligned */
 #define CP_ERR_CUDA           -4  /* a CUDA runtime/driver call failed */
 #define CP_ERR_DEVICE_TIMEOUT -5  /* a bounded device-side wait ran out (from cp_get_status) */
-#define CP_ERR_DEVICE_BOUNDS  -6  /* a device-side index check failed (from cp_get_status) */
+#define CP_ERR_DEVICE_BOUNDS  -6  /* a device-side index or data check failed (from cp_get_status) */
 #define CP_ERR_WORKSPACE      -7  /* workspace pointer null or smaller than cp_workspace_size() */
 #define CP_ERR_ARCH           -8  /* the current device is not sm_103 */
 
@@ -316,6 +316,132 @@ int cp_attn_bwd_step(const cp_plan_t *plan, int rank, int step, const void *q_ra
 int cp_merge_lse(int n_parts, int rows, int H, int d, const float *o_parts,
                  const float *lse_parts, void *o_out, float *lse_out, cudaStream_t stream);
 
+/* ---- Serving: attention over a paged key/value cache --------------------
+ * (no counterpart in the pages, which stop at the forward and backward of
+ * whole sequences: these calls serve the model afterwards, prompt by prompt
+ * and token by token.)
+ *
+ * The cache holds keys and values in pages of page_size tokens.  A step's
+ * batch is ragged: sequence s has the new tokens
+ * q_start[s] .. q_start[s+1]-1 (rows of q, o, ...), and kv_len[s] keys in
+ * its own pages, the new tokens' among them; key j of sequence s is row
+ * j % page_size of page page_table[s][j / page_size].  Consecutive sequences
+ * may share a prefix (a system prompt, a document): prefix p, with
+ * prefix_len[p] keys in the pages of prefix_table[p], precedes the own keys
+ * of sequences prefix_first[p] .. prefix_first[p+1]-1.  A prefix is held
+ * once and read once for all of its sequences; its length need not fill its
+ * last page.  Sequences before prefix_first[0] and from
+ * prefix_first[n_prefixes] on have none.
+ *
+ * A context-parallel cache: a rank that holds a share of a sequence's keys
+ * runs cp_attn_paged on its share (out_fp32, causal = 0 for a share that
+ * lies wholly in the past) and the ranks' (O, LSE) merge with cp_merge_lse,
+ * whose layout they have.  causal = 0 also serves cross attention to an
+ * encoder's states held in the pages.
+ *
+ * The int32 arrays of a batch are read on the device while the kernels run,
+ * so that a captured graph follows their contents: a replay reads the new
+ * lengths and pages.  Nothing in them is trusted.  A sequence whose rows,
+ * length or new-token count leave the bounds of the batch and the plan is
+ * skipped (its rows of o and lse, and its pages, stay as they were), a prefix
+ * likewise (its sequences then attend to their own keys alone), and keys in a
+ * page outside [0, num_pages) are neither read nor written and take no part
+ * in the softmax; each is recorded as CP_ERR_DEVICE_BOUNDS (cp_get_status).
+ * Rows behind q_start[n_seqs] (a padded batch) stay as they were.
+ * These arrays need only 4-byte alignment. */
+#define CP_PAGED_VERSION 1
+#define CP_DTYPE_BF16 0
+#define CP_DTYPE_FP16 1
+
+/* Plan description (host struct; copied by cp_paged_create). */
+typedef struct {
+  int32_t version;            /* CP_PAGED_VERSION */
+  int32_t dtype;              /* CP_DTYPE_*: q, k, v, the cache, and o unless out_fp32 */
+  int32_t Hq, Hkv;            /* query heads, KV heads; Hkv divides Hq, Hq/Hkv <= 128 */
+  int32_t d;                  /* head dimension: 64 or 128 */
+  int32_t page_size;          /* tokens per page: a power of two, 16 .. 65536 */
+  int32_t max_seqs;           /* most sequences, token rows and new tokens of one sequence */
+  int32_t max_tokens;         /* in a batch (2 * max_tokens * Hq < 2^30) */
+  int32_t max_new;
+  int32_t max_pages;          /* columns of page_table (max_pages * page_size < 2^30) */
+  int32_t max_prefixes;       /* most prefixes of a batch; 0: none */
+  int32_t max_prefix_pages;   /* columns of prefix_table (the same bound); 0 if max_prefixes is 0 */
+  int32_t causal;             /* 1: new token i of n sees the own keys j <= kv_len - n + i;
+                                 0: every own key.  Prefixes are seen whole. */
+  int32_t out_fp32;           /* 1: o is fp32, unrounded */
+  float softmax_scale;        /* 0 => 1/sqrt(d) */
+  int32_t rope_dim;           /* elements of a head turned by cp_cache_append: 0 (none) or a multiple
+                                 of 16 up to d, the first of the head */
+  int32_t rope_interleaved;   /* 0: pair j is elements (j, j + rope_dim/2); 1: (2j, 2j + 1) */
+  double rope_base;           /* pair j turns by pos * rope_base^(-2j/rope_dim) radians, */
+  const double *rope_freqs;   /* or, if not null, by pos * rope_freqs[j] (host, rope_dim/2 entries; copied) */
+} cp_paged_desc_t;
+
+/* The cache (host struct, read during the call).  Element x of head h of
+ * token t of page p is at p*page_stride + t*token_stride + h*head_stride + x
+ * in both k and v; strides in elements, multiples of 8, such that rows do not
+ * overlap ([pages][page_size][Hkv][d] and [pages][Hkv][page_size][d], for
+ * instance, or the two caches side by side in one buffer). */
+typedef struct {
+  void *k, *v;                /* device, 16-byte aligned */
+  int32_t num_pages;
+  int64_t page_stride, token_stride, head_stride;
+} cp_paged_cache_t;
+
+/* A step's batch (host struct of device arrays, read during the call). */
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_tokens;            /* rows of q, o, ...: q_start[n_seqs] and, in a padded batch, more */
+  const int32_t *q_start;      /* [n_seqs + 1], ascending */
+  const int32_t *kv_len;       /* [n_seqs] */
+  const int32_t *page_table;   /* [n_seqs][max_pages] */
+  int32_t n_prefixes;
+  const int32_t *prefix_first; /* [n_prefixes + 1], ascending */
+  const int32_t *prefix_len;   /* [n_prefixes] */
+  const int32_t *prefix_table; /* [n_prefixes][max_prefix_pages] */
+  const int32_t *positions;    /* [n_tokens] or null: where cp_cache_append's rotation places the token;
+                                  null => prefix_len + its place among the sequence's own keys */
+} cp_paged_batch_t;
+
+typedef struct cp_paged cp_paged_t; /* opaque; immutable after creation; usable from any stream */
+
+/* Validate `desc` and build the plan.  It holds no device memory and may be
+ * used on any sm_103 device. */
+int cp_paged_create(const cp_paged_desc_t *desc, cp_paged_t **out);
+void cp_paged_destroy(cp_paged_t *plan);
+
+/* Bytes of device workspace cp_attn_paged needs for any batch of this plan.
+ * Nothing in it has to be initialised or kept between calls; calls that may
+ * run at the same time need one each. */
+int cp_paged_workspace_size(const cp_paged_t *plan, size_t *bytes);
+
+/* Write the new tokens' keys (turned to their positions) and values into
+ * their pages, and the turned queries to q_out:
+ *   q [n_tokens][Hq][d], k, v [n_tokens][Hkv][d], q_out [n_tokens][Hq][d]; a token's
+ *   heads are contiguous, tokens q_stride, k_stride, v_stride, q_out_stride
+ *   elements apart (multiples of 8), so the three may lie side by side.
+ * Sums in fp32, one rounding.  q may be null (q_out is then ignored); q_out
+ * may be q itself with the same stride and must not overlap the inputs
+ * otherwise.  If two new tokens name the same row of a page, either may
+ * remain. */
+int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const cp_paged_batch_t *batch,
+                    const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, void *q_out, int64_t q_out_stride, cudaStream_t stream);
+
+/* Attention of the new tokens over their prefix's and their own keys:
+ *   q [n_tokens][Hq][d], tokens q_stride elements apart (a multiple of 8);
+ *   o [n_tokens][Hq][d] out (fp32 if out_fp32), contiguous;
+ *   lse [Hq][n_tokens] fp32 out (natural log); (0, -inf) for a row that sees no key.
+ * Keys behind a sequence's or a prefix's length are never part of the
+ * result, whatever their page holds.  A key below kv_len that the causal mask
+ * hides from some rows of its sequence must be finite.
+ * Deterministic: no atomics on results; the work is split by the batch's
+ * lengths alone.
+ * workspace: cp_paged_workspace_size() bytes (may be NULL when 0). */
+int cp_attn_paged(const cp_paged_t *plan, const cp_paged_cache_t *cache, const cp_paged_batch_t *batch,
+                  const void *q, int64_t q_stride, void *o, float *lse, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream);
+
 /* Debug table of the forward's tile classes (no counterpart in the pages: it
  * exposes which work the kernel skips).  For every work item of the plan's
  * forward -- a block of up to 256 query slots of one attention rank inside
@@ -419,13 +545,15 @@ int cp_get_status(cudaStream_t stream, int32_t *dev_code);
  * block, source line, file id}.  The last three are set only for
  * CP_ERR_DEVICE_BOUNDS, which only debug builds record (file ids: 1 the C-ABI
  * layer, 2 the forward kernel, 3 the backward kernels, 4 reshard and
- * gather, 5 merge); otherwise 0.  Reads and clears all four words.
+ * gather, 5 merge) except where the data of a paged batch leave their bounds,
+ * which every build records (6 cp_cache_append, 7 cp_attn_paged); otherwise 0.
+ * Reads and clears all four words.
  *
  * Debug builds (compiled with -DCP_DEBUG, the library libcpattn_debug.so)
  * check every work item, global index and TMA coordinate of the kernels;
  * a failed check records CP_ERR_DEVICE_BOUNDS here and skips the access
  * (a TMA load is still issued: the hardware fills out-of-range rows with
- * zeros).  Release builds contain no checks. */
+ * zeros).  Release builds contain none of these checks. */
 int cp_get_status_detail(cudaStream_t stream, int32_t *out4);
 
 /* 1 if this library was built with -DCP_DEBUG, else 0. */
