@@ -29,7 +29,7 @@ struct NvtxRange {
 };
 
 constexpr long long kMaxKeys = 1LL << 30;  // of one page table row; key indices and limits stay in 32 bits
-constexpr long long kMaxRows = 1LL << 30;
+constexpr long long kMaxRows = 1LL << 30;  // of the workspace's home rows
 constexpr int64_t kMaxStride = 1LL << 36;  // elements; a tensor map takes strides below 2^40 bytes
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -145,7 +145,8 @@ int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
   if (d.rope_dim < 0 || d.rope_dim > d.d) return CP_ERR_INVALID_ARG;
   if (static_cast<long long>(d.max_pages) * d.page_size >= kMaxKeys ||
       static_cast<long long>(d.max_prefix_pages) * d.page_size >= kMaxKeys ||
-      2LL * d.max_tokens * d.Hq >= kMaxRows || static_cast<long long>(d.max_seqs) + d.max_prefixes >= (1 << 20))
+      2LL * d.max_tokens * d.Hq >= kMaxRows ||
+      static_cast<long long>(d.max_seqs) + d.max_prefixes > cpattn::kMaxEntries)
     return CP_ERR_INVALID_ARG;
   if (d.d != 64 && d.d != 128) return CP_ERR_UNSUPPORTED;
   if (d.page_size < 16 || d.page_size > 65536 || (d.page_size & (d.page_size - 1))) return CP_ERR_UNSUPPORTED;
@@ -173,7 +174,8 @@ void cp_paged_destroy(cp_paged_t* p) { delete p; }
 
 int cp_paged_workspace_size(const cp_paged_t* p, size_t* bytes) {
   if (!p || !bytes) return CP_ERR_INVALID_ARG;
-  *bytes = 0;
+  const cp_paged_desc_t& d = p->desc;
+  *bytes = cpattn::paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0).total;
   return CP_OK;
 }
 
@@ -223,7 +225,7 @@ int cp_attn_paged(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_p
   if (rc == CP_OK && (!aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16))) rc = CP_ERR_ALIGNMENT;
   size_t need = 0;
   if (rc == CP_OK) rc = cp_paged_workspace_size(p, &need);
-  if (rc == CP_OK && need > 0 && (!workspace || workspace_bytes < need)) rc = CP_ERR_WORKSPACE;
+  if (rc == CP_OK && (!workspace || workspace_bytes < need)) rc = CP_ERR_WORKSPACE;
   if (rc == CP_OK) rc = check_arch();
   if (rc != CP_OK) return rc;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return CP_OK;
@@ -236,7 +238,14 @@ int cp_attn_paged(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_p
   a.o = o;
   a.out_fp32 = d.out_fp32;
   a.lse = lse;
-  a.workspace = workspace;
+  const cpattn::PagedWorkspace w = cpattn::paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0);
+  char* ws = static_cast<char*>(workspace);
+  a.parts = reinterpret_cast<cpattn::PagedParts*>(ws + w.parts);
+  a.part_lse = reinterpret_cast<float*>(ws + w.lse);
+  a.part_o = reinterpret_cast<float*>(ws + w.o);
+  a.rows_small = w.rows_small;
+  a.rows_large_end = w.rows_large_end;
+  a.max_tokens = d.max_tokens;
   a.status = cpattn::device_status_ptr();
   if (!a.status) return CP_ERR_CUDA;
   NvtxRange range("cp_attn_paged");

@@ -1,11 +1,15 @@
-// paged.cuh -- device helpers shared by the paged-cache kernels.
+// paged.cuh -- what the paged-cache kernels share: the walk over a worker's
+// units, the targets of its rows, TMA boxes of the cache, launches.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "debug.cuh"
 #include "paged.h"
 #include "ptx.cuh"
+#include "tmap.h"
 
 namespace cpattn {
 
@@ -37,6 +41,186 @@ __device__ __forceinline__ int warp_prefix_of(const PagedGeom& g, int s) {
   return p < g.NP ? p : -1;
 }
 
+// Programmatic dependent launch: `launch_dependents` lets the next kernel of
+// the stream begin as SMs fall free; `wait` returns once every kernel before
+// this one has completed and its writes are visible.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__device__ __forceinline__ long long shfl64(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
+
+// One run of key tiles of one token tile and KV head, as a worker gets it.
+struct PagedSegment {
+  int e, h;                   // entry, KV head
+  int t0, nt;                 // the tile's tokens
+  int keys, limit0;           // keys of the entry; token t0 + i sees min(keys, limit0 + i)
+  int tile0, tile1, tiles;    // this run, and all key tiles of the token tile
+  const int32_t* table;
+  int first_worker, parts;    // workers that share the token tile: consecutive
+  __device__ __forceinline__ bool complete() const { return parts == 1; }
+};
+
+// Walks a worker's units.  Every warp that needs the segments walks them by
+// itself: 32 entries at a time, an entry a lane.
+struct PagedWalker {
+  const PagedGeom& g;
+  const PagedCut cut;
+  int32_t* status;
+  int E, workers, worker;
+  long long units, u, end;    // all units; this worker's next and last + 1
+  int base;                   // first entry of the window
+  long long before;           // units before the window
+  // The lane's entry:
+  PagedEntry entry;
+  long long head_units, upto;  // its units of one head; units of the window up to and including it
+
+  __device__ __forceinline__ PagedWalker(const PagedGeom& g_, const PagedCut& c, int32_t* st)
+      : g(g_), cut(c), status(st), E(g_.B + g_.NP) {}
+
+  __device__ __forceinline__ void load(int first) {
+    const int lane = threadIdx.x & 31;
+    base = first;
+    entry = PagedEntry{0, 0, 0, 0, nullptr, false};
+    if (base + lane < E) entry = paged_entry(g, base + lane);
+    if (entry.bad) debug_bounds_fail(status, __LINE__, kTuPagedAttn);
+    head_units = paged_head_units(g, cut, entry);
+    upto = head_units * g.Hkv;
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+      if (lane >= x) upto += y;
+    }
+  }
+
+  // Called by the whole block; `sums` holds a number for each window of 32
+  // entries and is free again after the call.  False: nothing for this worker.
+  __device__ __forceinline__ bool start(long long* sums, int worker_, int max_workers, int min_units) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int windows = (E + 31) / 32;
+    worker = worker_;
+    if (windows > 1) {
+      for (int w = warp; w < windows; w += warps) {
+        load(w * 32);
+        if (lane == 31) sums[w] = upto;
+      }
+      __syncthreads();
+      units = 0;
+      for (int w0 = 0; w0 < windows; w0 += 32) {
+        long long x = w0 + lane < windows ? sums[w0 + lane] : 0;
+#pragma unroll
+        for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+        units += x;
+      }
+    } else {
+      load(0);
+      units = shfl64(upto, 31);
+      before = 0;
+    }
+    workers = paged_workers(units, max_workers, min_units);
+    const bool any = worker < workers;
+    u = any ? paged_first_unit(units, workers, worker) : 0;
+    end = any ? paged_first_unit(units, workers, worker + 1) : 0;
+    if (windows > 1) {
+      int w = 0;
+      before = 0;
+      if (any)
+        while (w + 1 < windows && before + sums[w] <= u) before += sums[w++];
+      __syncthreads();
+      if (any) load(w * 32);
+    }
+    return any;
+  }
+
+  // The next segment; warp-uniform.
+  __device__ __forceinline__ bool next(PagedSegment& s) {
+    if (u >= end) return false;
+    long long total = shfl64(upto, 31);
+    while (u >= before + total) {
+      if (base + 32 >= E) {  // only where the arrays changed under the kernel
+        end = u;
+        return false;
+      }
+      before += total;
+      load(base + 32);
+      total = shfl64(upto, 31);
+    }
+    long long rel = u - before;
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;
+    const long long hu = shfl64(head_units, at);
+    rel -= shfl64(upto, at) - hu * g.Hkv;
+    PagedEntry e;
+    s.e = base + at;
+    e.t0 = __shfl_sync(0xffffffffu, entry.t0, at);
+    e.n = __shfl_sync(0xffffffffu, entry.n, at);
+    e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
+    e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
+    s.table = s.e < g.B ? g.page_table + static_cast<size_t>(s.e) * g.table_stride
+                        : g.prefix_table + static_cast<size_t>(s.e - g.B) * g.prefix_stride;
+    s.h = static_cast<int>(rel / hu);
+    rel -= s.h * hu;
+    int rb = 0, tiles = paged_tile_units(cut, e, 0);
+    while (rel >= tiles) {
+      rel -= tiles;
+      tiles = paged_tile_units(cut, e, ++rb);
+    }
+    s.t0 = e.t0 + rb * cut.tile_tokens;
+    s.nt = min(cut.tile_tokens, e.n - rb * cut.tile_tokens);
+    s.keys = e.keys;
+    s.limit0 = e.limit0 + rb * cut.tile_tokens;
+    s.tiles = tiles;
+    s.tile0 = static_cast<int>(rel);
+    s.tile1 = static_cast<int>(min(static_cast<long long>(tiles), rel + (end - u)));
+    const long long u0 = u - s.tile0;
+    s.first_worker = s.tile0 == 0 ? worker : paged_worker_of(units, workers, u0);
+    s.parts = (s.tile1 == tiles ? worker : paged_worker_of(units, workers, u0 + tiles - 1)) - s.first_worker + 1;
+    u += s.tile1 - s.tile0;
+    return true;
+  }
+};
+
+// Whether sequence s (a valid entry) has a prefix with keys.  Warp-wide.
+__device__ __forceinline__ bool warp_has_prefix(const PagedGeom& g, int s) {
+  const int p = warp_prefix_of(g, s);
+  return p >= 0 && paged_entry(g, g.B + p).keys > 0;
+}
+
+// Where a segment's rows go: the output, or part rows from `row` on.
+struct PagedTarget {
+  bool final_rows;   // straight to o and lse
+  bool home;         // row of (token, head) is home + token * Hq + head
+  long long row;     // slot: row r of the token tile is row + r
+};
+
+// Target of a segment, and (for the run that begins its token tile) the
+// record of the tile's parts.  `slots` is the kernel's first slot row,
+// `slot_rows` the rows of one.  Warp-wide.
+__device__ __forceinline__ PagedTarget paged_target(const PagedAttnArgs& a, const PagedWalker& w, const PagedSegment& s,
+                                                    long long slots, int slot_rows, bool record) {
+  const PagedGeom& g = a.g;
+  const bool prefix = s.e >= g.B;
+  PagedTarget t{false, false, 0};
+  const long long home = a.rows_large_end + (prefix ? static_cast<long long>(a.max_tokens) * g.Hq : 0);
+  if (s.complete()) {
+    t.final_rows = !prefix && !warp_has_prefix(g, s.e);
+    t.home = !t.final_rows;
+    t.row = home;
+  } else {
+    t.row = slots + (2LL * w.worker + (s.tile0 == 0 ? 1 : 0)) * slot_rows;
+  }
+  if (record && s.tile0 == 0) {
+    PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
+    for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
+      PagedParts r;
+      r.first = static_cast<int>(t.home ? home + static_cast<long long>(s.t0 + i) * g.Hq + s.h * g.G : t.row + i * g.G);
+      r.second = static_cast<int>(slots + 2LL * (s.first_worker + 1) * slot_rows + i * g.G);
+      r.count = s.parts;
+      r.stride = 2 * slot_rows;
+      parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
+    }
+  }
+  return t;
+}
+
 template <typename T>
 struct Elem;
 template <>
@@ -57,5 +241,83 @@ struct Elem<__half> {
     return r;
   }
 };
+
+// Weights are 2^(s - m + kBias).  The running maximum m is raised only when a
+// score exceeds it by kSlack (log2 units), so O is rescaled rarely; the final
+// division uses the same m.  bf16 has fp32's exponents and needs no bias.  In
+// fp16 a weight below 2^-14 loses bits and one below 2^-25 vanishes, which the
+// flat tail of a long context would show: with the bias a weight keeps its
+// bits down to 2^-23 of the largest, and a million keys below that are off by
+// at most 2^-14 of the sum, under fp16's own half step of 2^-11.
+// kSpecSum and kSpecMax bound weights taken before their maximum is known
+// (paged_attn_large.cu): a sum of weights, and one score over m.
+template <typename T>
+struct Weight {
+  static constexpr float kBias = 0.f, kSlack = 8.f, kSpecSum = 65536.f, kSpecMax = 16.f;
+};
+template <>
+struct Weight<__half> {
+  static constexpr float kBias = 9.f, kSlack = 2.f, kSpecSum = 60000.f, kSpecMax = 6.5f;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- host side
+
+// 4-D map over the cache: columns, tokens of a page, heads, pages; boxes of
+// 64 columns (128 bytes, swizzled) x box_rows tokens.
+inline bool make_cache_map(CUtensorMap* m, const PagedGeom& g, const void* base, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(1) << g.page_shift,
+                        static_cast<cuuint64_t>(g.Hkv), static_cast<cuuint64_t>(g.num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(g.token_stride) * 2, static_cast<cuuint64_t>(g.head_stride) * 2,
+                           static_cast<cuuint64_t>(g.page_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, g.dtype == CP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch that may begin while the kernel before it in the stream still
+// runs (it calls griddepcontrol.wait before it reads that kernel's results).
+template <typename... P, typename... A>
+int launch(void (*kernel)(P...), unsigned grid, int threads, int smem, bool overlap, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+}
+
+// The current device's SM count, and the kernel's shared-memory limit raised
+// there; once per device (concurrent first calls do the same).
+template <typename K>
+int prepare_kernel(std::atomic<int> (&known)[64], K kernel, int smem, int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return CP_ERR_CUDA;
+    known[dev].store(n, std::memory_order_release);
+  }
+  *sms = n;
+  return CP_OK;
+}
 
 }  // namespace cpattn

@@ -36,6 +36,10 @@ struct PagedGeom {
   float scale;
 };
 
+// What the sequences share with the kernels' index arithmetic is in 32 bits:
+// keys, rows and workspace rows stay below 2^30; units of work, cache offsets
+// and byte offsets are 64-bit.
+
 // One set of keys and the token rows that attend to it: entry e < B is
 // sequence e with its own pages, entry B + p is prefix p with the rows of
 // all its sequences.  n == 0: nothing to do.  Row i (of n) sees the first
@@ -81,6 +85,91 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
   return r;
 }
 
+// How the attention of a batch is cut into work.  A kernel takes the entries
+// whose rows (tokens x query heads of a KV head) lie in [min_rows, max_rows],
+// cuts their tokens into tiles of tile_tokens and each tile's visible keys
+// into tiles of tile_keys.  One key tile of one token tile and KV head is a
+// unit; units are numbered entry by entry, KV head by KV head, token tile by
+// token tile, and each of the W workers (CTAs) takes an equal, contiguous
+// share of the numbers.  A token tile whose units fall to several workers
+// has as many parts, merged afterwards by their log-sum-exp.  The cut depends
+// on the batch's lengths alone, so the result does too.
+struct PagedCut {
+  int min_rows, max_rows;
+  int tile_tokens, tile_keys;
+};
+
+// Key tiles that token tile `rb` of entry `e` sees.
+__host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEntry& e, int rb) {
+  const int last = (rb + 1) * c.tile_tokens < e.n ? (rb + 1) * c.tile_tokens - 1 : e.n - 1;
+  const int seen = e.limit0 + last < e.keys ? e.limit0 + last : e.keys;
+  return seen > 0 ? (seen + c.tile_keys - 1) / c.tile_keys : 0;
+}
+
+// Units of entry `e` for one KV head.
+__host__ __device__ inline long long paged_head_units(const PagedGeom& g, const PagedCut& c, const PagedEntry& e) {
+  const long long rows = static_cast<long long>(e.n) * g.G;
+  if (e.n <= 0 || rows < c.min_rows || rows > c.max_rows) return 0;
+  const int tiles = (e.n + c.tile_tokens - 1) / c.tile_tokens;
+  if (e.limit0 >= e.keys) return static_cast<long long>(tiles) * paged_tile_units(c, e, 0);  // all rows see all keys
+  long long sum = 0;
+  for (int rb = 0; rb < tiles; ++rb) sum += paged_tile_units(c, e, rb);
+  return sum;
+}
+
+// Workers that get units: each at least `min_units`, so that a short batch is
+// not cut finer than its merge costs.
+__host__ __device__ inline int paged_workers(long long units, int workers, int min_units) {
+  const long long w = (units + min_units - 1) / min_units;
+  return w < workers ? static_cast<int>(w) : workers;
+}
+__host__ __device__ inline long long paged_first_unit(long long units, int workers, int w) {
+  return units * w / workers;
+}
+// The worker of unit u.
+__host__ __device__ inline int paged_worker_of(long long units, int workers, long long u) {
+  return static_cast<int>(((u + 1) * workers - 1) / units);
+}
+
+// Workers and slots.  A worker holds at most two incomplete token tiles: the
+// one its share begins in (its slot 2w) and the one its share ends in (slot
+// 2w + 1); a part that is complete but has a partner (own keys and a prefix)
+// goes to a home row of its own.
+constexpr int kSmallWorkers = 304, kSmallRows = 64, kSmallKeys = 64;
+constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeys = 128;
+constexpr int kMaxEntries = 8192;
+
+inline __host__ __device__ PagedCut paged_cut_small(int G) {
+  return PagedCut{1, kSmallRows, G <= kSmallRows ? kSmallRows / G : 1, kSmallKeys};
+}
+inline __host__ __device__ PagedCut paged_cut_large(int G) {
+  return PagedCut{kSmallRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeys};
+}
+
+// Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
+struct PagedParts {
+  int32_t first, second;  // rows of part 0 and part 1
+  int32_t count, stride;  // parts, and rows from part 1 to part 2, ...
+};
+
+// The workspace: parts [2][N][Hkv] (own, prefix), then the rows' log-sum-exp
+// (log2 units) and their normalised fp32 O.
+struct PagedWorkspace {
+  long long rows_small, rows_large_end, rows;  // small slots end, large slots end (home rows begin), all
+  size_t parts, lse, o, total;             // byte offsets
+};
+inline __host__ __device__ PagedWorkspace paged_workspace(long long max_tokens, int Hq, int Hkv, int d, bool prefixes) {
+  PagedWorkspace w;
+  w.rows_small = 2LL * kSmallWorkers * kSmallRows;
+  w.rows_large_end = w.rows_small + 2LL * kLargeWorkers * kLargeRows;
+  w.rows = w.rows_large_end + (prefixes ? 2LL * max_tokens * Hq : 0);
+  w.parts = 0;
+  w.lse = (static_cast<size_t>(2 * max_tokens) * Hkv * sizeof(PagedParts) + 255) & ~size_t(255);
+  w.o = w.lse + ((static_cast<size_t>(w.rows) * 4 + 255) & ~size_t(255));
+  w.total = w.o + static_cast<size_t>(w.rows) * d * 4;
+  return w;
+}
+
 struct AppendArgs {
   PagedGeom g;
   const void* q;           // or null
@@ -107,11 +196,17 @@ struct PagedAttnArgs {
   void* o;                 // [N][Hq][d], the plan's type or fp32 (out_fp32)
   int out_fp32;
   float* lse;              // [Hq][N]
-  void* workspace;
+  PagedParts* parts;       // the workspace (PagedWorkspace)
+  float* part_lse;
+  float* part_o;
+  long long rows_small, rows_large_end;
+  int max_tokens;          // of the plan: home rows of prefixes follow max_tokens * Hq of the own keys
   int32_t* status;
 };
 
 int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
+// The entries of more than kSmallRows rows (paged_attn_large.cu).
+int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream);
 
 // Device address of the status words on the current device (cp_attn.cu).
 int32_t* device_status_ptr();

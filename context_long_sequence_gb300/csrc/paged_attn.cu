@@ -4,11 +4,16 @@
 // For one token row and query head, over the keys that it sees (its
 // sequence's own, up to the causal limit, and its prefix's):
 //   m = max_k s_k,  l = sum_k e^(s_k - m),  O = sum_k e^(s_k - m) v_k / l,
-//   LSE = m + ln l,   s_k = scale * q . k_k.
+//   LSE = m + ln l,   s_k = scale * q . k_k,
+// in one pass over the keys with running m and l.  The keys are cut into
+// equal shares for the whole card (PagedCut); a row whose keys fall to several
+// workers, or that has a prefix, is joined by its parts' log-sum-exp.
 //
-// One warp takes one (token, query head): lane i holds elements i, i + 32, ..
-// of the row, the running maximum and sum stay in fp32, one pass over the
-// keys.
+//   paged_small_kernel   entries of up to 64 rows (tokens x query heads of a
+//                        KV head): bound by reading the cache.
+//   paged_large_kernel   the others (paged_attn_large.cu).
+//   paged_merge_kernel   joins the parts.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #define CP_TU_ID ::cpattn::kTuPagedAttn
@@ -17,68 +22,457 @@
 namespace cpattn {
 namespace {
 
-constexpr int kWarps = 4;
+// ---------------------------------------------------------------- few rows
+//
+// A CTA walks its share of 64-key tiles with a ring of shared-memory stages:
+// warp 4 fetches (TMA boxes of up to one page, 128-byte swizzle; page numbers
+// one tile ahead), warps 0..3 compute with mma.sync (at these row counts the
+// tensor work is a fraction of the time its keys take to arrive, and a row
+// block of 16 wastes less than tcgen05's 128).  Two CTAs share an SM, each
+// with 96 KB of keys in flight.
+//
+// Up to 16 rows: the four warps take 16 keys of the tile each, with running
+// maxima and sums of their own, and meet only at the end of a segment.  Up to
+// 32 rows: two row blocks, two key halves; up to 64: a row block each.
+constexpr int kSmallThreads = 160;
+constexpr int kBox = 64;  // keys per stage
+
+template <int D>
+struct SmallSmem {
+  static constexpr int kHalf = kBox * 128;               // 64 columns of a tile, 128 bytes a row
+  static constexpr int kKV = kBox * D * 2;               // K or V of a stage
+  static constexpr int kStages = 96 * 1024 / (2 * kKV);  // 3 (d = 128) or 6
+  static constexpr int offJoin = kStages * 2 * kKV;      // two warps' O; first the walker's window sums
+  static constexpr int kJoin = 2 * 16 * D * 4;
+  static constexpr int offMl = offJoin + kJoin;          // [4 warps][16 rows] m, l
+  static constexpr int offBar = offMl + 4 * 16 * 8;
+  static constexpr int offMask = offBar + 2 * kStages * 8;  // boxes of the stage that hold keys
+  static constexpr int offAbort = offMask + kStages * 4;
+  static constexpr int kBytes = offAbort + 8;
+};
+static_assert(SmallSmem<128>::kJoin >= kMaxEntries / 32 * 8 && SmallSmem<64>::kJoin >= kMaxEntries / 32 * 8, "window sums");
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) paged_attn_kernel(const __grid_constant__ PagedAttnArgs args) {
+__global__ void __launch_bounds__(kSmallThreads, 2)
+    paged_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ PagedAttnArgs args, const PagedCut cut, int min_units, int box_rows) {
+  using SM = SmallSmem<D>;
+  constexpr int NH = D / 64, S = SM::kStages;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t s0 = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedGeom& g = args.g;
+  int32_t* status = args.status;
+  auto full = [&](int i) { return s0 + SM::offBar + 8u * i; };
+  auto empty = [&](int i) { return s0 + SM::offBar + 8u * (S + i); };
+  volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + SM::offMask);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::offAbort);
+  pdl_launch_dependents();
+  if (s0 & 1023) {  // the swizzle is a function of the address
+    debug_bounds_fail(status, __LINE__, CP_TU_ID);
+    pdl_wait();
+    return;
+  }
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  PagedWalker walk(g, cut, status);
+  const bool any = walk.start(reinterpret_cast<long long*>(smem + SM::offJoin), blockIdx.x, gridDim.x, min_units);
+  PagedSegment seg;
+  if (!any) {
+    // nothing for this worker
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ fetch
+    // Lane: one box of the tile, one 64-column half, K or V.
+    const int boxes = kBox / box_rows;
+    const int kv = lane & 1, half = (lane >> 1) % NH, box = (lane >> 1) / NH;
+    const bool mine = box < boxes;
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
+    const uint32_t dst0 = s0 + kv * SM::kKV + half * SM::kHalf + box * box_rows * 128;
+    const int page_mask = (1 << g.page_shift) - 1;
+    int n = 0;
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      auto page_of = [&](int tile) {
+        const int key = tile * kBox + box * box_rows;
+        return mine && tile < seg.tile1 && key < seg.keys ? seg.table[key >> g.page_shift] : -2;
+      };
+      int page = page_of(seg.tile0);
+      for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
+        const int ahead = page_of(tile + 1);
+        const int st = n % S;
+        ok = __all_sync(0xffffffffu, mbar_wait(empty(st), ((n / S) & 1) ^ 1, abort_flag, status));
+        if (!ok) break;
+        const int key = tile * kBox + box * box_rows;
+        bool load = page != -2;
+        if (load && !CP_CHECK_DATA(page >= 0 && page < g.num_pages, status)) load = false;
+        const uint32_t all = __ballot_sync(0xffffffffu, load);
+        if (lane == 0) {
+          uint32_t held = 0;
+          for (int b = 0; b < boxes; ++b) held |= ((all >> (2 * NH * b)) & 1u) << b;
+          mask[st] = held;
+          mbar_arrive_expect_tx(full(st), __popc(all) * box_rows * 128);
+        }
+        __syncwarp();
+        if (load) tma_load_4d(dst0 + st * 2 * SM::kKV, map, full(st), half * 64, key & page_mask, seg.h, page);
+        page = ahead;
+      }
+    }
+    if (!ok)  // let every copy still in flight land
+      for (int i = n < S ? 0 : n - S; i < n; ++i) mbar_wait(full(i % S), (i / S) & 1, nullptr, status);
+  } else {
+    // ------------------------------------------------------------ compute
+    const float sl2 = g.scale * 1.4426950408889634f;
+    const uint32_t box_all = (1u << (kBox / box_rows)) - 1;
+    const int box_shift = 31 - __clz(box_rows);
+    const int qr = lane >> 2, qc = 2 * (lane & 3);  // row and first column of the lane in an MMA fragment
+    // ldmatrix rows of the lane: K (16 keys x 16 columns) and V (the same, transposed on the way).
+    const int k_row = ((lane >> 4) << 3) + (lane & 7), k_piece = (lane >> 3) & 1;
+    const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_piece = lane >> 4;
+    float* ml = reinterpret_cast<float*>(smem + SM::offMl);
+    float4* join = reinterpret_cast<float4*>(smem + SM::offJoin);
+    int n = 0;
+    bool ok = true;
+    while (walk.next(seg)) {  // after a failed wait too: the warps' barriers stay in step
+      const int rows = seg.nt * g.G;
+      const int nrb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, nks = 4 / nrb;
+      const int rb = warp % nrb, ks = warp / nrb;
+      const int r0 = rb * 16 + qr, r1 = r0 + 8;
+      const int i0 = r0 / g.G, i1 = r1 / g.G;  // tokens of the lane's two rows
+      const int lim0 = r0 < rows ? min(seg.keys, seg.limit0 + i0) : 0;
+      const int lim1 = r1 < rows ? min(seg.keys, seg.limit0 + i1) : 0;
+      const int lim_all = min(seg.keys, seg.limit0);                  // seen by every row
+      const int lim_any = min(seg.keys, seg.limit0 + seg.nt - 1);     // seen by some row
+      uint32_t q[D / 16][4];
+      {
+        const T* p0 = static_cast<const T*>(args.q) + (seg.t0 + i0) * args.q_stride + (seg.h * g.G + r0 - i0 * g.G) * D + qc;
+        const T* p1 = static_cast<const T*>(args.q) + (seg.t0 + i1) * args.q_stride + (seg.h * g.G + r1 - i1 * g.G) * D + qc;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          q[k][0] = r0 < rows ? *reinterpret_cast<const uint32_t*>(p0 + k * 16) : 0u;
+          q[k][1] = r1 < rows ? *reinterpret_cast<const uint32_t*>(p1 + k * 16) : 0u;
+          q[k][2] = r0 < rows ? *reinterpret_cast<const uint32_t*>(p0 + k * 16 + 8) : 0u;
+          q[k][3] = r1 < rows ? *reinterpret_cast<const uint32_t*>(p1 + k * 16 + 8) : 0u;
+        }
+      }
+      float o[D / 8][4];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+      for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
+        const int st = n % S;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full(st), (n / S) & 1, abort_flag, status));
+        if (!ok) continue;
+        const uint32_t held = mask[st];
+        const bool clean = held == box_all && (tile + 1) * kBox <= lim_all;
+        const uint32_t sk = s0 + st * 2 * SM::kKV, sv = sk + SM::kKV;
+        for (int sl = ks; sl < 4; sl += nks) {
+          const int key0 = tile * kBox + sl * 16;
+          if (key0 >= lim_any) break;
+          // S = Q K^T for 16 rows x 16 keys, two chains per 8 keys.
+          float c[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+          const int kr = sl * 16 + k_row;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t b[4];
+            ldmatrix4<false>(b, sk + (k >> 2) * SM::kHalf + kr * 128 + ((((k & 3) * 2 + k_piece) ^ (kr & 7)) << 4));
+            mma16816<T>(c[(k & 1) * 2], q[k], b[0], b[1]);
+            mma16816<T>(c[(k & 1) * 2 + 1], q[k], b[2], b[3]);
+          }
+          float x[8];  // row r0: 0, 1, 4, 5; row r1: 2, 3, 6, 7
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = (c[0][i] + c[2][i]) * sl2;
+            x[4 + i] = (c[1][i] + c[3][i]) * sl2;
+          }
+          uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;  // V rows that hold keys, for the lane's two pairs
+          if (!clean) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const int in = sl * 16 + half * 8 + qc + j, key = tile * kBox + in;
+                const bool there = (held >> (in >> box_shift)) & 1u;
+                if (!there || key >= lim0) x[half * 4 + j] = -INFINITY;
+                if (!there || key >= lim1) x[half * 4 + 2 + j] = -INFINITY;
+                // What lies behind the last key may be anything, NaN included: 0 * NaN would reach O.
+                if (!there || key >= seg.keys) (half ? keep1 : keep0) &= j ? 0x0000ffffu : 0xffff0000u;
+              }
+          }
+          const float mx0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5]));
+          const float mx1 = fmaxf(fmaxf(x[2], x[3]), fmaxf(x[6], x[7]));
+          if (!__all_sync(0xffffffffu, mx0 <= m0 + Weight<T>::kSlack && mx1 <= m1 + Weight<T>::kSlack)) {
+            float t0 = mx0, t1 = mx1;
+#pragma unroll
+            for (int y = 1; y < 4; y <<= 1) {
+              t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, y));
+              t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, y));
+            }
+            const float n0 = t0 > m0 + Weight<T>::kSlack ? t0 : m0, n1 = t1 > m1 + Weight<T>::kSlack ? t1 : m1;
+            const float a0 = n0 > m0 ? ex2_approx(m0 - n0) : 1.f, a1 = n1 > m1 ? ex2_approx(m1 - n1) : 1.f;
+            m0 = n0;
+            m1 = n1;
+            l0 *= a0;
+            l1 *= a1;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[i][0] *= a0;
+              o[i][1] *= a0;
+              o[i][2] *= a1;
+              o[i][3] *= a1;
+            }
+          }
+          const float b0 = Weight<T>::kBias - (m0 == -INFINITY ? 0.f : m0), b1 = Weight<T>::kBias - (m1 == -INFINITY ? 0.f : m1);
+          float p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = ex2_approx(x[i] + ((i & 2) ? b1 : b0));
+          l0 += (p[0] + p[1]) + (p[4] + p[5]);
+          l1 += (p[2] + p[3]) + (p[6] + p[7]);
+          // The weights are rounded to the cache's type for the product with V;
+          // their sum is not.
+          const uint32_t pa[4] = {Elem<T>::pack(p[0], p[1]), Elem<T>::pack(p[2], p[3]), Elem<T>::pack(p[4], p[5]),
+                                  Elem<T>::pack(p[6], p[7])};
+          const int vr = sl * 16 + v_row;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t b[4];
+            ldmatrix4<true>(b, sv + (i >> 2) * SM::kHalf + vr * 128 + ((((i & 3) * 2 + v_piece) ^ (vr & 7)) << 4));
+            if (!clean) {
+              b[0] &= keep0;
+              b[1] &= keep1;
+              b[2] &= keep0;
+              b[3] &= keep1;
+            }
+            mma16816<T>(o[2 * i], pa, b[0], b[1]);
+            mma16816<T>(o[2 * i + 1], pa, b[2], b[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(st));
+      }
+
+      // Join the warps that shared the rows.
+#pragma unroll
+      for (int y = 1; y < 4; y <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, y);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, y);
+      }
+      if (nks > 1) {
+        if ((lane & 3) == 0) {
+          ml[(warp * 16 + qr) * 2] = m0;
+          ml[(warp * 16 + qr) * 2 + 1] = l0;
+          ml[(warp * 16 + qr + 8) * 2] = m1;
+          ml[(warp * 16 + qr + 8) * 2 + 1] = l1;
+        }
+        named_bar_sync(1, 128);
+        float n0 = -INFINITY, n1 = -INFINITY;
+        for (int k = 0; k < nks; ++k) {
+          n0 = fmaxf(n0, ml[((rb + nrb * k) * 16 + qr) * 2]);
+          n1 = fmaxf(n1, ml[((rb + nrb * k) * 16 + qr + 8) * 2]);
+        }
+        const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+        const float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
+        l0 = l1 = 0.f;
+        for (int k = 0; k < nks; ++k) {
+          const float* x = ml + ((rb + nrb * k) * 16 + qr) * 2;
+          l0 += x[1] * ex2_approx(x[0] - z0);
+          l1 += x[17] * ex2_approx(x[16] - z1);
+        }
+        m0 = n0;
+        m1 = n1;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f0;
+          o[i][2] *= f1;
+          o[i][3] *= f1;
+        }
+        // Four key shares: 2 and 3 hand over to 0 and 1, then 1 to 0; two: 1 to 0.
+        for (int step = nks / 2; step > 0; step >>= 1) {
+          const bool give = ks >= step && ks < 2 * step, take = ks < step;
+          float4* slot = join + ((give ? ks - step : ks) * nrb + rb) * (D / 8) * 32 + lane;
+          if (give)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+          named_bar_sync(1, 128);
+          if (take)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              const float4 y = slot[i * 32];
+              o[i][0] += y.x;
+              o[i][1] += y.y;
+              o[i][2] += y.z;
+              o[i][3] += y.w;
+            }
+          if (step > 1) named_bar_sync(1, 128);  // the slots are read before the next step fills them
+        }
+      }
+      if (ks == 0 && ok) {
+        const PagedTarget to = paged_target(args, walk, seg, 0, kSmallRows, rb == 0);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = half ? r1 : r0, i = half ? i1 : i0;
+          if (r >= rows) continue;
+          const float l = half ? l1 : l0, m = half ? m1 : m0;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const float lse2 = l > 0.f ? m + log2f(l) - Weight<T>::kBias : -INFINITY;
+          const int token = seg.t0 + i, head = seg.h * g.G + r - i * g.G;
+          const long long row = static_cast<long long>(token) * g.Hq + head;
+          if (to.final_rows && !args.out_fp32) {
+            T* dst = static_cast<T*>(args.o) + row * D + qc;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+              *reinterpret_cast<uint32_t*>(dst + j * 8) = Elem<T>::pack(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
+          } else {
+            const long long at = to.home ? to.row + row : to.row + r;
+            float* dst = (to.final_rows ? static_cast<float*>(args.o) + row * D : args.part_o + at * D) + qc;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+              *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
+            if (!to.final_rows && (lane & 3) == 0) args.part_lse[at] = lse2;
+          }
+          if (to.final_rows && (lane & 3) == 0)
+            args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
+        }
+      }
+    }
+  }
+  pdl_wait();  // a kernel that waits for this one also waits for those before it
+}
+
+// ---------------------------------------------------------------- merge
+//
+// O = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m) over a row's parts, its own
+// keys' first, then its prefix's, in key order.  A warp per (token, query
+// head); rows whose only part went straight to the output are left alone.
+constexpr int kMergeWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttnArgs args) {
   constexpr int E = D / 32;
   const PagedGeom& g = args.g;
   const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long w = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(w / g.Hq), h = static_cast<int>(w % g.Hq);
   if (t >= g.N) return;
   const int s = warp_count_le(g.q_start + 1, g.B, t);
   if (s >= g.B) return;
   const PagedEntry own = paged_entry(g, s);
-  if (!CP_CHECK_DATA(!own.bad, args.status) || t < own.t0 || t >= own.t0 + own.n) return;
+  if (own.bad || t < own.t0 || t >= own.t0 + own.n) return;
   const int p = warp_prefix_of(g, s);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+  const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
+  const int hk = h / g.G, sub = h - hk * g.G;
+  const PagedParts* parts = args.parts + static_cast<size_t>(t) * g.Hkv + hk;
+  PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
+  pdl_wait();
+  if (min(own.keys, own.limit0 + (t - own.t0)) > 0) a = *parts;
+  if (prefix) b = parts[static_cast<size_t>(args.max_tokens) * g.Hkv];
+  if (a.count == 1 && b.count == 0) return;
+  auto row_of = [&](int i) -> long long {
+    const PagedParts& x = i < a.count ? a : b;
+    if (i >= a.count) i -= a.count;
+    return (i == 0 ? x.first : static_cast<long long>(x.second) + static_cast<long long>(i - 1) * x.stride) + sub;
+  };
+  const int n = a.count + b.count;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, args.part_lse[row_of(i)]);
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = static_cast<float>(static_cast<const T*>(args.q)[t * args.q_stride + h * D + i * 32 + lane]) * g.scale;
-    o[i] = 0.f;
-  }
-  for (int part = p >= 0 ? 0 : 1; part < 2; ++part) {
-    const PagedEntry e = part ? own : paged_entry(g, g.B + p);
-    if (!CP_CHECK_DATA(!e.bad, args.status)) continue;
-    const int keys = min(e.keys, e.limit0 + (t - e.t0));
-    for (int k = 0; k < keys; ++k) {
-      const int page = e.table[k >> g.page_shift];
-      if (!CP_CHECK_DATA(page >= 0 && page < g.num_pages, args.status)) continue;
-      const int64_t at = page * g.page_stride + (k & ((1 << g.page_shift) - 1)) * g.token_stride + (h / g.G) * g.head_stride;
-      float dot = 0.f;
+  for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+  const float z = m == -INFINITY ? 0.f : m;
+  float sum = 0.f, o[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) dot = fmaf(q[i], static_cast<float>(static_cast<const T*>(args.k_cache)[at + i * 32 + lane]), dot);
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-      const float m_new = fmaxf(m, dot);
-      const float alpha = expf(m - m_new), pk = expf(dot - m_new);
-      m = m_new;
-      l = l * alpha + pk;
-#pragma unroll
-      for (int i = 0; i < E; ++i)
-        o[i] = fmaf(pk, static_cast<float>(static_cast<const T*>(args.v_cache)[at + i * 32 + lane]), o[i] * alpha);
+  for (int j = 0; j < E; ++j) o[j] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long row = row_of(i);
+    const float wt = ex2_approx(args.part_lse[row] - z);
+    sum += wt;
+    const float* src = args.part_o + row * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      o[0] = fmaf(wt, x.x, o[0]);
+      o[1] = fmaf(wt, x.y, o[1]);
+      o[2] = fmaf(wt, x.z, o[2]);
+      o[3] = fmaf(wt, x.w, o[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      o[0] = fmaf(wt, x.x, o[0]);
+      o[1] = fmaf(wt, x.y, o[1]);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const int64_t row = (static_cast<int64_t>(t) * g.Hq + h) * D;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const long long at = (static_cast<long long>(t) * g.Hq + h) * D + lane * E;
+  if (args.out_fp32) {
+    float* dst = static_cast<float*>(args.o) + at;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if (args.out_fp32)
-      static_cast<float*>(args.o)[row + i * 32 + lane] = o[i] * inv;
-    else
-      static_cast<T*>(args.o)[row + i * 32 + lane] = static_cast<T>(o[i] * inv);
+    for (int j = 0; j < E; ++j) dst[j] = o[j] * inv;
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[2 * j] * inv, o[2 * j + 1] * inv);
   }
-  if (lane == 0) args.lse[static_cast<int64_t>(h) * g.N + t] = l > 0.f ? m + logf(l) : -INFINITY;
+  if (lane == 0)
+    args.lse[static_cast<long long>(h) * g.N + t] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
+
+// ---------------------------------------------------------------- launch
 
 template <typename T, int D>
 int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
-  const long long warps = static_cast<long long>(a.g.N) * a.g.Hq;
-  const long long grid = (warps + kWarps - 1) / kWarps;
-  if (grid > 0x7fffffffLL) return CP_ERR_UNSUPPORTED;
-  paged_attn_kernel<T, D><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  const PagedGeom& g = a.g;
+  static std::atomic<int> small_known[64];
+  int sms = 0;
+  int rc = prepare_kernel(small_known, paged_small_kernel<T, D>, SmallSmem<D>::kBytes, &sms);
+  if (rc != CP_OK) return rc;
+  const int page = 1 << g.page_shift, box = page < kBox ? page : kBox;
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box)) return CP_ERR_CUDA;
+  const int workers = 2 * sms < kSmallWorkers ? 2 * sms : kSmallWorkers;
+  // Whether an entry may have more rows than this kernel takes.
+  const long long most = static_cast<long long>(g.NP > 0 || g.N < g.max_new ? g.N : g.max_new) * g.G;
+  const bool large = most > kSmallRows;
+  if (large && (rc = launch_paged_large(a, stream)) != CP_OK) return rc;
+  rc = launch(paged_small_kernel<T, D>, workers, kSmallThreads, SmallSmem<D>::kBytes, large, stream, mk, mv, a,
+              paged_cut_small(g.G), 1, box);
+  if (rc != CP_OK) return rc;
+  const long long grid = (static_cast<long long>(g.N) * g.Hq + kMergeWarps - 1) / kMergeWarps;
+  return launch(paged_merge_kernel<T, D>, static_cast<unsigned>(grid), kMergeWarps * 32, 0, true, stream, a);
 }
 
 }  // namespace

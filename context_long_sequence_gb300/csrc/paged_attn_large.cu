@@ -1,0 +1,513 @@
+// paged_attn_large.cu -- attention over the paged cache for entries of many
+// rows: a prefix with the rows of all its sequences, or a sequence with a
+// chunk of new tokens.
+//
+// Rows are (token, query head of the KV head) pairs, token by token; a token
+// tile holds two blocks of up to 128 rows, whole tokens each, that share
+// every K and V tile.  Per 128-key tile, as in the forward over whole
+// sequences (attn_fwd.cu):
+//
+//   S_t = Q_t K^T        tcgen05.mma, operands in shared memory, S in TMEM
+//   online softmax       one thread per row; P_t packed back over S_t
+//   O_t += P_t V         tcgen05.mma with A read from TMEM
+//
+// and the two row blocks ping-pong on the tensor core (issue order QK_0,
+// PV_1 of the tile before, QK_1, PV_0).  Unlike there, a CTA is one of 152
+// workers that each walk an equal share of the batch's units (PagedCut): a
+// batch has few token tiles and many keys, so the keys are what is shared
+// out, and the runs' (O, LSE) are merged.  K and V come page by page.
+//
+// At 256 rows a 128-key tile is 256 flops a byte, the card's own balance:
+// fewer rows are bound by the cache's bytes, more by the tensor core.
+//
+// Warps (320 threads): 0 fetches, 1 issues the MMAs (and holds the TMEM),
+// 2..5 and 6..9 load Q, take the softmax and write the rows of block 0 and 1.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#define CP_TU_ID ::cpattn::kTuPagedAttn
+#include "paged.cuh"
+
+namespace cpattn {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr uint32_t HALF_BYTES = 128 * 128;  // one 64-column swizzled half of a 128-row tile
+constexpr int kThreads = 320;
+constexpr int kSlots = 5;      // K/V ring: K of key tile j is load 2j, V load 2j + 1
+constexpr int kTileBars = 3;   // key tiles in flight at most
+
+enum Bar {
+  BAR_Q = 0,                             // both blocks' Q written (8 warps)
+  BAR_T_FULL = 1,                        // +key tile % kTileBars: its K and V landed
+  BAR_KV_EMPTY = 1 + kTileBars,          // +slot
+  BAR_S_FULL = 1 + kTileBars + kSlots,   // +block
+  BAR_P_HALF = 3 + kTileBars + kSlots,   // +block: P of keys 0-63 written
+  BAR_P_FULL = 5 + kTileBars + kSlots,   // +block
+  BAR_O = 7 + kTileBars + kSlots,        // +block: every MMA of the segment's block completed
+  NUM_BARS = 9 + kTileBars + kSlots
+};
+
+template <int D>
+struct LargeSmem {
+  static constexpr uint32_t kQ = BM * D * 2;
+  static constexpr uint32_t kKV = BN * D * 2;
+  static constexpr uint32_t offKV = 2 * kQ;
+  static constexpr uint32_t offBar = offKV + kSlots * kKV;
+  static constexpr uint32_t offMisc = offBar + NUM_BARS * 8;  // TMEM address, abort flag, box masks
+  static constexpr uint32_t kUsed = offMisc + 8 + kTileBars * 4;
+  // D = 64 is padded so that one CTA (and its 512 TMEM columns) is on an SM.
+  static constexpr uint32_t kBytes = kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
+};
+
+__device__ __forceinline__ bool warp_all(bool x) { return __all_sync(0xffffffffu, x); }
+
+// kind::f16 instruction descriptor: fp32 accumulator, A and B both T.
+template <typename T>
+constexpr uint32_t idesc(int n, int b_mn_major) {
+  const uint32_t d = idesc_bf16_f32(BM, n, b_mn_major);
+  return sizeof(T) == 2 && Weight<T>::kBias > 0.f ? d & ~((1u << 7) | (1u << 10)) : d;
+}
+
+// A row block's view of the keys: its first row sees keys below lo, its last
+// those below hi; hi == 0: no rows.
+struct RowBlock {
+  int lo, hi;
+  __device__ __forceinline__ bool sees(int key0) const { return key0 < hi; }
+};
+__device__ __forceinline__ RowBlock row_block(const PagedSegment& s, int t, int tokens) {
+  const int first = t * tokens, n = min(tokens, s.nt - first);
+  if (n <= 0) return RowBlock{0, 0};
+  return RowBlock{min(s.keys, s.limit0 + first), min(s.keys, s.limit0 + first + n - 1)};
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_large_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ PagedAttnArgs args, const PagedCut cut, int min_units, int box_rows) {
+  using SM = LargeSmem<D>;
+  constexpr int NH = D / 64;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t s0 = smem_u32(smem), sQ = s0, sKV = s0 + SM::offKV;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PagedGeom& g = args.g;
+  int32_t* status = args.status;
+  auto bar = [&](int i) { return s0 + SM::offBar + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::offMisc + 4);
+  volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + SM::offMisc + 8);
+  pdl_launch_dependents();
+  if (s0 & 1023) {  // the swizzle is a function of the address
+    debug_bounds_fail(status, __LINE__, CP_TU_ID);
+    return;
+  }
+  PagedWalker walk(g, cut, status);
+  // The walker's sums lie where K and V will; nothing has been fetched yet.
+  const bool any = walk.start(reinterpret_cast<long long*>(smem + SM::offKV), blockIdx.x, gridDim.x, min_units);
+  if (!any) return;  // the whole block
+  const int block_tokens = cut.tile_tokens / 2;
+  const uint32_t box_all = (1u << (BN / box_rows)) - 1;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    mbar_init(bar(BAR_Q), 8);
+    for (int i = 0; i < kTileBars; ++i) mbar_init(bar(BAR_T_FULL + i), 1);
+    for (int i = 0; i < kSlots; ++i) mbar_init(bar(BAR_KV_EMPTY + i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(BAR_S_FULL + i), 1);
+      mbar_init(bar(BAR_P_HALF + i), 4);
+      mbar_init(bar(BAR_P_FULL + i), 4);
+      mbar_init(bar(BAR_O + i), 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  fence_proxy_async_smem();  // the sums were read before the first copy lands on them
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S_t at 128 t (P_t packed in its first 64 columns), O_t at 256 + D t
+  PagedSegment seg;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ fetch
+    // Lane: one box of the tile, one 64-column half, K or V (at most 8 x 2 x 2).
+    const int boxes = BN / box_rows;
+    const int kv = lane & 1, half = (lane >> 1) % NH, box = (lane >> 1) / NH;
+    const bool mine = box < boxes;
+    const CUtensorMap* map = kv ? &tm_v : &tm_k;
+    const uint32_t dst0 = sKV + half * HALF_BYTES + box * box_rows * 128;
+    const int page_mask = (1 << g.page_shift) - 1;
+    int nt = 0;  // key tiles fetched
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      auto page_of = [&](int tile) {
+        const int key = tile * BN + box * box_rows;
+        return mine && tile < seg.tile1 && key < seg.keys ? seg.table[key >> g.page_shift] : -2;
+      };
+      int page = page_of(seg.tile0);
+      for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++nt) {
+        const int ahead = page_of(tile + 1);
+        const int n = 2 * nt, slk = n % kSlots, slv = (n + 1) % kSlots;
+        ok = warp_all(mbar_wait(bar(BAR_KV_EMPTY + slk), ((n / kSlots) & 1) ^ 1, abort_flag, status) &&
+                      mbar_wait(bar(BAR_KV_EMPTY + slv), (((n + 1) / kSlots) & 1) ^ 1, abort_flag, status));
+        if (!ok) break;
+        const uint32_t tb = bar(BAR_T_FULL + nt % kTileBars);
+        bool load = page != -2;
+        if (load && !CP_CHECK_DATA(page >= 0 && page < g.num_pages, status)) load = false;
+        const uint32_t all = __ballot_sync(0xffffffffu, load);
+        if (lane == 0) {
+          uint32_t held = 0;
+          for (int b = 0; b < boxes; ++b) held |= ((all >> (2 * NH * b)) & 1u) << b;
+          mask[nt % kTileBars] = held;
+          mbar_arrive_expect_tx(tb, __popc(all) * box_rows * 128);
+        }
+        __syncwarp();
+        const int key = tile * BN + box * box_rows;
+        if (load) tma_load_4d(dst0 + (kv ? slv : slk) * SM::kKV, map, tb, half * 64, key & page_mask, seg.h, page);
+        page = ahead;
+      }
+    }
+    if (!ok)  // let every copy still in flight land
+      for (int i = max(0, nt - kTileBars); i < nt; ++i)
+        mbar_wait(bar(BAR_T_FULL + i % kTileBars), (i / kTileBars) & 1, nullptr, status);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc_qk = idesc<T>(BN, 0), idesc_pv = idesc<T>(D, 1);
+    const uint64_t dq0 = smem_desc_sw128(sQ, 16, 1024), dq1 = smem_desc_sw128(sQ + SM::kQ, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(sKV, 16, 1024);          // slot 0 read as K (K-major)
+    const uint64_t dv0 = smem_desc_sw128(sKV, HALF_BYTES, 1024);  // slot 0 read as V (MN-major)
+    constexpr uint64_t kSlotStep = SM::kKV >> 4;
+    int npv[2] = {0, 0};   // PVs issued per block, over all segments
+    bool fresh[2] = {true, true};  // the segment's first PV overwrites O
+    auto issue_qk = [&](int t, int slot) {
+      const uint64_t a0 = t ? dq1 : dq0, b0 = dk0 + static_cast<uint64_t>(slot) * kSlotStep;
+      if constexpr (D == 128)
+        mma_bf16_ss_k128_warp<HALF_BYTES>(tmem + 128 * t, a0, b0, idesc_qk, 0u);
+      else
+        mma_bf16_ss_k64_warp(tmem + 128 * t, a0, b0, idesc_qk, 0u);
+      mma_commit_warp(bar(BAR_S_FULL + t));
+    };
+    auto issue_pv = [&](int t, int sl, bool release_v) -> bool {
+      if (!warp_all(mbar_wait(bar(BAR_P_HALF + t), npv[t] & 1, abort_flag, status))) return false;
+      tc_fence_after();
+      const uint64_t b0 = dv0 + static_cast<uint64_t>(sl) * kSlotStep;
+      mma_bf16_ts_k64_warp(tmem + 256 + D * t, tmem + 128 * t, b0, idesc_pv, fresh[t] ? 0u : 1u);
+      if (!warp_all(mbar_wait(bar(BAR_P_FULL + t), npv[t] & 1, abort_flag, status))) return false;
+      tc_fence_after();
+      mma_bf16_ts_k64_warp(tmem + 256 + D * t, tmem + 128 * t + 32, b0 + 512, idesc_pv, 1u);
+      if (release_v) mma_commit_warp(bar(BAR_KV_EMPTY + sl));
+      fresh[t] = false;
+      ++npv[t];
+      return true;
+    };
+    int j = 0, ring = 0, nseg = 0;  // key tiles walked, slot of the next K, segments
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      const RowBlock b0 = row_block(seg, 0, block_tokens), b1 = row_block(seg, 1, block_tokens);
+      fresh[0] = fresh[1] = true;
+      int pend = -1;  // V slot of a PV_1 still to issue
+      ok = warp_all(mbar_wait(bar(BAR_Q), nseg & 1, abort_flag, status));
+      for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
+        const bool v0 = b0.sees(tile * BN), v1 = b1.sees(tile * BN);
+        const int kslot = ring, vslot = ring + 1 == kSlots ? 0 : ring + 1;
+        ring = vslot + 1 == kSlots ? 0 : vslot + 1;
+        ok = warp_all(mbar_wait(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status));
+        if (!ok) break;
+        tc_fence_after();
+        if (v0) issue_qk(0, kslot);
+        if (pend >= 0) {
+          if (!(ok = issue_pv(1, pend, true))) break;
+          pend = -1;
+        }
+        if (v1) issue_qk(1, kslot);
+        mma_commit_warp(bar(BAR_KV_EMPTY + kslot));
+        if (v0 && !(ok = issue_pv(0, vslot, !v1))) break;
+        if (v1) pend = vslot;
+      }
+      mma_commit_warp(bar(BAR_O));  // block 0's rows are written while block 1's last PV runs
+      if (ok && pend >= 0) ok = issue_pv(1, pend, true);
+      mma_commit_warp(bar(BAR_O + 1));
+      ++nseg;
+    }
+    // Every MMA issued has completed before TMEM and shared memory are
+    // released: the last commit tracks them all.
+    if (nseg > 0) mbar_wait(bar(BAR_O + 1), (nseg - 1) & 1, nullptr, status);
+  } else {
+    // ------------------------------------------------------------ rows
+    const int t = (warp - 2) >> 2;  // row block
+    const int wq = warp & 3, row = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tSt = tmem + 128 * t + lane_off, tOt = tmem + 256 + D * t + lane_off;
+    const float sl2 = g.scale * 1.4426950408889634f;
+    constexpr float kBias = Weight<T>::kBias;
+    const int tok = row / g.G;  // of the block's, and query head within the KV head's
+    const int sub = row - tok * g.G;
+    int j = 0, k = 0, nseg = 0;  // key tiles walked, seen, segments
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      const RowBlock w = row_block(seg, t, block_tokens);
+      const int first = t * block_tokens;
+      const int n_rows = max(0, min(block_tokens, seg.nt - first)) * g.G;
+      const bool row_valid = row < n_rows;
+      const int my_lim = row_valid ? min(seg.keys, seg.limit0 + first + tok) : 0;
+      // Q: 16 bytes a thread and step, rows of the block that do not exist zero.
+      {
+        constexpr int P = D / 8;  // pieces of a row
+        const int piece = threadIdx.x % P;
+        const T* q0 = static_cast<const T*>(args.q) + (static_cast<long long>(seg.t0) + first) * args.q_stride +
+                      static_cast<long long>(seg.h) * g.G * D + piece * 8;
+        const uint32_t dst = sQ + t * SM::kQ + (piece >> 3) * HALF_BYTES;
+#pragma unroll 4
+        for (int r = ((threadIdx.x - 64) & 127) / P; r < BM; r += 128 / P) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (r < n_rows) {
+            const int i = r / g.G;
+            x = *reinterpret_cast<const uint4*>(q0 + i * args.q_stride + (r - i * g.G) * D);
+          }
+          st_shared_v4(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_Q));
+      }
+      float m = -INFINITY, l = 0.f;
+      const int k0 = k;
+      for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
+        const int key0 = tile * BN;
+        if (!w.sees(key0)) continue;
+        // K, V and the box mask of the tile are visible through the tile's barrier.
+        ok = warp_all(mbar_wait(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
+                      mbar_wait(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t held = mask[j % kTileBars];
+        const bool full = held == box_all && key0 + BN <= w.lo;
+        uint32_t sr[BN];
+        float* x = reinterpret_cast<float*>(sr);
+        auto col32 = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]); };
+        const f32x2 sl2x2 = make_f32x2(sl2, sl2);
+        auto exp32 = [&](int c, float mb, f32x2 (&rs2)[4], uint32_t (&pk)[16]) {
+          const f32x2 nmbx2 = make_f32x2(kBias - mb, kBias - mb);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float a0, a1;
+            split_f32x2(fma_f32x2(make_f32x2(x[c * 32 + e], x[c * 32 + e + 1]), sl2x2, nmbx2), a0, a1);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], make_f32x2(p0, p1));
+            pk[e >> 1] = Elem<T>::pack(p0, p1);
+          }
+        };
+        auto sum4 = [](const f32x2 (&rs2)[4]) {
+          float lo[4], hi[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split_f32x2(rs2[i], lo[i], hi[i]);
+          return ((lo[0] + hi[0]) + (lo[1] + hi[1])) + ((lo[2] + hi[2]) + (lo[3] + hi[3]));
+        };
+        auto signal = [&](int b) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(b + t));
+        };
+        // Wholly visible tile, running max set: keys 0-63 are exponentiated
+        // against it before any maximum is taken; their sum bounds each of
+        // them and the maximum of keys 64-127 the rest.
+        if (full && warp_all(m != -INFINITY || !row_valid)) {
+          const float mb = row_valid ? m : 0.f;
+          tmem_ld32(tSt, col32(0));
+          tmem_ld32(tSt + 32, col32(1));
+          tmem_wait_ld();
+          reg_fence(col32(0));
+          reg_fence(col32(1));
+          tmem_ld32(tSt + 64, col32(2));
+          tmem_ld32(tSt + 96, col32(3));
+          f32x2 rs2[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+          uint32_t pk0[16], pk1[16];
+          exp32(0, mb, rs2, pk0);
+          exp32(1, mb, rs2, pk1);
+          tmem_wait_ld();
+          reg_fence(col32(2));
+          reg_fence(col32(3));
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(x[64 + i], x[68 + i]);
+#pragma unroll
+          for (int e = 72; e < BN; e += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], x[e + i], x[e + 4 + i]);
+          const float mx_hi = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          const float s_lo = sum4(rs2);
+          if (warp_all(s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < mb + Weight<T>::kSpecMax)) {
+            tmem_st16(tSt, pk0);
+            tmem_st16(tSt + 16, pk1);
+            signal(BAR_P_HALF);
+            f32x2 rh[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+            exp32(2, mb, rh, pk0);
+            tmem_st16(tSt + 32, pk0);
+            exp32(3, mb, rh, pk1);
+            tmem_st16(tSt + 48, pk1);
+            signal(BAR_P_FULL);
+            l += s_lo + sum4(rh);
+            ++k;
+            continue;
+          }
+        }
+        // Masked tiles, the first of a segment, and tiles that outgrew the max.
+        if (held != box_all || key0 + BN > seg.keys) {
+          // V rows behind the last key (or in a page that was not fetched) may
+          // hold anything, NaN included; a zero weight does not remove a NaN.
+          const int box_shift = 31 - __clz(box_rows);
+          if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
+            const uint32_t v = sKV + ((2 * j + 1) % kSlots) * SM::kKV + row * 128;
+            for (int hh = 0; hh < NH; ++hh)
+              for (int b = 0; b < 8; ++b) st_shared_v4(v + hh * HALF_BYTES + b * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) tmem_ld32(tSt + c * 32, col32(c));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) reg_fence(col32(c));
+        if (!full) {
+          const int c_hi = my_lim - key0;
+#pragma unroll
+          for (int e = 0; e < BN; ++e)
+            if (e >= c_hi) x[e] = -INFINITY;
+          if (held != box_all) {
+            const int box_shift = 31 - __clz(box_rows);
+#pragma unroll
+            for (int e = 0; e < BN; e += 16)  // a box is 16 keys or more
+              if (!((held >> (e >> box_shift)) & 1u))
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[e + i] = -INFINITY;
+          }
+        }
+        float m8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(x[i], x[8 + i]);
+#pragma unroll
+        for (int e = 16; e < BN; e += 16)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m8[i] = fmax3(m8[i], x[e + i], x[e + 8 + i]);
+        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        const float m_new = fmaxf(m, mx * sl2);
+        float alpha = 1.f;
+        if (m_new > m + Weight<T>::kSlack) {
+          alpha = ex2_approx(m - m_new);
+          m = m_new;
+        }
+        const float mb = (m == -INFINITY) ? 0.f : m;
+        f32x2 rs2[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+        auto exp_chunk = [&](int c) {
+          uint32_t pk[16];
+          exp32(c, mb, rs2, pk);
+          tmem_st16(tSt + c * 16, pk);
+        };
+        exp_chunk(0);
+        exp_chunk(1);
+        if (k > k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(tOt + c * 32, ov);
+            tmem_wait_ld();
+            reg_fence(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+            tmem_st32(tOt + c * 32, ov);
+          }
+        }
+        signal(BAR_P_HALF);
+        exp_chunk(2);
+        exp_chunk(3);
+        signal(BAR_P_FULL);
+        l = l * alpha + sum4(rs2);
+        ++k;
+      }
+      // The block's MMAs of this segment have completed: O is whole, and Q's
+      // shared memory free for the next segment.
+      if (ok) ok = warp_all(mbar_wait(bar(BAR_O + t), nseg & 1, abort_flag, status));
+      ++nseg;
+      if (!ok) break;
+      tc_fence_after();
+      const PagedTarget to = paged_target(args, walk, seg, args.rows_small, kLargeRows, t == 0 && wq == 0);
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m + log2f(l) - kBias : -INFINITY;
+      const int token = seg.t0 + first + tok, head = seg.h * g.G + sub;
+      const long long out_row = static_cast<long long>(token) * g.Hq + head;
+      const long long at = to.home ? to.row + out_row : to.row + first * g.G + row;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t ov[32];
+        if (k > k0) {
+          tmem_ld32(tOt + c * 32, ov);
+          tmem_wait_ld();
+          reg_fence(ov);
+        }
+        if (!row_valid) continue;
+        float o[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = k > k0 ? __uint_as_float(ov[e]) * inv : 0.f;
+        if (to.final_rows && !args.out_fp32) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(args.o) + out_row * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            dst[e / 8] = make_uint4(Elem<T>::pack(o[e], o[e + 1]), Elem<T>::pack(o[e + 2], o[e + 3]),
+                                    Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(
+              (to.final_rows ? static_cast<float*>(args.o) + out_row * D : args.part_o + at * D) + c * 32);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      if (row_valid) {
+        if (to.final_rows)
+          args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
+        else
+          args.part_lse[at] = lse2;
+      }
+      tc_fence_before();  // O was read before this warp's next arrival lets a PV overwrite it
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <typename T, int D>
+int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
+  const PagedGeom& g = a.g;
+  static std::atomic<int> known[64];
+  int sms = 0;
+  int rc = prepare_kernel(known, paged_large_kernel<T, D>, LargeSmem<D>::kBytes, &sms);
+  if (rc != CP_OK) return rc;
+  const int page = 1 << g.page_shift, box = page < BN ? page : BN;
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box)) return CP_ERR_CUDA;
+  const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
+  return launch(paged_large_kernel<T, D>, workers, kThreads, LargeSmem<D>::kBytes, false, stream, mk, mv, a,
+                paged_cut_large(g.G), 1, box);
+}
+
+}  // namespace
+
+int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream) {
+  const bool bf16 = a.g.dtype == CP_DTYPE_BF16;
+  if (a.g.d == 128) return bf16 ? launch_large_d<__nv_bfloat16, 128>(a, stream) : launch_large_d<__half, 128>(a, stream);
+  if (a.g.d == 64) return bf16 ? launch_large_d<__nv_bfloat16, 64>(a, stream) : launch_large_d<__half, 64>(a, stream);
+  return CP_ERR_UNSUPPORTED;
+}
+
+}  // namespace cpattn

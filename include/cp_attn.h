@@ -360,9 +360,9 @@ typedef struct {
   int32_t Hq, Hkv;            /* query heads, KV heads; Hkv divides Hq, Hq/Hkv <= 128 */
   int32_t d;                  /* head dimension: 64 or 128 */
   int32_t page_size;          /* tokens per page: a power of two, 16 .. 65536 */
-  int32_t max_seqs;           /* most sequences, token rows and new tokens of one sequence */
-  int32_t max_tokens;         /* in a batch (2 * max_tokens * Hq < 2^30) */
-  int32_t max_new;
+  int32_t max_seqs;           /* most sequences of a batch (with max_prefixes at most 8192), */
+  int32_t max_tokens;         /* most token rows (2 * max_tokens * Hq < 2^30) */
+  int32_t max_new;            /* and most new tokens of one sequence */
   int32_t max_pages;          /* columns of page_table (max_pages * page_size < 2^30) */
   int32_t max_prefixes;       /* most prefixes of a batch; 0: none */
   int32_t max_prefix_pages;   /* columns of prefix_table (the same bound); 0 if max_prefixes is 0 */
@@ -437,7 +437,7 @@ int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const
  * hides from some rows of its sequence must be finite.
  * Deterministic: no atomics on results; the work is split by the batch's
  * lengths alone.
- * workspace: cp_paged_workspace_size() bytes (may be NULL when 0). */
+ * workspace: cp_paged_workspace_size() bytes. */
 int cp_attn_paged(const cp_paged_t *plan, const cp_paged_cache_t *cache, const cp_paged_batch_t *batch,
                   const void *q, int64_t q_stride, void *o, float *lse, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);
