@@ -209,7 +209,10 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        # The address alone: a torch.cuda.Stream object takes 3 us to make.
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -489,7 +492,8 @@ class PagedCache:
         if k.dim() != 4 or k.shape != v.shape or strides[0] != strides[1] or k.dtype != v.dtype or k.device != v.device \
                 or k.stride(3) != 1:
             _refuse("PagedCache", "k and v are [pages][page_size][Hkv][d] tensors alike, the last dimension contiguous")
-        self.k, self.v = k, v
+        self.k, self.v, self.device = k, v, k.device
+        self.page = (k.shape[1], k.shape[2], k.shape[3], k.dtype)
         self.c = cp_paged_cache_t(k.data_ptr(), v.data_ptr(), k.shape[0], *strides[0][:3])
         self.ref = ctypes.addressof(self.c)
 
@@ -528,60 +532,60 @@ class PagedBatch:
 def _paged_stream(where, plan, cache, batch, stream):
     """The checks that need the tensors' shapes, types and devices (the
     library sees addresses); the stream the call goes to."""
-    import torch
-    k = cache.k
-    if k.shape[1] != plan.page_size or k.shape[2] != plan.Hkv or k.shape[3] != plan.d or k.dtype != plan.dtype:
-        _refuse(where, f"the cache is {k.dtype} {tuple(k.shape)}, the plan's pages are {plan.dtype} "
-                       f"[{plan.page_size}][{plan.Hkv}][{plan.d}]")
+    if cache.page != (plan.page_size, plan.Hkv, plan.d, plan.dtype):
+        _refuse(where, f"the cache's pages are {cache.page}, the plan's {(plan.page_size, plan.Hkv, plan.d, plan.dtype)}")
     if batch.max_pages != plan.max_pages or (batch.n_prefixes and batch.max_prefix_pages != plan.max_prefix_pages):
         _refuse(where, "the page tables' columns differ from the plan's")
-    if batch.device != k.device:
-        _refuse(where, f"the batch is on {batch.device}, the cache on {k.device}")
-    if k.device.type != "cuda" or k.device.index != torch.cuda.current_device():
-        _refuse(where, f"the tensors are on {k.device}, which is not the current device")
+    if batch.device != cache.device:
+        _refuse(where, f"the batch is on {batch.device}, the cache on {cache.device}")
+    import torch
+    if cache.device.type != "cuda" or cache.device.index != torch._C._cuda_getDevice():
+        _refuse(where, f"the tensors are on {cache.device}, which is not the current device")
     return _stream(stream)
 
 
-def _tokens(where, name, x, batch, heads, d, dtype, device):
+def _tokens(where, name, x, n, heads, plan, device):
     """Address and token stride of a [n_tokens][heads][d] tensor."""
-    s = x.stride()
-    if x.dim() != 3 or x.shape[0] != batch.n_tokens or x.shape[1] != heads or x.shape[2] != d or x.dtype != dtype \
-            or s[2] != 1 or (heads > 1 and s[1] != d) or x.device != device:
-        _refuse(where, f"{name} is [{batch.n_tokens}][{heads}][{d}] {dtype} with contiguous heads on {device}, got "
+    s, d = x.stride(), plan.d
+    if x.shape != (n, heads, d) or x.dtype != plan.dtype or s[2] != 1 or (heads > 1 and s[1] != d) or x.device != device:
+        _refuse(where, f"{name} is [{n}][{heads}][{d}] {plan.dtype} with contiguous heads on {device}, got "
                        f"{x.dtype} {tuple(x.shape)} with strides {s} on {x.device}")
-    return x.data_ptr(), s[0] if x.shape[0] > 1 else heads * d
+    return x.data_ptr(), s[0] if n > 1 else heads * d
 
 
 def cp_cache_append(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, k, v, q_out=None, stream=None):
     where = "cp_cache_append"
     st = _paged_stream(where, plan, cache, batch, stream)
-    dev = cache.k.device
-    if q is not None and q_out is None:
-        _refuse(where, "q needs q_out")
-    qa = _tokens(where, "q", q, batch, plan.Hq, plan.d, plan.dtype, dev) if q is not None else (None, 0)
-    ka = _tokens(where, "k", k, batch, plan.Hkv, plan.d, plan.dtype, dev)
-    va = _tokens(where, "v", v, batch, plan.Hkv, plan.d, plan.dtype, dev)
-    oa = _tokens(where, "q_out", q_out, batch, plan.Hq, plan.d, plan.dtype, dev) if q is not None else (None, 0)
+    n, dev = batch.n_tokens, cache.device
+    qa = oa = (None, 0)
+    if q is not None:
+        if q_out is None:
+            _refuse(where, "q needs q_out")
+        qa = _tokens(where, "q", q, n, plan.Hq, plan, dev)
+        oa = _tokens(where, "q_out", q_out, n, plan.Hq, plan, dev)
+    ka = _tokens(where, "k", k, n, plan.Hkv, plan, dev)
+    va = _tokens(where, "v", v, n, plan.Hkv, plan, dev)
     rc = _L().cp_cache_append(plan._h, cache.ref, batch.ref, *qa, *ka, *va, *oa, st)
     if rc != CP_OK:
         _check(rc, where)
 
 
 def cp_attn_paged(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, o, lse, workspace=None, stream=None):
+    import torch
     where = "cp_attn_paged"
     st = _paged_stream(where, plan, cache, batch, stream)
-    dev = cache.k.device
-    qa = _tokens(where, "q", q, batch, plan.Hq, plan.d, plan.dtype, dev)
-    if tuple(o.shape) != (batch.n_tokens, plan.Hq, plan.d) or o.dtype != plan.o_dtype or not o.is_contiguous() \
-            or o.device != dev:
-        _refuse(where, f"o is a contiguous [{batch.n_tokens}][{plan.Hq}][{plan.d}] {plan.o_dtype} on {dev}")
-    if tuple(lse.shape) != (plan.Hq, batch.n_tokens) or lse.element_size() != 4 or not lse.is_floating_point() \
-            or not lse.is_contiguous() or lse.device != dev:
-        _refuse(where, f"lse is a contiguous [{plan.Hq}][{batch.n_tokens}] float32 on {dev}")
-    n = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if n and workspace.device != dev:
-        _refuse(where, f"the workspace is on {workspace.device}")
-    rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), _ptr(workspace), n, st)
+    n, dev = batch.n_tokens, cache.device
+    qa = _tokens(where, "q", q, n, plan.Hq, plan, dev)
+    if o.shape != (n, plan.Hq, plan.d) or o.dtype != plan.o_dtype or not o.is_contiguous() or o.device != dev:
+        _refuse(where, f"o is a contiguous [{n}][{plan.Hq}][{plan.d}] {plan.o_dtype} on {dev}")
+    if lse.shape != (plan.Hq, n) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        _refuse(where, f"lse is a contiguous [{plan.Hq}][{n}] float32 on {dev}")
+    wa = wn = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            _refuse(where, f"the workspace is a contiguous tensor on {dev}")
+        wa, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), wa, wn, st)
     if rc != CP_OK:
         _check(rc, where)
 

@@ -49,33 +49,43 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ long long shfl64(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
-// One run of key tiles of one token tile and KV head, as a worker gets it.
+// One run of key tiles of one token tile and KV head, as a worker gets it and
+// as the fetching warp hands it to the others through shared memory.
 struct PagedSegment {
-  int e, h;                   // entry, KV head
-  int t0, nt;                 // the tile's tokens
+  int t0, nt;                 // the tile's tokens; nt == 0: no more segments
+  int h;                      // KV head
   int keys, limit0;           // keys of the entry; token t0 + i sees min(keys, limit0 + i)
-  int tile0, tile1, tiles;    // this run, and all key tiles of the token tile
-  const int32_t* table;
-  int first_worker, parts;    // workers that share the token tile: consecutive
-  __device__ __forceinline__ bool complete() const { return parts == 1; }
+  int tile0, tile1;           // key tiles of this run
+  // Where the rows go: straight to o and lse (final), or to part rows: row of
+  // (token, head) is row + token * Hq + head (home), row r of the token tile
+  // is row + r (slot).
+  int mode, row;
 };
+enum : int { kRowsFinal = 0, kRowsHome = 1, kRowsSlot = 2 };
 
-// Walks a worker's units.  Every warp that needs the segments walks them by
-// itself: 32 entries at a time, an entry a lane.
+// Walks a worker's units, one warp, 32 entries at a time, an entry a lane.
 struct PagedWalker {
+  const PagedAttnArgs& a;
   const PagedGeom& g;
   const PagedCut cut;
   int32_t* status;
-  int E, workers, worker;
-  long long units, u, end;    // all units; this worker's next and last + 1
-  int base;                   // first entry of the window
+  const int slot_rows;         // rows of a worker's slot; `slots`: the kernel's first slot row
+  const int slots;
+  int E, worker;
+  PagedShares shares;
+  long long u, end;           // this worker's next unit and last + 1
+  int base = -1;              // first entry of the window; -1: none is held
   long long before;           // units before the window
+  const int32_t* table;       // page table of the last segment's entry
   // The lane's entry:
   PagedEntry entry;
   long long head_units, upto;  // its units of one head; units of the window up to and including it
 
-  __device__ __forceinline__ PagedWalker(const PagedGeom& g_, const PagedCut& c, int32_t* st)
-      : g(g_), cut(c), status(st), E(g_.B + g_.NP) {}
+  int covered0, covered1;      // sequences of some prefix: [covered0, covered1)
+
+  __device__ __forceinline__ PagedWalker(const PagedAttnArgs& args, const PagedCut& c, int slot_rows_, long long slots_)
+      : a(args), g(args.g), cut(c), status(args.status), slot_rows(slot_rows_), slots(static_cast<int>(slots_)),
+        E(args.g.B + args.g.NP), shares(0, 1, 1) {}
 
   __device__ __forceinline__ void load(int first) {
     const int lane = threadIdx.x & 31;
@@ -98,13 +108,15 @@ struct PagedWalker {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int windows = (E + 31) / 32;
     worker = worker_;
+    covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
+    covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
+    long long units = 0;
     if (windows > 1) {
       for (int w = warp; w < windows; w += warps) {
         load(w * 32);
         if (lane == 31) sums[w] = upto;
       }
       __syncthreads();
-      units = 0;
       for (int w0 = 0; w0 < windows; w0 += 32) {
         long long x = w0 + lane < windows ? sums[w0 + lane] : 0;
 #pragma unroll
@@ -114,52 +126,54 @@ struct PagedWalker {
     } else {
       load(0);
       units = shfl64(upto, 31);
-      before = 0;
     }
-    workers = paged_workers(units, max_workers, min_units);
-    const bool any = worker < workers;
-    u = any ? paged_first_unit(units, workers, worker) : 0;
-    end = any ? paged_first_unit(units, workers, worker + 1) : 0;
+    before = 0;
+    shares = PagedShares(units, max_workers, min_units);
+    const bool any = worker < shares.workers;
+    u = any ? shares.first(worker) : 0;
+    end = any ? shares.first(worker + 1) : 0;
     if (windows > 1) {
       int w = 0;
-      before = 0;
       if (any)
         while (w + 1 < windows && before + sums[w] <= u) before += sums[w++];
       __syncthreads();
-      if (any) load(w * 32);
+      if (any && base != w * 32) load(w * 32);
     }
     return any;
   }
 
-  // The next segment; warp-uniform.
-  __device__ __forceinline__ bool next(PagedSegment& s) {
-    if (u >= end) return false;
+  // The next segment (warp-uniform), nt == 0 behind the last.  The run that
+  // begins a token tile also records where the tile's parts are.
+  __device__ __forceinline__ PagedSegment next() {
+    PagedSegment s{0, 0, 0, 0, 0, 0, 0, 0, 0};
+    if (u >= end) return s;
     long long total = shfl64(upto, 31);
     while (u >= before + total) {
       if (base + 32 >= E) {  // only where the arrays changed under the kernel
         end = u;
-        return false;
+        return s;
       }
       before += total;
       load(base + 32);
       total = shfl64(upto, 31);
     }
     long long rel = u - before;
-    const int at = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;  // exists: rel < total
     const long long hu = shfl64(head_units, at);
     rel -= shfl64(upto, at) - hu * g.Hkv;
+    const int id = base + at;
     PagedEntry e;
-    s.e = base + at;
     e.t0 = __shfl_sync(0xffffffffu, entry.t0, at);
     e.n = __shfl_sync(0xffffffffu, entry.n, at);
     e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
     e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
-    s.table = s.e < g.B ? g.page_table + static_cast<size_t>(s.e) * g.table_stride
-                        : g.prefix_table + static_cast<size_t>(s.e - g.B) * g.prefix_stride;
-    s.h = static_cast<int>(rel / hu);
+    const bool prefix = id >= g.B;
+    table = prefix ? g.prefix_table + static_cast<size_t>(id - g.B) * g.prefix_stride
+                   : g.page_table + static_cast<size_t>(id) * g.table_stride;
+    s.h = static_cast<int>(paged_div(rel, hu));
     rel -= s.h * hu;
     int rb = 0, tiles = paged_tile_units(cut, e, 0);
-    while (rel >= tiles) {
+    while (rel >= tiles && (rb + 1) * cut.tile_tokens < e.n) {
       rel -= tiles;
       tiles = paged_tile_units(cut, e, ++rb);
     }
@@ -167,59 +181,34 @@ struct PagedWalker {
     s.nt = min(cut.tile_tokens, e.n - rb * cut.tile_tokens);
     s.keys = e.keys;
     s.limit0 = e.limit0 + rb * cut.tile_tokens;
-    s.tiles = tiles;
     s.tile0 = static_cast<int>(rel);
     s.tile1 = static_cast<int>(min(static_cast<long long>(tiles), rel + (end - u)));
     const long long u0 = u - s.tile0;
-    s.first_worker = s.tile0 == 0 ? worker : paged_worker_of(units, workers, u0);
-    s.parts = (s.tile1 == tiles ? worker : paged_worker_of(units, workers, u0 + tiles - 1)) - s.first_worker + 1;
     u += s.tile1 - s.tile0;
-    return true;
-  }
-};
-
-// Whether sequence s (a valid entry) has a prefix with keys.  Warp-wide.
-__device__ __forceinline__ bool warp_has_prefix(const PagedGeom& g, int s) {
-  const int p = warp_prefix_of(g, s);
-  return p >= 0 && paged_entry(g, g.B + p).keys > 0;
-}
-
-// Where a segment's rows go: the output, or part rows from `row` on.
-struct PagedTarget {
-  bool final_rows;   // straight to o and lse
-  bool home;         // row of (token, head) is home + token * Hq + head
-  long long row;     // slot: row r of the token tile is row + r
-};
-
-// Target of a segment, and (for the run that begins its token tile) the
-// record of the tile's parts.  `slots` is the kernel's first slot row,
-// `slot_rows` the rows of one.  Warp-wide.
-__device__ __forceinline__ PagedTarget paged_target(const PagedAttnArgs& a, const PagedWalker& w, const PagedSegment& s,
-                                                    long long slots, int slot_rows, bool record) {
-  const PagedGeom& g = a.g;
-  const bool prefix = s.e >= g.B;
-  PagedTarget t{false, false, 0};
-  const long long home = a.rows_large_end + (prefix ? static_cast<long long>(a.max_tokens) * g.Hq : 0);
-  if (s.complete()) {
-    t.final_rows = !prefix && !warp_has_prefix(g, s.e);
-    t.home = !t.final_rows;
-    t.row = home;
-  } else {
-    t.row = slots + (2LL * w.worker + (s.tile0 == 0 ? 1 : 0)) * slot_rows;
-  }
-  if (record && s.tile0 == 0) {
-    PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
-    for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
-      PagedParts r;
-      r.first = static_cast<int>(t.home ? home + static_cast<long long>(s.t0 + i) * g.Hq + s.h * g.G : t.row + i * g.G);
-      r.second = static_cast<int>(slots + 2LL * (s.first_worker + 1) * slot_rows + i * g.G);
-      r.count = s.parts;
-      r.stride = 2 * slot_rows;
-      parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
+    const bool begins = s.tile0 == 0, whole = begins && s.tile1 == tiles;
+    const int home = static_cast<int>(a.rows_large_end) + (prefix ? a.max_tokens * g.Hq : 0);
+    if (whole) {
+      s.mode = prefix || (id >= covered0 && id < covered1) ? kRowsHome : kRowsFinal;
+      s.row = home;
+    } else {
+      s.mode = kRowsSlot;
+      s.row = slots + (2 * worker + (begins ? 1 : 0)) * slot_rows;
     }
+    if (begins) {
+      const int last = whole ? worker : shares.worker_of(u0 + tiles - 1);
+      PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
+      for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
+        PagedParts r;
+        r.first = s.mode == kRowsSlot ? s.row + i * g.G : s.row + (s.t0 + i) * g.Hq + s.h * g.G;
+        r.second = slots + 2 * (worker + 1) * slot_rows + i * g.G;
+        r.count = last - worker + 1;
+        r.stride = 2 * slot_rows;
+        parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
+      }
+    }
+    return s;
   }
-  return t;
-}
+};
 
 template <typename T>
 struct Elem;

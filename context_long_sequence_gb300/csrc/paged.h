@@ -96,20 +96,21 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 // on the batch's lengths alone, so the result does too.
 struct PagedCut {
   int min_rows, max_rows;
-  int tile_tokens, tile_keys;
+  int tile_tokens, key_shift;  // tiles of 2^key_shift keys
 };
 
 // Key tiles that token tile `rb` of entry `e` sees.
 __host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEntry& e, int rb) {
   const int last = (rb + 1) * c.tile_tokens < e.n ? (rb + 1) * c.tile_tokens - 1 : e.n - 1;
   const int seen = e.limit0 + last < e.keys ? e.limit0 + last : e.keys;
-  return seen > 0 ? (seen + c.tile_keys - 1) / c.tile_keys : 0;
+  return seen > 0 ? (seen + (1 << c.key_shift) - 1) >> c.key_shift : 0;
 }
 
 // Units of entry `e` for one KV head.
 __host__ __device__ inline long long paged_head_units(const PagedGeom& g, const PagedCut& c, const PagedEntry& e) {
   const long long rows = static_cast<long long>(e.n) * g.G;
   if (e.n <= 0 || rows < c.min_rows || rows > c.max_rows) return 0;
+  if (e.n <= c.tile_tokens) return paged_tile_units(c, e, 0);
   const int tiles = (e.n + c.tile_tokens - 1) / c.tile_tokens;
   if (e.limit0 >= e.keys) return static_cast<long long>(tiles) * paged_tile_units(c, e, 0);  // all rows see all keys
   long long sum = 0;
@@ -117,33 +118,46 @@ __host__ __device__ inline long long paged_head_units(const PagedGeom& g, const 
   return sum;
 }
 
-// Workers that get units: each at least `min_units`, so that a short batch is
-// not cut finer than its merge costs.
-__host__ __device__ inline int paged_workers(long long units, int workers, int min_units) {
-  const long long w = (units + min_units - 1) / min_units;
-  return w < workers ? static_cast<int>(w) : workers;
+// Quotient of numbers that nearly always fit in 32 bits: a 64-bit division
+// takes the device some 500 clocks, and a worker's start is a chain of them.
+__host__ __device__ inline long long paged_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
-__host__ __device__ inline long long paged_first_unit(long long units, int workers, int w) {
-  return units * w / workers;
-}
-// The worker of unit u.
-__host__ __device__ inline int paged_worker_of(long long units, int workers, long long u) {
-  return static_cast<int>(((u + 1) * workers - 1) / units);
-}
+
+// `units` in `workers` contiguous shares, the first `extra` one larger.  At
+// least min_units each, so that a short batch is not cut finer than its merge
+// costs.
+struct PagedShares {
+  long long units, per;
+  int workers, extra;
+  __host__ __device__ PagedShares(long long n, int max_workers, int min_units) : units(n), per(0), workers(0), extra(0) {
+    if (n <= 0) return;
+    const long long most = paged_div(n + min_units - 1, min_units);
+    workers = most < max_workers ? static_cast<int>(most) : max_workers;
+    per = paged_div(n, workers);
+    extra = static_cast<int>(n - per * workers);
+  }
+  __host__ __device__ long long first(int w) const { return w * per + (w < extra ? w : extra); }
+  __host__ __device__ int worker_of(long long u) const {
+    const long long large = extra * (per + 1);
+    return static_cast<int>(u < large ? paged_div(u, per + 1) : extra + paged_div(u - large, per));
+  }
+};
 
 // Workers and slots.  A worker holds at most two incomplete token tiles: the
 // one its share begins in (its slot 2w) and the one its share ends in (slot
 // 2w + 1); a part that is complete but has a partner (own keys and a prefix)
 // goes to a home row of its own.
-constexpr int kSmallWorkers = 304, kSmallRows = 64, kSmallKeys = 64;
-constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeys = 128;
+constexpr int kSmallWorkers = 304, kSmallRows = 64, kSmallKeyShift = 6;
+constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
 constexpr int kMaxEntries = 8192;
 
 inline __host__ __device__ PagedCut paged_cut_small(int G) {
-  return PagedCut{1, kSmallRows, G <= kSmallRows ? kSmallRows / G : 1, kSmallKeys};
+  return PagedCut{1, kSmallRows, G <= kSmallRows ? kSmallRows / G : 1, kSmallKeyShift};
 }
 inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kSmallRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeys};
+  return PagedCut{kSmallRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift};
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.

@@ -16,6 +16,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #define CP_TU_ID ::cpattn::kTuPagedAttn
 #include "paged.cuh"
 
@@ -42,14 +44,19 @@ struct SmallSmem {
   static constexpr int kHalf = kBox * 128;               // 64 columns of a tile, 128 bytes a row
   static constexpr int kKV = kBox * D * 2;               // K or V of a stage
   static constexpr int kStages = 96 * 1024 / (2 * kKV);  // 3 (d = 128) or 6
-  static constexpr int offJoin = kStages * 2 * kKV;      // two warps' O; first the walker's window sums
+  static constexpr int offJoin = kStages * 2 * kKV;      // half of four warps' O; first the walker's window sums
   static constexpr int kJoin = 2 * 16 * D * 4;
   static constexpr int offMl = offJoin + kJoin;          // [4 warps][16 rows] m, l
-  static constexpr int offBar = offMl + 4 * 16 * 8;
-  static constexpr int offMask = offBar + 2 * kStages * 8;  // boxes of the stage that hold keys
+  // Segments on their way: one more than stages, so that the segment whose
+  // place is taken has given its last stage back.
+  static constexpr int kSegs = kStages + 1;
+  static constexpr int offBar = offMl + 4 * 16 * 8;      // full, empty (stages), segment, join, read
+  static constexpr int offSeg = offBar + (2 * kStages + kSegs + 2) * 8;
+  static constexpr int offMask = offSeg + kSegs * static_cast<int>(sizeof(PagedSegment));  // boxes of the stage that hold keys
   static constexpr int offAbort = offMask + kStages * 4;
-  static constexpr int kBytes = offAbort + 8;
+  static constexpr int kBytes = offAbort + 4;
 };
+static_assert(2 * (SmallSmem<128>::kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 static_assert(SmallSmem<128>::kJoin >= kMaxEntries / 32 * 8 && SmallSmem<64>::kJoin >= kMaxEntries / 32 * 8, "window sums");
 
 template <typename T>
@@ -90,6 +97,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
   int32_t* status = args.status;
   auto full = [&](int i) { return s0 + SM::offBar + 8u * i; };
   auto empty = [&](int i) { return s0 + SM::offBar + 8u * (S + i); };
+  auto seg_full = [&](int i) { return s0 + SM::offBar + 8u * (2 * S + i); };
+  const uint32_t join_bar = s0 + SM::offBar + 8u * (2 * S + SM::kSegs), read_bar = join_bar + 8;
+  PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
   volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + SM::offMask);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::offAbort);
   pdl_launch_dependents();
@@ -105,13 +115,15 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
       mbar_init(full(i), 1);
       mbar_init(empty(i), 4);
     }
+    for (int i = 0; i < SM::kSegs; ++i) mbar_init(seg_full(i), 1);
+    mbar_init(join_bar, 4);
+    mbar_init(read_bar, 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
-  PagedWalker walk(g, cut, status);
+  PagedWalker walk(args, cut, kSmallRows, 0);
   const bool any = walk.start(reinterpret_cast<long long*>(smem + SM::offJoin), blockIdx.x, gridDim.x, min_units);
-  PagedSegment seg;
   if (!any) {
     // nothing for this worker
   } else if (warp == 4) {
@@ -123,12 +135,19 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const uint32_t dst0 = s0 + kv * SM::kKV + half * SM::kHalf + box * box_rows * 128;
     const int page_mask = (1 << g.page_shift) - 1;
-    int n = 0;
+    int n = 0, nseg = 0;
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    while (ok) {
+      const PagedSegment seg = walk.next();
+      if (lane == 0) {
+        segs[nseg % SM::kSegs] = seg;
+        mbar_arrive(seg_full(nseg % SM::kSegs));
+      }
+      ++nseg;
+      if (seg.nt == 0) break;
       auto page_of = [&](int tile) {
         const int key = tile * kBox + box * box_rows;
-        return mine && tile < seg.tile1 && key < seg.keys ? seg.table[key >> g.page_shift] : -2;
+        return mine && tile < seg.tile1 && key < seg.keys ? walk.table[key >> g.page_shift] : -2;
       };
       int page = page_of(seg.tile0);
       for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
@@ -164,9 +183,21 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
     const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_piece = lane >> 4;
     float* ml = reinterpret_cast<float*>(smem + SM::offMl);
     float4* join = reinterpret_cast<float4*>(smem + SM::offJoin);
-    int n = 0;
+    int n = 0, nseg = 0;
+    uint32_t joins = 0, njoin = 0;
     bool ok = true;
-    while (walk.next(seg)) {  // after a failed wait too: the warps' barriers stay in step
+    // All four warps here: a bounded wait, unlike a hardware barrier.
+    auto join_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(join_bar);
+      return __all_sync(0xffffffffu, mbar_wait(join_bar, joins++ & 1, abort_flag, status));
+    };
+    while (true) {
+      ok = __all_sync(0xffffffffu, mbar_wait(seg_full(nseg % SM::kSegs), (nseg / SM::kSegs) & 1, abort_flag, status));
+      if (!ok) break;
+      const PagedSegment seg = segs[nseg % SM::kSegs];
+      ++nseg;
+      if (seg.nt == 0) break;
       const int rows = seg.nt * g.G;
       const int nrb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, nks = 4 / nrb;
       const int rb = warp % nrb, ks = warp / nrb;
@@ -195,8 +226,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 
       for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
         const int st = n % S;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(full(st), (n / S) & 1, abort_flag, status));
-        if (!ok) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(full(st), (n / S) & 1, abort_flag, status));
+        if (!ok) break;
         const uint32_t held = mask[st];
         const bool clean = held == box_all && (tile + 1) * kBox <= lim_all;
         const uint32_t sk = s0 + st * 2 * SM::kKV, sv = sk + SM::kKV;
@@ -287,88 +318,117 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
         if (lane == 0) mbar_arrive(empty(st));
       }
 
-      // Join the warps that shared the rows.
+      if (!ok) break;
+
+      // Join the warps that shared the rows.  Each pair (w, w ^ 2) swaps
+      // halves of the columns, then, where four warps share, (w, w ^ 1)
+      // quarters, so every warp ends with the whole sum of its share of the
+      // columns and all four write.
 #pragma unroll
       for (int y = 1; y < 4; y <<= 1) {
         l0 += __shfl_xor_sync(0xffffffffu, l0, y);
         l1 += __shfl_xor_sync(0xffffffffu, l1, y);
       }
+      constexpr int H = D / 16, Q = D / 32;  // 8-column pieces of half and a quarter of a row
+      int col = 0, pieces = D / 8;           // the warp's share
       if (nks > 1) {
+        const bool upper = warp & 2;
+        // The last readers of these places were two joins ago or have passed `read_bar`.
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(read_bar, (njoin & 1) ^ 1, abort_flag, status)))) break;
         if ((lane & 3) == 0) {
           ml[(warp * 16 + qr) * 2] = m0;
           ml[(warp * 16 + qr) * 2 + 1] = l0;
           ml[(warp * 16 + qr + 8) * 2] = m1;
           ml[(warp * 16 + qr + 8) * 2 + 1] = l1;
         }
-        named_bar_sync(1, 128);
+        float4* give = join + (warp ^ 2) * H * 32 + lane;
+        float4* got = join + warp * H * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < H; ++i)
+          give[i * 32] = upper ? make_float4(o[i][0], o[i][1], o[i][2], o[i][3])
+                               : make_float4(o[H + i][0], o[H + i][1], o[H + i][2], o[H + i][3]);
+        if (!(ok = join_sync())) break;
         float n0 = -INFINITY, n1 = -INFINITY;
         for (int k = 0; k < nks; ++k) {
-          n0 = fmaxf(n0, ml[((rb + nrb * k) * 16 + qr) * 2]);
-          n1 = fmaxf(n1, ml[((rb + nrb * k) * 16 + qr + 8) * 2]);
+          const float* x = ml + ((rb + nrb * k) * 16 + qr) * 2;
+          n0 = fmaxf(n0, x[0]);
+          n1 = fmaxf(n1, x[16]);
         }
         const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-        const float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
         l0 = l1 = 0.f;
         for (int k = 0; k < nks; ++k) {
           const float* x = ml + ((rb + nrb * k) * 16 + qr) * 2;
           l0 += x[1] * ex2_approx(x[0] - z0);
           l1 += x[17] * ex2_approx(x[16] - z1);
         }
+        const float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
+        const float* x = ml + ((warp ^ 2) * 16 + qr) * 2;
+        const float g0 = ex2_approx(x[0] - z0), g1 = ex2_approx(x[16] - z1);
         m0 = n0;
         m1 = n1;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][0] *= f0;
-          o[i][1] *= f0;
-          o[i][2] *= f1;
-          o[i][3] *= f1;
+        for (int i = 0; i < H; ++i) {
+          const float4 y = got[i * 32];
+          o[i][0] = (upper ? o[H + i][0] : o[i][0]) * f0 + y.x * g0;
+          o[i][1] = (upper ? o[H + i][1] : o[i][1]) * f0 + y.y * g0;
+          o[i][2] = (upper ? o[H + i][2] : o[i][2]) * f1 + y.z * g1;
+          o[i][3] = (upper ? o[H + i][3] : o[i][3]) * f1 + y.w * g1;
         }
-        // Four key shares: 2 and 3 hand over to 0 and 1, then 1 to 0; two: 1 to 0.
-        for (int step = nks / 2; step > 0; step >>= 1) {
-          const bool give = ks >= step && ks < 2 * step, take = ks < step;
-          float4* slot = join + ((give ? ks - step : ks) * nrb + rb) * (D / 8) * 32 + lane;
-          if (give)
+        col = upper ? D / 2 : 0;
+        pieces = H;
+        if (nks == 4) {
+          const bool odd = warp & 1;
+          // Over what this warp has just read; only its partner reads it there.
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) slot[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-          named_bar_sync(1, 128);
-          if (take)
+          for (int i = 0; i < Q; ++i)
+            got[i * 32] = odd ? make_float4(o[i][0], o[i][1], o[i][2], o[i][3])
+                              : make_float4(o[Q + i][0], o[Q + i][1], o[Q + i][2], o[Q + i][3]);
+          if (!(ok = join_sync())) break;
+          const float4* other = join + (warp ^ 1) * H * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              const float4 y = slot[i * 32];
-              o[i][0] += y.x;
-              o[i][1] += y.y;
-              o[i][2] += y.z;
-              o[i][3] += y.w;
-            }
-          if (step > 1) named_bar_sync(1, 128);  // the slots are read before the next step fills them
-        }
-      }
-      if (ks == 0 && ok) {
-        const PagedTarget to = paged_target(args, walk, seg, 0, kSmallRows, rb == 0);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int r = half ? r1 : r0, i = half ? i1 : i0;
-          if (r >= rows) continue;
-          const float l = half ? l1 : l0, m = half ? m1 : m0;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          const float lse2 = l > 0.f ? m + log2f(l) - Weight<T>::kBias : -INFINITY;
-          const int token = seg.t0 + i, head = seg.h * g.G + r - i * g.G;
-          const long long row = static_cast<long long>(token) * g.Hq + head;
-          if (to.final_rows && !args.out_fp32) {
-            T* dst = static_cast<T*>(args.o) + row * D + qc;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              *reinterpret_cast<uint32_t*>(dst + j * 8) = Elem<T>::pack(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
-          } else {
-            const long long at = to.home ? to.row + row : to.row + r;
-            float* dst = (to.final_rows ? static_cast<float*>(args.o) + row * D : args.part_o + at * D) + qc;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
-            if (!to.final_rows && (lane & 3) == 0) args.part_lse[at] = lse2;
+          for (int i = 0; i < Q; ++i) {
+            const float4 y = other[i * 32];
+            o[i][0] = (odd ? o[Q + i][0] : o[i][0]) + y.x;
+            o[i][1] = (odd ? o[Q + i][1] : o[i][1]) + y.y;
+            o[i][2] = (odd ? o[Q + i][2] : o[i][2]) + y.z;
+            o[i][3] = (odd ? o[Q + i][3] : o[i][3]) + y.w;
           }
-          if (to.final_rows && (lane & 3) == 0)
+          col += odd ? D / 4 : 0;
+          pieces = Q;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(read_bar);
+        ++njoin;
+      }
+      const bool final_rows = seg.mode == kRowsFinal;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = half ? r1 : r0, i = half ? i1 : i0;
+        if (r >= rows) continue;
+        const float l = half ? l1 : l0, m = half ? m1 : m0;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int token = seg.t0 + i, head = seg.h * g.G + r - i * g.G;
+        const long long row = static_cast<long long>(token) * g.Hq + head;
+        const long long at = seg.row + (seg.mode == kRowsHome ? row : r);
+        if (final_rows && !args.out_fp32) {
+          T* dst = static_cast<T*>(args.o) + row * D + col + qc;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            if (j < pieces)
+              *reinterpret_cast<uint32_t*>(dst + j * 8) = Elem<T>::pack(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
+        } else {
+          float* dst = (final_rows ? static_cast<float*>(args.o) + row * D : args.part_o + at * D) + col + qc;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            if (j < pieces)
+              *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * half] * inv, o[j][2 * half + 1] * inv);
+        }
+        if (ks == 0 && (lane & 3) == 0) {
+          const float lse2 = l > 0.f ? m + log2f(l) - Weight<T>::kBias : -INFINITY;
+          if (final_rows)
             args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
+          else
+            args.part_lse[at] = lse2;
         }
       }
     }
@@ -379,76 +439,119 @@ __global__ void __launch_bounds__(kSmallThreads, 2)
 // ---------------------------------------------------------------- merge
 //
 // O = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m) over a row's parts, its own
-// keys' first, then its prefix's, in key order.  A warp per (token, query
-// head); rows whose only part went straight to the output are left alone.
+// keys' first, then its prefix's, in key order; rows whose only part went
+// straight to the output are left alone.  What it reads is in L2 and small, so
+// its time is latency: a lane asks for eight parts at once, and with few rows
+// (SPLIT) the four warps of a block share the parts of one row.
 constexpr int kMergeWarps = 4;
+constexpr int kMergeAhead = 8;
+constexpr long long kMergeSplitRows = 2048;
 
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttnArgs args) {
   constexpr int E = D / 32;
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ float joint[SPLIT ? kMergeWarps : 1][32][E + 2];
   const PagedGeom& g = args.g;
-  const int lane = threadIdx.x & 31;
-  const long long w = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w / g.Hq), h = static_cast<int>(w % g.Hq);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // SPLIT: a block per (token, query head); else a warp per (token, KV head).
+  const long long w = SPLIT ? static_cast<long long>(blockIdx.x) : static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
+  const int per_token = SPLIT ? g.Hq : g.Hkv;
+  const int t = static_cast<int>(w / per_token), x = static_cast<int>(w % per_token);
   if (t >= g.N) return;
   const int s = warp_count_le(g.q_start + 1, g.B, t);
   if (s >= g.B) return;
   const PagedEntry own = paged_entry(g, s);
   if (own.bad || t < own.t0 || t >= own.t0 + own.n) return;
   const int p = warp_prefix_of(g, s);
+  const bool covered = g.NP > 0 && s >= g.prefix_first[0] && s < g.prefix_first[g.NP];  // as PagedWalker has it
   const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
-  const int hk = h / g.G, sub = h - hk * g.G;
+  const int hk = SPLIT ? x / g.G : x;
   const PagedParts* parts = args.parts + static_cast<size_t>(t) * g.Hkv + hk;
   PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
   pdl_wait();
   if (min(own.keys, own.limit0 + (t - own.t0)) > 0) a = *parts;
   if (prefix) b = parts[static_cast<size_t>(args.max_tokens) * g.Hkv];
-  if (a.count == 1 && b.count == 0) return;
-  auto row_of = [&](int i) -> long long {
-    const PagedParts& x = i < a.count ? a : b;
-    if (i >= a.count) i -= a.count;
-    return (i == 0 ? x.first : static_cast<long long>(x.second) + static_cast<long long>(i - 1) * x.stride) + sub;
-  };
+  if (a.count == 1 && !covered) return;
   const int n = a.count + b.count;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, args.part_lse[row_of(i)]);
+  const int sub0 = SPLIT ? x - hk * g.G : 0, sub1 = SPLIT ? sub0 + 1 : g.G;
+  for (int sub = sub0; sub < sub1; ++sub) {
+    float m = -INFINITY, sum = 0.f, o[E];
 #pragma unroll
-  for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-  const float z = m == -INFINITY ? 0.f : m;
-  float sum = 0.f, o[E];
+    for (int j = 0; j < E; ++j) o[j] = 0.f;
+    for (int i0 = SPLIT ? warp : 0; i0 < n; i0 += kMergeAhead * (SPLIT ? kMergeWarps : 1)) {
+      float lse[kMergeAhead];
+      Vec v[kMergeAhead];
 #pragma unroll
-  for (int j = 0; j < E; ++j) o[j] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const long long row = row_of(i);
-    const float wt = ex2_approx(args.part_lse[row] - z);
-    sum += wt;
-    const float* src = args.part_o + row * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      o[0] = fmaf(wt, x.x, o[0]);
-      o[1] = fmaf(wt, x.y, o[1]);
-      o[2] = fmaf(wt, x.z, o[2]);
-      o[3] = fmaf(wt, x.w, o[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      o[0] = fmaf(wt, x.x, o[0]);
-      o[1] = fmaf(wt, x.y, o[1]);
+      for (int k = 0; k < kMergeAhead; ++k) {
+        const int i = i0 + k * (SPLIT ? kMergeWarps : 1);
+        const bool in_a = i < a.count;
+        const int at = in_a ? i : i - a.count;
+        const int first = in_a ? a.first : b.first, second = in_a ? a.second : b.second, stride = in_a ? a.stride : b.stride;
+        const long long row = (at == 0 ? first : second + (at - 1) * stride) + sub;
+        lse[k] = -INFINITY;
+        if (i < n) {
+          lse[k] = args.part_lse[row];
+          v[k] = *reinterpret_cast<const Vec*>(args.part_o + row * D + lane * E);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) top = fmaxf(top, lse[k]);
+      const float z = top == -INFINITY ? 0.f : top;
+      const float f = ex2_approx(m - z);
+      m = top;
+      sum *= f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] *= f;
+#pragma unroll
+      for (int k = 0; k < kMergeAhead; ++k) {
+        if (lse[k] == -INFINITY) continue;
+        const float wt = ex2_approx(lse[k] - z);
+        sum += wt;
+        const float* y = reinterpret_cast<const float*>(&v[k]);
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[j] = fmaf(wt, y[j], o[j]);
+      }
     }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const long long at = (static_cast<long long>(t) * g.Hq + h) * D + lane * E;
-  if (args.out_fp32) {
-    float* dst = static_cast<float*>(args.o) + at;
+    if constexpr (SPLIT) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) dst[j] = o[j] * inv;
-  } else {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
+      for (int j = 0; j < E; ++j) joint[warp][lane][j] = o[j];
+      joint[warp][lane][E] = m;
+      joint[warp][lane][E + 1] = sum;
+      __syncthreads();
+      if (warp > 0) return;
+      float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[2 * j] * inv, o[2 * j + 1] * inv);
+      for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, joint[k][lane][E]);
+      const float z = top == -INFINITY ? 0.f : top;
+      m = top;
+      sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) {
+        const float f = ex2_approx(joint[k][lane][E] - z);
+        sum = fmaf(f, joint[k][lane][E + 1], sum);
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[j] = fmaf(f, joint[k][lane][j], o[j]);
+      }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int h = hk * g.G + sub;
+    const long long at = (static_cast<long long>(t) * g.Hq + h) * D + lane * E;
+    if (args.out_fp32) {
+      float* dst = static_cast<float*>(args.o) + at;
+#pragma unroll
+      for (int j = 0; j < E; ++j) dst[j] = o[j] * inv;
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[2 * j] * inv, o[2 * j + 1] * inv);
+    }
+    if (lane == 0)
+      args.lse[static_cast<long long>(h) * g.N + t] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
-  if (lane == 0)
-    args.lse[static_cast<long long>(h) * g.N + t] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---------------------------------------------------------------- launch
@@ -471,8 +574,12 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   rc = launch(paged_small_kernel<T, D>, workers, kSmallThreads, SmallSmem<D>::kBytes, large, stream, mk, mv, a,
               paged_cut_small(g.G), 1, box);
   if (rc != CP_OK) return rc;
-  const long long grid = (static_cast<long long>(g.N) * g.Hq + kMergeWarps - 1) / kMergeWarps;
-  return launch(paged_merge_kernel<T, D>, static_cast<unsigned>(grid), kMergeWarps * 32, 0, true, stream, a);
+  const long long rows = static_cast<long long>(g.N) * g.Hq;
+  if (rows <= kMergeSplitRows)
+    return launch(paged_merge_kernel<T, D, true>, static_cast<unsigned>(rows), kMergeWarps * 32, 0, true, stream, a);
+  const long long warps = static_cast<long long>(g.N) * g.Hkv;
+  return launch(paged_merge_kernel<T, D, false>, static_cast<unsigned>((warps + kMergeWarps - 1) / kMergeWarps),
+                kMergeWarps * 32, 0, true, stream, a);
 }
 
 }  // namespace

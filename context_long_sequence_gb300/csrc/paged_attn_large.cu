@@ -45,8 +45,13 @@ enum Bar {
   BAR_P_HALF = 3 + kTileBars + kSlots,   // +block: P of keys 0-63 written
   BAR_P_FULL = 5 + kTileBars + kSlots,   // +block
   BAR_O = 7 + kTileBars + kSlots,        // +block: every MMA of the segment's block completed
-  NUM_BARS = 9 + kTileBars + kSlots
+  BAR_SEG = 9 + kTileBars + kSlots,      // +segment % kSegs: handed over
+  NUM_BARS = 9 + kTileBars + kSlots + 4
 };
+// Segments on their way.  A tile's slots are those of the tile three before it
+// (5 slots, 2 a tile), so a segment four back has given its last tile back,
+// and everybody has read it: its MMAs waited for all row warps' Q.
+constexpr int kSegs = 4;
 
 template <int D>
 struct LargeSmem {
@@ -55,7 +60,8 @@ struct LargeSmem {
   static constexpr uint32_t offKV = 2 * kQ;
   static constexpr uint32_t offBar = offKV + kSlots * kKV;
   static constexpr uint32_t offMisc = offBar + NUM_BARS * 8;  // TMEM address, abort flag, box masks
-  static constexpr uint32_t kUsed = offMisc + 8 + kTileBars * 4;
+  static constexpr uint32_t offSeg = offMisc + 8 + kTileBars * 4;
+  static constexpr uint32_t kUsed = offSeg + kSegs * sizeof(PagedSegment);
   // D = 64 is padded so that one CTA (and its 512 TMEM columns) is on an SM.
   static constexpr uint32_t kBytes = kUsed < 120 * 1024 ? 120 * 1024 : kUsed;
 };
@@ -101,7 +107,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     debug_bounds_fail(status, __LINE__, CP_TU_ID);
     return;
   }
-  PagedWalker walk(g, cut, status);
+  PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
+  PagedWalker walk(args, cut, kLargeRows, args.rows_small);
   // The walker's sums lie where K and V will; nothing has been fetched yet.
   const bool any = walk.start(reinterpret_cast<long long*>(smem + SM::offKV), blockIdx.x, gridDim.x, min_units);
   if (!any) return;  // the whole block
@@ -120,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(BAR_P_FULL + i), 4);
       mbar_init(bar(BAR_O + i), 1);
     }
+    for (int i = 0; i < kSegs; ++i) mbar_init(bar(BAR_SEG + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -132,7 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;  // S_t at 128 t (P_t packed in its first 64 columns), O_t at 256 + D t
-  PagedSegment seg;
+  // Segment number n, once handed over.
+  auto take = [&](int n, PagedSegment& seg) {
+    if (!warp_all(mbar_wait(bar(BAR_SEG + n % kSegs), (n / kSegs) & 1, abort_flag, status))) return false;
+    seg = segs[n % kSegs];
+    return seg.nt > 0;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ fetch
@@ -143,12 +156,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap* map = kv ? &tm_v : &tm_k;
     const uint32_t dst0 = sKV + half * HALF_BYTES + box * box_rows * 128;
     const int page_mask = (1 << g.page_shift) - 1;
-    int nt = 0;  // key tiles fetched
+    int nt = 0, nseg = 0;  // key tiles fetched, segments handed over
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    while (ok) {
+      const PagedSegment seg = walk.next();
+      if (lane == 0) {
+        segs[nseg % kSegs] = seg;
+        mbar_arrive(bar(BAR_SEG + nseg % kSegs));
+      }
+      ++nseg;
+      if (seg.nt == 0) break;
       auto page_of = [&](int tile) {
         const int key = tile * BN + box * box_rows;
-        return mine && tile < seg.tile1 && key < seg.keys ? seg.table[key >> g.page_shift] : -2;
+        return mine && tile < seg.tile1 && key < seg.keys ? walk.table[key >> g.page_shift] : -2;
       };
       int page = page_of(seg.tile0);
       for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++nt) {
@@ -208,7 +228,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int j = 0, ring = 0, nseg = 0;  // key tiles walked, slot of the next K, segments
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    PagedSegment seg;
+    while (ok && take(nseg, seg)) {
       const RowBlock b0 = row_block(seg, 0, block_tokens), b1 = row_block(seg, 1, block_tokens);
       fresh[0] = fresh[1] = true;
       int pend = -1;  // V slot of a PV_1 still to issue
@@ -250,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int sub = row - tok * g.G;
     int j = 0, k = 0, nseg = 0;  // key tiles walked, seen, segments
     bool ok = true;
-    while (ok && walk.next(seg)) {
+    PagedSegment seg;
+    while (ok && take(nseg, seg)) {
       const RowBlock w = row_block(seg, t, block_tokens);
       const int first = t * block_tokens;
       const int n_rows = max(0, min(block_tokens, seg.nt - first)) * g.G;
@@ -263,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const T* q0 = static_cast<const T*>(args.q) + (static_cast<long long>(seg.t0) + first) * args.q_stride +
                       static_cast<long long>(seg.h) * g.G * D + piece * 8;
         const uint32_t dst = sQ + t * SM::kQ + (piece >> 3) * HALF_BYTES;
-#pragma unroll 4
+#pragma unroll
         for (int r = ((threadIdx.x - 64) & 127) / P; r < BM; r += 128 / P) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
           if (r < n_rows) {
@@ -438,12 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nseg;
       if (!ok) break;
       tc_fence_after();
-      const PagedTarget to = paged_target(args, walk, seg, args.rows_small, kLargeRows, t == 0 && wq == 0);
+      const bool final_rows = seg.mode == kRowsFinal;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? m + log2f(l) - kBias : -INFINITY;
       const int token = seg.t0 + first + tok, head = seg.h * g.G + sub;
       const long long out_row = static_cast<long long>(token) * g.Hq + head;
-      const long long at = to.home ? to.row + out_row : to.row + first * g.G + row;
+      const long long at = seg.row + (seg.mode == kRowsHome ? out_row : first * g.G + row);
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t ov[32];
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = k > k0 ? __uint_as_float(ov[e]) * inv : 0.f;
-        if (to.final_rows && !args.out_fp32) {
+        if (final_rows && !args.out_fp32) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(args.o) + out_row * D + c * 32);
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
@@ -464,13 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
         } else {
           float4* dst = reinterpret_cast<float4*>(
-              (to.final_rows ? static_cast<float*>(args.o) + out_row * D : args.part_o + at * D) + c * 32);
+              (final_rows ? static_cast<float*>(args.o) + out_row * D : args.part_o + at * D) + c * 32);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (row_valid) {
-        if (to.final_rows)
+        if (final_rows)
           args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
         else
           args.part_lse[at] = lse2;
