@@ -17,6 +17,15 @@ namespace cpattn {
 // these checks are therefore in every build, unlike CP_IN_BOUNDS.
 #define CP_CHECK_DATA(cond, status) ((cond) || ::cpattn::debug_bounds_fail((status), __LINE__, CP_TU_ID))
 
+// mbar_wait (ptx.cuh) with the clock first looked at after 16 failed tries:
+// reading %globaltimer takes longer than most of these kernels' waits.  The
+// same limit, abort flag and status.
+__device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, status);
+}
+
 // Number of the n elements of the ascending array `a` that are <= t.  Executed
 // by a whole warp: 32 probes a round, so 1024 elements take two dependent
 // loads.  Ends after log32(n) rounds whatever the data.
@@ -64,35 +73,42 @@ struct PagedSegment {
 enum : int { kRowsFinal = 0, kRowsHome = 1, kRowsSlot = 2 };
 
 // Walks a worker's units, one warp, 32 entries at a time, an entry a lane.
+// Every warp of a block totals the units and chooses; the one that fetches
+// goes on to walk.
 struct PagedWalker {
   const PagedAttnArgs& a;
   const PagedGeom& g;
-  const PagedCut cut;
-  int32_t* status;
-  const int slot_rows;         // rows of a worker's slot; `slots`: the kernel's first slot row
-  const int slots;
+  PagedCut cut;
+  int slots, slot_rows;        // the cut's first slot row, rows of a slot
   int E, worker;
   PagedShares shares;
-  long long u, end;           // this worker's next unit and last + 1
-  int base = -1;              // first entry of the window; -1: none is held
-  long long before;           // units before the window
-  const int32_t* table;       // page table of the last segment's entry
-  // The lane's entry:
-  PagedEntry entry;
+  long long u, end;            // this worker's next unit and last + 1
+  int base = -1;               // first entry of the window; -1: none is held
+  long long before;            // units before the window
+  PagedEntry entry;            // the lane's
   long long head_units, upto;  // its units of one head; units of the window up to and including it
-
+  const int32_t* table;        // page table of the last segment's entry
   int covered0, covered1;      // sequences of some prefix: [covered0, covered1)
 
-  __device__ __forceinline__ PagedWalker(const PagedAttnArgs& args, const PagedCut& c, int slot_rows_, long long slots_)
-      : a(args), g(args.g), cut(c), status(args.status), slot_rows(slot_rows_), slots(static_cast<int>(slots_)),
-        E(args.g.B + args.g.NP), shares(0, 1, 1) {}
+  __device__ __forceinline__ explicit PagedWalker(const PagedAttnArgs& args)
+      : a(args), g(args.g), E(args.g.B + args.g.NP), shares(0, 1, 1) {}
 
   __device__ __forceinline__ void load(int first) {
     const int lane = threadIdx.x & 31;
     base = first;
     entry = PagedEntry{0, 0, 0, 0, nullptr, false};
     if (base + lane < E) entry = paged_entry(g, base + lane);
-    if (entry.bad) debug_bounds_fail(status, __LINE__, kTuPagedAttn);
+    if (entry.bad) debug_bounds_fail(a.status, __LINE__, kTuPagedAttn);
+  }
+  // Units of the window's entries under cut `c`.
+  __device__ __forceinline__ long long window_units(const PagedCut& c) const {
+    long long x = paged_head_units(g, c, entry) * g.Hkv;
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+    return x;
+  }
+  __device__ __forceinline__ void scan() {
+    const int lane = threadIdx.x & 31;
     head_units = paged_head_units(g, cut, entry);
     upto = head_units * g.Hkv;
 #pragma unroll
@@ -102,44 +118,61 @@ struct PagedWalker {
     }
   }
 
-  // Called by the whole block; `sums` holds a number for each window of 32
-  // entries and is free again after the call.  False: nothing for this worker.
-  __device__ __forceinline__ bool start(long long* sums, int worker_, int max_workers, int min_units) {
+  // All units under the N cuts.  Called by the whole block; `sums` (N numbers
+  // for each window of 32 entries) holds the windows' until begin().
+  template <int N>
+  __device__ __forceinline__ void totals(long long* sums, const PagedCut (&cuts)[N], long long (&units)[N]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int windows = (E + 31) / 32;
-    worker = worker_;
     covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
     covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
-    long long units = 0;
-    if (windows > 1) {
-      for (int w = warp; w < windows; w += warps) {
-        load(w * 32);
-        if (lane == 31) sums[w] = upto;
-      }
-      __syncthreads();
-      for (int w0 = 0; w0 < windows; w0 += 32) {
-        long long x = w0 + lane < windows ? sums[w0 + lane] : 0;
-#pragma unroll
-        for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-        units += x;
-      }
-    } else {
+    if (windows == 1) {
       load(0);
-      units = shfl64(upto, 31);
+#pragma unroll
+      for (int i = 0; i < N; ++i) units[i] = window_units(cuts[i]);
+      return;
     }
-    before = 0;
+    for (int w = warp; w < windows; w += warps) {
+      load(w * 32);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const long long x = window_units(cuts[i]);
+        if (lane == 0) sums[w * N + i] = x;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      long long x = 0;
+      for (int w = lane; w < windows; w += 32) x += sums[w * N + i];
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
+      units[i] = x;
+    }
+  }
+
+  // Take up worker `worker_`'s share of cut `c`, number `i` of the N totalled.
+  // False: nothing for it.  Not called by the whole block; `sums` may be
+  // overwritten once all its warps are through.
+  template <int N>
+  __device__ __forceinline__ bool begin(const long long* sums, int i, const PagedCut& c, long long units, int worker_,
+                                        int max_workers, int min_units, int slots_, int slot_rows_) {
+    cut = c;
+    slots = slots_;
+    slot_rows = slot_rows_;
+    worker = worker_;
     shares = PagedShares(units, max_workers, min_units);
-    const bool any = worker < shares.workers;
-    u = any ? shares.first(worker) : 0;
-    end = any ? shares.first(worker + 1) : 0;
-    if (windows > 1) {
-      int w = 0;
-      if (any)
-        while (w + 1 < windows && before + sums[w] <= u) before += sums[w++];
-      __syncthreads();
-      if (any && base != w * 32) load(w * 32);
-    }
-    return any;
+    before = 0;
+    if (worker >= shares.workers) return false;
+    u = shares.first(worker);
+    end = shares.first(worker + 1);
+    const int windows = (E + 31) / 32;
+    int w = 0;
+    if (windows > 1)
+      while (w + 1 < windows && before + sums[w * N + i] <= u) before += sums[w++ * N + i];
+    if (base != w * 32) load(w * 32);
+    scan();
+    return true;
   }
 
   // The next segment (warp-uniform), nt == 0 behind the last.  The run that
@@ -155,6 +188,7 @@ struct PagedWalker {
       }
       before += total;
       load(base + 32);
+      scan();
       total = shfl64(upto, 31);
     }
     long long rel = u - before;

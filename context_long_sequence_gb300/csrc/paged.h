@@ -85,7 +85,7 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
   return r;
 }
 
-// How the attention of a batch is cut into work.  A kernel takes the entries
+// How the attention of a batch is cut into work.  A cut takes the entries
 // whose rows (tokens x query heads of a KV head) lie in [min_rows, max_rows],
 // cuts their tokens into tiles of tile_tokens and each tile's visible keys
 // into tiles of tile_keys.  One key tile of one token tile and KV head is a
@@ -149,15 +149,20 @@ struct PagedShares {
 // one its share begins in (its slot 2w) and the one its share ends in (slot
 // 2w + 1); a part that is complete but has a partner (own keys and a prefix)
 // goes to a home row of its own.
-constexpr int kSmallWorkers = 304, kSmallRows = 64, kSmallKeyShift = 6;
+//
+// Small: a warp (paged_small.cuh), 16 keys a tile, up to 16 rows, or 32 where
+// the batch has nothing larger; at least kSmallMinUnits tiles each.  Large: a
+// CTA (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
+constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallRowsBeside = 16, kSmallKeyShift = 4;
+constexpr int kSmallMinUnits = 4;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
 constexpr int kMaxEntries = 8192;
 
-inline __host__ __device__ PagedCut paged_cut_small(int G) {
-  return PagedCut{1, kSmallRows, G <= kSmallRows ? kSmallRows / G : 1, kSmallKeyShift};
+inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
+  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift};
 }
 inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kSmallRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift};
+  return PagedCut{kSmallRowsBeside + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift};
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
@@ -219,7 +224,7 @@ struct PagedAttnArgs {
 };
 
 int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
-// The entries of more than kSmallRows rows (paged_attn_large.cu).
+// For batches that may have entries of more than kSmallRows rows (paged_attn_large.cu).
 int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream);
 
 // Device address of the status words on the current device (cp_attn.cu).

@@ -1,5 +1,5 @@
-// paged_attn_large.cu -- attention over the paged cache for entries of many
-// rows: a prefix with the rows of all its sequences, or a sequence with a
+// paged_attn_large.cu -- attention over the paged cache for batches with
+// entries of many rows: a prefix with the rows of all its sequences, or a sequence with a
 // chunk of new tokens.
 //
 // Rows are (token, query head of the KV head) pairs, token by token; a token
@@ -20,6 +20,11 @@
 // At 256 rows a 128-key tile is 256 flops a byte, the card's own balance:
 // fewer rows are bound by the cache's bytes, more by the tensor core.
 //
+// A batch's entries of few rows are taken by other CTAs of the same launch
+// (paged_small.cuh, eight workers a CTA), in proportion to their work: one
+// kernel bound by the tensor core and one by the cache's bytes share the card
+// better side by side than one after the other.
+//
 // Warps (320 threads): 0 fetches, 1 issues the MMAs (and holds the TMEM),
 // 2..5 and 6..9 load Q, take the softmax and write the rows of block 0 and 1.
 #include <cuda.h>
@@ -27,6 +32,7 @@
 
 #define CP_TU_ID ::cpattn::kTuPagedAttn
 #include "paged.cuh"
+#include "paged_small.cuh"
 
 namespace cpattn {
 namespace {
@@ -87,10 +93,27 @@ __device__ __forceinline__ RowBlock row_block(const PagedSegment& s, int t, int 
   return RowBlock{min(s.keys, s.limit0 + first), min(s.keys, s.limit0 + first + n - 1)};
 }
 
+template <int D>
+constexpr uint32_t kLaunchBytes =
+    LargeSmem<D>::kBytes > SmallSmem<D>::kBytes ? LargeSmem<D>::kBytes : static_cast<uint32_t>(SmallSmem<D>::kBytes);
+static_assert(kLaunchBytes<128> <= 227 * 1024, "one CTA an SM");
+
+// CTAs for the entries of many rows, by the time of their units: one is 256
+// rows x 128 keys, some 2750 clocks on the tensor core and the exponentials;
+// one of few rows is 16 keys, about a twelfth of that for a CTA's eight warps.
+__device__ __forceinline__ int paged_large_ctas(long long small, long long large, int ctas) {
+  if (large == 0) return 0;
+  if (small == 0) return ctas;
+  const long long all = 12 * large + small;
+  const int n = static_cast<int>(paged_div(12 * large * ctas + all / 2, all));
+  return n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_large_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ PagedAttnArgs args, const PagedCut cut, int min_units, int box_rows) {
+                       const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                       const __grid_constant__ PagedAttnArgs args, int box_rows) {
   using SM = LargeSmem<D>;
   constexpr int NH = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -108,11 +131,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
-  PagedWalker walk(args, cut, kLargeRows, args.rows_small);
-  // The walker's sums lie where K and V will; nothing has been fetched yet.
-  const bool any = walk.start(reinterpret_cast<long long*>(smem + SM::offKV), blockIdx.x, gridDim.x, min_units);
+  PagedWalker walk(args);
+  const PagedCut cuts[2] = {paged_cut_small(g.G, kSmallRowsBeside), paged_cut_large(g.G)};
+  long long units[2];
+  // Behind the small workers' stages; where V will be, for the large.
+  long long* sums = reinterpret_cast<long long*>(smem + SmallSmem<D>::offSums);
+  walk.totals(sums, cuts, units);
+  const int large = paged_large_ctas(units[0], units[1], gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= large) {
+    // Entries of few rows: a warp each, eight of the ten.
+    if (warp >= kSmallWarps) return;
+    const int ctas = gridDim.x - large;
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k16);
+      tma_prefetch_desc(&tm_v16);
+      small_init<D>(smem, warp);
+    }
+    __syncwarp();
+    if (walk.begin<2>(sums, 0, cuts[0], units[0], warp * ctas + blockIdx.x - large, kSmallWarps * ctas, kSmallMinUnits, 0,
+                      kSmallRows))
+      small_worker<T, D, 1>(smem, warp, tm_k16, tm_v16, walk);
+    return;
+  }
+  const bool any = walk.begin<2>(sums, 1, cuts[1], units[1], blockIdx.x, large, 1, args.rows_small, kLargeRows);
   if (!any) return;  // the whole block
-  const int block_tokens = cut.tile_tokens / 2;
+  const int block_tokens = cuts[1].tile_tokens / 2;
   const uint32_t box_all = (1u << (BN / box_rows)) - 1;
 
   if (threadIdx.x == 0) {
@@ -142,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;  // S_t at 128 t (P_t packed in its first 64 columns), O_t at 256 + D t
   // Segment number n, once handed over.
   auto take = [&](int n, PagedSegment& seg) {
-    if (!warp_all(mbar_wait(bar(BAR_SEG + n % kSegs), (n / kSegs) & 1, abort_flag, status))) return false;
+    if (!warp_all(mbar_wait_short(bar(BAR_SEG + n % kSegs), (n / kSegs) & 1, abort_flag, status))) return false;
     seg = segs[n % kSegs];
     return seg.nt > 0;
   };
@@ -214,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_warp(bar(BAR_S_FULL + t));
     };
     auto issue_pv = [&](int t, int sl, bool release_v) -> bool {
-      if (!warp_all(mbar_wait(bar(BAR_P_HALF + t), npv[t] & 1, abort_flag, status))) return false;
+      if (!warp_all(mbar_wait_short(bar(BAR_P_HALF + t), npv[t] & 1, abort_flag, status))) return false;
       tc_fence_after();
       const uint64_t b0 = dv0 + static_cast<uint64_t>(sl) * kSlotStep;
       mma_bf16_ts_k64_warp(tmem + 256 + D * t, tmem + 128 * t, b0, idesc_pv, fresh[t] ? 0u : 1u);
-      if (!warp_all(mbar_wait(bar(BAR_P_FULL + t), npv[t] & 1, abort_flag, status))) return false;
+      if (!warp_all(mbar_wait_short(bar(BAR_P_FULL + t), npv[t] & 1, abort_flag, status))) return false;
       tc_fence_after();
       mma_bf16_ts_k64_warp(tmem + 256 + D * t, tmem + 128 * t + 32, b0 + 512, idesc_pv, 1u);
       if (release_v) mma_commit_warp(bar(BAR_KV_EMPTY + sl));
@@ -233,12 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowBlock b0 = row_block(seg, 0, block_tokens), b1 = row_block(seg, 1, block_tokens);
       fresh[0] = fresh[1] = true;
       int pend = -1;  // V slot of a PV_1 still to issue
-      ok = warp_all(mbar_wait(bar(BAR_Q), nseg & 1, abort_flag, status));
+      ok = warp_all(mbar_wait_short(bar(BAR_Q), nseg & 1, abort_flag, status));
       for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
         const bool v0 = b0.sees(tile * BN), v1 = b1.sees(tile * BN);
         const int kslot = ring, vslot = ring + 1 == kSlots ? 0 : ring + 1;
         ring = vslot + 1 == kSlots ? 0 : vslot + 1;
-        ok = warp_all(mbar_wait(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status));
+        ok = warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
         if (v0) issue_qk(0, kslot);
@@ -261,14 +304,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nseg > 0) mbar_wait(bar(BAR_O + 1), (nseg - 1) & 1, nullptr, status);
   } else {
     // ------------------------------------------------------------ rows
+    // A warp loads, exponentiates and writes 32 rows; one without rows only
+    // keeps the barriers going (its lanes of S, P and O hold anything: rows do
+    // not mix).  Loops that run once a segment are kept short rather than
+    // unrolled: cold code costs some 10 clocks an instruction here.
     const int t = (warp - 2) >> 2;  // row block
     const int wq = warp & 3, row = wq * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tSt = tmem + 128 * t + lane_off, tOt = tmem + 256 + D * t + lane_off;
+    const uint32_t sW = sQ + t * SM::kQ + wq * 32 * 128;  // the warp's rows of Q, first half; then its staging
     const float sl2 = g.scale * 1.4426950408889634f;
     constexpr float kBias = Weight<T>::kBias;
-    const int tok = row / g.G;  // of the block's, and query head within the KV head's
+    const int tok = row / g.G;  // token of the block's, and query head within the KV head's
     const int sub = row - tok * g.G;
+    const int box_shift = 31 - __clz(box_rows);
     int j = 0, k = 0, nseg = 0;  // key tiles walked, seen, segments
     bool ok = true;
     PagedSegment seg;
@@ -276,50 +325,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       const RowBlock w = row_block(seg, t, block_tokens);
       const int first = t * block_tokens;
       const int n_rows = max(0, min(block_tokens, seg.nt - first)) * g.G;
-      const bool row_valid = row < n_rows;
+      const bool row_valid = row < n_rows, busy = wq * 32 < n_rows;
       const int my_lim = row_valid ? min(seg.keys, seg.limit0 + first + tok) : 0;
-      // Q: 16 bytes a thread and step, rows of the block that do not exist zero.
-      {
+      // Row of (token, head) from the tile's first token on.
+      const int my_off = tok * g.Hq + sub;
+      const long long tile_row = (static_cast<long long>(seg.t0) + first) * g.Hq + seg.h * g.G;
+      if (busy) {
+        // Q: 16 bytes a lane and step; a row's pieces side by side.
         constexpr int P = D / 8;  // pieces of a row
-        const int piece = threadIdx.x % P;
+        const int piece = lane % P;
         const T* q0 = static_cast<const T*>(args.q) + (static_cast<long long>(seg.t0) + first) * args.q_stride +
                       static_cast<long long>(seg.h) * g.G * D + piece * 8;
-        const uint32_t dst = sQ + t * SM::kQ + (piece >> 3) * HALF_BYTES;
-#pragma unroll
-        for (int r = ((threadIdx.x - 64) & 127) / P; r < BM; r += 128 / P) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (r < n_rows) {
-            const int i = r / g.G;
-            x = *reinterpret_cast<const uint4*>(q0 + i * args.q_stride + (r - i * g.G) * D);
-          }
-          st_shared_v4(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+        const uint32_t dst = sW + (piece >> 3) * HALF_BYTES;
+        const int mine = min(32, n_rows - wq * 32);
+        // Straight to shared memory, every row's copy in flight at once.
+#pragma unroll 4
+        for (int n = 0; n < P; ++n) {
+          const int r = n * (32 / P) + lane / P;
+          const int i = __shfl_sync(0xffffffffu, tok, r), h = __shfl_sync(0xffffffffu, sub, r);
+          if (r < mine) cp_async16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), q0 + i * args.q_stride + h * D);
         }
+        cp_async_wait_all();
         fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_Q));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(BAR_Q));
       float m = -INFINITY, l = 0.f;
       const int k0 = k;
       for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
         const int key0 = tile * BN;
         if (!w.sees(key0)) continue;
         // K, V and the box mask of the tile are visible through the tile's barrier.
-        ok = warp_all(mbar_wait(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
-                      mbar_wait(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
+        ok = warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
+                      mbar_wait_short(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
         const uint32_t held = mask[j % kTileBars];
         const bool full = held == box_all && key0 + BN <= w.lo;
+        auto signal = [&](int b) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(b + t));
+        };
+        if (held != box_all || key0 + BN > seg.keys) {
+          // V rows behind the last key (or in a page that was not fetched) may
+          // hold anything, NaN included; a zero weight does not remove a NaN.
+          if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
+            const uint32_t v = sKV + ((2 * j + 1) % kSlots) * SM::kKV + row * 128;
+#pragma unroll 1
+            for (int b = 0; b < 8 * NH; ++b) st_shared_v4(v + (b >> 3) * HALF_BYTES + (b & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        if (!busy) {
+          signal(BAR_P_HALF);
+          signal(BAR_P_FULL);
+          ++k;
+          continue;
+        }
         uint32_t sr[BN];
         float* x = reinterpret_cast<float*>(sr);
         auto col32 = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]); };
         const f32x2 sl2x2 = make_f32x2(sl2, sl2);
-        auto exp32 = [&](int c, float mb, f32x2 (&rs2)[4], uint32_t (&pk)[16]) {
+        auto exp32 = [&](const uint32_t* s32, float mb, f32x2 (&rs2)[4], uint32_t (&pk)[16]) {
           const f32x2 nmbx2 = make_f32x2(kBias - mb, kBias - mb);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float a0, a1;
-            split_f32x2(fma_f32x2(make_f32x2(x[c * 32 + e], x[c * 32 + e + 1]), sl2x2, nmbx2), a0, a1);
+            split_f32x2(fma_f32x2(make_f32x2(__uint_as_float(s32[e]), __uint_as_float(s32[e + 1])), sl2x2, nmbx2), a0, a1);
             const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
             rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], make_f32x2(p0, p1));
             pk[e >> 1] = Elem<T>::pack(p0, p1);
@@ -331,17 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) split_f32x2(rs2[i], lo[i], hi[i]);
           return ((lo[0] + hi[0]) + (lo[1] + hi[1])) + ((lo[2] + hi[2]) + (lo[3] + hi[3]));
         };
-        auto signal = [&](int b) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(b + t));
-        };
+        const f32x2 zero2 = make_f32x2(0.f, 0.f);
         // Wholly visible tile, running max set: keys 0-63 are exponentiated
         // against it before any maximum is taken; their sum bounds each of
         // them and the maximum of keys 64-127 the rest.
         if (full && warp_all(m != -INFINITY || !row_valid)) {
-          const float mb = row_valid ? m : 0.f;
           tmem_ld32(tSt, col32(0));
           tmem_ld32(tSt + 32, col32(1));
           tmem_wait_ld();
@@ -349,10 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           reg_fence(col32(1));
           tmem_ld32(tSt + 64, col32(2));
           tmem_ld32(tSt + 96, col32(3));
-          f32x2 rs2[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
+          f32x2 rs2[4] = {zero2, zero2, zero2, zero2};
           uint32_t pk0[16], pk1[16];
-          exp32(0, mb, rs2, pk0);
-          exp32(1, mb, rs2, pk1);
+          exp32(sr, m, rs2, pk0);
+          exp32(sr + 32, m, rs2, pk1);
           tmem_wait_ld();
           reg_fence(col32(2));
           reg_fence(col32(3));
@@ -365,14 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], x[e + i], x[e + 4 + i]);
           const float mx_hi = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float s_lo = sum4(rs2);
-          if (warp_all(s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < mb + Weight<T>::kSpecMax)) {
+          if (warp_all((s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < m + Weight<T>::kSpecMax) || !row_valid)) {
             tmem_st16(tSt, pk0);
             tmem_st16(tSt + 16, pk1);
             signal(BAR_P_HALF);
-            f32x2 rh[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
-            exp32(2, mb, rh, pk0);
+            f32x2 rh[4] = {zero2, zero2, zero2, zero2};
+            exp32(sr + 64, m, rh, pk0);
             tmem_st16(tSt + 32, pk0);
-            exp32(3, mb, rh, pk1);
+            exp32(sr + 96, m, rh, pk1);
             tmem_st16(tSt + 48, pk1);
             signal(BAR_P_FULL);
             l += s_lo + sum4(rh);
@@ -380,46 +448,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             continue;
           }
         }
-        // Masked tiles, the first of a segment, and tiles that outgrew the max.
-        if (held != box_all || key0 + BN > seg.keys) {
-          // V rows behind the last key (or in a page that was not fetched) may
-          // hold anything, NaN included; a zero weight does not remove a NaN.
-          const int box_shift = 31 - __clz(box_rows);
-          if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
-            const uint32_t v = sKV + ((2 * j + 1) % kSlots) * SM::kKV + row * 128;
-            for (int hh = 0; hh < NH; ++hh)
-              for (int b = 0; b < 8; ++b) st_shared_v4(v + hh * HALF_BYTES + b * 16, 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+        // Masked tiles, the first of a segment, and tiles that outgrew the
+        // max: 32 columns at a time, once for the maximum and once for the
+        // weights.
+        auto load = [&](int c, uint32_t (&r)[32]) {
+          tmem_ld32(tSt + c * 32, r);
+          tmem_wait_ld();
+          reg_fence(r);
+          if (full) return;
+          // Boxes are 16 keys or more: two bits cover 32 columns.
+          const uint32_t in0 = (held >> ((c * 32) >> box_shift)) & 1u, in1 = (held >> ((c * 32 + 16) >> box_shift)) & 1u;
+          const int left = my_lim - key0 - c * 32;
+          const int n0 = in0 ? left : 0, n1 = in1 ? left : 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e >= (e < 16 ? n0 : n1)) r[e] = 0xff800000u;
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t r[32];
+          load(c, r);
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(r[i]);
+#pragma unroll
+          for (int e = 4; e < 32; e += 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(r[e + i]));
+          mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) tmem_ld32(tSt + c * 32, col32(c));
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) reg_fence(col32(c));
-        if (!full) {
-          const int c_hi = my_lim - key0;
-#pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (e >= c_hi) x[e] = -INFINITY;
-          if (held != box_all) {
-            const int box_shift = 31 - __clz(box_rows);
-#pragma unroll
-            for (int e = 0; e < BN; e += 16)  // a box is 16 keys or more
-              if (!((held >> (e >> box_shift)) & 1u))
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[e + i] = -INFINITY;
-          }
-        }
-        float m8[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m8[i] = fmaxf(x[i], x[8 + i]);
-#pragma unroll
-        for (int e = 16; e < BN; e += 16)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = fmax3(m8[i], x[e + i], x[e + 8 + i]);
-        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
         const float m_new = fmaxf(m, mx * sl2);
         float alpha = 1.f;
         if (m_new > m + Weight<T>::kSlack) {
@@ -427,14 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m_new;
         }
         const float mb = (m == -INFINITY) ? 0.f : m;
-        f32x2 rs2[4] = {make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f), make_f32x2(0.f, 0.f)};
-        auto exp_chunk = [&](int c) {
-          uint32_t pk[16];
-          exp32(c, mb, rs2, pk);
-          tmem_st16(tSt + c * 16, pk);
-        };
-        exp_chunk(0);
-        exp_chunk(1);
         if (k > k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -447,56 +497,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(tOt + c * 32, ov);
           }
         }
-        signal(BAR_P_HALF);
-        exp_chunk(2);
-        exp_chunk(3);
-        signal(BAR_P_FULL);
+        f32x2 rs2[4] = {zero2, zero2, zero2, zero2};
+        // P of columns 32c.. goes over columns 16c..: read already.
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t r[32], pk[16];
+          load(c, r);
+          exp32(r, mb, rs2, pk);
+          tmem_st16(tSt + c * 16, pk);
+          if (c & 1) signal(c == 1 ? BAR_P_HALF : BAR_P_FULL);
+        }
         l = l * alpha + sum4(rs2);
         ++k;
       }
       // The block's MMAs of this segment have completed: O is whole, and Q's
-      // shared memory free for the next segment.
-      if (ok) ok = warp_all(mbar_wait(bar(BAR_O + t), nseg & 1, abort_flag, status));
+      // shared memory free for staging and for the next segment.
+      if (ok) ok = warp_all(mbar_wait_short(bar(BAR_O + t), nseg & 1, abort_flag, status));
       ++nseg;
       if (!ok) break;
+      if (!busy) continue;
       tc_fence_after();
       const bool final_rows = seg.mode == kRowsFinal;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m + log2f(l) - kBias : -INFINITY;
-      const int token = seg.t0 + first + tok, head = seg.h * g.G + sub;
-      const long long out_row = static_cast<long long>(token) * g.Hq + head;
-      const long long at = seg.row + (seg.mode == kRowsHome ? out_row : first * g.G + row);
+      // A thread holds a row, but rows leave as whole lines: 128 bytes of 32
+      // rows at a time pass through shared memory (16-byte pieces, swizzled).
+      const bool narrow = final_rows && !args.out_fp32;  // 64 columns are 128 bytes, else 32
+      const int lines = narrow ? D / 64 : D / 32;
+      char* base;
+      int my_line;  // the row's number from base on
+      if (seg.mode == kRowsSlot) {
+        base = reinterpret_cast<char*>(args.part_o + (seg.row + first * static_cast<long long>(g.G)) * D);
+        my_line = row;
+      } else {
+        base = final_rows ? static_cast<char*>(args.o) + tile_row * D * (narrow ? 2 : 4)
+                          : reinterpret_cast<char*>(args.part_o + (seg.row + tile_row) * D);
+        my_line = my_off;
+      }
+      const int row_bytes = D * (narrow ? 2 : 4);
+      const int mine = min(32, n_rows - wq * 32);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < lines; ++c) {
+        const uint32_t stage = sW + (NH > 1 ? (c & 1) * HALF_BYTES : 0);
+        const uint32_t my_stage = stage + lane * 128;
         uint32_t ov[32];
-        if (k > k0) {
-          tmem_ld32(tOt + c * 32, ov);
-          tmem_wait_ld();
-          reg_fence(ov);
-        }
-        if (!row_valid) continue;
-        float o[32];
+        auto fetch = [&](int col) {
+          if (k > k0) {
+            tmem_ld32(tOt + col, ov);
+            tmem_wait_ld();
+            reg_fence(ov);
+          }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = k > k0 ? __uint_as_float(ov[e]) * inv : 0.f;
-        if (final_rows && !args.out_fp32) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(args.o) + out_row * D + c * 32);
+          for (int e = 0; e < 32; ++e) ov[e] = k > k0 ? __float_as_uint(__uint_as_float(ov[e]) * inv) : 0u;
+        };
+        if (narrow) {
+#pragma unroll 1
+          for (int hh = 0; hh < 2; ++hh) {
+            fetch(c * 64 + hh * 32);
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            dst[e / 8] = make_uint4(Elem<T>::pack(o[e], o[e + 1]), Elem<T>::pack(o[e + 2], o[e + 3]),
-                                    Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
+            for (int p = 0; p < 4; ++p) {
+              auto two = [&](int e) { return Elem<T>::pack(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])); };
+              st_shared_v4(my_stage + (((hh * 4 + p) ^ (lane & 7)) << 4), two(8 * p), two(8 * p + 2), two(8 * p + 4), two(8 * p + 6));
+            }
+          }
         } else {
-          float4* dst = reinterpret_cast<float4*>(
-              (final_rows ? static_cast<float*>(args.o) + out_row * D : args.part_o + at * D) + c * 32);
+          fetch(c * 32);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          for (int p = 0; p < 8; ++p)
+            st_shared_v4(my_stage + ((p ^ (lane & 7)) << 4), ov[4 * p], ov[4 * p + 1], ov[4 * p + 2], ov[4 * p + 3]);
         }
+        __syncwarp();
+        uint4 y[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int r = n * 4 + (lane >> 3), p = lane & 7;
+          y[n] = ld_shared_v4(stage + r * 128 + ((p ^ (r & 7)) << 4));
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const int r = n * 4 + (lane >> 3), p = lane & 7;
+          const int line = __shfl_sync(0xffffffffu, my_line, r);
+          if (r < mine) *reinterpret_cast<uint4*>(base + static_cast<long long>(line) * row_bytes + c * 128 + p * 16) = y[n];
+        }
+        if (NH == 1) __syncwarp();  // one staging place; with two, the step between orders them
       }
       if (row_valid) {
+        const float lse2 = l > 0.f ? m + log2f(l) - kBias : -INFINITY;
         if (final_rows)
-          args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
+          args.lse[static_cast<long long>(seg.h * g.G + sub) * g.N + seg.t0 + first + tok] = lse2 * 0.69314718055994531f;
         else
-          args.part_lse[at] = lse2;
+          args.part_lse[seg.row + (seg.mode == kRowsHome ? tile_row + my_off : first * g.G + row)] = lse2;
       }
+      __syncwarp();      // the staging is read before the next segment's Q lands on it
       tc_fence_before();  // O was read before this warp's next arrival lets a PV overwrite it
     }
   }
@@ -513,14 +604,16 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const PagedGeom& g = a.g;
   static std::atomic<int> known[64];
   int sms = 0;
-  int rc = prepare_kernel(known, paged_large_kernel<T, D>, LargeSmem<D>::kBytes, &sms);
+  int rc = prepare_kernel(known, paged_large_kernel<T, D>, kLaunchBytes<D>, &sms);
   if (rc != CP_OK) return rc;
   const int page = 1 << g.page_shift, box = page < BN ? page : BN;
-  CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box)) return CP_ERR_CUDA;
+  CUtensorMap mk, mv, mk16, mv16;
+  if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box) ||
+      !make_cache_map(&mk16, g, a.k_cache, 16) || !make_cache_map(&mv16, g, a.v_cache, 16))
+    return CP_ERR_CUDA;
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D>, workers, kThreads, LargeSmem<D>::kBytes, false, stream, mk, mv, a,
-                paged_cut_large(g.G), 1, box);
+  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, false, stream, mk, mv, mk16, mv16, a,
+                box);
 }
 
 }  // namespace

@@ -1,0 +1,296 @@
+// paged_small.cuh -- attention over the paged cache for entries of few rows
+// (a decode step, short drafts), by single warps.
+//
+// Bound by reading the cache: at 16 rows a key's 4 d bytes take 64 d flops.
+// A warp is a worker of its own: it fetches its 16-key tiles (TMA boxes,
+// 128-byte swizzle) into a ring of stages, multiplies with mma.sync (16 rows a
+// block, where tcgen05 would waste 112 of 128) and writes its part.  Nothing is
+// shared between warps, so none waits for another, and the eight of an SM hide
+// each other's latencies; the many parts cost little to merge, a row of d
+// floats each for few rows.
+#pragma once
+#include "paged.cuh"
+
+namespace cpattn {
+
+constexpr int kSmallWarps = 8;  // workers of a CTA, one CTA an SM
+
+template <int D>
+struct SmallSmem {
+  static constexpr int kHalf = 16 * 128;                 // 64 columns of a tile, 128 bytes a row
+  static constexpr int kKV = 16 * D * 2;                 // K or V of a stage
+  static constexpr int kStages = 24 * 1024 / (2 * kKV);  // 3 (d = 128) or 6: 192 KB in flight on an SM
+  static constexpr int kWarp = kStages * 2 * kKV;        // of one warp; a multiple of 1 KB
+  // Segments known: those of the tiles in flight (a segment may be one tile)
+  // and the end mark.
+  static constexpr int kSegs = kStages + 1;
+  static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, two cuts
+  static constexpr int offBar = offSums + 2 * kMaxEntries / 32 * 8;
+  static constexpr int offSeg = offBar + kSmallWarps * kStages * 8;
+  static constexpr int offHeld = offSeg + kSmallWarps * kSegs * static_cast<int>(sizeof(PagedSegment));
+  static constexpr int kBytes = offHeld + kSmallWarps * kStages * 4;  // held: whether the stage's page was fetched
+};
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// The barriers of warp `warp`, by one lane.
+template <int D>
+__device__ __forceinline__ void small_init(uint8_t* smem, int warp) {
+  using SM = SmallSmem<D>;
+  for (int i = 0; i < SM::kStages; ++i) mbar_init(smem_u32(smem) + SM::offBar + 8u * (warp * SM::kStages + i), 1);
+  fence_mbar_init();
+}
+
+// The share of the block's warp `warp`, whose walk has begun and whose
+// barriers are set.  Entries have up to 16 NRB rows.
+template <typename T, int D, int NRB>
+__device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                             PagedWalker& walk) {
+  using SM = SmallSmem<D>;
+  constexpr int NH = D / 64, S = SM::kStages;
+  constexpr uint32_t kAll = 0xffffffffu;
+  const uint32_t s0 = smem_u32(smem) + warp * SM::kWarp;
+  const uint32_t full0 = smem_u32(smem) + SM::offBar + 8u * (warp * S);
+  const int lane = threadIdx.x & 31;
+  const PagedAttnArgs& args = walk.a;
+  const PagedGeom& g = args.g;
+  int32_t* status = args.status;
+  PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg) + warp * SM::kSegs;
+  volatile int* held = reinterpret_cast<volatile int*>(smem + SM::offHeld) + warp * S;
+
+  // ---- Fetching, S tiles ahead of the computing.  Lane: K or V, column half.
+  const int f_kv = lane & 1, f_half = lane >> 1;
+  const CUtensorMap* f_map = f_kv ? &tm_v : &tm_k;
+  const uint32_t f_dst = s0 + f_kv * SM::kKV + f_half * SM::kHalf;
+  int f_seg = 0, f_n = 0;              // segments walked, tiles fetched
+  int f_tile = 0, f_end = 0, f_h = 0;  // of the segment being fetched
+  int f_pages = -1, f_next = -1;       // lane: page of tile (f_tile & ~31) + lane, and of the 32 after
+  bool f_more = true;
+  auto pages_of = [&](int tile) {
+    return tile < f_end ? walk.table[static_cast<long long>(tile) * 16 >> g.page_shift] : -1;
+  };
+  auto fetch = [&]() {
+    if (!f_more) return;
+    if (f_tile == f_end) {
+      const PagedSegment s = walk.next();
+      if (lane == 0) segs[f_seg % SM::kSegs] = s;
+      __syncwarp();
+      ++f_seg;
+      if (!(f_more = s.nt > 0)) return;
+      f_tile = s.tile0;
+      f_end = s.tile1;
+      f_h = s.h;
+      f_pages = pages_of((f_tile & ~31) + lane);
+      f_next = pages_of((f_tile & ~31) + 32 + lane);
+    } else if ((f_tile & 31) == 0) {
+      f_pages = f_next;
+      f_next = pages_of(f_tile + 32 + lane);
+    }
+    const int page = __shfl_sync(kAll, f_pages, f_tile & 31), st = f_n % S;
+    const bool there = page >= 0 && page < g.num_pages;
+    if (lane == 0) {
+      (void)CP_CHECK_DATA(there, status);
+      held[st] = there;
+      mbar_arrive_expect_tx(full0 + 8u * st, there ? 2 * SM::kKV : 0);
+    }
+    __syncwarp();
+    if (there && lane < 2 * NH)
+      tma_load_4d(f_dst + st * 2 * SM::kKV, f_map, full0 + 8u * st, f_half * 64, (f_tile * 16) & ((1 << g.page_shift) - 1), f_h, page);
+    ++f_n;
+    ++f_tile;
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) fetch();
+
+  // ---- Computing.
+  const float sl2 = g.scale * 1.4426950408889634f;
+  const int qr = lane >> 2, qc = 2 * (lane & 3);  // row and first column of the lane in an MMA fragment
+  // ldmatrix rows of the lane: K (16 keys x 16 columns) and V (the same, transposed on the way).
+  const int k_row = ((lane >> 4) << 3) + (lane & 7), k_piece = (lane >> 3) & 1;
+  const int v_row = (((lane >> 3) & 1) << 3) + (lane & 7), v_piece = lane >> 4;
+  int n = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (int c_seg = 0; ok; ++c_seg) {
+    const PagedSegment seg = segs[c_seg % SM::kSegs];
+    if (seg.nt == 0) break;
+    const int rows = seg.nt * g.G;
+    const int lim_all = min(seg.keys, seg.limit0);               // seen by every row
+    int lim[NRB][2];                                             // seen by the lane's rows
+    uint32_t q[NRB][D / 16][4];
+#pragma unroll
+    for (int b = 0; b < NRB; ++b) {
+      const T* p[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = b * 16 + x * 8 + qr, i = r / g.G;
+        lim[b][x] = r < rows ? min(seg.keys, seg.limit0 + i) : 0;
+        p[x] = static_cast<const T*>(args.q) + (static_cast<long long>(seg.t0) + i) * args.q_stride + (seg.h * g.G + r - i * g.G) * D + qc;
+      }
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          q[b][k][x] = b * 16 + (x & 1) * 8 + qr < rows ? *reinterpret_cast<const uint32_t*>(p[x & 1] + k * 16 + (x >> 1) * 8) : 0u;
+    }
+    float o[NRB][D / 8][4], m[NRB][2], l[NRB][2];
+#pragma unroll
+    for (int b = 0; b < NRB; ++b) {
+      m[b][0] = m[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
+    }
+#pragma unroll 1
+    for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
+      const int st = n % S, key0 = tile * 16;
+      ok = __all_sync(kAll, mbar_wait_short(full0 + 8u * st, (n / S) & 1, nullptr, status));
+      if (!ok) break;
+      const bool there = held[st];
+      const bool clean = there && key0 + 16 <= lim_all;
+      const uint32_t sk = s0 + st * 2 * SM::kKV, sv = sk + SM::kKV;
+      // S = Q K^T for 16 keys; with one row block two chains per 8 keys.
+      constexpr int CH = NRB == 1 ? 2 : 1;
+      float c[NRB][CH][2][4];
+#pragma unroll
+      for (int b = 0; b < NRB; ++b)
+#pragma unroll
+        for (int i = 0; i < CH * 8; ++i) c[b][i / 8][(i / 4) & 1][i & 3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t f[4];
+        ldmatrix4<false>(f, sk + (k >> 2) * SM::kHalf + k_row * 128 + ((((k & 3) * 2 + k_piece) ^ (k_row & 7)) << 4));
+#pragma unroll
+        for (int b = 0; b < NRB; ++b) {
+          mma16816<T>(c[b][k % CH][0], q[b][k], f[0], f[1]);
+          mma16816<T>(c[b][k % CH][1], q[b][k], f[2], f[3]);
+        }
+      }
+      uint32_t keep0 = kAll, keep1 = kAll;  // V rows that hold keys, for the lane's two pairs
+      uint32_t pa[NRB][4];
+#pragma unroll
+      for (int b = 0; b < NRB; ++b) {
+        float x[8];  // first row: 0, 1, 4, 5; second: 2, 3, 6, 7
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (c[b][0][i >> 2][i & 3] + (CH == 2 ? c[b][CH - 1][i >> 2][i & 3] : 0.f)) * sl2;
+        if (!clean) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int key = key0 + (i >> 2) * 8 + qc + (i & 1);
+            if (!there || key >= lim[b][(i >> 1) & 1]) x[i] = -INFINITY;
+            // What lies behind the last key may be anything, NaN included: 0 * NaN would reach O.
+            if (b == 0 && !(i & 2) && (!there || key >= seg.keys)) (i & 4 ? keep1 : keep0) &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+          }
+        }
+        const float mx0 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])), mx1 = fmaxf(fmaxf(x[2], x[3]), fmaxf(x[6], x[7]));
+        if (!__all_sync(kAll, mx0 <= m[b][0] + Weight<T>::kSlack && mx1 <= m[b][1] + Weight<T>::kSlack)) {
+          float t[2] = {mx0, mx1};
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], 1));
+            t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], 2));
+            const float up = t[y] > m[b][y] + Weight<T>::kSlack ? t[y] : m[b][y];
+            const float f = up > m[b][y] ? ex2_approx(m[b][y] - up) : 1.f;
+            m[b][y] = up;
+            l[b][y] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              o[b][i][2 * y] *= f;
+              o[b][i][2 * y + 1] *= f;
+            }
+          }
+        }
+        const float off[2] = {Weight<T>::kBias - (m[b][0] == -INFINITY ? 0.f : m[b][0]),
+                              Weight<T>::kBias - (m[b][1] == -INFINITY ? 0.f : m[b][1])};
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = ex2_approx(x[i] + off[(i >> 1) & 1]);
+        l[b][0] += (p[0] + p[1]) + (p[4] + p[5]);
+        l[b][1] += (p[2] + p[3]) + (p[6] + p[7]);
+        // The weights are rounded to the cache's type for the product with V;
+        // their sum is not.
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pa[b][i] = Elem<T>::pack(p[2 * i], p[2 * i + 1]);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t f[4];
+        ldmatrix4<true>(f, sv + (i >> 2) * SM::kHalf + v_row * 128 + ((((i & 3) * 2 + v_piece) ^ (v_row & 7)) << 4));
+        if (!clean) {
+          f[0] &= keep0;
+          f[1] &= keep1;
+          f[2] &= keep0;
+          f[3] &= keep1;
+        }
+#pragma unroll
+        for (int b = 0; b < NRB; ++b) {
+          mma16816<T>(o[b][2 * i], pa[b], f[0], f[1]);
+          mma16816<T>(o[b][2 * i + 1], pa[b], f[2], f[3]);
+        }
+      }
+      __syncwarp();  // the stage is read: the next tile may land on it
+      fetch();
+    }
+    if (!ok) break;
+    const bool final_rows = seg.mode == kRowsFinal;
+#pragma unroll
+    for (int b = 0; b < NRB; ++b)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float sum = l[b][y];
+        sum += __shfl_xor_sync(kAll, sum, 1);
+        sum += __shfl_xor_sync(kAll, sum, 2);
+        const int r = b * 16 + y * 8 + qr, i = r / g.G;
+        if (r >= rows) continue;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int token = seg.t0 + i, head = seg.h * g.G + r - i * g.G;
+        const long long row = static_cast<long long>(token) * g.Hq + head;
+        const long long at = seg.row + (seg.mode == kRowsHome ? row : r);
+        if (final_rows && !args.out_fp32) {
+          T* dst = static_cast<T*>(args.o) + row * D + qc;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<uint32_t*>(dst + j * 8) = Elem<T>::pack(o[b][j][2 * y] * inv, o[b][j][2 * y + 1] * inv);
+        } else {
+          float* dst = (final_rows ? static_cast<float*>(args.o) + row * D : args.part_o + at * D) + qc;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[b][j][2 * y] * inv, o[b][j][2 * y + 1] * inv);
+        }
+        if ((lane & 3) == 0) {
+          const float lse2 = sum > 0.f ? m[b][y] + log2f(sum) - Weight<T>::kBias : -INFINITY;
+          if (final_rows)
+            args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
+          else
+            args.part_lse[at] = lse2;
+        }
+      }
+  }
+  if (!ok)  // let every copy still in flight land
+    for (; n < f_n; ++n) mbar_wait(full0 + 8u * (n % S), (n / S) & 1, nullptr, status);
+}
+
+}  // namespace cpattn
