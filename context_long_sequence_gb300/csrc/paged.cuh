@@ -72,6 +72,12 @@ struct PagedSegment {
 };
 enum : int { kRowsFinal = 0, kRowsHome = 1, kRowsSlot = 2 };
 
+// Which share a warp takes up: cut number `cut`, as worker `worker` of at most
+// max_workers with at least min_units units each; its slots.
+struct PagedRole {
+  int cut, worker, max_workers, min_units, slots, slot_rows;
+};
+
 // Walks a worker's units, one warp, 32 entries at a time, an entry a lane.
 // Every warp of a block totals the units and chooses; the one that fetches
 // goes on to walk.
@@ -102,143 +108,155 @@ struct PagedWalker {
   }
   // Units of the window's entries under cut `c`.
   __device__ __forceinline__ long long window_units(const PagedCut& c) const {
-    long long x = paged_head_units(g, c, entry) * g.Hkv;
-#pragma unroll
-    for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-    return x;
+    const long long x = paged_head_units(g, c, entry) * g.Hkv;  // below 2^48: two 24-bit sums of 32 each
+    const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x & 0xffffff));
+    const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x >> 24));
+    return (static_cast<long long>(hi) << 24) + lo;
   }
   __device__ __forceinline__ void scan() {
     const int lane = threadIdx.x & 31;
     head_units = paged_head_units(g, cut, entry);
     upto = head_units * g.Hkv;
-#pragma unroll
+#pragma unroll 1
     for (int x = 1; x < 32; x <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, upto, x);
       if (lane >= x) upto += y;
     }
   }
 
-  // All units under the N cuts.  Called by the whole block; `sums` (N numbers
-  // for each window of 32 entries) holds the windows' until begin().
-  template <int N>
-  __device__ __forceinline__ void totals(long long* sums, const PagedCut (&cuts)[N], long long (&units)[N]) {
+  // The worker's place among the units.  Called by the whole block: every
+  // warp totals the units under the N cuts (`sums`: N numbers in shared
+  // memory for each window of 32 entries), and choose(units) returns the
+  // PagedRole of the calling warp.  False: nothing for it.  `sums` is free
+  // once every warp has returned.
+  //
+  // Code that a CTA runs once comes from L2 line by line, the same lines for
+  // all SMs at once, some 15 clocks an instruction: this is written to be
+  // short, with one copy of load().
+  template <int N, typename F>
+  __device__ __forceinline__ bool start(long long* sums, const PagedCut (&cuts)[N], F&& choose) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int windows = (E + 31) / 32;
+    const bool alone = windows == 1;
     covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
     covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
-    if (windows == 1) {
-      load(0);
+    long long units[N];
+    bool chosen = false, any = false;
+    int w = alone ? 0 : warp;
+#pragma unroll 1
+    while (true) {
+      if (w < windows) load(w * 32);
+      if (chosen) break;
+      if (w < windows) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) units[i] = window_units(cuts[i]);
-      return;
-    }
-    for (int w = warp; w < windows; w += warps) {
-      load(w * 32);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const long long x = window_units(cuts[i]);
-        if (lane == 0) sums[w * N + i] = x;
+        for (int i = 0; i < N; ++i) {
+          units[i] = window_units(cuts[i]);
+          if (!alone && lane == 0) sums[w * N + i] = units[i];
+        }
       }
-    }
-    __syncthreads();
+      if (!alone) {
+        w += warps;
+        if (w < windows) continue;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      long long x = 0;
-      for (int w = lane; w < windows; w += 32) x += sums[w * N + i];
-#pragma unroll
-      for (int y = 16; y > 0; y >>= 1) x += __shfl_xor_sync(0xffffffffu, x, y);
-      units[i] = x;
+        for (int i = 0; i < N; ++i) {
+          units[i] = 0;
+#pragma unroll 1
+          for (int k = 0; k < windows; ++k) units[i] += sums[k * N + i];
+        }
+      }
+      const PagedRole r = choose(units);
+      cut = cuts[r.cut];
+      slots = r.slots;
+      slot_rows = r.slot_rows;
+      worker = r.worker;
+      shares = PagedShares(units[r.cut], r.max_workers, r.min_units);
+      before = 0;
+      any = worker < shares.workers;
+      if (!any) break;
+      u = shares.first(worker);
+      end = shares.first(worker + 1);
+      if (alone) break;
+#pragma unroll 1
+      for (w = 0; w + 1 < windows && before + sums[w * N + r.cut] <= u; ++w) before += sums[w * N + r.cut];
+      chosen = true;
     }
-  }
-
-  // Take up worker `worker_`'s share of cut `c`, number `i` of the N totalled.
-  // False: nothing for it.  Not called by the whole block; `sums` may be
-  // overwritten once all its warps are through.
-  template <int N>
-  __device__ __forceinline__ bool begin(const long long* sums, int i, const PagedCut& c, long long units, int worker_,
-                                        int max_workers, int min_units, int slots_, int slot_rows_) {
-    cut = c;
-    slots = slots_;
-    slot_rows = slot_rows_;
-    worker = worker_;
-    shares = PagedShares(units, max_workers, min_units);
-    before = 0;
-    if (worker >= shares.workers) return false;
-    u = shares.first(worker);
-    end = shares.first(worker + 1);
-    const int windows = (E + 31) / 32;
-    int w = 0;
-    if (windows > 1)
-      while (w + 1 < windows && before + sums[w * N + i] <= u) before += sums[w++ * N + i];
-    if (base != w * 32) load(w * 32);
-    scan();
-    return true;
+    if (any) scan();
+    return any;
   }
 
   // The next segment (warp-uniform), nt == 0 behind the last.  The run that
-  // begins a token tile also records where the tile's parts are.
+  // begins a token tile's keys also records where the tile's parts are.
   __device__ __forceinline__ PagedSegment next() {
     PagedSegment s{0, 0, 0, 0, 0, 0, 0, 0, 0};
-    if (u >= end) return s;
-    long long total = shfl64(upto, 31);
-    while (u >= before + total) {
-      if (base + 32 >= E) {  // only where the arrays changed under the kernel
-        end = u;
-        return s;
+    while (u < end) {
+      long long total = shfl64(upto, 31);
+      while (u >= before + total) {
+        if (base + 32 >= E) {  // only where the arrays changed under the kernel
+          end = u;
+          return s;
+        }
+        before += total;
+        load(base + 32);
+        scan();
+        total = shfl64(upto, 31);
       }
-      before += total;
-      load(base + 32);
-      scan();
-      total = shfl64(upto, 31);
-    }
-    long long rel = u - before;
-    const int at = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;  // exists: rel < total
-    const long long hu = shfl64(head_units, at);
-    rel -= shfl64(upto, at) - hu * g.Hkv;
-    const int id = base + at;
-    PagedEntry e;
-    e.t0 = __shfl_sync(0xffffffffu, entry.t0, at);
-    e.n = __shfl_sync(0xffffffffu, entry.n, at);
-    e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
-    e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
-    const bool prefix = id >= g.B;
-    table = prefix ? g.prefix_table + static_cast<size_t>(id - g.B) * g.prefix_stride
-                   : g.page_table + static_cast<size_t>(id) * g.table_stride;
-    s.h = static_cast<int>(paged_div(rel, hu));
-    rel -= s.h * hu;
-    int rb = 0, tiles = paged_tile_units(cut, e, 0);
-    while (rel >= tiles && (rb + 1) * cut.tile_tokens < e.n) {
-      rel -= tiles;
-      tiles = paged_tile_units(cut, e, ++rb);
-    }
-    s.t0 = e.t0 + rb * cut.tile_tokens;
-    s.nt = min(cut.tile_tokens, e.n - rb * cut.tile_tokens);
-    s.keys = e.keys;
-    s.limit0 = e.limit0 + rb * cut.tile_tokens;
-    s.tile0 = static_cast<int>(rel);
-    s.tile1 = static_cast<int>(min(static_cast<long long>(tiles), rel + (end - u)));
-    const long long u0 = u - s.tile0;
-    u += s.tile1 - s.tile0;
-    const bool begins = s.tile0 == 0, whole = begins && s.tile1 == tiles;
-    const int home = static_cast<int>(a.rows_large_end) + (prefix ? a.max_tokens * g.Hq : 0);
-    if (whole) {
-      s.mode = prefix || (id >= covered0 && id < covered1) ? kRowsHome : kRowsFinal;
-      s.row = home;
-    } else {
-      s.mode = kRowsSlot;
-      s.row = slots + (2 * worker + (begins ? 1 : 0)) * slot_rows;
-    }
-    if (begins) {
-      const int last = whole ? worker : shares.worker_of(u0 + tiles - 1);
-      PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
-      for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
-        PagedParts r;
-        r.first = s.mode == kRowsSlot ? s.row + i * g.G : s.row + (s.t0 + i) * g.Hq + s.h * g.G;
-        r.second = slots + 2 * (worker + 1) * slot_rows + i * g.G;
-        r.count = last - worker + 1;
-        r.stride = 2 * slot_rows;
-        parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
+      long long rel = u - before;
+      const int at = __ffs(__ballot_sync(0xffffffffu, upto > rel)) - 1;  // exists: rel < total
+      const long long hu = shfl64(head_units, at);
+      rel -= shfl64(upto, at) - hu * g.Hkv;
+      const int id = base + at;
+      PagedEntry e;
+      e.t0 = __shfl_sync(0xffffffffu, entry.t0, at);
+      e.n = __shfl_sync(0xffffffffu, entry.n, at);
+      e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
+      e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
+      const bool prefix = id >= g.B;
+      table = prefix ? g.prefix_table + static_cast<size_t>(id - g.B) * g.prefix_stride
+                     : g.page_table + static_cast<size_t>(id) * g.table_stride;
+      s.h = static_cast<int>(paged_div(rel, hu));
+      rel -= s.h * hu;
+      int rb = 0, tiles = paged_tile_units(cut, e, 0);
+      while (rel >= tiles && (rb + 1) * cut.tile_tokens < e.n) {
+        rel -= tiles;
+        tiles = paged_tile_units(cut, e, ++rb);
       }
+      s.t0 = e.t0 + rb * cut.tile_tokens;
+      s.nt = min(cut.tile_tokens, e.n - rb * cut.tile_tokens);
+      s.keys = e.keys;
+      s.limit0 = e.limit0 + rb * cut.tile_tokens;
+      const long long u0 = u - rel;  // the token tile's first unit
+      const int left = static_cast<int>(min(static_cast<long long>(tiles), rel + (end - u))) - cut.lead;
+      u += left + cut.lead - rel;
+      s.tile0 = max(0, static_cast<int>(rel) - cut.lead);
+      s.tile1 = left;
+      tiles -= cut.lead;
+      if (s.tile1 <= s.tile0) {  // only its lead falls to this worker
+        s.nt = 0;
+        continue;
+      }
+      const bool begins = s.tile0 == 0, whole = begins && s.tile1 == tiles;
+      const int home = static_cast<int>(a.rows_large_end) + (prefix ? a.max_tokens * g.Hq : 0);
+      if (whole) {
+        s.mode = prefix || (id >= covered0 && id < covered1) ? kRowsHome : kRowsFinal;
+        s.row = home;
+      } else {
+        s.mode = kRowsSlot;
+        s.row = slots + (2 * worker + (begins ? 1 : 0)) * slot_rows;
+      }
+      if (begins) {
+        const int last = whole ? worker : shares.worker_of(u0 + cut.lead + tiles - 1);
+        PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
+        for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
+          PagedParts r;
+          r.first = s.mode == kRowsSlot ? s.row + i * g.G : s.row + (s.t0 + i) * g.Hq + s.h * g.G;
+          r.second = slots + 2 * (worker + 1) * slot_rows + i * g.G;
+          r.count = last - worker + 1;
+          r.stride = 2 * slot_rows;
+          parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
+        }
+      }
+      break;
     }
     return s;
   }

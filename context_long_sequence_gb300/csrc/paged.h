@@ -88,8 +88,8 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 // How the attention of a batch is cut into work.  A cut takes the entries
 // whose rows (tokens x query heads of a KV head) lie in [min_rows, max_rows],
 // cuts their tokens into tiles of tile_tokens and each tile's visible keys
-// into tiles of tile_keys.  One key tile of one token tile and KV head is a
-// unit; units are numbered entry by entry, KV head by KV head, token tile by
+// into tiles of 2^key_shift.  One key tile of one token tile and KV head is a
+// unit, and the loading and writing of its rows a few more; units are numbered entry by entry, KV head by KV head, token tile by
 // token tile, and each of the W workers (CTAs) takes an equal, contiguous
 // share of the numbers.  A token tile whose units fall to several workers
 // has as many parts, merged afterwards by their log-sum-exp.  The cut depends
@@ -97,13 +97,15 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 struct PagedCut {
   int min_rows, max_rows;
   int tile_tokens, key_shift;  // tiles of 2^key_shift keys
+  int lead;                    // units without keys that stand for a token tile's own cost
 };
 
-// Key tiles that token tile `rb` of entry `e` sees.
+// Units of token tile `rb` of entry `e`: `lead`, then the key tiles it sees;
+// none if it sees no key.
 __host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEntry& e, int rb) {
   const int last = (rb + 1) * c.tile_tokens < e.n ? (rb + 1) * c.tile_tokens - 1 : e.n - 1;
   const int seen = e.limit0 + last < e.keys ? e.limit0 + last : e.keys;
-  return seen > 0 ? (seen + (1 << c.key_shift) - 1) >> c.key_shift : 0;
+  return seen > 0 ? c.lead + ((seen + (1 << c.key_shift) - 1) >> c.key_shift) : 0;
 }
 
 // Units of entry `e` for one KV head.
@@ -155,14 +157,16 @@ struct PagedShares {
 // CTA (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
 constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallRowsBeside = 16, kSmallKeyShift = 4;
 constexpr int kSmallMinUnits = 4;
+constexpr int kSmallLead = 2;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
+constexpr int kLargeLead = 4;
 constexpr int kMaxEntries = 8192;
 
 inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
-  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift};
+  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead};
 }
 inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kSmallRowsBeside + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift};
+  return PagedCut{kSmallRowsBeside + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.

@@ -22,6 +22,8 @@ namespace cpattn {
 namespace {
 
 constexpr int kAppendWarps = 4;
+constexpr int kAhead = 4;            // groups of heads whose loads are in flight together
+constexpr int kFillWarps = 152 * 32;  // warps that keep the memory busy
 
 // Eight pairs: a[i], b[i].  Halves: the pairs are (a, b) of the two pieces.
 // Interleaved: neighbours, four pairs in each piece.
@@ -84,35 +86,50 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
       sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &sn[i], &c[i]);  // 2^-31
     }
   }
-  const int heads = g.Hq + 2 * g.Hkv;
-  for (int h0 = unit * HPG; h0 < heads; h0 += units * HPG) {
-    const int h = h0 + sub;
-    if (h >= heads) continue;
-    const T* src;
-    T* dst;
-    if (h < g.Hq) {
-      if (!args.q) continue;
-      src = static_cast<const T*>(args.q) + t * args.q_stride + h * D;
-      dst = static_cast<T*>(args.q_out) + t * args.q_out_stride + h * D;
-    } else if (h < g.Hq + g.Hkv) {
-      src = static_cast<const T*>(args.k) + t * args.k_stride + (h - g.Hq) * D;
-      dst = static_cast<T*>(args.k_cache) + row + (h - g.Hq) * g.head_stride;
-    } else {
-      src = static_cast<const T*>(args.v) + t * args.v_stride + (h - g.Hq - g.Hkv) * D;
-      dst = static_cast<T*>(args.v_cache) + row + (h - g.Hq - g.Hkv) * g.head_stride;
+  const int heads = g.Hq + 2 * g.Hkv, groups = (heads + HPG - 1) / HPG;
+  // Four groups at a time, their loads before the first store.
+  for (int g0 = unit; g0 < groups; g0 += kAhead * units) {
+    uint4 a[kAhead], b[kAhead];
+    T* dst[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = (g0 + i * units) * HPG + sub;
+      const T* src = nullptr;
+      dst[i] = nullptr;
+      if (h < g.Hq) {
+        if (args.q) {
+          src = static_cast<const T*>(args.q) + t * args.q_stride + h * D;
+          dst[i] = static_cast<T*>(args.q_out) + t * args.q_out_stride + h * D;
+        }
+      } else if (h < g.Hq + g.Hkv) {
+        src = static_cast<const T*>(args.k) + t * args.k_stride + (h - g.Hq) * D;
+        dst[i] = static_cast<T*>(args.k_cache) + row + (h - g.Hq) * g.head_stride;
+      } else if (h < heads) {
+        src = static_cast<const T*>(args.v) + t * args.v_stride + (h - g.Hq - g.Hkv) * D;
+        dst[i] = static_cast<T*>(args.v_cache) + row + (h - g.Hq - g.Hkv) * g.head_stride;
+      }
+      if (src) {
+        a[i] = *reinterpret_cast<const uint4*>(src + ea);
+        b[i] = *reinterpret_cast<const uint4*>(src + eb);
+      }
     }
-    uint4 a = *reinterpret_cast<const uint4*>(src + ea);
-    uint4 b = *reinterpret_cast<const uint4*>(src + eb);
-    if (rotated && h < g.Hq + g.Hkv) turn<T>(a, b, c, sn, args.interleaved != 0);
-    *reinterpret_cast<uint4*>(dst + ea) = a;
-    *reinterpret_cast<uint4*>(dst + eb) = b;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!dst[i]) continue;
+      if (rotated && (g0 + i * units) * HPG + sub < g.Hq + g.Hkv) turn<T>(a[i], b[i], c, sn, args.interleaved != 0);
+      *reinterpret_cast<uint4*>(dst[i] + ea) = a[i];
+      *reinterpret_cast<uint4*>(dst[i] + eb) = b[i];
+    }
   }
 }
 
 template <typename T, int D>
 int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const int groups = (a.g.Hq + 2 * a.g.Hkv + 512 / D - 1) / (512 / D);
-  const int units = groups;
+  // Few tokens: a warp for each group of heads, for latency.  Many: a warp
+  // takes more of its token's heads, as one set of sines serves them all.
+  int units = (kFillWarps + a.g.N - 1) / a.g.N;
+  units = units < 1 ? 1 : units > groups ? groups : units;
   const long long warps = static_cast<long long>(a.g.N) * units;
   const long long grid = (warps + kAppendWarps - 1) / kAppendWarps;
   if (grid > 0x7fffffffLL) return CP_ERR_UNSUPPORTED;

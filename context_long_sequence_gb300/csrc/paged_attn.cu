@@ -47,12 +47,12 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
   __syncwarp();
   PagedWalker walk(args);
   const PagedCut cuts[1] = {paged_cut_small(args.g.G, 16 * NRB)};
-  long long units[1];
-  long long* sums = reinterpret_cast<long long*>(smem + SM::offSums);
-  walk.totals(sums, cuts, units);
   // Workers of different SMs first, so that a short batch has the whole card.
-  if (walk.begin<1>(sums, 0, cuts[0], units[0], warp * gridDim.x + blockIdx.x, kSmallWarps * gridDim.x, kSmallMinUnits, 0,
-                    kSmallRows))
+  const auto role = [&](const long long (&)[1]) {
+    return PagedRole{0, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kSmallWarps * static_cast<int>(gridDim.x),
+                     kSmallMinUnits, 0, kSmallRows};
+  };
+  if (walk.start(reinterpret_cast<long long*>(smem + SM::offSums), cuts, role))
     small_worker<T, D, NRB>(smem, warp, tm_k, tm_v, walk);
 }
 

@@ -133,27 +133,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
   PagedWalker walk(args);
   const PagedCut cuts[2] = {paged_cut_small(g.G, kSmallRowsBeside), paged_cut_large(g.G)};
-  long long units[2];
-  // Behind the small workers' stages; where V will be, for the large.
-  long long* sums = reinterpret_cast<long long*>(smem + SmallSmem<D>::offSums);
-  walk.totals(sums, cuts, units);
-  const int large = paged_large_ctas(units[0], units[1], gridDim.x);
+  int large = 0;  // CTAs that take the entries of many rows
+  const auto role = [&](const long long (&units)[2]) {
+    const int ctas = gridDim.x, b = blockIdx.x;
+    large = paged_large_ctas(units[0], units[1], ctas);
+    return b < large ? PagedRole{1, b, large, 1, static_cast<int>(args.rows_small), kLargeRows}
+                     : PagedRole{0, warp * (ctas - large) + b - large, kSmallWarps * (ctas - large), kSmallMinUnits, 0, kSmallRows};
+  };
+  // The sums lie behind the small workers' stages, and where V will be for the large.
+  const bool any = walk.start(reinterpret_cast<long long*>(smem + SmallSmem<D>::offSums), cuts, role);
   if (static_cast<int>(blockIdx.x) >= large) {
     // Entries of few rows: a warp each, eight of the ten.
-    if (warp >= kSmallWarps) return;
-    const int ctas = gridDim.x - large;
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k16);
-      tma_prefetch_desc(&tm_v16);
-      small_init<D>(smem, warp);
-    }
-    __syncwarp();
-    if (walk.begin<2>(sums, 0, cuts[0], units[0], warp * ctas + blockIdx.x - large, kSmallWarps * ctas, kSmallMinUnits, 0,
-                      kSmallRows))
+    if (warp < kSmallWarps && any) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k16);
+        tma_prefetch_desc(&tm_v16);
+        small_init<D>(smem, warp);
+      }
+      __syncwarp();
       small_worker<T, D, 1>(smem, warp, tm_k16, tm_v16, walk);
+    }
     return;
   }
-  const bool any = walk.begin<2>(sums, 1, cuts[1], units[1], blockIdx.x, large, 1, args.rows_small, kLargeRows);
   if (!any) return;  // the whole block
   const int block_tokens = cuts[1].tile_tokens / 2;
   const uint32_t box_all = (1u << (BN / box_rows)) - 1;
@@ -321,6 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     int j = 0, k = 0, nseg = 0;  // key tiles walked, seen, segments
     bool ok = true;
     PagedSegment seg;
+    // The first segment begins with two tiles of zeros that are not there,
+    // one down the path of a segment's first tile and one down that of whole
+    // tiles: they bring that code into the caches while the first K and V are
+    // on their way.  They wait for nothing, signal nothing, and work on TMEM
+    // that holds nothing yet.
+    const uint32_t tDry = tmem + (D == 128 ? 256 + D * t : 384) + lane_off;
+    {
+      const uint32_t zero[16] = {};
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 16) tmem_st16(tDry + c, zero);
+      tmem_wait_st();
+    }
     while (ok && take(nseg, seg)) {
       const RowBlock w = row_block(seg, t, block_tokens);
       const int first = t * block_tokens;
@@ -352,23 +365,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(BAR_Q));
       float m = -INFINITY, l = 0.f;
       const int k0 = k;
-      for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
+      for (int tile = nseg == 0 ? seg.tile0 - 2 : seg.tile0; ok && tile < seg.tile1; ++tile, j += tile > seg.tile0) {
+        const bool dry = tile < seg.tile0;
+        const uint32_t tS = dry ? tDry : tSt;
         const int key0 = tile * BN;
-        if (!w.sees(key0)) continue;
+        if (tile == seg.tile0) {
+          m = -INFINITY;
+          l = 0.f;
+        }
+        if (!dry && !w.sees(key0)) continue;
         // K, V and the box mask of the tile are visible through the tile's barrier.
-        ok = warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
-                      mbar_wait_short(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
+        ok = dry || warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
+                             mbar_wait_short(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t held = mask[j % kTileBars];
-        const bool full = held == box_all && key0 + BN <= w.lo;
+        const uint32_t held = dry ? box_all : mask[j % kTileBars];
+        const bool full = dry ? tile + 1 == seg.tile0 : held == box_all && key0 + BN <= w.lo;
         auto signal = [&](int b) {
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(b + t));
+          if (lane == 0 && !dry) mbar_arrive(bar(b + t));
         };
-        if (held != box_all || key0 + BN > seg.keys) {
+        if (!dry && (held != box_all || key0 + BN > seg.keys)) {
           // V rows behind the last key (or in a page that was not fetched) may
           // hold anything, NaN included; a zero weight does not remove a NaN.
           if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
@@ -381,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!busy) {
           signal(BAR_P_HALF);
           signal(BAR_P_FULL);
-          ++k;
+          k += !dry;
           continue;
         }
         uint32_t sr[BN];
@@ -410,13 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // against it before any maximum is taken; their sum bounds each of
         // them and the maximum of keys 64-127 the rest.
         if (full && warp_all(m != -INFINITY || !row_valid)) {
-          tmem_ld32(tSt, col32(0));
-          tmem_ld32(tSt + 32, col32(1));
+          tmem_ld32(tS, col32(0));
+          tmem_ld32(tS + 32, col32(1));
           tmem_wait_ld();
           reg_fence(col32(0));
           reg_fence(col32(1));
-          tmem_ld32(tSt + 64, col32(2));
-          tmem_ld32(tSt + 96, col32(3));
+          tmem_ld32(tS + 64, col32(2));
+          tmem_ld32(tS + 96, col32(3));
           f32x2 rs2[4] = {zero2, zero2, zero2, zero2};
           uint32_t pk0[16], pk1[16];
           exp32(sr, m, rs2, pk0);
@@ -434,17 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mx_hi = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float s_lo = sum4(rs2);
           if (warp_all((s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < m + Weight<T>::kSpecMax) || !row_valid)) {
-            tmem_st16(tSt, pk0);
-            tmem_st16(tSt + 16, pk1);
+            tmem_st16(tS, pk0);
+            tmem_st16(tS + 16, pk1);
             signal(BAR_P_HALF);
             f32x2 rh[4] = {zero2, zero2, zero2, zero2};
             exp32(sr + 64, m, rh, pk0);
-            tmem_st16(tSt + 32, pk0);
+            tmem_st16(tS + 32, pk0);
             exp32(sr + 96, m, rh, pk1);
-            tmem_st16(tSt + 48, pk1);
+            tmem_st16(tS + 48, pk1);
             signal(BAR_P_FULL);
             l += s_lo + sum4(rh);
-            ++k;
+            k += !dry;
             continue;
           }
         }
@@ -452,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // max: 32 columns at a time, once for the maximum and once for the
         // weights.
         auto load = [&](int c, uint32_t (&r)[32]) {
-          tmem_ld32(tSt + c * 32, r);
+          tmem_ld32(tS + c * 32, r);
           tmem_wait_ld();
           reg_fence(r);
           if (full) return;
@@ -504,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t r[32], pk[16];
           load(c, r);
           exp32(r, mb, rs2, pk);
-          tmem_st16(tSt + c * 16, pk);
+          tmem_st16(tS + c * 16, pk);
           if (c & 1) signal(c == 1 ? BAR_P_HALF : BAR_P_FULL);
         }
         l = l * alpha + sum4(rs2);
-        ++k;
+        k += !dry;
       }
       // The block's MMAs of this segment have completed: O is whole, and Q's
       // shared memory free for staging and for the next segment.
