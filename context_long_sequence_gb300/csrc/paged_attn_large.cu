@@ -322,18 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     int j = 0, k = 0, nseg = 0;  // key tiles walked, seen, segments
     bool ok = true;
     PagedSegment seg;
-    // The first segment begins with two tiles of zeros that are not there,
-    // one down the path of a segment's first tile and one down that of whole
-    // tiles: they bring that code into the caches while the first K and V are
-    // on their way.  They wait for nothing, signal nothing, and work on TMEM
-    // that holds nothing yet.
-    const uint32_t tDry = tmem + (D == 128 ? 256 + D * t : 384) + lane_off;
-    {
-      const uint32_t zero[16] = {};
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 16) tmem_st16(tDry + c, zero);
-      tmem_wait_st();
-    }
     while (ok && take(nseg, seg)) {
       const RowBlock w = row_block(seg, t, block_tokens);
       const int first = t * block_tokens;
@@ -365,29 +353,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(BAR_Q));
       float m = -INFINITY, l = 0.f;
       const int k0 = k;
-      for (int tile = nseg == 0 ? seg.tile0 - 2 : seg.tile0; ok && tile < seg.tile1; ++tile, j += tile > seg.tile0) {
-        const bool dry = tile < seg.tile0;
-        const uint32_t tS = dry ? tDry : tSt;
+      for (int tile = seg.tile0; ok && tile < seg.tile1; ++tile, ++j) {
         const int key0 = tile * BN;
-        if (tile == seg.tile0) {
-          m = -INFINITY;
-          l = 0.f;
-        }
-        if (!dry && !w.sees(key0)) continue;
+        if (!w.sees(key0)) continue;
         // K, V and the box mask of the tile are visible through the tile's barrier.
-        ok = dry || warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
-                             mbar_wait_short(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
+        ok = warp_all(mbar_wait_short(bar(BAR_T_FULL + j % kTileBars), (j / kTileBars) & 1, abort_flag, status) &&
+                      mbar_wait_short(bar(BAR_S_FULL + t), k & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t held = dry ? box_all : mask[j % kTileBars];
-        const bool full = dry ? tile + 1 == seg.tile0 : held == box_all && key0 + BN <= w.lo;
+        const uint32_t held = mask[j % kTileBars];
+        const bool full = held == box_all && key0 + BN <= w.lo;
         auto signal = [&](int b) {
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0 && !dry) mbar_arrive(bar(b + t));
+          if (lane == 0) mbar_arrive(bar(b + t));
         };
-        if (!dry && (held != box_all || key0 + BN > seg.keys)) {
+        if (held != box_all || key0 + BN > seg.keys) {
           // V rows behind the last key (or in a page that was not fetched) may
           // hold anything, NaN included; a zero weight does not remove a NaN.
           if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
@@ -400,46 +382,100 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!busy) {
           signal(BAR_P_HALF);
           signal(BAR_P_FULL);
-          k += !dry;
+          ++k;
           continue;
         }
-        uint32_t sr[BN];
-        float* x = reinterpret_cast<float*>(sr);
-        auto col32 = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]); };
-        const f32x2 sl2x2 = make_f32x2(sl2, sl2);
-        auto exp32 = [&](const uint32_t* s32, float mb, f32x2 (&rs2)[4], uint32_t (&pk)[16]) {
-          const f32x2 nmbx2 = make_f32x2(kBias - mb, kBias - mb);
+        // A tile that all rows see whole is exponentiated against the running
+        // maximum m before its own is taken: the sum of keys 0-63 bounds each
+        // of them, and the maximum of keys 64-127 (found while those
+        // exponentials run) the rest.  `exact`: m is raised first -- on a
+        // segment's first tile, on masked ones, and where the bounds fail.
+        // Both ways share the exponentials' code, whose first pass through the
+        // instruction caches costs as much as five tiles.
+        bool exact = !(full && warp_all(m != -INFINITY || !row_valid));
+        float alpha = 1.f;
+        while (true) {
+          if (exact) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t r[32];
+              tmem_ld32(tSt + c * 32, r);
+              tmem_wait_ld();
+              reg_fence(r);
+              if (!full) {
+                // Hidden keys become -inf in S.  Boxes are 16 keys or more:
+                // two bits cover 32 columns.
+                const uint32_t in0 = (held >> ((c * 32) >> box_shift)) & 1u, in1 = (held >> ((c * 32 + 16) >> box_shift)) & 1u;
+                const int left = my_lim - key0 - c * 32;
+                const int n0 = in0 ? left : 0, n1 = in1 ? left : 0;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a0, a1;
-            split_f32x2(fma_f32x2(make_f32x2(__uint_as_float(s32[e]), __uint_as_float(s32[e + 1])), sl2x2, nmbx2), a0, a1);
-            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
-            rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], make_f32x2(p0, p1));
-            pk[e >> 1] = Elem<T>::pack(p0, p1);
+                for (int e = 0; e < 32; ++e)
+                  if (e >= (e < 16 ? n0 : n1)) r[e] = 0xff800000u;
+                tmem_st32(tSt + c * 32, r);
+              }
+              float m4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(r[i]);
+#pragma unroll
+              for (int e = 4; e < 32; e += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(r[e + i]));
+              mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            }
+            tmem_wait_st();
+            const float m_new = fmaxf(m, mx * sl2);
+            if (m_new > m + Weight<T>::kSlack) {
+              alpha = ex2_approx(m - m_new);
+              m = m_new;
+            }
+            // O is stable here: this tile's S came after the PV before it.
+            if (k > k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t ov[32];
+                tmem_ld32(tOt + c * 32, ov);
+                tmem_wait_ld();
+                reg_fence(ov);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                tmem_st32(tOt + c * 32, ov);
+              }
+            }
           }
-        };
-        auto sum4 = [](const f32x2 (&rs2)[4]) {
-          float lo[4], hi[4];
+          uint32_t sr[BN];
+          float* x = reinterpret_cast<float*>(sr);
+          auto col32 = [&](int c) -> uint32_t(&)[32] { return *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]); };
+          const f32x2 sl2x2 = make_f32x2(sl2, sl2), zero2 = make_f32x2(0.f, 0.f);
+          const float off = kBias - (m == -INFINITY ? 0.f : m);
+          auto exp32 = [&](int c, f32x2 (&rs2)[4], uint32_t (&pk)[16]) {
+            const f32x2 off2 = make_f32x2(off, off);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split_f32x2(rs2[i], lo[i], hi[i]);
-          return ((lo[0] + hi[0]) + (lo[1] + hi[1])) + ((lo[2] + hi[2]) + (lo[3] + hi[3]));
-        };
-        const f32x2 zero2 = make_f32x2(0.f, 0.f);
-        // Wholly visible tile, running max set: keys 0-63 are exponentiated
-        // against it before any maximum is taken; their sum bounds each of
-        // them and the maximum of keys 64-127 the rest.
-        if (full && warp_all(m != -INFINITY || !row_valid)) {
-          tmem_ld32(tS, col32(0));
-          tmem_ld32(tS + 32, col32(1));
+            for (int e = 0; e < 32; e += 2) {
+              float a0, a1;
+              split_f32x2(fma_f32x2(make_f32x2(x[c * 32 + e], x[c * 32 + e + 1]), sl2x2, off2), a0, a1);
+              const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+              rs2[(e >> 1) & 3] = add_f32x2(rs2[(e >> 1) & 3], make_f32x2(p0, p1));
+              pk[e >> 1] = Elem<T>::pack(p0, p1);
+            }
+          };
+          auto sum4 = [](const f32x2 (&rs2)[4]) {
+            float lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_f32x2(rs2[i], lo[i], hi[i]);
+            return ((lo[0] + hi[0]) + (lo[1] + hi[1])) + ((lo[2] + hi[2]) + (lo[3] + hi[3]));
+          };
+          tmem_ld32(tSt, col32(0));
+          tmem_ld32(tSt + 32, col32(1));
           tmem_wait_ld();
           reg_fence(col32(0));
           reg_fence(col32(1));
-          tmem_ld32(tS + 64, col32(2));
-          tmem_ld32(tS + 96, col32(3));
+          tmem_ld32(tSt + 64, col32(2));  // in flight while keys 0-63 are exponentiated
+          tmem_ld32(tSt + 96, col32(3));
           f32x2 rs2[4] = {zero2, zero2, zero2, zero2};
           uint32_t pk0[16], pk1[16];
-          exp32(sr, m, rs2, pk0);
-          exp32(sr + 32, m, rs2, pk1);
+          exp32(0, rs2, pk0);
+          exp32(1, rs2, pk1);
           tmem_wait_ld();
           reg_fence(col32(2));
           reg_fence(col32(3));
@@ -452,82 +488,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) m4[i] = fmax3(m4[i], x[e + i], x[e + 4 + i]);
           const float mx_hi = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           const float s_lo = sum4(rs2);
-          if (warp_all((s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < m + Weight<T>::kSpecMax) || !row_valid)) {
-            tmem_st16(tS, pk0);
-            tmem_st16(tS + 16, pk1);
-            signal(BAR_P_HALF);
-            f32x2 rh[4] = {zero2, zero2, zero2, zero2};
-            exp32(sr + 64, m, rh, pk0);
-            tmem_st16(tS + 32, pk0);
-            exp32(sr + 96, m, rh, pk1);
-            tmem_st16(tS + 48, pk1);
-            signal(BAR_P_FULL);
-            l += s_lo + sum4(rh);
-            k += !dry;
+          if (!exact && !warp_all((s_lo < Weight<T>::kSpecSum && mx_hi * sl2 < m + Weight<T>::kSpecMax) || !row_valid)) {
+            exact = true;  // S is as it was
             continue;
           }
+          tmem_st16(tSt, pk0);
+          tmem_st16(tSt + 16, pk1);
+          signal(BAR_P_HALF);
+          f32x2 rh[4] = {zero2, zero2, zero2, zero2};
+          exp32(2, rh, pk0);
+          tmem_st16(tSt + 32, pk0);
+          exp32(3, rh, pk1);
+          tmem_st16(tSt + 48, pk1);
+          signal(BAR_P_FULL);
+          l = l * alpha + (s_lo + sum4(rh));
+          ++k;
+          break;
         }
-        // Masked tiles, the first of a segment, and tiles that outgrew the
-        // max: 32 columns at a time, once for the maximum and once for the
-        // weights.
-        auto load = [&](int c, uint32_t (&r)[32]) {
-          tmem_ld32(tS + c * 32, r);
-          tmem_wait_ld();
-          reg_fence(r);
-          if (full) return;
-          // Boxes are 16 keys or more: two bits cover 32 columns.
-          const uint32_t in0 = (held >> ((c * 32) >> box_shift)) & 1u, in1 = (held >> ((c * 32 + 16) >> box_shift)) & 1u;
-          const int left = my_lim - key0 - c * 32;
-          const int n0 = in0 ? left : 0, n1 = in1 ? left : 0;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e >= (e < 16 ? n0 : n1)) r[e] = 0xff800000u;
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t r[32];
-          load(c, r);
-          float m4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(r[i]);
-#pragma unroll
-          for (int e = 4; e < 32; e += 4)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(r[e + i]));
-          mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        }
-        const float m_new = fmaxf(m, mx * sl2);
-        float alpha = 1.f;
-        if (m_new > m + Weight<T>::kSlack) {
-          alpha = ex2_approx(m - m_new);
-          m = m_new;
-        }
-        const float mb = (m == -INFINITY) ? 0.f : m;
-        if (k > k0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld32(tOt + c * 32, ov);
-            tmem_wait_ld();
-            reg_fence(ov);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(tOt + c * 32, ov);
-          }
-        }
-        f32x2 rs2[4] = {zero2, zero2, zero2, zero2};
-        // P of columns 32c.. goes over columns 16c..: read already.
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t r[32], pk[16];
-          load(c, r);
-          exp32(r, mb, rs2, pk);
-          tmem_st16(tS + c * 16, pk);
-          if (c & 1) signal(c == 1 ? BAR_P_HALF : BAR_P_FULL);
-        }
-        l = l * alpha + sum4(rs2);
-        k += !dry;
       }
       // The block's MMAs of this segment have completed: O is whole, and Q's
       // shared memory free for staging and for the next segment.
