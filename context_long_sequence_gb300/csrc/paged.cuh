@@ -94,6 +94,7 @@ struct PagedWalker {
   PagedEntry entry;            // the lane's
   long long head_units, upto;  // its units of one head; units of the window up to and including it
   const int32_t* table;        // page table of the last segment's entry
+  bool once;                   // no other token tile reads its keys
   int covered0, covered1;      // sequences of some prefix: [covered0, covered1)
 
   __device__ __forceinline__ explicit PagedWalker(const PagedAttnArgs& args)
@@ -212,6 +213,7 @@ struct PagedWalker {
       e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
       e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
       const bool prefix = id >= g.B;
+      once = e.n <= cut.tile_tokens;
       table = prefix ? g.prefix_table + static_cast<size_t>(id - g.B) * g.prefix_stride
                      : g.page_table + static_cast<size_t>(id) * g.table_stride;
       s.h = static_cast<int>(paged_div(rel, hu));
@@ -301,10 +303,25 @@ struct Weight<__half> {
   static constexpr float kBias = 9.f, kSlack = 2.f, kSpecSum = 60000.f, kSpecMax = 6.5f;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w) {
+// L2 policy of keys that are read once: first to go, so that a step's stream of
+// keys does not push out the queries, the parts and the kernels' own code.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t read_again_policy() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w,
+                                            uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, "
+      "%5, %6}], [%2], %7;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w),
+      "l"(policy)
       : "memory");
 }
 

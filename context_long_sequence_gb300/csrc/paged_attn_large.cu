@@ -210,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++nseg;
       if (seg.nt == 0) break;
+      const uint64_t policy = walk.once ? read_once_policy() : read_again_policy();
       auto page_of = [&](int tile) {
         const int key = tile * BN + box * box_rows;
         return mine && tile < seg.tile1 && key < seg.keys ? walk.table[key >> g.page_shift] : -2;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         const int key = tile * BN + box * box_rows;
-        if (load) tma_load_4d(dst0 + (kv ? slv : slk) * SM::kKV, map, tb, half * 64, key & page_mask, seg.h, page);
+        if (load) tma_load_4d(dst0 + (kv ? slv : slk) * SM::kKV, map, tb, half * 64, key & page_mask, seg.h, page, policy);
         page = ahead;
       }
     }

@@ -84,6 +84,7 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
   // ---- Fetching, S tiles ahead of the computing.  Lane: K or V, column half.
   const int f_kv = lane & 1, f_half = lane >> 1;
   const CUtensorMap* f_map = f_kv ? &tm_v : &tm_k;
+  const uint64_t policy = read_once_policy();
   const uint32_t f_dst = s0 + f_kv * SM::kKV + f_half * SM::kHalf;
   int f_seg = 0, f_n = 0;              // segments walked, tiles fetched
   int f_tile = 0, f_end = 0, f_h = 0;  // of the segment being fetched
@@ -118,7 +119,8 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
     }
     __syncwarp();
     if (there && lane < 2 * NH)
-      tma_load_4d(f_dst + st * 2 * SM::kKV, f_map, full0 + 8u * st, f_half * 64, (f_tile * 16) & ((1 << g.page_shift) - 1), f_h, page);
+      tma_load_4d(f_dst + st * 2 * SM::kKV, f_map, full0 + 8u * st, f_half * 64, (f_tile * 16) & ((1 << g.page_shift) - 1), f_h, page,
+                  policy);
     ++f_n;
     ++f_tile;
   };
