@@ -51,8 +51,13 @@ __device__ __forceinline__ int warp_prefix_of(const PagedGeom& g, int s) {
 }
 
 // Programmatic dependent launch: `launch_dependents` lets the next kernel of
-// the stream begin as SMs fall free; `wait` returns once every kernel before
-// this one has completed and its writes are visible.
+// the stream begin as SMs fall free; `wait` returns once the kernel before
+// this one has completed and its writes are visible.  Every kernel here is
+// launched so, and
+//   - touches no memory before its wait, except the merge, which reads the
+//     batch's arrays first: the attention kernel lets it begin only after its
+//     own wait, that is, when all that the arrays may come from is done;
+//   - waits in every block, so that whoever waits for it waits for all before.
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

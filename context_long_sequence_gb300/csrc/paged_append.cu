@@ -52,6 +52,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   constexpr int LPH = D / 16;       // lanes per head
   constexpr int HPG = 32 / LPH;     // heads per group
   const PagedGeom& g = args.g;
+  pdl_wait();
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const long long w = static_cast<long long>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
   const int t = static_cast<int>(w / units), unit = static_cast<int>(w % units);
@@ -133,8 +135,7 @@ int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const long long warps = static_cast<long long>(a.g.N) * units;
   const long long grid = (warps + kAppendWarps - 1) / kAppendWarps;
   if (grid > 0x7fffffffLL) return CP_ERR_UNSUPPORTED;
-  paged_append_kernel<T, D><<<static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream>>>(a, units);
-  return cudaGetLastError() == cudaSuccess ? CP_OK : CP_ERR_CUDA;
+  return launch(paged_append_kernel<T, D>, static_cast<unsigned>(grid), kAppendWarps * 32, 0, true, stream, a, units);
 }
 
 }  // namespace

@@ -34,17 +34,18 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
   using SM = SmallSmem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5;
-  pdl_launch_dependents();
-  if (smem_u32(smem) & 1023) {  // the swizzle is a function of the address
-    debug_bounds_fail(args.status, __LINE__, CP_TU_ID);
-    return;
-  }
   if ((threadIdx.x & 31) == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     small_init<D>(smem, warp);
   }
   __syncwarp();
+  pdl_wait();
+  pdl_launch_dependents();
+  if (smem_u32(smem) & 1023) {  // the swizzle is a function of the address
+    debug_bounds_fail(args.status, __LINE__, CP_TU_ID);
+    return;
+  }
   PagedWalker walk(args);
   const PagedCut cuts[1] = {paged_cut_small(args.g.G, 16 * NRB)};
   // Workers of different SMs first, so that a short batch has the whole card.
@@ -60,118 +61,145 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 //
 // O = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m) over a row's parts, its own
 // keys' first, then its prefix's, in key order; rows whose only part went
-// straight to the output are left alone.  What it reads is in L2 and small, so
-// its time is latency: a lane asks for eight parts at once, and with few rows
-// (SPLIT) the four warps of a block share the parts of one row.
+// straight to the output are left alone.  What it reads is small and in L2, so
+// its time is latency: eight loads of 16 bytes a lane are in flight.
+//   kMergeBlock  a block per (token, query head), its warps share the parts:
+//                few rows, many parts.
+//   kMergeHead   a warp per (token, query head), eight parts at a time.
+//   kMergeGroup  a warp per (token, KV head), four heads x two parts at a
+//                time: prompts, whose rows have one part (and are left) or two.
+enum MergeBy { kMergeBlock, kMergeHead, kMergeGroup };
 constexpr int kMergeWarps = 4;
-constexpr int kMergeAhead = 8;
-constexpr long long kMergeSplitRows = 2048;
+constexpr int kMergeBlocks = 152 * 12;  // at most; they loop
+constexpr long long kMergeBlockRows = 608, kMergeHeadRows = 16384;
 
-template <typename T, int D, bool SPLIT>
+template <typename T, int D, MergeBy BY>
 __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttnArgs args) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, HB = BY == kMergeGroup ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
+  constexpr int step = BY == kMergeBlock ? kMergeWarps : 1;               // between a warp's parts
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  __shared__ float joint[SPLIT ? kMergeWarps : 1][32][E + 2];
+  __shared__ float joint[BY == kMergeBlock ? kMergeWarps : 1][32][E + 2];
+  pdl_launch_dependents();
   const PagedGeom& g = args.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // SPLIT: a block per (token, query head); else a warp per (token, KV head).
-  const long long w = SPLIT ? static_cast<long long>(blockIdx.x) : static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
-  const int per_token = SPLIT ? g.Hq : g.Hkv;
-  const int t = static_cast<int>(w / per_token), x = static_cast<int>(w % per_token);
-  if (t >= g.N) return;
-  const int s = warp_count_le(g.q_start + 1, g.B, t);
-  if (s >= g.B) return;
-  const PagedEntry own = paged_entry(g, s);
-  if (own.bad || t < own.t0 || t >= own.t0 + own.n) return;
-  const int p = warp_prefix_of(g, s);
-  const bool covered = g.NP > 0 && s >= g.prefix_first[0] && s < g.prefix_first[g.NP];  // as PagedWalker has it
-  const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
-  const int hk = SPLIT ? x / g.G : x;
-  const PagedParts* parts = args.parts + static_cast<size_t>(t) * g.Hkv + hk;
-  PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
-  pdl_wait();
-  if (min(own.keys, own.limit0 + (t - own.t0)) > 0) a = *parts;
-  if (prefix) b = parts[static_cast<size_t>(args.max_tokens) * g.Hkv];
-  if (a.count == 1 && !covered) return;
-  const int n = a.count + b.count;
-  const int sub0 = SPLIT ? x - hk * g.G : 0, sub1 = SPLIT ? sub0 + 1 : g.G;
-  for (int sub = sub0; sub < sub1; ++sub) {
-    float m = -INFINITY, sum = 0.f, o[E];
+  const int per_token = BY == kMergeGroup ? g.Hkv : g.Hq;
+  const long long items = static_cast<long long>(g.N) * per_token;
+  const long long stride = static_cast<long long>(gridDim.x) * (BY == kMergeBlock ? 1 : kMergeWarps);
+  const int covered0 = g.NP > 0 ? g.prefix_first[0] : 0, covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;  // as PagedWalker has it
+  bool waited = false;
+  for (long long w = BY == kMergeBlock ? blockIdx.x : static_cast<long long>(blockIdx.x) * kMergeWarps + warp; w < items; w += stride) {
+    const int t = static_cast<int>(w / per_token), x = static_cast<int>(w - static_cast<long long>(t) * per_token);
+    const int s = warp_count_le(g.q_start + 1, g.B, t);
+    if (s >= g.B) break;  // this token and those after it belong to no sequence
+    const PagedEntry own = paged_entry(g, s);
+    if (own.bad || t < own.t0 || t >= own.t0 + own.n) continue;
+    const bool covered = s >= covered0 && s < covered1;
+    const int p = covered ? warp_prefix_of(g, s) : -1;
+    const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
+    const int hk = BY == kMergeGroup ? x : x / g.G;
+    const PagedParts* parts = args.parts + static_cast<size_t>(t) * g.Hkv + hk;
+    PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
+    if (!waited) pdl_wait();
+    waited = true;
+    if (min(own.keys, own.limit0 + (t - own.t0)) > 0) a = *parts;
+    if (prefix) b = parts[static_cast<size_t>(args.max_tokens) * g.Hkv];
+    if (a.count == 1 && !covered) continue;
+    const int n = a.count + b.count;
+    const int h0 = BY == kMergeGroup ? 0 : x - hk * g.G, h1 = BY == kMergeGroup ? g.G : h0 + 1;
+    for (int sub = h0; sub < h1; sub += HB) {
+      float m[HB], sum[HB], o[HB][E];
 #pragma unroll
-    for (int j = 0; j < E; ++j) o[j] = 0.f;
-    for (int i0 = SPLIT ? warp : 0; i0 < n; i0 += kMergeAhead * (SPLIT ? kMergeWarps : 1)) {
-      float lse[kMergeAhead];
-      Vec v[kMergeAhead];
+      for (int h = 0; h < HB; ++h) {
+        m[h] = -INFINITY;
+        sum[h] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k) {
-        const int i = i0 + k * (SPLIT ? kMergeWarps : 1);
-        const bool in_a = i < a.count;
-        const int at = in_a ? i : i - a.count;
-        const int first = in_a ? a.first : b.first, second = in_a ? a.second : b.second, stride = in_a ? a.stride : b.stride;
-        const long long row = (at == 0 ? first : second + (at - 1) * stride) + sub;
-        lse[k] = -INFINITY;
-        if (i < n) {
-          lse[k] = args.part_lse[row];
-          v[k] = *reinterpret_cast<const Vec*>(args.part_o + row * D + lane * E);
+        for (int j = 0; j < E; ++j) o[h][j] = 0.f;
+      }
+      for (int i0 = BY == kMergeBlock ? warp : 0; i0 < n; i0 += PB * step) {
+        float lse[PB][HB];
+        Vec v[PB][HB];
+#pragma unroll
+        for (int k = 0; k < PB; ++k) {
+          const int i = i0 + k * step;
+          const bool in_a = i < a.count;
+          const int at = in_a ? i : i - a.count;
+          const int first = in_a ? a.first : b.first, second = in_a ? a.second : b.second, next = in_a ? a.stride : b.stride;
+          const long long row = (at == 0 ? first : second + (at - 1) * next) + sub;
+#pragma unroll
+          for (int h = 0; h < HB; ++h) {
+            lse[k][h] = -INFINITY;
+            if (i < n && sub + h < h1) {
+              lse[k][h] = args.part_lse[row + h];
+              v[k][h] = *reinterpret_cast<const Vec*>(args.part_o + (row + h) * D + lane * E);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          float top = m[h];
+#pragma unroll
+          for (int k = 0; k < PB; ++k) top = fmaxf(top, lse[k][h]);
+          const float z = top == -INFINITY ? 0.f : top, f = ex2_approx(m[h] - z);
+          m[h] = top;
+          sum[h] *= f;
+#pragma unroll
+          for (int j = 0; j < E; ++j) o[h][j] *= f;
+#pragma unroll
+          for (int k = 0; k < PB; ++k) {
+            if (lse[k][h] == -INFINITY) continue;
+            const float wt = ex2_approx(lse[k][h] - z);
+            sum[h] += wt;
+            const float* y = reinterpret_cast<const float*>(&v[k][h]);
+#pragma unroll
+            for (int j = 0; j < E; ++j) o[h][j] = fmaf(wt, y[j], o[h][j]);
+          }
         }
       }
-      float top = m;
+      if constexpr (BY == kMergeBlock) {
+        __syncthreads();  // the last item's are read
 #pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k) top = fmaxf(top, lse[k]);
-      const float z = top == -INFINITY ? 0.f : top;
-      const float f = ex2_approx(m - z);
-      m = top;
-      sum *= f;
+        for (int j = 0; j < E; ++j) joint[warp][lane][j] = o[0][j];
+        joint[warp][lane][E] = m[0];
+        joint[warp][lane][E + 1] = sum[0];
+        __syncthreads();
+        if (warp > 0) continue;
+        float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < E; ++j) o[j] *= f;
+        for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, joint[k][lane][E]);
+        const float z = top == -INFINITY ? 0.f : top;
+        m[0] = top;
+        sum[0] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kMergeAhead; ++k) {
-        if (lse[k] == -INFINITY) continue;
-        const float wt = ex2_approx(lse[k] - z);
-        sum += wt;
-        const float* y = reinterpret_cast<const float*>(&v[k]);
+        for (int j = 0; j < E; ++j) o[0][j] = 0.f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = fmaf(wt, y[j], o[j]);
+        for (int k = 0; k < kMergeWarps; ++k) {
+          const float f = ex2_approx(joint[k][lane][E] - z);
+          sum[0] = fmaf(f, joint[k][lane][E + 1], sum[0]);
+#pragma unroll
+          for (int j = 0; j < E; ++j) o[0][j] = fmaf(f, joint[k][lane][j], o[0][j]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        if (sub + h >= h1) continue;
+        const float inv = sum[h] > 0.f ? 1.f / sum[h] : 0.f;
+        const int head = hk * g.G + sub + h;
+        const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
+        if (args.out_fp32) {
+          float* dst = static_cast<float*>(args.o) + at;
+#pragma unroll
+          for (int j = 0; j < E; ++j) dst[j] = o[h][j] * inv;
+        } else {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
+#pragma unroll
+          for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[h][2 * j] * inv, o[h][2 * j + 1] * inv);
+        }
+        if (lane == 0)
+          args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + log2f(sum[h])) * 0.69314718055994531f : -INFINITY;
       }
     }
-    if constexpr (SPLIT) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) joint[warp][lane][j] = o[j];
-      joint[warp][lane][E] = m;
-      joint[warp][lane][E + 1] = sum;
-      __syncthreads();
-      if (warp > 0) return;
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, joint[k][lane][E]);
-      const float z = top == -INFINITY ? 0.f : top;
-      m = top;
-      sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < E; ++j) o[j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < kMergeWarps; ++k) {
-        const float f = ex2_approx(joint[k][lane][E] - z);
-        sum = fmaf(f, joint[k][lane][E + 1], sum);
-#pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = fmaf(f, joint[k][lane][j], o[j]);
-      }
-    }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int h = hk * g.G + sub;
-    const long long at = (static_cast<long long>(t) * g.Hq + h) * D + lane * E;
-    if (args.out_fp32) {
-      float* dst = static_cast<float*>(args.o) + at;
-#pragma unroll
-      for (int j = 0; j < E; ++j) dst[j] = o[j] * inv;
-    } else {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
-#pragma unroll
-      for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[2 * j] * inv, o[2 * j + 1] * inv);
-    }
-    if (lane == 0)
-      args.lse[static_cast<long long>(h) * g.N + t] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : -INFINITY;
   }
+  if (!waited) pdl_wait();  // whoever waits for this kernel waits for those before it too
 }
 
 // ---------------------------------------------------------------- launch
@@ -185,7 +213,7 @@ int launch_small(const PagedAttnArgs& a, cudaStream_t stream) {
   CUtensorMap mk, mv;
   if (!make_cache_map(&mk, a.g, a.k_cache, 16) || !make_cache_map(&mv, a.g, a.v_cache, 16)) return CP_ERR_CUDA;
   const int ctas = sms < kSmallWorkers / kSmallWarps ? sms : kSmallWorkers / kSmallWarps;
-  return launch(paged_small_kernel<T, D, NRB>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, false, stream, mk, mv, a);
+  return launch(paged_small_kernel<T, D, NRB>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, true, stream, mk, mv, a);
 }
 
 template <typename T, int D>
@@ -202,10 +230,12 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
     rc = launch_paged_large(a, stream);
   if (rc != CP_OK) return rc;
   const long long rows = static_cast<long long>(g.N) * g.Hq;
-  if (rows <= kMergeSplitRows)
-    return launch(paged_merge_kernel<T, D, true>, static_cast<unsigned>(rows), kMergeWarps * 32, 0, true, stream, a);
-  const long long warps = static_cast<long long>(g.N) * g.Hkv;
-  return launch(paged_merge_kernel<T, D, false>, static_cast<unsigned>((warps + kMergeWarps - 1) / kMergeWarps),
+  const auto blocks = [](long long n) { return static_cast<unsigned>(n < kMergeBlocks ? n : kMergeBlocks); };
+  if (rows <= kMergeBlockRows)
+    return launch(paged_merge_kernel<T, D, kMergeBlock>, blocks(rows), kMergeWarps * 32, 0, true, stream, a);
+  if (rows <= kMergeHeadRows)
+    return launch(paged_merge_kernel<T, D, kMergeHead>, blocks((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
+  return launch(paged_merge_kernel<T, D, kMergeGroup>, blocks((static_cast<long long>(g.N) * g.Hkv + kMergeWarps - 1) / kMergeWarps),
                 kMergeWarps * 32, 0, true, stream, a);
 }
 

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::offMisc + 4);
   volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + SM::offMisc + 8);
+  pdl_wait();
   pdl_launch_dependents();
   if (s0 & 1023) {  // the swizzle is a function of the address
     debug_bounds_fail(status, __LINE__, CP_TU_ID);
@@ -609,7 +610,7 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
       !make_cache_map(&mk16, g, a.k_cache, 16) || !make_cache_map(&mv16, g, a.v_cache, 16))
     return CP_ERR_CUDA;
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, false, stream, mk, mv, mk16, mv16, a,
+  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, a,
                 box);
 }
 
