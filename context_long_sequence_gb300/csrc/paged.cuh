@@ -330,6 +330,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, int w,
+                                            int v, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%3, %4, "
+      "%5, %6, %7}], [%2], %8;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w),
+      "r"(v), "l"(policy)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- host side
 
 // 4-D map over the cache: columns, tokens of a page, heads, pages; boxes of
@@ -344,6 +353,24 @@ inline bool make_cache_map(CUtensorMap* m, const PagedGeom& g, const void* base,
   cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, g.dtype == CP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same with the 64-column pieces of a head as a dimension of their own: a
+// box is box_rows tokens of the whole head, piece by piece.
+inline bool make_cache_map_whole(CUtensorMap* m, const PagedGeom& g, const void* base, int box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t pieces = g.d / 64;
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(1) << g.page_shift, pieces, static_cast<cuuint64_t>(g.Hkv),
+                        static_cast<cuuint64_t>(g.num_pages)};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(g.token_stride) * 2, 128, static_cast<cuuint64_t>(g.head_stride) * 2,
+                           static_cast<cuuint64_t>(g.page_stride) * 2};
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), pieces, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, g.dtype == CP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

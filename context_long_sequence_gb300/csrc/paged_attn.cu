@@ -211,7 +211,7 @@ int launch_small(const PagedAttnArgs& a, cudaStream_t stream) {
   const int rc = prepare_kernel(known, paged_small_kernel<T, D, NRB>, SmallSmem<D>::kBytes, &sms);
   if (rc != CP_OK) return rc;
   CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, a.g, a.k_cache, 16) || !make_cache_map(&mv, a.g, a.v_cache, 16)) return CP_ERR_CUDA;
+  if (!make_cache_map_whole(&mk, a.g, a.k_cache, 16) || !make_cache_map_whole(&mv, a.g, a.v_cache, 16)) return CP_ERR_CUDA;
   const int ctas = sms < kSmallWorkers / kSmallWarps ? sms : kSmallWorkers / kSmallWarps;
   return launch(paged_small_kernel<T, D, NRB>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, true, stream, mk, mv, a);
 }

@@ -607,7 +607,7 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const int page = 1 << g.page_shift, box = page < BN ? page : BN;
   CUtensorMap mk, mv, mk16, mv16;
   if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box) ||
-      !make_cache_map(&mk16, g, a.k_cache, 16) || !make_cache_map(&mv16, g, a.v_cache, 16))
+      !make_cache_map_whole(&mk16, g, a.k_cache, 16) || !make_cache_map_whole(&mv16, g, a.v_cache, 16))
     return CP_ERR_CUDA;
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
   return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, a,

@@ -81,11 +81,8 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg) + warp * SM::kSegs;
   volatile int* held = reinterpret_cast<volatile int*>(smem + SM::offHeld) + warp * S;
 
-  // ---- Fetching, S tiles ahead of the computing.  Lane: K or V, column half.
-  const int f_kv = lane & 1, f_half = lane >> 1;
-  const CUtensorMap* f_map = f_kv ? &tm_v : &tm_k;
+  // ---- Fetching, S tiles ahead of the computing.
   const uint64_t policy = read_once_policy();
-  const uint32_t f_dst = s0 + f_kv * SM::kKV + f_half * SM::kHalf;
   int f_seg = 0, f_n = 0;              // segments walked, tiles fetched
   int f_tile = 0, f_end = 0, f_h = 0;  // of the segment being fetched
   int f_pages = -1, f_next = -1;       // lane: page of tile (f_tile & ~31) + lane, and of the 32 after
@@ -113,14 +110,16 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
     const int page = __shfl_sync(kAll, f_pages, f_tile & 31), st = f_n % S;
     const bool there = page >= 0 && page < g.num_pages;
     if (lane == 0) {
-      (void)CP_CHECK_DATA(there, status);
+      const uint32_t full = full0 + 8u * st, dst = s0 + st * 2 * SM::kKV;
+      const int row = (f_tile * 16) & ((1 << g.page_shift) - 1);
       held[st] = there;
-      mbar_arrive_expect_tx(full0 + 8u * st, there ? 2 * SM::kKV : 0);
+      mbar_arrive_expect_tx(full, there ? 2 * SM::kKV : 0);
+      if (CP_CHECK_DATA(there, status)) {
+        tma_load_5d(dst, &tm_k, full, 0, row, 0, f_h, page, policy);
+        tma_load_5d(dst + SM::kKV, &tm_v, full, 0, row, 0, f_h, page, policy);
+      }
     }
     __syncwarp();
-    if (there && lane < 2 * NH)
-      tma_load_4d(f_dst + st * 2 * SM::kKV, f_map, full0 + 8u * st, f_half * 64, (f_tile * 16) & ((1 << g.page_shift) - 1), f_h, page,
-                  policy);
     ++f_n;
     ++f_tile;
   };
