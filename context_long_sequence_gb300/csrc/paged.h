@@ -152,10 +152,10 @@ struct PagedShares {
 // 2w + 1); a part that is complete but has a partner (own keys and a prefix)
 // goes to a home row of its own.
 //
-// Small: a warp (paged_small.cuh), 16 keys a tile, up to 16 rows, or 32 where
-// the batch has nothing larger; at least kSmallMinUnits tiles each.  Large: a
+// Small: a warp (paged_small.cuh), 16 keys a tile, up to 8 or 16 rows, or 32
+// where the batch has nothing larger; at least kSmallMinUnits tiles each.  Large: a
 // CTA (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
-constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallRowsBeside = 16, kSmallKeyShift = 4;
+constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
 constexpr int kSmallMinUnits = 4;
 constexpr int kSmallLead = 2;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
@@ -165,8 +165,8 @@ constexpr int kMaxEntries = 8192;
 inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
   return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead};
 }
-inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kSmallRowsBeside + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
+inline __host__ __device__ PagedCut paged_cut_large(int G, int small_rows) {
+  return PagedCut{small_rows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
