@@ -27,7 +27,7 @@ namespace cpattn {
 namespace {
 
 // ---------------------------------------------------------------- few rows
-template <typename T, int D, int NT>
+template <typename T, int D, int ROWS>
 __global__ void __launch_bounds__(kSmallWarps * 32, 1)
     paged_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ PagedAttnArgs args) {
@@ -47,14 +47,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
     return;
   }
   PagedWalker walk(args);
-  const PagedCut cuts[1] = {paged_cut_small(args.g.G, 8 * NT)};
+  const PagedCut cuts[1] = {paged_cut_small(args.g.G, ROWS)};
   // Workers of different SMs first, so that a short batch has the whole card.
   const auto role = [&](const long long (&)[1]) {
     return PagedRole{0, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kSmallWarps * static_cast<int>(gridDim.x),
                      kSmallMinUnits, 0, kSmallRows};
   };
   if (walk.start(reinterpret_cast<long long*>(smem + SM::offSums), cuts, role))
-    small_worker<T, D, NT>(smem, warp, tm_k, tm_v, walk);
+    small_worker<SmallRows<T, D, ROWS>, D>(smem, warp, tm_k, tm_v, walk);
 }
 
 // ---------------------------------------------------------------- merge
@@ -204,16 +204,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
 
 // ---------------------------------------------------------------- launch
 
-template <typename T, int D, int NT>
+template <typename T, int D, int ROWS>
 int launch_small(const PagedAttnArgs& a, cudaStream_t stream) {
   static std::atomic<int> known[64];
   int sms = 0;
-  const int rc = prepare_kernel(known, paged_small_kernel<T, D, NT>, SmallSmem<D>::kBytes, &sms);
+  const int rc = prepare_kernel(known, paged_small_kernel<T, D, ROWS>, SmallSmem<D>::kBytes, &sms);
   if (rc != CP_OK) return rc;
   CUtensorMap mk, mv;
   if (!make_cache_map_whole(&mk, a.g, a.k_cache, 16) || !make_cache_map_whole(&mv, a.g, a.v_cache, 16)) return CP_ERR_CUDA;
   const int ctas = sms < kSmallWorkers / kSmallWarps ? sms : kSmallWorkers / kSmallWarps;
-  return launch(paged_small_kernel<T, D, NT>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, true, stream, mk, mv, a);
+  return launch(paged_small_kernel<T, D, ROWS>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, true, stream, mk, mv, a);
 }
 
 template <typename T, int D>
@@ -223,11 +223,11 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const long long most = static_cast<long long>(g.NP > 0 || g.N < g.max_new ? g.N : g.max_new) * g.G;
   int rc;
   if (most <= 8)
-    rc = launch_small<T, D, 1>(a, stream);
+    rc = launch_small<T, D, 8>(a, stream);
   else if (most <= 16)
-    rc = launch_small<T, D, 2>(a, stream);
+    rc = launch_small<T, D, 16>(a, stream);
   else if (most <= kSmallRows)
-    rc = launch_small<T, D, 4>(a, stream);
+    rc = launch_small<T, D, kSmallRows>(a, stream);
   else
     rc = launch_paged_large(a, stream);
   if (rc != CP_OK) return rc;

@@ -109,8 +109,8 @@ __device__ __forceinline__ int paged_large_ctas(long long small, long long large
   return n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
 }
 
-// NT: entries of up to 8 NT rows are the small workers'.
-template <typename T, int D, int NT>
+// BESIDE: entries of up to so many rows are the small workers'.
+template <typename T, int D, int BESIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_large_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
   PagedWalker walk(args);
-  const PagedCut cuts[2] = {paged_cut_small(g.G, 8 * NT), paged_cut_large(g.G, 8 * NT)};
+  const PagedCut cuts[2] = {paged_cut_small(g.G, BESIDE), paged_cut_large(g.G, BESIDE)};
   int large = 0;  // CTAs that take the entries of many rows
   const auto role = [&](const long long (&units)[2]) {
     const int ctas = gridDim.x, b = blockIdx.x;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         small_init<D>(smem, warp);
       }
       __syncwarp();
-      small_worker<T, D, NT>(smem, warp, tm_k16, tm_v16, walk);
+      small_worker<SmallRows<T, D, BESIDE>, D>(smem, warp, tm_k16, tm_v16, walk);
     }
     return;
   }
@@ -598,12 +598,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int BESIDE>
 int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const PagedGeom& g = a.g;
   static std::atomic<int> known[64];
   int sms = 0;
-  int rc = prepare_kernel(known, paged_large_kernel<T, D, NT>, kLaunchBytes<D>, &sms);
+  int rc = prepare_kernel(known, paged_large_kernel<T, D, BESIDE>, kLaunchBytes<D>, &sms);
   if (rc != CP_OK) return rc;
   const int page = 1 << g.page_shift, box = page < BN ? page : BN;
   CUtensorMap mk, mv, mk16, mv16;
@@ -611,14 +611,14 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
       !make_cache_map_whole(&mk16, g, a.k_cache, 16) || !make_cache_map_whole(&mv16, g, a.v_cache, 16))
     return CP_ERR_CUDA;
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D, NT>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, a,
+  return launch(paged_large_kernel<T, D, BESIDE>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, a,
                 box);
 }
 
-template <typename T, int NT>
+template <typename T, int BESIDE>
 int launch_large_t(const PagedAttnArgs& a, cudaStream_t stream) {
-  if (a.g.d == 128) return launch_large_d<T, 128, NT>(a, stream);
-  if (a.g.d == 64) return launch_large_d<T, 64, NT>(a, stream);
+  if (a.g.d == 128) return launch_large_d<T, 128, BESIDE>(a, stream);
+  if (a.g.d == 64) return launch_large_d<T, 64, BESIDE>(a, stream);
   return CP_ERR_UNSUPPORTED;
 }
 
@@ -628,8 +628,8 @@ int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream) {
   // Own keys of sequences with up to 8 rows at most (a decode step), or more.
   const long long own = static_cast<long long>(a.g.N < a.g.max_new ? a.g.N : a.g.max_new) * a.g.G;
   if (a.g.dtype == CP_DTYPE_BF16)
-    return own <= 8 ? launch_large_t<__nv_bfloat16, 1>(a, stream) : launch_large_t<__nv_bfloat16, 2>(a, stream);
-  return own <= 8 ? launch_large_t<__half, 1>(a, stream) : launch_large_t<__half, 2>(a, stream);
+    return own <= 8 ? launch_large_t<__nv_bfloat16, 8>(a, stream) : launch_large_t<__nv_bfloat16, 16>(a, stream);
+  return own <= 8 ? launch_large_t<__half, 8>(a, stream) : launch_large_t<__half, 16>(a, stream);
 }
 
 }  // namespace cpattn

@@ -9,6 +9,8 @@
 // each other's latencies; the many parts cost little to merge, a row of d
 // floats each for few rows.
 #pragma once
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace cpattn {
@@ -71,14 +73,312 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return r;
 }
 
+// Places of the lane's ldmatrix rows in a 16 x D tile, for 16-column steps
+// k = 0..3 (steps 4..7 lie kHalf further): `a` takes the 8 x 8 pieces in the
+// order of the MMA's A operand (rows first), `b` columns first.
+__device__ __forceinline__ uint32_t place_a(int k) {
+  const int lane = threadIdx.x & 31, row = (((lane >> 3) & 1) << 3) + (lane & 7);
+  return row * 128 + (((k * 2 + (lane >> 4)) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t place_b(int k) {
+  const int lane = threadIdx.x & 31, row = ((lane >> 4) << 3) + (lane & 7);
+  return row * 128 + (((k * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4);
+}
+
+// Raise a running maximum (log2 units) to t, the score's, if it exceeds it by
+// kSlack; the factor for what was summed under the old one.
+template <typename T>
+__device__ __forceinline__ float raise_max(float& m, float t) {
+  const float up = t > m + Weight<T>::kSlack ? t : m;
+  const float f = up > m ? ex2_approx(m - up) : 1.f;
+  m = up;
+  return f;
+}
+
+// One row's weight sum, maximum and place, for its log-sum-exp.
+template <typename T>
+__device__ __forceinline__ void store_lse(const PagedAttnArgs& a, const PagedSegment& seg, int token, int head, long long at,
+                                          float sum, float m) {
+  const float lse2 = sum > 0.f ? m + log2f(sum) - Weight<T>::kBias : -INFINITY;
+  if (seg.mode == kRowsFinal)
+    a.lse[static_cast<long long>(head) * a.g.N + token] = lse2 * 0.69314718055994531f;
+  else
+    a.part_lse[at] = lse2;
+}
+
+// Up to 8 rows, as the MMAs' columns: S^T = K Q^T and O^T = V^T P^T, with 16
+// keys (then 16 columns of V) as the rows.  A group of 4 or 8 query heads
+// fills half or all of the 8 columns; as the MMA's 16 rows it would take twice
+// the products, exponentials and accumulators.  (One SM reads 112 GB/s of
+// keys this way, 87 the other.)
+template <typename T, int D>
+struct SmallColumns {
+  static constexpr int kRows = 8;
+  int lim[2];  // keys seen by rows c2, c2 + 1
+  uint32_t q[D / 16][2];
+  float o[D / 16][4], m[2], l[2];
+  uint32_t at_k[4], at_v[4];
+
+  __device__ __forceinline__ SmallColumns(uint32_t k, uint32_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at_k[i] = k + place_a(i);
+      at_v[i] = v + place_b(i);
+    }
+  }
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const PagedSegment& seg) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c2 = 2 * (lane & 3), G = a.g.G, rows = seg.nt * G;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      lim[y] = c2 + y < rows ? min(seg.keys, seg.limit0 + (c2 + y) / G) : 0;
+      m[y] = -INFINITY;
+      l[y] = 0.f;
+    }
+    const int i = r / G;
+    const T* p = static_cast<const T*>(a.q) + (static_cast<long long>(seg.t0) + i) * a.q_stride + (seg.h * G + r - i * G) * D + c2;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      q[k][0] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
+      q[k][1] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
+    }
+  }
+
+  // 16 keys from key0 on; `clean`: fetched and seen by every row; keep[]: V's
+  // keys that hold something, for the lane's pairs.
+  __device__ __forceinline__ void tile(uint32_t stage, int key0, bool there, bool clean, const uint32_t (&keep)[2], float sl2) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    float c[2][4];  // two chains
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i >> 2][i & 3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t f[4];
+      ldmatrix4<false>(f, at_k[k & 3] + stage + (k >> 2) * SmallSmem<D>::kHalf);
+      mma16816<T>(c[k & 1], f, q[k][0], q[k][1]);
+    }
+    float x[4];  // keys lane / 4 (0, 1) and 8 further (2, 3) of rows c2, c2 + 1
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = c[0][i] + c[1][i];
+      if (!clean && (!there || key0 + (lane >> 2) + (i >> 1) * 8 >= lim[i & 1])) x[i] = -INFINITY;
+    }
+    float t[2] = {fmaxf(x[0], x[2]) * sl2, fmaxf(x[1], x[3]) * sl2};
+    if (!__all_sync(kAll, t[0] <= m[0] + Weight<T>::kSlack && t[1] <= m[1] + Weight<T>::kSlack)) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+#pragma unroll
+        for (int z = 4; z < 32; z <<= 1) t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], z));
+        const float f = raise_max<T>(m[y], t[y]);
+        l[y] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][y] *= f;
+          o[i][2 + y] *= f;
+        }
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = ex2_approx(fmaf(x[i], sl2, Weight<T>::kBias - (m[i & 1] == -INFINITY ? 0.f : m[i & 1])));
+    l[0] += p[0] + p[2];
+    l[1] += p[1] + p[3];
+    // The weights are rounded to the cache's type for the product with V;
+    // their sum is not.
+    const uint32_t b0 = movmatrix_trans(Elem<T>::pack(p[0], p[1])), b1 = movmatrix_trans(Elem<T>::pack(p[2], p[3]));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t f[4];
+      ldmatrix4<true>(f, at_v[i & 3] + stage + (i >> 2) * SmallSmem<D>::kHalf);
+      if (!clean) {
+        f[0] &= keep[0];
+        f[1] &= keep[0];
+        f[2] &= keep[1];
+        f[3] &= keep[1];
+      }
+      mma16816<T>(o[i], f, b0, b1);
+    }
+  }
+
+  __device__ __forceinline__ void finish(const PagedAttnArgs& a, const PagedSegment& seg) {
+    const int lane = threadIdx.x & 31, d0 = lane >> 2, G = a.g.G;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float sum = l[y];
+#pragma unroll
+      for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+      const int r = 2 * (lane & 3) + y, i = r / G;
+      if (r >= seg.nt * G) continue;
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const int token = seg.t0 + i, head = seg.h * G + r - i * G;
+      const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
+      // Column 8 j + d0.
+      if (seg.mode == kRowsFinal && !a.out_fp32) {
+        T* dst = static_cast<T*>(a.o) + row * D + d0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) dst[j * 8] = static_cast<T>(o[j >> 1][(j & 1) * 2 + y] * inv);
+      } else {
+        float* dst = (seg.mode == kRowsFinal ? static_cast<float*>(a.o) + row * D : a.part_o + at * D) + d0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) dst[j * 8] = o[j >> 1][(j & 1) * 2 + y] * inv;
+      }
+      if (d0 == 0) store_lse<T>(a, seg, token, head, at, sum, m[y]);
+    }
+  }
+};
+
+// Up to 16 NB rows, as the MMAs' rows: S = Q K^T, O = P V.
+template <typename T, int D, int NB>
+struct SmallBlocks {
+  static constexpr int kRows = 16 * NB;
+  int lim[NB][2];  // keys seen by rows lane / 4 and 8 further of a block
+  uint32_t q[NB][D / 16][4];
+  float o[NB][D / 8][4], m[NB][2], l[NB][2];
+  uint32_t at_k[4], at_v[4];
+
+  __device__ __forceinline__ SmallBlocks(uint32_t k, uint32_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at_k[i] = k + place_b(i);
+      at_v[i] = v + place_a(i);
+    }
+  }
+
+  __device__ __forceinline__ void begin(const PagedAttnArgs& a, const PagedSegment& seg) {
+    const int lane = threadIdx.x & 31, G = a.g.G, rows = seg.nt * G;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = b * 16 + y * 8 + (lane >> 2), i = r / G;
+        lim[b][y] = r < rows ? min(seg.keys, seg.limit0 + i) : 0;
+        m[b][y] = -INFINITY;
+        l[b][y] = 0.f;
+        const T* p = static_cast<const T*>(a.q) + (static_cast<long long>(seg.t0) + i) * a.q_stride +
+                     (seg.h * G + r - i * G) * D + 2 * (lane & 3);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          q[b][k][y] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
+          q[b][k][2 + y] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
+    }
+  }
+
+  __device__ __forceinline__ void tile(uint32_t stage, int key0, bool there, bool clean, const uint32_t (&keep)[2], float sl2) {
+    constexpr uint32_t kAll = 0xffffffffu;
+    constexpr int CH = NB == 1 ? 2 : 1;  // chains per 8 keys
+    const int c2 = 2 * (threadIdx.x & 3);
+    float c[NB][CH][2][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < CH * 8; ++i) c[b][i / 8][(i / 4) & 1][i & 3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t f[4];
+      ldmatrix4<false>(f, at_k[k & 3] + stage + (k >> 2) * SmallSmem<D>::kHalf);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        mma16816<T>(c[b][k % CH][0], q[b][k], f[0], f[1]);
+        mma16816<T>(c[b][k % CH][1], q[b][k], f[2], f[3]);
+      }
+    }
+    uint32_t pa[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float x[8];  // first row: 0, 1, 4, 5; second: 2, 3, 6, 7
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = c[b][0][i >> 2][i & 3] + (CH == 2 ? c[b][CH - 1][i >> 2][i & 3] : 0.f);
+        if (!clean && (!there || key0 + (i >> 2) * 8 + c2 + (i & 1) >= lim[b][(i >> 1) & 1])) x[i] = -INFINITY;
+      }
+      float t[2] = {fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])) * sl2, fmaxf(fmaxf(x[2], x[3]), fmaxf(x[6], x[7])) * sl2};
+      if (!__all_sync(kAll, t[0] <= m[b][0] + Weight<T>::kSlack && t[1] <= m[b][1] + Weight<T>::kSlack)) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], 1));
+          t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], 2));
+          const float f = raise_max<T>(m[b][y], t[y]);
+          l[b][y] *= f;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[b][i][2 * y] *= f;
+            o[b][i][2 * y + 1] *= f;
+          }
+        }
+      }
+      float p[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float top = m[b][(i >> 1) & 1];
+        p[i] = ex2_approx(fmaf(x[i], sl2, Weight<T>::kBias - (top == -INFINITY ? 0.f : top)));
+      }
+      l[b][0] += (p[0] + p[1]) + (p[4] + p[5]);
+      l[b][1] += (p[2] + p[3]) + (p[6] + p[7]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pa[b][i] = Elem<T>::pack(p[2 * i], p[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t f[4];
+      ldmatrix4<true>(f, at_v[i & 3] + stage + (i >> 2) * SmallSmem<D>::kHalf);
+      if (!clean) {
+        f[0] &= keep[0];
+        f[1] &= keep[1];
+        f[2] &= keep[0];
+        f[3] &= keep[1];
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        mma16816<T>(o[b][2 * i], pa[b], f[0], f[1]);
+        mma16816<T>(o[b][2 * i + 1], pa[b], f[2], f[3]);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void finish(const PagedAttnArgs& a, const PagedSegment& seg) {
+    const int lane = threadIdx.x & 31, G = a.g.G;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float sum = l[b][y];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = b * 16 + y * 8 + (lane >> 2), i = r / G;
+        if (r >= seg.nt * G) continue;
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const int token = seg.t0 + i, head = seg.h * G + r - i * G;
+        const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
+        if (seg.mode == kRowsFinal && !a.out_fp32) {
+          T* dst = static_cast<T*>(a.o) + row * D + 2 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<uint32_t*>(dst + j * 8) = Elem<T>::pack(o[b][j][2 * y] * inv, o[b][j][2 * y + 1] * inv);
+        } else {
+          float* dst = (seg.mode == kRowsFinal ? static_cast<float*>(a.o) + row * D : a.part_o + at * D) + 2 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j)
+            *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[b][j][2 * y] * inv, o[b][j][2 * y + 1] * inv);
+        }
+        if ((lane & 3) == 0) store_lse<T>(a, seg, token, head, at, sum, m[b][y]);
+      }
+  }
+};
+
+// The kind for entries of up to 8, 16 or 32 rows.
+template <typename T, int D, int ROWS>
+using SmallRows = typename std::conditional<ROWS == 8, SmallColumns<T, D>, SmallBlocks<T, D, ROWS <= 16 ? 1 : 2>>::type;
+
 // The share of the block's warp `warp`, whose walk has begun and whose
-// barriers are set.  Entries have up to 8 NT rows.
-//
-// The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with keys
-// (then columns of V) as the 16 rows of an MMA and 8 query rows as its
-// columns: a group of 4 or 8 query heads fills half or all of that, where as
-// the MMA's rows it would fill a quarter or half.
-template <typename T, int D, int NT>
+// barriers are set.
+template <typename Rows, int D>
 __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                              PagedWalker& walk) {
   using SM = SmallSmem<D>;
@@ -140,170 +440,35 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
 
   // ---- Computing.
   const float sl2 = g.scale * 1.4426950408889634f;
-  const int r8 = lane >> 2, c2 = 2 * (lane & 3);  // row and first column of the lane in an MMA fragment
-  // ldmatrix places of the lane, relative to a stage: K as [keys][columns] and
-  // V, transposed on the way, as [columns][keys]; 16-column steps k and k + 4
-  // lie kHalf apart.
-  uint32_t at_k[4], at_v[4];
-  {
-    const int row_k = (((lane >> 3) & 1) << 3) + (lane & 7), piece_k = lane >> 4;
-    const int row_v = ((lane >> 4) << 3) + (lane & 7), piece_v = (lane >> 3) & 1;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      at_k[k] = s0 + row_k * 128 + (((k * 2 + piece_k) ^ (row_k & 7)) << 4);
-      at_v[k] = s0 + SM::kKV + row_v * 128 + (((k * 2 + piece_v) ^ (row_v & 7)) << 4);
-    }
-  }
+  Rows rows(s0, s0 + SM::kKV);
   int n = 0;
   bool ok = true;
 #pragma unroll 1
   for (int c_seg = 0; ok; ++c_seg) {
     const PagedSegment seg = segs[c_seg % SM::kSegs];
     if (seg.nt == 0) break;
-    const int rows = seg.nt * g.G;
     const int lim_all = min(seg.keys, seg.limit0);  // seen by every row
-    int lim[NT][2];                                 // seen by rows c2, c2 + 1 of each eight
-    uint32_t q[NT][D / 16][2];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int r = b * 8 + c2 + y;
-        lim[b][y] = r < rows ? min(seg.keys, seg.limit0 + r / g.G) : 0;
-      }
-      const int r = b * 8 + r8, i = r / g.G;
-      const T* p = static_cast<const T*>(args.q) + (static_cast<long long>(seg.t0) + i) * args.q_stride + (seg.h * g.G + r - i * g.G) * D + c2;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) q[b][k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16 + x * 8) : 0u;
-    }
-    float o[NT][D / 16][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) {
-      m[b][0] = m[b][1] = -INFINITY;
-      l[b][0] = l[b][1] = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
-    }
+    rows.begin(args, seg);
 #pragma unroll 1
     for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
       const int st = n % S, key0 = tile * 16;
       ok = __all_sync(kAll, mbar_wait_short(full0 + 8u * st, (n / S) & 1, nullptr, status));
       if (!ok) break;
-      const bool there = held[st];
-      const bool clean = there && key0 + 16 <= lim_all;
-      const uint32_t stage = st * 2 * SM::kKV;
-      // S^T for 16 keys; few rows leave room for two chains.
-      constexpr int CH = NT <= 2 ? 2 : 1;
-      float c[NT][CH][4];
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int i = 0; i < CH * 4; ++i) c[b][i / 4][i & 3] = 0.f;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        uint32_t f[4];
-        ldmatrix4<false>(f, at_k[k & 3] + stage + (k >> 2) * SM::kHalf);
-#pragma unroll
-        for (int b = 0; b < NT; ++b) mma16816<T>(c[b][k % CH], f, q[b][k][0], q[b][k][1]);
-      }
-      uint32_t keep0 = kAll, keep1 = kAll;  // V rows that hold keys, for the lane's two pairs
+      const bool there = held[st], clean = there && key0 + 16 <= lim_all;
+      uint32_t keep[2] = {kAll, kAll};
       if (!clean) {
-        // What lies behind the last key may be anything, NaN included: 0 * NaN would reach O.
+        // What lies behind the last key may be anything, NaN included: 0 * NaN
+        // would reach O.  An MMA's lane holds V's keys c, c + 1 and 8 further.
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!there || key0 + (i >> 1) * 8 + c2 + (i & 1) >= seg.keys) (i & 2 ? keep1 : keep0) &= i & 1 ? 0x0000ffffu : 0xffff0000u;
+          if (!there || key0 + (i >> 1) * 8 + 2 * (lane & 3) + (i & 1) >= seg.keys) keep[i >> 1] &= i & 1 ? 0x0000ffffu : 0xffff0000u;
       }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int b = 0; b < NT; ++b) {
-        float x[4];  // keys r8 (0, 1) and r8 + 8 (2, 3) of rows c2, c2 + 1
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = CH == 2 ? c[b][0][i] + c[b][CH - 1][i] : c[b][0][i];
-        if (!clean) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!there || key0 + r8 + (i >> 1) * 8 >= lim[b][i & 1]) x[i] = -INFINITY;
-        }
-        const float mx0 = fmaxf(x[0], x[2]) * sl2, mx1 = fmaxf(x[1], x[3]) * sl2;
-        if (!__all_sync(kAll, mx0 <= m[b][0] + Weight<T>::kSlack && mx1 <= m[b][1] + Weight<T>::kSlack)) {
-          float t[2] = {mx0, mx1};
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-#pragma unroll
-            for (int z = 4; z < 32; z <<= 1) t[y] = fmaxf(t[y], __shfl_xor_sync(kAll, t[y], z));
-            const float up = t[y] > m[b][y] + Weight<T>::kSlack ? t[y] : m[b][y];
-            const float f = up > m[b][y] ? ex2_approx(m[b][y] - up) : 1.f;
-            m[b][y] = up;
-            l[b][y] *= f;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[b][i][y] *= f;
-              o[b][i][2 + y] *= f;
-            }
-          }
-        }
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[i] = ex2_approx(fmaf(x[i], sl2, Weight<T>::kBias - (m[b][i & 1] == -INFINITY ? 0.f : m[b][i & 1])));
-        l[b][0] += p[0] + p[2];
-        l[b][1] += p[1] + p[3];
-        // The weights are rounded to the cache's type for the product with V;
-        // their sum is not.
-        pb[b][0] = movmatrix_trans(Elem<T>::pack(p[0], p[1]));
-        pb[b][1] = movmatrix_trans(Elem<T>::pack(p[2], p[3]));
-      }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        uint32_t f[4];
-        ldmatrix4<true>(f, at_v[i & 3] + stage + (i >> 2) * SM::kHalf);
-        if (!clean) {
-          f[0] &= keep0;
-          f[1] &= keep0;
-          f[2] &= keep1;
-          f[3] &= keep1;
-        }
-#pragma unroll
-        for (int b = 0; b < NT; ++b) mma16816<T>(o[b][i], f, pb[b][0], pb[b][1]);
-      }
+      rows.tile(st * 2 * SM::kKV, key0, there, clean, keep, sl2);
       __syncwarp();  // the stage is read: the next tile may land on it
       fetch();
     }
     if (!ok) break;
-    const bool final_rows = seg.mode == kRowsFinal;
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float sum = l[b][y];
-#pragma unroll
-        for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(kAll, sum, z);
-        const int r = b * 8 + c2 + y, i = r / g.G;
-        if (r >= rows) continue;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const int token = seg.t0 + i, head = seg.h * g.G + r - i * g.G;
-        const long long row = static_cast<long long>(token) * g.Hq + head;
-        const long long at = seg.row + (seg.mode == kRowsHome ? row : r);
-        // Column 16 j + 8 half + r8.
-        if (final_rows && !args.out_fp32) {
-          T* dst = static_cast<T*>(args.o) + row * D + r8;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) dst[j * 8] = static_cast<T>(o[b][j >> 1][(j & 1) * 2 + y] * inv);
-        } else {
-          float* dst = (final_rows ? static_cast<float*>(args.o) + row * D : args.part_o + at * D) + r8;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) dst[j * 8] = o[b][j >> 1][(j & 1) * 2 + y] * inv;
-        }
-        if (r8 == 0) {
-          const float lse2 = sum > 0.f ? m[b][y] + log2f(sum) - Weight<T>::kBias : -INFINITY;
-          if (final_rows)
-            args.lse[static_cast<long long>(head) * g.N + token] = lse2 * 0.69314718055994531f;
-          else
-            args.part_lse[at] = lse2;
-        }
-      }
+    rows.finish(args, seg);
   }
   if (!ok)  // let every copy still in flight land
     for (; n < f_n; ++n) mbar_wait(full0 + 8u * (n % S), (n / S) & 1, nullptr, status);
