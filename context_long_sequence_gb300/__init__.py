@@ -162,6 +162,8 @@ def _L():
     lib.cp_paged_destroy.argtypes = [_vp]
     lib.cp_paged_destroy.restype = None
     lib.cp_paged_workspace_size.argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.cp_paged_shares.argtypes = [_vp, _vp, ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), ctypes.c_int64,
+                                    ctypes.POINTER(ctypes.c_int64)]
     lib.cp_cache_append.argtypes = [_vp, _vp, _vp] + [_vp, ctypes.c_int64] * 4 + [_vp]
     lib.cp_attn_paged.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     lib.cp_debug_build.argtypes = []
@@ -177,7 +179,7 @@ EXPORTED = ["cp_plan_create", "cp_plan_destroy", "cp_index_map", "cp_workspace_s
             "ulysses_reshard_batch",
             "cp_attn_fwd", "cp_attn_fwd_local", "cp_attn_fwd_rank", "cp_attn_fwd_noalloc", "cp_attn_bwd",
             "cp_attn_fwd_step", "cp_attn_bwd_delta", "cp_attn_bwd_step",
-            "cp_paged_create", "cp_paged_destroy", "cp_paged_workspace_size", "cp_cache_append", "cp_attn_paged",
+            "cp_paged_create", "cp_paged_destroy", "cp_paged_workspace_size", "cp_paged_shares", "cp_cache_append", "cp_attn_paged",
             "cp_merge_lse", "cp_get_status", "cp_get_status_detail", "cp_debug_build", "cp_strerror",
             "cp_selftest_wait_timeout", "cp_selftest_bounds", "cp_tile_classes", "cp_measure_rates", "cp_measure_barrier_check"]
 
@@ -588,6 +590,22 @@ def cp_attn_paged(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, o, l
     rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), wa, wn, st)
     if rc != CP_OK:
         _check(rc, where)
+
+
+def cp_paged_shares(plan: PagedPlan, batch: PagedBatch, ctas=152) -> np.ndarray:
+    """How cp_attn_paged shares out `batch` (whose tensors are on the CPU here):
+    int32 [n][14] rows {large, worker, entry, KV head, first token, tokens,
+    first key, end key, mode, row, parts, first part row, second part row, row
+    stride} (see include/cp_attn.h)."""
+    if batch.device.type != "cpu" or batch.max_pages != plan.max_pages \
+            or (batch.n_prefixes and batch.max_prefix_pages != plan.max_prefix_pages):
+        _refuse("cp_paged_shares", "a batch on the CPU with the plan's page tables is wanted")
+    n = ctypes.c_int64()
+    _check(_L().cp_paged_shares(plan._h, batch.ref, int(ctas), None, 0, ctypes.byref(n)), "cp_paged_shares")
+    out = np.zeros((max(n.value, 1), 14), dtype=np.int32)
+    _check(_L().cp_paged_shares(plan._h, batch.ref, int(ctas), out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+                                n.value, ctypes.byref(n)), "cp_paged_shares")
+    return out[:n.value]
 
 
 def alloc_paged_workspace(plan: PagedPlan, device="cuda"):

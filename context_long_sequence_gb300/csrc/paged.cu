@@ -179,6 +179,71 @@ int cp_paged_workspace_size(const cp_paged_t* p, size_t* bytes) {
   return CP_OK;
 }
 
+int cp_paged_shares(const cp_paged_t* p, const cp_paged_batch_t* batch, int32_t ctas, int32_t* rows, int64_t capacity,
+                    int64_t* n_rows) {
+  if (!p || !batch || !n_rows || ctas < 2 || ctas > cpattn::kLargeWorkers || capacity < 0 || (capacity > 0 && !rows))
+    return CP_ERR_INVALID_ARG;
+  const cp_paged_desc_t& d = p->desc;
+  const int rc = check_batch(d, *batch);
+  if (rc != CP_OK) return rc;
+  *n_rows = 0;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return CP_OK;
+  using namespace cpattn;
+  cp_paged_cache_t none = {};
+  const PagedGeom g = geom(*p, none, *batch);
+  const PagedWorkspace w = paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0);
+  const long long most = paged_most_rows(g);
+  const bool both = most > kSmallRows;
+  const PagedCut cuts[2] = {paged_cut_small(g.G, both ? paged_beside_rows(paged_most_own_rows(g)) : paged_small_rows(most)),
+                            paged_cut_large(g.G, paged_beside_rows(paged_most_own_rows(g)))};
+  long long units[2] = {0, 0};
+  for (int e = 0; e < g.B + g.NP; ++e)
+    for (int c = 0; c < (both ? 2 : 1); ++c) units[c] += paged_head_units(g, cuts[c], paged_entry(g, e)) * g.Hkv;
+  const int large = both ? paged_large_ctas(units[0], units[1], ctas) : 0;
+  for (int c = 0; c < 2; ++c) {
+    const PagedShares shares(units[c], c ? large : kSmallWarps * (ctas - large), c ? 1 : kSmallMinUnits);
+    PagedPlace at;
+    at.slots = c ? static_cast<int>(w.rows_small) : 0;
+    at.slot_rows = c ? kLargeRows : kSmallRows;
+    at.home = static_cast<int>(w.rows_large_end);
+    at.home_prefix = at.home + d.max_tokens * d.Hq;
+    at.covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
+    at.covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
+    at.B = g.B;
+    at.G = g.G;
+    at.Hq = g.Hq;
+    long long before = 0;  // units of the entries before
+    int e = 0;
+    for (at.worker = 0; at.worker < shares.workers; ++at.worker) {
+      long long u = shares.first(at.worker);
+      const long long end = shares.first(at.worker + 1);
+      while (u < end) {
+        const PagedEntry entry = paged_entry(g, e);
+        const long long hu = paged_head_units(g, cuts[c], entry);
+        if (u >= before + hu * g.Hkv) {
+          before += hu * g.Hkv;
+          ++e;
+          continue;
+        }
+        PagedSegment s;
+        PagedRecord rec;
+        u += paged_take(cuts[c], shares, at, e, entry, hu, u - before, u, end - u, s, rec);
+        if (s.nt == 0) continue;
+        if (*n_rows < capacity) {
+          int32_t* o = rows + *n_rows * 14;
+          const int key1 = s.tile1 << cuts[c].key_shift;
+          const int32_t v[14] = {c, at.worker, e, s.h, s.t0, s.nt, s.tile0 << cuts[c].key_shift, key1 < s.keys ? key1 : s.keys,
+                                 s.mode, s.row, rec.count, rec.count ? rec.first : 0, rec.count ? rec.second : 0,
+                                 rec.count ? rec.stride : 0};
+          for (int i = 0; i < 14; ++i) o[i] = v[i];
+        }
+        ++*n_rows;
+      }
+    }
+  }
+  return capacity > 0 && *n_rows > capacity ? CP_ERR_WORKSPACE : CP_OK;
+}
+
 int cp_cache_append(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_paged_batch_t* batch, const void* q,
                     int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* q_out,
                     int64_t q_out_stride, cudaStream_t stream) {

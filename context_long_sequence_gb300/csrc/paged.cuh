@@ -63,20 +63,6 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ long long shfl64(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
-// One run of key tiles of one token tile and KV head, as a worker gets it and
-// as the fetching warp hands it to the others through shared memory.
-struct PagedSegment {
-  int t0, nt;                 // the tile's tokens; nt == 0: no more segments
-  int h;                      // KV head
-  int keys, limit0;           // keys of the entry; token t0 + i sees min(keys, limit0 + i)
-  int tile0, tile1;           // key tiles of this run
-  // Where the rows go: straight to o and lse (final), or to part rows: row of
-  // (token, head) is row + token * Hq + head (home), row r of the token tile
-  // is row + r (slot).
-  int mode, row;
-};
-enum : int { kRowsFinal = 0, kRowsHome = 1, kRowsSlot = 2 };
-
 // Which share a warp takes up: cut number `cut`, as worker `worker` of at most
 // max_workers with at least min_units units each; its slots.
 struct PagedRole {
@@ -90,8 +76,8 @@ struct PagedWalker {
   const PagedAttnArgs& a;
   const PagedGeom& g;
   PagedCut cut;
-  int slots, slot_rows;        // the cut's first slot row, rows of a slot
-  int E, worker;
+  PagedPlace place;
+  int E;
   PagedShares shares;
   long long u, end;            // this worker's next unit and last + 1
   int base = -1;               // first entry of the window; -1: none is held
@@ -100,7 +86,6 @@ struct PagedWalker {
   long long head_units, upto;  // its units of one head; units of the window up to and including it
   const int32_t* table;        // page table of the last segment's entry
   bool once;                   // no other token tile reads its keys
-  int covered0, covered1;      // sequences of some prefix: [covered0, covered1)
 
   __device__ __forceinline__ explicit PagedWalker(const PagedAttnArgs& args)
       : a(args), g(args.g), E(args.g.B + args.g.NP), shares(0, 1, 1) {}
@@ -144,8 +129,8 @@ struct PagedWalker {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int windows = (E + 31) / 32;
     const bool alone = windows == 1;
-    covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
-    covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
+    place.covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
+    place.covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
     long long units[N];
     bool chosen = false, any = false;
     int w = alone ? 0 : warp;
@@ -173,15 +158,20 @@ struct PagedWalker {
       }
       const PagedRole r = choose(units);
       cut = cuts[r.cut];
-      slots = r.slots;
-      slot_rows = r.slot_rows;
-      worker = r.worker;
+      place.worker = r.worker;
+      place.slots = r.slots;
+      place.slot_rows = r.slot_rows;
+      place.home = static_cast<int>(a.rows_large_end);
+      place.home_prefix = place.home + a.max_tokens * g.Hq;
+      place.B = g.B;
+      place.G = g.G;
+      place.Hq = g.Hq;
       shares = PagedShares(units[r.cut], r.max_workers, r.min_units);
       before = 0;
-      any = worker < shares.workers;
+      any = r.worker < shares.workers;
       if (!any) break;
-      u = shares.first(worker);
-      end = shares.first(worker + 1);
+      u = shares.first(r.worker);
+      end = shares.first(r.worker + 1);
       if (alone) break;
 #pragma unroll 1
       for (w = 0; w + 1 < windows && before + sums[w * N + r.cut] <= u; ++w) before += sums[w * N + r.cut];
@@ -217,51 +207,18 @@ struct PagedWalker {
       e.n = __shfl_sync(0xffffffffu, entry.n, at);
       e.keys = __shfl_sync(0xffffffffu, entry.keys, at);
       e.limit0 = __shfl_sync(0xffffffffu, entry.limit0, at);
-      const bool prefix = id >= g.B;
       once = e.n <= cut.tile_tokens;
+      const bool prefix = id >= g.B;
       table = prefix ? g.prefix_table + static_cast<size_t>(id - g.B) * g.prefix_stride
                      : g.page_table + static_cast<size_t>(id) * g.table_stride;
-      s.h = static_cast<int>(paged_div(rel, hu));
-      rel -= s.h * hu;
-      int rb = 0, tiles = paged_tile_units(cut, e, 0);
-      while (rel >= tiles && (rb + 1) * cut.tile_tokens < e.n) {
-        rel -= tiles;
-        tiles = paged_tile_units(cut, e, ++rb);
-      }
-      s.t0 = e.t0 + rb * cut.tile_tokens;
-      s.nt = min(cut.tile_tokens, e.n - rb * cut.tile_tokens);
-      s.keys = e.keys;
-      s.limit0 = e.limit0 + rb * cut.tile_tokens;
-      const long long u0 = u - rel;  // the token tile's first unit
-      const int left = static_cast<int>(min(static_cast<long long>(tiles), rel + (end - u))) - cut.lead;
-      u += left + cut.lead - rel;
-      s.tile0 = max(0, static_cast<int>(rel) - cut.lead);
-      s.tile1 = left;
-      tiles -= cut.lead;
-      if (s.tile1 <= s.tile0) {  // only its lead falls to this worker
-        s.nt = 0;
-        continue;
-      }
-      const bool begins = s.tile0 == 0, whole = begins && s.tile1 == tiles;
-      const int home = static_cast<int>(a.rows_large_end) + (prefix ? a.max_tokens * g.Hq : 0);
-      if (whole) {
-        s.mode = prefix || (id >= covered0 && id < covered1) ? kRowsHome : kRowsFinal;
-        s.row = home;
-      } else {
-        s.mode = kRowsSlot;
-        s.row = slots + (2 * worker + (begins ? 1 : 0)) * slot_rows;
-      }
-      if (begins) {
-        const int last = whole ? worker : shares.worker_of(u0 + cut.lead + tiles - 1);
+      PagedRecord rec;
+      u += paged_take(cut, shares, place, id, e, hu, rel, u, end - u, s, rec);
+      if (s.nt == 0) continue;
+      if (rec.count > 0) {
         PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
-        for (int i = threadIdx.x & 31; i < s.nt; i += 32) {
-          PagedParts r;
-          r.first = s.mode == kRowsSlot ? s.row + i * g.G : s.row + (s.t0 + i) * g.Hq + s.h * g.G;
-          r.second = slots + 2 * (worker + 1) * slot_rows + i * g.G;
-          r.count = last - worker + 1;
-          r.stride = 2 * slot_rows;
-          parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] = r;
-        }
+        for (int i = threadIdx.x & 31; i < s.nt; i += 32)
+          parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] =
+              PagedParts{rec.first + i * rec.first_step, rec.second + i * g.G, rec.count, rec.stride};
       }
       break;
     }

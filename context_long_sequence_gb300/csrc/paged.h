@@ -155,11 +155,12 @@ struct PagedShares {
 // Small: a warp (paged_small.cuh), 16 keys a tile, up to 8 or 16 rows, or 32
 // where the batch has nothing larger; at least kSmallMinUnits tiles each.  Large: a
 // CTA (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
+constexpr int kSmallWarps = 8;  // workers of a CTA
 constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
-constexpr int kSmallMinUnits = 4;
-constexpr int kSmallLead = 2;
+constexpr int kSmallMinUnits = 3;
+constexpr int kSmallLead = 3;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
-constexpr int kLargeLead = 4;
+constexpr int kLargeLead = 6;
 constexpr int kMaxEntries = 8192;
 
 inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
@@ -174,6 +175,105 @@ struct PagedParts {
   int32_t first, second;  // rows of part 0 and part 1
   int32_t count, stride;  // parts, and rows from part 1 to part 2, ...
 };
+
+// CTAs for the entries of many rows, where a batch has both, by the time of
+// their units: one is 256 rows x 128 keys, some 2750 clocks on the tensor core
+// and the exponentials; one of few rows is 16 keys, about a twentieth of that
+// for a CTA's eight warps (112 GB/s).  (prefix_64x32k, prefix_256x16k in us at
+// weights 12: 66.8, 109.8; 16: 62.6, 105.4; 20: 60.7, 101.0; 24: 60.6, 105.5;
+// 28: 65.0, 109.5.)
+__host__ __device__ inline int paged_large_ctas(long long small, long long large, int ctas) {
+  if (large == 0) return 0;
+  if (small == 0) return ctas;
+  const long long all = 20 * large + small;
+  const int n = static_cast<int>(paged_div(20 * large * ctas + all / 2, all));
+  return n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
+}
+
+// The most rows that an entry of the batch may have, and those that an entry
+// of own keys may have.
+__host__ __device__ inline long long paged_most_own_rows(const PagedGeom& g) {
+  return static_cast<long long>(g.N < g.max_new ? g.N : g.max_new) * g.G;
+}
+__host__ __device__ inline long long paged_most_rows(const PagedGeom& g) {
+  return g.NP > 0 ? static_cast<long long>(g.N) * g.G : paged_most_own_rows(g);
+}
+// Rows up to which entries are the small workers', for a batch of at most
+// `most` rows an entry, and beside the large ones for at most `own` own rows.
+__host__ __device__ inline int paged_small_rows(long long most) { return most <= 8 ? 8 : most <= 16 ? 16 : kSmallRows; }
+__host__ __device__ inline int paged_beside_rows(long long own) { return own <= 8 ? 8 : 16; }
+
+// One run of key tiles of one token tile and KV head, as a worker gets it and
+// as the fetching warp hands it to the others through shared memory.
+struct PagedSegment {
+  int t0, nt;                 // the tile's tokens; nt == 0: no more segments
+  int h;                      // KV head
+  int keys, limit0;           // keys of the entry; token t0 + i sees min(keys, limit0 + i)
+  int tile0, tile1;           // key tiles of this run
+  // Where the rows go: straight to o and lse (final), or to part rows: row of
+  // (token, head) is row + token * Hq + head (home), row r of the token tile
+  // is row + r (slot).
+  int mode, row;
+};
+enum : int { kRowsFinal = 0, kRowsHome = 1, kRowsSlot = 2 };
+
+// Where the parts of token `i` of a segment's tile are, for the run that
+// begins the tile's keys: the token's G rows from first + i * first_step and
+// second + i * G on.
+struct PagedRecord {
+  int first, first_step, second, count, stride;
+};
+
+// What a worker takes of entry `id` from unit `rel` of the entry on, of the
+// `left` units that it still has: fills `s` (nt == 0: only a lead) and `rec`
+// (count == 0: the run does not begin its token tile), and returns the units
+// taken.
+struct PagedPlace {
+  int worker, slots, slot_rows;  // the cut's first slot row and rows of a slot
+  int home, home_prefix;         // first home row of own keys and of prefixes
+  int covered0, covered1;        // sequences that belong to some prefix
+  int B, G, Hq;
+};
+__host__ __device__ inline long long paged_take(const PagedCut& c, const PagedShares& shares, const PagedPlace& at, int id,
+                                                const PagedEntry& e, long long head_units, long long rel, long long u,
+                                                long long left, PagedSegment& s, PagedRecord& rec) {
+  s.h = static_cast<int>(paged_div(rel, head_units));
+  rel -= s.h * head_units;
+  int rb = 0, tiles = paged_tile_units(c, e, 0);
+  while (rel >= tiles && (rb + 1) * c.tile_tokens < e.n) {
+    rel -= tiles;
+    tiles = paged_tile_units(c, e, ++rb);
+  }
+  const long long u0 = u - rel;  // the token tile's first unit
+  const int stop = static_cast<int>(rel + left < tiles ? rel + left : tiles);
+  s.t0 = e.t0 + rb * c.tile_tokens;
+  s.nt = e.n - rb * c.tile_tokens < c.tile_tokens ? e.n - rb * c.tile_tokens : c.tile_tokens;
+  s.keys = e.keys;
+  s.limit0 = e.limit0 + rb * c.tile_tokens;
+  s.tile0 = rel > c.lead ? static_cast<int>(rel) - c.lead : 0;
+  s.tile1 = stop - c.lead;
+  rec.count = 0;
+  if (s.tile1 <= s.tile0) {  // only its lead falls to this worker
+    s.nt = 0;
+    return stop - rel;
+  }
+  const bool prefix = id >= at.B, begins = s.tile0 == 0, whole = begins && stop == tiles;
+  if (whole) {
+    s.mode = prefix || (id >= at.covered0 && id < at.covered1) ? kRowsHome : kRowsFinal;
+    s.row = prefix ? at.home_prefix : at.home;
+  } else {
+    s.mode = kRowsSlot;
+    s.row = at.slots + (2 * at.worker + (begins ? 1 : 0)) * at.slot_rows;
+  }
+  if (begins) {
+    rec.first = s.mode == kRowsSlot ? s.row : s.row + s.t0 * at.Hq + s.h * at.G;
+    rec.first_step = s.mode == kRowsSlot ? at.G : at.Hq;
+    rec.second = at.slots + 2 * (at.worker + 1) * at.slot_rows;
+    rec.count = (whole ? at.worker : shares.worker_of(u0 + tiles - 1)) - at.worker + 1;
+    rec.stride = 2 * at.slot_rows;
+  }
+  return stop - rel;
+}
 
 // The workspace: parts [2][N][Hkv] (own, prefix), then the rows' log-sum-exp
 // (log2 units) and their normalised fp32 O.

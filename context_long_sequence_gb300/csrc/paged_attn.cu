@@ -219,17 +219,16 @@ int launch_small(const PagedAttnArgs& a, cudaStream_t stream) {
 template <typename T, int D>
 int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const PagedGeom& g = a.g;
-  // The most rows that an entry may have.
-  const long long most = static_cast<long long>(g.NP > 0 || g.N < g.max_new ? g.N : g.max_new) * g.G;
+  const long long most = paged_most_rows(g);
   int rc;
-  if (most <= 8)
-    rc = launch_small<T, D, 8>(a, stream);
-  else if (most <= 16)
-    rc = launch_small<T, D, 16>(a, stream);
-  else if (most <= kSmallRows)
-    rc = launch_small<T, D, kSmallRows>(a, stream);
-  else
+  if (most > kSmallRows)
     rc = launch_paged_large(a, stream);
+  else if (paged_small_rows(most) == 8)
+    rc = launch_small<T, D, 8>(a, stream);
+  else if (paged_small_rows(most) == 16)
+    rc = launch_small<T, D, 16>(a, stream);
+  else
+    rc = launch_small<T, D, kSmallRows>(a, stream);
   if (rc != CP_OK) return rc;
   const long long rows = static_cast<long long>(g.N) * g.Hq;
   const auto blocks = [](long long n) { return static_cast<unsigned>(n < kMergeBlocks ? n : kMergeBlocks); };

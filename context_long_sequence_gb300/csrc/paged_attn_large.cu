@@ -98,17 +98,6 @@ constexpr uint32_t kLaunchBytes =
     LargeSmem<D>::kBytes > SmallSmem<D>::kBytes ? LargeSmem<D>::kBytes : static_cast<uint32_t>(SmallSmem<D>::kBytes);
 static_assert(kLaunchBytes<128> <= 227 * 1024, "one CTA an SM");
 
-// CTAs for the entries of many rows, by the time of their units: one is 256
-// rows x 128 keys, some 2750 clocks on the tensor core and the exponentials;
-// one of few rows is 16 keys, about a twelfth of that for a CTA's eight warps.
-__device__ __forceinline__ int paged_large_ctas(long long small, long long large, int ctas) {
-  if (large == 0) return 0;
-  if (small == 0) return ctas;
-  const long long all = 12 * large + small;
-  const int n = static_cast<int>(paged_div(12 * large * ctas + all / 2, all));
-  return n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
-}
-
 // BESIDE: entries of up to so many rows are the small workers'.
 template <typename T, int D, int BESIDE>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -625,11 +614,10 @@ int launch_large_t(const PagedAttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream) {
-  // Own keys of sequences with up to 8 rows at most (a decode step), or more.
-  const long long own = static_cast<long long>(a.g.N < a.g.max_new ? a.g.N : a.g.max_new) * a.g.G;
+  const bool few = paged_beside_rows(paged_most_own_rows(a.g)) == 8;
   if (a.g.dtype == CP_DTYPE_BF16)
-    return own <= 8 ? launch_large_t<__nv_bfloat16, 8>(a, stream) : launch_large_t<__nv_bfloat16, 16>(a, stream);
-  return own <= 8 ? launch_large_t<__half, 8>(a, stream) : launch_large_t<__half, 16>(a, stream);
+    return few ? launch_large_t<__nv_bfloat16, 8>(a, stream) : launch_large_t<__nv_bfloat16, 16>(a, stream);
+  return few ? launch_large_t<__half, 8>(a, stream) : launch_large_t<__half, 16>(a, stream);
 }
 
 }  // namespace cpattn

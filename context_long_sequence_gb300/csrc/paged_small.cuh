@@ -15,8 +15,6 @@
 
 namespace cpattn {
 
-constexpr int kSmallWarps = 8;  // workers of a CTA, one CTA an SM
-
 template <int D>
 struct SmallSmem {
   static constexpr int kHalf = 16 * 128;                 // 64 columns of a tile, 128 bytes a row

@@ -442,6 +442,21 @@ int cp_attn_paged(const cp_paged_t *plan, const cp_paged_cache_t *cache, const c
                   const void *q, int64_t q_stride, void *o, float *lse, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);
 
+/* Debug table of how cp_attn_paged shares a batch out (no counterpart in the
+ * pages), as the kernels compute it: one row of 14 int32 for each run of key
+ * tiles, {large, worker, entry, KV head, first token, tokens, first key, key
+ * behind the last, mode, row, parts, first part row, second part row, row
+ * stride}.  large: 0 a warp, 16 keys a tile; 1 a CTA, 128 keys a tile.  entry:
+ * the sequence, or n_seqs + the prefix.  mode: 0 the rows go to o and lse, 1
+ * to the workspace rows row + token * Hq + head, 2 to row + r (r: token of the
+ * run x query heads of the KV head).  parts, ...: the record of the first
+ * token, 0 for a run that does not begin its tokens' keys.  The batch's int32
+ * arrays are host arrays here; ctas: CTAs of the launch (152 on a GB300).
+ * Entries whose data leave their bounds have no rows.  host_rows may be null
+ * with capacity 0 to ask for the count.  Host only. */
+int cp_paged_shares(const cp_paged_t *plan, const cp_paged_batch_t *host_batch, int32_t ctas,
+                    int32_t *host_rows, int64_t capacity, int64_t *n_rows);
+
 /* Debug table of the forward's tile classes (no counterpart in the pages: it
  * exposes which work the kernel skips).  For every work item of the plan's
  * forward -- a block of up to 256 query slots of one attention rank inside
