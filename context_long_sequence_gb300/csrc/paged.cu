@@ -251,6 +251,7 @@ int cp_cache_append(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp
   const cp_paged_desc_t& d = p->desc;
   int rc = check_cache(d, *cache);
   if (rc == CP_OK) rc = check_batch(d, *batch);
+  if (rc == CP_OK && (batch->n_seqs == 0 || batch->n_tokens == 0)) return CP_OK;
   if (rc == CP_OK) rc = check_tokens(k, k_stride, d.Hkv, d.d);
   if (rc == CP_OK) rc = check_tokens(v, v_stride, d.Hkv, d.d);
   if (rc == CP_OK && q) rc = check_tokens(q, q_stride, d.Hq, d.d);
@@ -258,7 +259,6 @@ int cp_cache_append(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp
   if (rc == CP_OK && q && q == q_out && q_stride != q_out_stride) rc = CP_ERR_INVALID_ARG;
   if (rc == CP_OK) rc = check_arch();
   if (rc != CP_OK) return rc;
-  if (batch->n_seqs == 0 || batch->n_tokens == 0) return CP_OK;
   cpattn::AppendArgs a;
   a.g = geom(*p, *cache, *batch);
   a.q = q;
@@ -282,10 +282,12 @@ int cp_cache_append(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp
 
 int cp_attn_paged(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_paged_batch_t* batch, const void* q,
                   int64_t q_stride, void* o, float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-  if (!p || !cache || !batch || !o || !lse) return CP_ERR_INVALID_ARG;
+  if (!p || !cache || !batch) return CP_ERR_INVALID_ARG;
   const cp_paged_desc_t& d = p->desc;
   int rc = check_cache(d, *cache);
   if (rc == CP_OK) rc = check_batch(d, *batch);
+  if (rc == CP_OK && (batch->n_seqs == 0 || batch->n_tokens == 0)) return CP_OK;
+  if (rc == CP_OK && (!o || !lse)) rc = CP_ERR_INVALID_ARG;
   if (rc == CP_OK) rc = check_tokens(q, q_stride, d.Hq, d.d);
   if (rc == CP_OK && (!aligned(o, 16) || !aligned(lse, 16) || !aligned(workspace, 16))) rc = CP_ERR_ALIGNMENT;
   size_t need = 0;
@@ -293,7 +295,6 @@ int cp_attn_paged(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_p
   if (rc == CP_OK && (!workspace || workspace_bytes < need)) rc = CP_ERR_WORKSPACE;
   if (rc == CP_OK) rc = check_arch();
   if (rc != CP_OK) return rc;
-  if (batch->n_seqs == 0 || batch->n_tokens == 0) return CP_OK;
   cpattn::PagedAttnArgs a;
   a.g = geom(*p, *cache, *batch);
   a.q = q;

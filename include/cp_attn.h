@@ -347,7 +347,8 @@ int cp_merge_lse(int n_parts, int rows, int H, int d, const float *o_parts,
  * likewise (its sequences then attend to their own keys alone), and keys in a
  * page outside [0, num_pages) are neither read nor written and take no part
  * in the softmax; each is recorded as CP_ERR_DEVICE_BOUNDS (cp_get_status).
- * Rows behind q_start[n_seqs] (a padded batch) stay as they were.
+ * Rows behind q_start[n_seqs] (a padded batch) stay as they were; a batch
+ * without sequences or rows is no work, whatever the tensors.
  * These arrays need only 4-byte alignment. */
 #define CP_PAGED_VERSION 1
 #define CP_DTYPE_BF16 0
