@@ -66,29 +66,131 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 //   kMergeBlock  a block per (token, query head), its warps share the parts:
 //                few rows, many parts.
 //   kMergeHead   a warp per (token, query head), eight parts at a time.
-//   kMergeGroup  a warp per (token, KV head), four heads x two parts at a
-//                time: prompts, whose rows have one part (and are left) or two.
-enum MergeBy { kMergeBlock, kMergeHead, kMergeGroup };
+//   kMergeToken  a warp per token, four heads x two parts at a time: prompts,
+//                whose rows have one part (and are left) or two.
+enum MergeBy { kMergeBlock, kMergeHead, kMergeToken };
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBlocks = 152 * 12;  // at most; they loop
 constexpr long long kMergeBlockRows = 608, kMergeHeadRows = 16384;
 
+// Join the parts `a` (own keys) and `b` (prefix) of token t's query heads
+// h0 .. h1 - 1 of KV head hk.  `joint`: kMergeBlock's warps' sums.
 template <typename T, int D, MergeBy BY>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttnArgs args) {
-  constexpr int E = D / 32, HB = BY == kMergeGroup ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
+__device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const PagedParts& a, const PagedParts& b, int t, int hk,
+                                           int h0, int h1, float (*joint)[32][D / 32 + 2]) {
+  constexpr int E = D / 32, HB = BY == kMergeToken ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
   constexpr int step = BY == kMergeBlock ? kMergeWarps : 1;               // between a warp's parts
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  __shared__ float joint[BY == kMergeBlock ? kMergeWarps : 1][32][E + 2];
+  const PagedGeom& g = args.g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = a.count + b.count;
+  for (int sub = h0; sub < h1; sub += HB) {
+    float m[HB], sum[HB], o[HB][E];
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      m[h] = -INFINITY;
+      sum[h] = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[h][j] = 0.f;
+    }
+    for (int i0 = BY == kMergeBlock ? warp : 0; i0 < n; i0 += PB * step) {
+      float lse[PB][HB];
+      Vec v[PB][HB];
+#pragma unroll
+      for (int k = 0; k < PB; ++k) {
+        const int i = i0 + k * step;
+        const bool in_a = i < a.count;
+        const int at = in_a ? i : i - a.count;
+        const int first = in_a ? a.first : b.first, second = in_a ? a.second : b.second, next = in_a ? a.stride : b.stride;
+        const long long row = (at == 0 ? first : second + (at - 1) * next) + sub;
+#pragma unroll
+        for (int h = 0; h < HB; ++h) {
+          lse[k][h] = -INFINITY;
+          if (i < n && sub + h < h1) {
+            lse[k][h] = args.part_lse[row + h];
+            v[k][h] = *reinterpret_cast<const Vec*>(args.part_o + (row + h) * D + lane * E);
+          }
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < HB; ++h) {
+        float top = m[h];
+#pragma unroll
+        for (int k = 0; k < PB; ++k) top = fmaxf(top, lse[k][h]);
+        const float z = top == -INFINITY ? 0.f : top, f = ex2_approx(m[h] - z);
+        m[h] = top;
+        sum[h] *= f;
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[h][j] *= f;
+#pragma unroll
+        for (int k = 0; k < PB; ++k) {
+          if (lse[k][h] == -INFINITY) continue;
+          const float wt = ex2_approx(lse[k][h] - z);
+          sum[h] += wt;
+          const float* y = reinterpret_cast<const float*>(&v[k][h]);
+#pragma unroll
+          for (int j = 0; j < E; ++j) o[h][j] = fmaf(wt, y[j], o[h][j]);
+        }
+      }
+    }
+    if constexpr (BY == kMergeBlock) {
+      __syncthreads();  // the last item's are read
+#pragma unroll
+      for (int j = 0; j < E; ++j) joint[warp][lane][j] = o[0][j];
+      joint[warp][lane][E] = m[0];
+      joint[warp][lane][E + 1] = sum[0];
+      __syncthreads();
+      if (warp > 0) return;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, joint[k][lane][E]);
+      const float z = top == -INFINITY ? 0.f : top;
+      m[0] = top;
+      sum[0] = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) o[0][j] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMergeWarps; ++k) {
+        const float f = ex2_approx(joint[k][lane][E] - z);
+        sum[0] = fmaf(f, joint[k][lane][E + 1], sum[0]);
+#pragma unroll
+        for (int j = 0; j < E; ++j) o[0][j] = fmaf(f, joint[k][lane][j], o[0][j]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      if (sub + h >= h1) continue;
+      const float inv = sum[h] > 0.f ? 1.f / sum[h] : 0.f;
+      const int head = hk * g.G + sub + h;
+      const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
+      if (args.out_fp32) {
+        float* dst = static_cast<float*>(args.o) + at;
+#pragma unroll
+        for (int j = 0; j < E; ++j) dst[j] = o[h][j] * inv;
+      } else {
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[h][2 * j] * inv, o[h][2 * j + 1] * inv);
+      }
+      if (lane == 0)
+        args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + log2f(sum[h])) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+}
+
+template <typename T, int D, MergeBy BY>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __grid_constant__ PagedAttnArgs args) {
+  __shared__ float joint[BY == kMergeBlock ? kMergeWarps : 1][32][D / 32 + 2];
   pdl_launch_dependents();
   const PagedGeom& g = args.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_token = BY == kMergeGroup ? g.Hkv : g.Hq;
+  const int per_token = BY == kMergeToken ? 1 : g.Hq;
   const long long items = static_cast<long long>(g.N) * per_token;
   const long long stride = static_cast<long long>(gridDim.x) * (BY == kMergeBlock ? 1 : kMergeWarps);
   const int covered0 = g.NP > 0 ? g.prefix_first[0] : 0, covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;  // as PagedWalker has it
   bool waited = false;
   for (long long w = BY == kMergeBlock ? blockIdx.x : static_cast<long long>(blockIdx.x) * kMergeWarps + warp; w < items; w += stride) {
-    const int t = static_cast<int>(w / per_token), x = static_cast<int>(w - static_cast<long long>(t) * per_token);
+    const int t = static_cast<int>(w / per_token);
     const int s = warp_count_le(g.q_start + 1, g.B, t);
     if (s >= g.B) break;  // this token and those after it belong to no sequence
     const PagedEntry own = paged_entry(g, s);
@@ -96,106 +198,33 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     const bool covered = s >= covered0 && s < covered1;
     const int p = covered ? warp_prefix_of(g, s) : -1;
     const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
-    const int hk = BY == kMergeGroup ? x : x / g.G;
-    const PagedParts* parts = args.parts + static_cast<size_t>(t) * g.Hkv + hk;
-    PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
+    const bool sees_own = min(own.keys, own.limit0 + (t - own.t0)) > 0;
+    const PagedParts* own_parts = args.parts + static_cast<size_t>(t) * g.Hkv;
+    const PagedParts* prefix_parts = own_parts + static_cast<size_t>(args.max_tokens) * g.Hkv;
     if (!waited) pdl_wait();
     waited = true;
-    if (min(own.keys, own.limit0 + (t - own.t0)) > 0) a = *parts;
-    if (prefix) b = parts[static_cast<size_t>(args.max_tokens) * g.Hkv];
-    if (a.count == 1 && !covered) continue;
-    const int n = a.count + b.count;
-    const int h0 = BY == kMergeGroup ? 0 : x - hk * g.G, h1 = BY == kMergeGroup ? g.G : h0 + 1;
-    for (int sub = h0; sub < h1; sub += HB) {
-      float m[HB], sum[HB], o[HB][E];
-#pragma unroll
-      for (int h = 0; h < HB; ++h) {
-        m[h] = -INFINITY;
-        sum[h] = 0.f;
-#pragma unroll
-        for (int j = 0; j < E; ++j) o[h][j] = 0.f;
-      }
-      for (int i0 = BY == kMergeBlock ? warp : 0; i0 < n; i0 += PB * step) {
-        float lse[PB][HB];
-        Vec v[PB][HB];
-#pragma unroll
-        for (int k = 0; k < PB; ++k) {
-          const int i = i0 + k * step;
-          const bool in_a = i < a.count;
-          const int at = in_a ? i : i - a.count;
-          const int first = in_a ? a.first : b.first, second = in_a ? a.second : b.second, next = in_a ? a.stride : b.stride;
-          const long long row = (at == 0 ? first : second + (at - 1) * next) + sub;
-#pragma unroll
-          for (int h = 0; h < HB; ++h) {
-            lse[k][h] = -INFINITY;
-            if (i < n && sub + h < h1) {
-              lse[k][h] = args.part_lse[row + h];
-              v[k][h] = *reinterpret_cast<const Vec*>(args.part_o + (row + h) * D + lane * E);
-            }
-          }
+    if constexpr (BY != kMergeToken) {
+      const int head = static_cast<int>(w - static_cast<long long>(t) * per_token), hk = head / g.G, h = head - hk * g.G;
+      PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
+      if (sees_own) a = own_parts[hk];
+      if (prefix) b = prefix_parts[hk];
+      if (a.count != 1 || covered) join_parts<T, D, BY>(args, a, b, t, hk, h, h + 1, joint);
+    } else {
+      // A lane looks up one of 32 KV heads; the warp goes through those that
+      // have parts to join.
+      for (int h0 = 0; h0 < g.Hkv; h0 += 32) {
+        PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
+        const bool there = h0 + lane < g.Hkv;
+        if (there && sees_own) a = own_parts[h0 + lane];
+        if (there && prefix) b = prefix_parts[h0 + lane];
+        for (unsigned todo = __ballot_sync(0xffffffffu, there && (a.count != 1 || covered)); todo; todo &= todo - 1) {
+          const int from = __ffs(todo) - 1;
+          auto of = [&](const PagedParts& x) {
+            return PagedParts{__shfl_sync(0xffffffffu, x.first, from), __shfl_sync(0xffffffffu, x.second, from),
+                              __shfl_sync(0xffffffffu, x.count, from), __shfl_sync(0xffffffffu, x.stride, from)};
+          };
+          join_parts<T, D, BY>(args, of(a), of(b), t, h0 + from, 0, g.G, joint);
         }
-#pragma unroll
-        for (int h = 0; h < HB; ++h) {
-          float top = m[h];
-#pragma unroll
-          for (int k = 0; k < PB; ++k) top = fmaxf(top, lse[k][h]);
-          const float z = top == -INFINITY ? 0.f : top, f = ex2_approx(m[h] - z);
-          m[h] = top;
-          sum[h] *= f;
-#pragma unroll
-          for (int j = 0; j < E; ++j) o[h][j] *= f;
-#pragma unroll
-          for (int k = 0; k < PB; ++k) {
-            if (lse[k][h] == -INFINITY) continue;
-            const float wt = ex2_approx(lse[k][h] - z);
-            sum[h] += wt;
-            const float* y = reinterpret_cast<const float*>(&v[k][h]);
-#pragma unroll
-            for (int j = 0; j < E; ++j) o[h][j] = fmaf(wt, y[j], o[h][j]);
-          }
-        }
-      }
-      if constexpr (BY == kMergeBlock) {
-        __syncthreads();  // the last item's are read
-#pragma unroll
-        for (int j = 0; j < E; ++j) joint[warp][lane][j] = o[0][j];
-        joint[warp][lane][E] = m[0];
-        joint[warp][lane][E + 1] = sum[0];
-        __syncthreads();
-        if (warp > 0) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kMergeWarps; ++k) top = fmaxf(top, joint[k][lane][E]);
-        const float z = top == -INFINITY ? 0.f : top;
-        m[0] = top;
-        sum[0] = 0.f;
-#pragma unroll
-        for (int j = 0; j < E; ++j) o[0][j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMergeWarps; ++k) {
-          const float f = ex2_approx(joint[k][lane][E] - z);
-          sum[0] = fmaf(f, joint[k][lane][E + 1], sum[0]);
-#pragma unroll
-          for (int j = 0; j < E; ++j) o[0][j] = fmaf(f, joint[k][lane][j], o[0][j]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < HB; ++h) {
-        if (sub + h >= h1) continue;
-        const float inv = sum[h] > 0.f ? 1.f / sum[h] : 0.f;
-        const int head = hk * g.G + sub + h;
-        const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
-        if (args.out_fp32) {
-          float* dst = static_cast<float*>(args.o) + at;
-#pragma unroll
-          for (int j = 0; j < E; ++j) dst[j] = o[h][j] * inv;
-        } else {
-          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(args.o) + at);
-#pragma unroll
-          for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[h][2 * j] * inv, o[h][2 * j + 1] * inv);
-        }
-        if (lane == 0)
-          args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + log2f(sum[h])) * 0.69314718055994531f : -INFINITY;
       }
     }
   }
@@ -236,7 +265,7 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
     return launch(paged_merge_kernel<T, D, kMergeBlock>, blocks(rows), kMergeWarps * 32, 0, true, stream, a);
   if (rows <= kMergeHeadRows)
     return launch(paged_merge_kernel<T, D, kMergeHead>, blocks((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
-  return launch(paged_merge_kernel<T, D, kMergeGroup>, blocks((static_cast<long long>(g.N) * g.Hkv + kMergeWarps - 1) / kMergeWarps),
+  return launch(paged_merge_kernel<T, D, kMergeToken>, blocks((static_cast<long long>(g.N) + kMergeWarps - 1) / kMergeWarps),
                 kMergeWarps * 32, 0, true, stream, a);
 }
 
