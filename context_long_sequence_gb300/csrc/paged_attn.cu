@@ -66,19 +66,22 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 //   kMergeBlock  a block per (token, query head), its warps share the parts:
 //                few rows, many parts.
 //   kMergeHead   a warp per (token, query head), eight parts at a time.
+//   kMergeGroup  a warp per (token, KV head), four heads x two parts at a time:
+//                a batch whose rows would be several waves of warps.
 //   kMergeToken  a warp per token, four heads x two parts at a time: prompts,
 //                whose rows have one part (and are left) or two.
-enum MergeBy { kMergeBlock, kMergeHead, kMergeToken };
+enum MergeBy { kMergeBlock, kMergeHead, kMergeGroup, kMergeToken };
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBlocks = 152 * 12;  // at most; they loop
-constexpr long long kMergeBlockRows = 608, kMergeHeadRows = 16384;
+constexpr long long kMergeBlockRows = 608;                         // (token, query head)s up to which BY is kMergeBlock,
+constexpr long long kMergeHeadGroups = 1216, kMergeGroups = 8192;  // (token, KV head)s: kMergeHead, kMergeGroup
 
 // Join the parts `a` (own keys) and `b` (prefix) of token t's query heads
 // h0 .. h1 - 1 of KV head hk.  `joint`: kMergeBlock's warps' sums.
 template <typename T, int D, MergeBy BY>
 __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const PagedParts& a, const PagedParts& b, int t, int hk,
                                            int h0, int h1, float (*joint)[32][D / 32 + 2]) {
-  constexpr int E = D / 32, HB = BY == kMergeToken ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
+  constexpr int E = D / 32, HB = BY >= kMergeGroup ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
   constexpr int step = BY == kMergeBlock ? kMergeWarps : 1;               // between a warp's parts
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   const PagedGeom& g = args.g;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
   pdl_launch_dependents();
   const PagedGeom& g = args.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_token = BY == kMergeToken ? 1 : g.Hq;
+  const int per_token = BY == kMergeToken ? 1 : BY == kMergeGroup ? g.Hkv : g.Hq;
   const long long items = static_cast<long long>(g.N) * per_token;
   const long long stride = static_cast<long long>(gridDim.x) * (BY == kMergeBlock ? 1 : kMergeWarps);
   const int covered0 = g.NP > 0 ? g.prefix_first[0] : 0, covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;  // as PagedWalker has it
@@ -204,11 +207,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     if (!waited) pdl_wait();
     waited = true;
     if constexpr (BY != kMergeToken) {
-      const int head = static_cast<int>(w - static_cast<long long>(t) * per_token), hk = head / g.G, h = head - hk * g.G;
+      const int x = static_cast<int>(w - static_cast<long long>(t) * per_token);
+      const int hk = BY == kMergeGroup ? x : x / g.G, h = BY == kMergeGroup ? 0 : x - hk * g.G;
       PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
       if (sees_own) a = own_parts[hk];
       if (prefix) b = prefix_parts[hk];
-      if (a.count != 1 || covered) join_parts<T, D, BY>(args, a, b, t, hk, h, h + 1, joint);
+      if (a.count != 1 || covered) join_parts<T, D, BY>(args, a, b, t, hk, h, BY == kMergeGroup ? g.G : h + 1, joint);
     } else {
       // A lane looks up one of 32 KV heads; the warp goes through those that
       // have parts to join.
@@ -263,8 +267,11 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const auto blocks = [](long long n) { return static_cast<unsigned>(n < kMergeBlocks ? n : kMergeBlocks); };
   if (rows <= kMergeBlockRows)
     return launch(paged_merge_kernel<T, D, kMergeBlock>, blocks(rows), kMergeWarps * 32, 0, true, stream, a);
-  if (rows <= kMergeHeadRows)
+  const long long groups = static_cast<long long>(g.N) * g.Hkv;
+  if (groups <= kMergeHeadGroups)
     return launch(paged_merge_kernel<T, D, kMergeHead>, blocks((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
+  if (groups <= kMergeGroups)
+    return launch(paged_merge_kernel<T, D, kMergeGroup>, blocks((groups + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
   return launch(paged_merge_kernel<T, D, kMergeToken>, blocks((static_cast<long long>(g.N) + kMergeWarps - 1) / kMergeWarps),
                 kMergeWarps * 32, 0, true, stream, a);
 }
