@@ -163,7 +163,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
       if (sub + h >= h1) continue;
-      const float inv = sum[h] > 0.f ? 1.f / sum[h] : 0.f;
+      const float inv = sum[h] > 0.f ? __fdividef(1.f, sum[h]) : 0.f;
       const int head = hk * g.G + sub + h;
       const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
       if (args.out_fp32) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
         for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[h][2 * j] * inv, o[h][2 * j + 1] * inv);
       }
       if (lane == 0)
-        args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + log2f(sum[h])) * 0.69314718055994531f : -INFINITY;
+        args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + lg2_approx(sum[h])) * 0.69314718055994531f : -INFINITY;
     }
   }
 }

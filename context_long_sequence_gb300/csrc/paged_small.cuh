@@ -83,6 +83,14 @@ __device__ __forceinline__ uint32_t place_b(int k) {
   return row * 128 + (((k * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4);
 }
 
+// r / G for a row r < 256 of a token tile: with 65536 / G rounded up, the
+// product is too large by less than r / 65536 < 1 / G.
+struct RowsOf {
+  uint32_t inverse;
+  __device__ __forceinline__ explicit RowsOf(int G) : inverse((65535u + G) / G) {}
+  __device__ __forceinline__ int token(int r) const { return static_cast<int>((r * inverse) >> 16); }
+};
+
 // Raise a running maximum (log2 units) to t, the score's, if it exceeds it by
 // kSlack; the factor for what was summed under the old one.
 template <typename T>
@@ -97,7 +105,7 @@ __device__ __forceinline__ float raise_max(float& m, float t) {
 template <typename T>
 __device__ __forceinline__ void store_lse(const PagedAttnArgs& a, const PagedSegment& seg, int token, int head, long long at,
                                           float sum, float m) {
-  const float lse2 = sum > 0.f ? m + log2f(sum) - Weight<T>::kBias : -INFINITY;
+  const float lse2 = sum > 0.f ? m + lg2_approx(sum) - Weight<T>::kBias : -INFINITY;
   if (seg.mode == kRowsFinal)
     a.lse[static_cast<long long>(head) * a.g.N + token] = lse2 * 0.69314718055994531f;
   else
@@ -116,8 +124,9 @@ struct SmallColumns {
   uint32_t q[D / 16][2];
   float o[D / 16][4], m[2], l[2];
   uint32_t at_k[4], at_v[4];
+  const RowsOf of;
 
-  __device__ __forceinline__ SmallColumns(uint32_t k, uint32_t v) {
+  __device__ __forceinline__ SmallColumns(uint32_t k, uint32_t v, int G) : of(G) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       at_k[i] = k + place_a(i);
@@ -129,11 +138,11 @@ struct SmallColumns {
     const int lane = threadIdx.x & 31, r = lane >> 2, c2 = 2 * (lane & 3), G = a.g.G, rows = seg.nt * G;
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      lim[y] = c2 + y < rows ? min(seg.keys, seg.limit0 + (c2 + y) / G) : 0;
+      lim[y] = c2 + y < rows ? min(seg.keys, seg.limit0 + of.token(c2 + y)) : 0;
       m[y] = -INFINITY;
       l[y] = 0.f;
     }
-    const int i = r / G;
+    const int i = of.token(r);
     const T* p = static_cast<const T*>(a.q) + (static_cast<long long>(seg.t0) + i) * a.q_stride + (seg.h * G + r - i * G) * D + c2;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
@@ -208,9 +217,9 @@ struct SmallColumns {
       float sum = l[y];
 #pragma unroll
       for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
-      const int r = 2 * (lane & 3) + y, i = r / G;
+      const int r = 2 * (lane & 3) + y, i = of.token(r);
       if (r >= seg.nt * G) continue;
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
       const int token = seg.t0 + i, head = seg.h * G + r - i * G;
       const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
       // Column 8 j + d0.
@@ -236,8 +245,9 @@ struct SmallBlocks {
   uint32_t q[NB][D / 16][4];
   float o[NB][D / 8][4], m[NB][2], l[NB][2];
   uint32_t at_k[4], at_v[4];
+  const RowsOf of;
 
-  __device__ __forceinline__ SmallBlocks(uint32_t k, uint32_t v) {
+  __device__ __forceinline__ SmallBlocks(uint32_t k, uint32_t v, int G) : of(G) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       at_k[i] = k + place_b(i);
@@ -251,7 +261,7 @@ struct SmallBlocks {
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        const int r = b * 16 + y * 8 + (lane >> 2), i = r / G;
+        const int r = b * 16 + y * 8 + (lane >> 2), i = of.token(r);
         lim[b][y] = r < rows ? min(seg.keys, seg.limit0 + i) : 0;
         m[b][y] = -INFINITY;
         l[b][y] = 0.f;
@@ -349,9 +359,9 @@ struct SmallBlocks {
         float sum = l[b][y];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const int r = b * 16 + y * 8 + (lane >> 2), i = r / G;
+        const int r = b * 16 + y * 8 + (lane >> 2), i = of.token(r);
         if (r >= seg.nt * G) continue;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
         const int token = seg.t0 + i, head = seg.h * G + r - i * G;
         const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
         if (seg.mode == kRowsFinal && !a.out_fp32) {
@@ -438,7 +448,7 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
 
   // ---- Computing.
   const float sl2 = g.scale * 1.4426950408889634f;
-  Rows rows(s0, s0 + SM::kKV);
+  Rows rows(s0, s0 + SM::kKV, g.G);
   int n = 0;
   bool ok = true;
 #pragma unroll 1
