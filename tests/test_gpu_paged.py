@@ -83,6 +83,31 @@ def test_attention_matches_fp64(cpa, name):
     assert torch.isnan(o[n:]).all() and torch.isnan(lse[:, n:]).all()
 
 
+MORE = {
+    # The ways in which parts are joined, by the batch's size (a block, a head,
+    # a KV head or a token to a warp), beyond the small batches above.
+    "rows_1000": (dict(past=[300] * 64, new=[1] * 64, d=64, Hq=16, Hkv=2), {}),
+    "groups_2800": (dict(past=[0, 500], new=[300, 400], d=64, Hq=8, Hkv=4), {}),
+    "tokens_4200": (dict(past=[0] * 14, new=[300] * 14, d=64, Hq=4, Hkv=2), {}),
+    "forty_kv_heads": (dict(past=[0, 90], new=[150, 100], d=64, Hq=40, Hkv=40), {}),
+    "prefix_tokens": (dict(past=[0] * 6, new=[200] * 6, prefixes=[(4, 300)], first=1, d=64, Hq=8, Hkv=8), {}),
+}
+for page in (16, 32, 64, 128, 256):
+    for dtype, d in ((BF, 128), (FP, 64)):
+        MORE[f"few_page{page}_d{d}"] = (dict(past=[page - 1, 2 * page, 300 + page], new=[1, 2, 1], page_size=page, d=d, dtype=dtype,
+                                             Hq=8, Hkv=2, heads_first=page == 32), {})
+        MORE[f"many_page{page}_d{d}"] = (dict(past=[page - 1, 5, 300 + page], new=[40, 129, 70], page_size=page, d=d, dtype=dtype,
+                                              Hq=8, Hkv=2, heads_first=page == 64), {})
+
+
+@pytest.mark.parametrize("name", list(MORE))
+def test_attention_more_shapes(cpa, name):
+    kw, plan_kw = MORE[name]
+    b = Batch(seed=len(name), **kw)
+    o, lse = run_attention(cpa, b, **plan_kw)
+    check_attention(o, lse, b.attention(), b.dtype, b.d, b.N, name)
+
+
 APPEND = {
     "one_token": (dict(past=[100], new=[1], d=128, Hq=8, Hkv=2), dict(rope_dim=128)),
     "decode_ragged": (dict(past=[0, 15, 16, 31, 500], new=[1] * 5, d=64, Hq=4, Hkv=4), dict(rope_dim=64)),
