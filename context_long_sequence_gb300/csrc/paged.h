@@ -160,7 +160,7 @@ constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
 constexpr int kSmallMinUnits = 3;
 constexpr int kSmallLead = 3;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
-constexpr int kLargeLead = 6;
+constexpr int kLargeLead = 4;
 constexpr int kMaxEntries = 8192;
 
 inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
@@ -179,14 +179,14 @@ struct PagedParts {
 // CTAs for the entries of many rows, where a batch has both, by the time of
 // their units: one is 256 rows x 128 keys, some 2750 clocks on the tensor core
 // and the exponentials; one of few rows is 16 keys, about a twentieth of that
-// for a CTA's eight warps (112 GB/s).  (prefix_64x32k, prefix_256x16k in us at
-// weights 12: 66.8, 109.8; 16: 62.6, 105.4; 20: 60.7, 101.0; 24: 60.6, 105.5;
-// 28: 65.0, 109.5.)
+// for a CTA's eight warps (112 GB/s).  (64 sequences on a prefix of 32K keys,
+// and 256 on two of 16K and 9K, in us at weights 12: 66.8, 109.8; 16: 62.6,
+// 105.4; 20: 60.7, 101.0; 24: 60.6, 105.5; 28: 65.0, 109.5.)
 __host__ __device__ inline int paged_large_ctas(long long small, long long large, int ctas) {
   if (large == 0) return 0;
   if (small == 0) return ctas;
-  const long long all = 20 * large + small;
-  const int n = static_cast<int>(paged_div(20 * large * ctas + all / 2, all));
+  const long long all = 22 * large + small;
+  const int n = static_cast<int>(paged_div(22 * large * ctas + all / 2, all));
   return n < 1 ? 1 : n > ctas - 1 ? ctas - 1 : n;
 }
 

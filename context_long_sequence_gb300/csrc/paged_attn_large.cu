@@ -103,7 +103,8 @@ template <typename T, int D, int BESIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_large_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
-                       const __grid_constant__ PagedAttnArgs args, int box_rows) {
+                       const __grid_constant__ CUtensorMap tm_part, const __grid_constant__ CUtensorMap tm_o,
+                       const __grid_constant__ PagedAttnArgs args, int box_rows, int o_boxes) {
   using SM = LargeSmem<D>;
   constexpr int NH = D / 64;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -523,10 +524,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int row_bytes = D * (narrow ? 2 : 4);
       const int mine = min(32, n_rows - wq * 32);
+      // 32 rows that lie together (a slot's; or whole tokens' heads of o) go as
+      // TMA boxes, others as lines of 128 bytes by plain stores.
+      const bool boxes = mine == 32 && (seg.mode == kRowsSlot || (narrow && o_boxes));
 #pragma unroll 1
       for (int c = 0; c < lines; ++c) {
         const uint32_t stage = sW + (NH > 1 ? (c & 1) * HALF_BYTES : 0);
         const uint32_t my_stage = stage + lane * 128;
+        if (boxes && c >= NH) {  // the box before has left this place
+          if (lane == 0) bulk_wait_read<NH - 1>();
+          __syncwarp();
+        }
         uint32_t ov[32];
         auto fetch = [&](int col) {
           if (k > k0) {
@@ -553,6 +561,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int p = 0; p < 8; ++p)
             st_shared_v4(my_stage + ((p ^ (lane & 7)) << 4), ov[4 * p], ov[4 * p + 1], ov[4 * p + 2], ov[4 * p + 3]);
         }
+        if (boxes) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (seg.mode == kRowsSlot)
+              tma_store_2d(&tm_part, stage, c * 32, seg.row + first * g.G + wq * 32);
+            else
+              tma_store_3d(&tm_o, stage, c * 64, seg.h * g.G, seg.t0 + first + wq * 32 / g.G);
+            bulk_commit();
+          }
+          continue;
+        }
         __syncwarp();
         uint4 y[8];
 #pragma unroll
@@ -568,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (NH == 1) __syncwarp();  // one staging place; with two, the step between orders them
       }
+      if (boxes && lane == 0) bulk_wait_read<0>();
       if (row_valid) {
         const float lse2 = l > 0.f ? m + lg2_approx(l) - kBias : -INFINITY;
         if (final_rows)
@@ -578,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();      // the staging is read before the next segment's Q lands on it
       tc_fence_before();  // O was read before this warp's next arrival lets a PV overwrite it
     }
+    bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -585,6 +607,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Boxes of 32 rows x 128 bytes (swizzled) over the part rows, and over o as
+// [tokens][heads][columns].
+bool make_part_map(CUtensorMap* m, const void* base, int d, long long rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(d) * 4};
+  cuuint32_t box[2] = {32, 32}, estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool make_o_map(CUtensorMap* m, const PagedGeom& g, const void* base) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.d), static_cast<cuuint64_t>(g.Hq), static_cast<cuuint64_t>(g.N)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.d) * 2, static_cast<cuuint64_t>(g.d) * 2 * g.Hq};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(g.G), static_cast<cuuint32_t>(32 / g.G)}, estr[3] = {1, 1, 1};
+  return enc(m, g.dtype == CP_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, int D, int BESIDE>
@@ -599,9 +645,14 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_cache_map(&mk, g, a.k_cache, box) || !make_cache_map(&mv, g, a.v_cache, box) ||
       !make_cache_map_whole(&mk16, g, a.k_cache, 16) || !make_cache_map_whole(&mv16, g, a.v_cache, 16))
     return CP_ERR_CUDA;
+  // Boxes of 32 rows: of the slots, and of o where 32 rows are whole tokens.
+  const bool o_boxes = !a.out_fp32 && 32 % g.G == 0;
+  CUtensorMap mp, mo;
+  if (!make_part_map(&mp, a.part_o, g.d, a.rows_large_end) || (o_boxes && !make_o_map(&mo, g, a.o))) return CP_ERR_CUDA;
+  if (!o_boxes) mo = mp;  // not used
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D, BESIDE>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, a,
-                box);
+  return launch(paged_large_kernel<T, D, BESIDE>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, mp, mo,
+                a, box, o_boxes ? 1 : 0);
 }
 
 template <typename T, int BESIDE>

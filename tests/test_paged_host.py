@@ -224,7 +224,7 @@ def test_shares_cover_everything_once(cpa, seed):
     for large in (0, 1):
         w = t[t[:, 0] == large]
         if len(w):
-            size, lead = (128, 6) if large else (16, 3)
+            size, lead = (128, 4) if large else (16, 3)
             cost = {}
             for r in w.tolist():
                 cost[r[1]] = cost.get(r[1], 0) + -(-(r[7] - r[6]) // size)
