@@ -163,8 +163,9 @@ int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
   p->scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.d));
   for (int j = 0; j < d.rope_dim / 2; ++j) {
     const double f = d.rope_freqs ? d.rope_freqs[j] : std::pow(d.rope_base, -2.0 * j / d.rope_dim);
-    const double x = f / 6.283185307179586476925;
-    p->turns[j] = static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64));
+    const double x = std::fabs(f) / 6.283185307179586476925;  // below 2^64 once its whole turns are off
+    const uint64_t turns = static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64));
+    p->turns[j] = f < 0 ? 0 - turns : turns;
   }
   *out = p;
   return CP_OK;
@@ -311,6 +312,7 @@ int cp_attn_paged(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp_p
   a.part_o = reinterpret_cast<float*>(ws + w.o);
   a.rows_small = w.rows_small;
   a.rows_large_end = w.rows_large_end;
+  a.rows = static_cast<uint32_t>(w.rows);
   a.max_tokens = d.max_tokens;
   a.status = cpattn::device_status_ptr();
   if (!a.status) return CP_ERR_CUDA;

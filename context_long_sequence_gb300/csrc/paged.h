@@ -171,10 +171,20 @@ inline __host__ __device__ PagedCut paged_cut_large(int G, int small_rows) {
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
-struct PagedParts {
+struct alignas(16) PagedParts {
   int32_t first, second;  // rows of part 0 and part 1
   int32_t count, stride;  // parts, and rows from part 1 to part 2, ...
 };
+// Whether the parts of G rows each lie among `rows` rows.  Where the batch's
+// arrays are not ascending, entries overlap, and a row's record may be
+// another entry's or none of this call's.
+__host__ __device__ inline bool paged_parts_in(const PagedParts& p, int G, uint32_t rows) {
+  if (p.count == 0) return true;
+  const uint32_t count = static_cast<uint32_t>(p.count), first = static_cast<uint32_t>(p.first);
+  const uint32_t second = static_cast<uint32_t>(p.second), stride = static_cast<uint32_t>(p.stride), last = rows - G;
+  if (count > kSmallWorkers || first > last) return false;
+  return count == 1 || (second <= last && stride <= 2 * kLargeRows && second + (count - 2) * stride <= last);
+}
 
 // CTAs for the entries of many rows, where a batch has both, by the time of
 // their units: one is 256 rows x 128 keys, some 2750 clocks on the tensor core
@@ -323,6 +333,7 @@ struct PagedAttnArgs {
   float* part_lse;
   float* part_o;
   long long rows_small, rows_large_end;
+  uint32_t rows;           // all of them
   int max_tokens;          // of the plan: home rows of prefixes follow max_tokens * Hq of the own keys
   int32_t* status;
 };

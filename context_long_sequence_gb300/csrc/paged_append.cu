@@ -73,15 +73,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   const int ea = halves ? 8 * j : 16 * j;                       // first elements of the lane's two pieces
   const int eb = halves ? args.rope_dim / 2 + 8 * j : 16 * j + 8;
   float c[8], sn[8];
+  int pos = at;
+  if (g.positions) {
+    pos = g.positions[t];
+  } else if (args.rope_dim > 0) {
+    const int p = warp_prefix_of(g, s);  // by the whole warp, the lanes behind rope_dim too
+    if (p >= 0) pos += g.prefix_len[p];
+  }
   if (rotated) {
-    int pos;
-    if (g.positions) {
-      pos = g.positions[t];
-    } else {
-      pos = at;
-      const int p = warp_prefix_of(g, s);
-      if (p >= 0) pos += g.prefix_len[p];
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * args.turns[8 * j + i];

@@ -163,7 +163,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
 #pragma unroll
     for (int h = 0; h < HB; ++h) {
       if (sub + h >= h1) continue;
-      const float inv = sum[h] > 0.f ? __fdividef(1.f, sum[h]) : 0.f;
+      const float inv = sum[h] != 0.f ? __fdividef(1.f, sum[h]) : 0.f;
       const int head = hk * g.G + sub + h;
       const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
       if (args.out_fp32) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
         for (int j = 0; j < E / 2; ++j) dst[j] = Elem<T>::pack(o[h][2 * j] * inv, o[h][2 * j + 1] * inv);
       }
       if (lane == 0)
-        args.lse[static_cast<long long>(head) * g.N + t] = sum[h] > 0.f ? (m[h] + lg2_approx(sum[h])) * 0.69314718055994531f : -INFINITY;
+        args.lse[static_cast<long long>(head) * g.N + t] = sum[h] != 0.f ? (m[h] + lg2_approx(sum[h])) * 0.69314718055994531f : -INFINITY;
     }
   }
 }
@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
     if (own.bad || t < own.t0 || t >= own.t0 + own.n) continue;
     const bool covered = s >= covered0 && s < covered1;
     const int p = covered ? warp_prefix_of(g, s) : -1;
-    const bool prefix = p >= 0 && paged_entry(g, g.B + p).keys > 0;
+    const PagedEntry pre = p >= 0 ? paged_entry(g, g.B + p) : PagedEntry{0, 0, 0, 0, nullptr, false};
+    const bool prefix = pre.keys > 0 && t >= pre.t0 && t < pre.t0 + pre.n;
     const bool sees_own = min(own.keys, own.limit0 + (t - own.t0)) > 0;
     const PagedParts* own_parts = args.parts + static_cast<size_t>(t) * g.Hkv;
     const PagedParts* prefix_parts = own_parts + static_cast<size_t>(args.max_tokens) * g.Hkv;
@@ -212,7 +213,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
       PagedParts a{0, 0, 0, 0}, b{0, 0, 0, 0};
       if (sees_own) a = own_parts[hk];
       if (prefix) b = prefix_parts[hk];
-      if (a.count != 1 || covered) join_parts<T, D, BY>(args, a, b, t, hk, h, BY == kMergeGroup ? g.G : h + 1, joint);
+      if ((a.count != 1 || covered) &&
+          CP_CHECK_DATA(paged_parts_in(a, g.G, args.rows) && paged_parts_in(b, g.G, args.rows), args.status))
+        join_parts<T, D, BY>(args, a, b, t, hk, h, BY == kMergeGroup ? g.G : h + 1, joint);
     } else {
       // A lane looks up one of 32 KV heads; the warp goes through those that
       // have parts to join.
@@ -221,7 +224,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const __g
         const bool there = h0 + lane < g.Hkv;
         if (there && sees_own) a = own_parts[h0 + lane];
         if (there && prefix) b = prefix_parts[h0 + lane];
-        for (unsigned todo = __ballot_sync(0xffffffffu, there && (a.count != 1 || covered)); todo; todo &= todo - 1) {
+        const bool joins = there && (a.count != 1 || covered) &&
+                           CP_CHECK_DATA(paged_parts_in(a, g.G, args.rows) && paged_parts_in(b, g.G, args.rows), args.status);
+        for (unsigned todo = __ballot_sync(0xffffffffu, joins); todo; todo &= todo - 1) {
           const int from = __ffs(todo) - 1;
           auto of = [&](const PagedParts& x) {
             return PagedParts{__shfl_sync(0xffffffffu, x.first, from), __shfl_sync(0xffffffffu, x.second, from),

@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!busy) continue;
       tc_fence_after();
       const bool final_rows = seg.mode == kRowsFinal;
-      const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+      const float inv = l != 0.f ? __fdividef(1.f, l) : 0.f;
       // A thread holds a row, but rows leave as whole lines: 128 bytes of 32
       // rows at a time pass through shared memory (16-byte pieces, swizzled).
       const bool narrow = final_rows && !args.out_fp32;  // 64 columns are 128 bytes, else 32
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (boxes && lane == 0) bulk_wait_read<0>();
       if (row_valid) {
-        const float lse2 = l > 0.f ? m + lg2_approx(l) - kBias : -INFINITY;
+        const float lse2 = l != 0.f ? m + lg2_approx(l) - kBias : -INFINITY;
         if (final_rows)
           args.lse[static_cast<long long>(seg.h * g.G + sub) * g.N + seg.t0 + first + tok] = lse2 * 0.69314718055994531f;
         else

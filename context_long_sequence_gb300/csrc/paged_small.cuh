@@ -101,11 +101,12 @@ __device__ __forceinline__ float raise_max(float& m, float t) {
   return f;
 }
 
-// One row's weight sum, maximum and place, for its log-sum-exp.
+// One row's weight sum, maximum and place, for its log-sum-exp.  A NaN among
+// the scores is one in the sum (the maximum passes over it) and in the result.
 template <typename T>
 __device__ __forceinline__ void store_lse(const PagedAttnArgs& a, const PagedSegment& seg, int token, int head, long long at,
                                           float sum, float m) {
-  const float lse2 = sum > 0.f ? m + lg2_approx(sum) - Weight<T>::kBias : -INFINITY;
+  const float lse2 = sum != 0.f ? m + lg2_approx(sum) - Weight<T>::kBias : -INFINITY;
   if (seg.mode == kRowsFinal)
     a.lse[static_cast<long long>(head) * a.g.N + token] = lse2 * 0.69314718055994531f;
   else
@@ -219,7 +220,7 @@ struct SmallColumns {
       for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
       const int r = 2 * (lane & 3) + y, i = of.token(r);
       if (r >= seg.nt * G) continue;
-      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+      const float inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
       const int token = seg.t0 + i, head = seg.h * G + r - i * G;
       const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
       // Column 8 j + d0.
@@ -361,7 +362,7 @@ struct SmallBlocks {
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = b * 16 + y * 8 + (lane >> 2), i = of.token(r);
         if (r >= seg.nt * G) continue;
-        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+        const float inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
         const int token = seg.t0 + i, head = seg.h * G + r - i * G;
         const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
         if (seg.mode == kRowsFinal && !a.out_fp32) {

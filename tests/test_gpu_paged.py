@@ -117,6 +117,8 @@ APPEND = {
     "no_rotation": (dict(past=[3, 60], new=[4, 2], d=64, Hq=4, Hkv=2), dict(rope_dim=0)),
     "with_prefix": (dict(past=[2, 0, 9, 4], new=[1, 2, 1, 1], prefixes=[(2, 77), (1, 500)], d=64, Hq=4, Hkv=2), dict(rope_dim=64)),
     "padded_and_empty": (dict(past=[2, 0, 9], new=[1, 0, 3], pad=5, d=64, Hq=4, Hkv=2), dict(rope_dim=64)),
+    "partial_with_prefix": (dict(past=[2, 0, 9, 4], new=[1, 2, 1, 1], prefixes=[(2, 77), (1, 500)], d=128, Hq=4, Hkv=2), dict(rope_dim=32)),
+    "no_rotation_with_prefix": (dict(past=[2, 0], new=[1, 2], prefixes=[(2, 77)], d=64, Hq=4, Hkv=2), dict(rope_dim=0)),
 }
 
 
@@ -174,6 +176,14 @@ def test_append_far_positions(cpa, far):
     freqs = np.linspace(1.0, 1e-6, 64)
     q_out, cache = run_append(cpa, b, positions=positions, rope_dim=128, rope_freqs=list(freqs))
     check_append(b, q_out, cache, 128, False, freqs, positions)
+
+
+def test_append_backward_frequencies(cpa):
+    """Negative numbers turn the other way; -1e-20 is no turn at all."""
+    b = Batch(past=[5, 100], new=[30, 2], d=128, Hq=4, Hkv=2, dtype=FP, seed=5, appended=False)
+    freqs = np.concatenate([np.linspace(-1.0, -1e-3, 60), [-1e-20, 0.0, 7.5, -100.0]])
+    q_out, cache = run_append(cpa, b, rope_dim=128, rope_freqs=list(freqs))
+    check_append(b, q_out, cache, 128, False, freqs)
 
 
 def test_append_in_place_and_without_queries(cpa):

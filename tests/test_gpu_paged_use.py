@@ -365,6 +365,56 @@ def test_bad_sequences_are_skipped(cpa, what):
         assert torch.equal(x[mine].view(torch.int16), y[mine].view(torch.int16))
 
 
+@pytest.mark.parametrize("new", [1, 20, 70])
+def test_overlapping_entries(cpa, new):
+    """Prefixes or sequences out of order, so that some overlap and some rows
+    have no part of this call's: nothing outside the workspace is read (it
+    holds other numbers before), and whatever stands apart is right."""
+    b = Batch(past=[20, 3, 64] * 4, new=[new] * 12, prefixes=[(2, 100), (3, 50), (2, 300), (3, 20)], d=64, Hq=4, Hkv=2, seed=15)
+    ref = b.attention()
+    plan = b.plan(cpa, max_new=2 * new)
+    cache, _, q, _, _ = b.to_gpu(cpa)
+    pre = ints([100, 50, 300, 20]), ints(b.prefix_table)
+    for first, start in (([0, 9, 1, 2, 10], b.start), ([0, 10, 3, 5, 10], b.start),
+                         (b.first, np.r_[0, new + new // 2, new, b.start[3:]])):
+        batch = cpa.PagedBatch(ints(start), ints(b.kv), ints(b.page_table), n_tokens=b.N, prefix_first=ints(first),
+                               prefix_len=pre[0], prefix_table=pre[1])
+        o, lse = outputs(plan, b.N)
+        ws = cpa.alloc_paged_workspace(plan)
+        for fill in (0x7f, 0xff, 0x81):
+            ws.fill_(fill)
+            cpa.cp_attn_paged(plan, cache, batch, q, o, lse, ws)
+            rec = cpa.cp_get_status_detail()
+            assert rec[0] == cpa.CP_ERR_DEVICE_BOUNDS or (new == 1 and first is b.first)  # those rows are in order
+        at = 10 * new                                    # sequences 10 and 11 have no prefix in any of these
+        check_attention(o[at:], lse[:, at:], tuple(x[at:] if i != 1 else x[:, at:] for i, x in enumerate(ref)), BF, 64, 2 * new, "apart")
+
+
+@pytest.mark.parametrize("where", ["few_rows", "one_part", "many_rows", "prefix", "many_rows_prefix"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_seen_nan_reaches_the_result(cpa, where, bad):
+    """A key that is not a number makes the rows that see it so, O and LSE, in
+    whichever part of a row it lies; no other sequence's."""
+    kw = {"few_rows": dict(past=[2000, 300], new=[1, 1], Hq=8, Hkv=2), "one_part": dict(past=[20, 30], new=[1, 1], Hq=4, Hkv=2),
+          "many_rows": dict(past=[900, 100], new=[60, 1], Hq=8, Hkv=2),
+          "prefix": dict(past=[5, 3, 7], new=[1, 1, 1], prefixes=[(2, 400)], Hq=8, Hkv=2),
+          "many_rows_prefix": dict(past=[5] * 20 + [7], new=[1] * 21, prefixes=[(20, 400)], Hq=16, Hkv=2)}[where]
+    b = Batch(d=128, seed=16, **kw)
+    if b.plen:
+        hit, row = int(b.start[b.first[1]]), (b.prefix_table[0][6], 3)
+    else:
+        hit, row = int(b.start[1]), (b.page_table[0][1], 3)
+    ref = b.attention()
+    b.k_cache[int(row[0]), int(row[1])] = bad
+    plan = b.plan(cpa)
+    cache, batch, q, _, _ = b.to_gpu(cpa)
+    o, lse = outputs(plan, b.N)
+    o.zero_(), lse.zero_()
+    cpa.cp_attn_paged(plan, cache, batch, q, o, lse, cpa.alloc_paged_workspace(plan))
+    assert torch.isnan(o[:hit]).all() and torch.isnan(lse[:, :hit]).all()
+    check_attention(o[hit:], lse[:, hit:], tuple(x[hit:] if i != 1 else x[:, hit:] for i, x in enumerate(ref)), BF, 128, b.N - hit, where)
+
+
 def test_append_beyond_the_pages_and_before_the_first(cpa):
     """A new token whose page is not the cache's, and one that would lie before
     the sequence's first key, are not written."""
