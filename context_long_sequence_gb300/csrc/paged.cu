@@ -194,12 +194,16 @@ int cp_paged_shares(const cp_paged_t* p, const cp_paged_batch_t* batch, int32_t 
   const PagedGeom g = geom(*p, none, *batch);
   const PagedWorkspace w = paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0);
   const long long most = paged_most_rows(g);
-  const bool both = most > kSmallRows;
-  const PagedCut cuts[2] = {paged_cut_small(g.G, both ? paged_beside_rows(paged_most_own_rows(g)) : paged_small_rows(most)),
-                            paged_cut_large(g.G, paged_beside_rows(paged_most_own_rows(g)))};
-  long long units[2] = {0, 0};
+  const bool both = paged_has_large(most, g.d);
+  PagedCut cuts[3] = {paged_cut_small(g.G, both ? kBesideRows : paged_small_rows(most)), paged_cut_large(g.G), paged_cut_light(g.G)};
+  long long units[3] = {0, 0, 0};
   for (int e = 0; e < g.B + g.NP; ++e)
-    for (int c = 0; c < (both ? 2 : 1); ++c) units[c] += paged_head_units(g, cuts[c], paged_entry(g, e)) * g.Hkv;
+    for (int c = 0; c < (both ? 3 : 1); ++c) units[c] += paged_head_units(g, cuts[c], paged_entry(g, e)) * g.Hkv;
+  if (paged_is_light(units[2], ctas)) {
+    cuts[0] = cuts[2];
+    units[0] = units[2];
+    units[1] = 0;
+  }
   const int large = both ? paged_large_ctas(units[0], units[1], ctas) : 0;
   for (int c = 0; c < 2; ++c) {
     const PagedShares shares(units[c], c ? large : kSmallWarps * (ctas - large), c ? 1 : kSmallMinUnits);

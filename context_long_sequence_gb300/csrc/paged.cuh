@@ -69,9 +69,19 @@ struct PagedRole {
   int cut, worker, max_workers, min_units, slots, slot_rows;
 };
 
+__device__ __noinline__ inline long long paged_head_units_call(int n, int keys, int limit0, int G, PagedCut c) {
+  PagedGeom g;
+  g.G = G;
+  return paged_head_units(g, c, PagedEntry{0, n, keys, limit0, nullptr, false});
+}
+
 // Walks a worker's units, one warp, 32 entries at a time, an entry a lane.
+// ONE_COPY: with a call to the entries' unit counts, which the walk has in
+// three places and for several cuts (a call costs a kernel of one cut more
+// than it saves: decode_1x1000 8.0 -> 8.2 us).
 // Every warp of a block totals the units and chooses; the one that fetches
 // goes on to walk.
+template <bool ONE_COPY>
 struct PagedWalker {
   const PagedAttnArgs& a;
   const PagedGeom& g;
@@ -97,16 +107,19 @@ struct PagedWalker {
     if (base + lane < E) entry = paged_entry(g, base + lane);
     if (entry.bad) debug_bounds_fail(a.status, __LINE__, kTuPagedAttn);
   }
+  __device__ __forceinline__ long long units_of(const PagedCut& c) const {
+    return ONE_COPY ? paged_head_units_call(entry.n, entry.keys, entry.limit0, g.G, c) : paged_head_units(g, c, entry);
+  }
   // Units of the window's entries under cut `c`.
   __device__ __forceinline__ long long window_units(const PagedCut& c) const {
-    const long long x = paged_head_units(g, c, entry) * g.Hkv;  // below 2^48: two 24-bit sums of 32 each
+    const long long x = units_of(c) * g.Hkv;  // below 2^48: two 24-bit sums of 32 each
     const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x & 0xffffff));
     const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x >> 24));
     return (static_cast<long long>(hi) << 24) + lo;
   }
   __device__ __forceinline__ void scan() {
     const int lane = threadIdx.x & 31;
-    head_units = paged_head_units(g, cut, entry);
+    head_units = units_of(cut);
     upto = head_units * g.Hkv;
 #pragma unroll 1
     for (int x = 1; x < 32; x <<= 1) {

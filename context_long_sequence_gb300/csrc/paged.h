@@ -36,9 +36,8 @@ struct PagedGeom {
   float scale;
 };
 
-// What the sequences share with the kernels' index arithmetic is in 32 bits:
-// keys, rows and workspace rows stay below 2^30; units of work, cache offsets
-// and byte offsets are 64-bit.
+// Keys, rows and workspace rows stay below 2^30 and are held in 32 bits; units
+// of work, cache offsets and byte offsets are 64-bit.
 
 // One set of keys and the token rows that attend to it: entry e < B is
 // sequence e with its own pages, entry B + p is prefix p with the rows of
@@ -89,15 +88,16 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 // whose rows (tokens x query heads of a KV head) lie in [min_rows, max_rows],
 // cuts their tokens into tiles of tile_tokens and each tile's visible keys
 // into tiles of 2^key_shift.  One key tile of one token tile and KV head is a
-// unit, and the loading and writing of its rows a few more; units are numbered entry by entry, KV head by KV head, token tile by
-// token tile, and each of the W workers (CTAs) takes an equal, contiguous
-// share of the numbers.  A token tile whose units fall to several workers
+// unit, and the loading and writing of its rows a few more; units are numbered
+// entry by entry, KV head by KV head, token tile by token tile, and each of
+// the workers (warps or CTAs) takes an equal, contiguous share of the numbers.  A token tile whose units fall to several workers
 // has as many parts, merged afterwards by their log-sum-exp.  The cut depends
 // on the batch's lengths alone, so the result does too.
 struct PagedCut {
   int min_rows, max_rows;
   int tile_tokens, key_shift;  // tiles of 2^key_shift keys
   int lead;                    // units without keys that stand for a token tile's own cost
+  int above;                   // units of an entry of more than max_rows
 };
 
 // Units of token tile `rb` of entry `e`: `lead`, then the key tiles it sees;
@@ -111,7 +111,8 @@ __host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEn
 // Units of entry `e` for one KV head.
 __host__ __device__ inline long long paged_head_units(const PagedGeom& g, const PagedCut& c, const PagedEntry& e) {
   const long long rows = static_cast<long long>(e.n) * g.G;
-  if (e.n <= 0 || rows < c.min_rows || rows > c.max_rows) return 0;
+  if (e.n <= 0 || rows < c.min_rows) return 0;
+  if (rows > c.max_rows) return c.above;
   if (e.n <= c.tile_tokens) return paged_tile_units(c, e, 0);
   const int tiles = (e.n + c.tile_tokens - 1) / c.tile_tokens;
   if (e.limit0 >= e.keys) return static_cast<long long>(tiles) * paged_tile_units(c, e, 0);  // all rows see all keys
@@ -152,22 +153,46 @@ struct PagedShares {
 // 2w + 1); a part that is complete but has a partner (own keys and a prefix)
 // goes to a home row of its own.
 //
-// Small: a warp (paged_small.cuh), 16 keys a tile, up to 8 or 16 rows, or 32
-// where the batch has nothing larger; at least kSmallMinUnits tiles each.  Large: a
-// CTA (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
+// Small: a warp (paged_small.cuh), 16 keys a tile; up to 8, 16 or (d = 64) 32
+// rows in a batch that has nothing larger, up to kBesideRows beside larger
+// entries; at least kSmallMinUnits units each.  Large: a CTA
+// (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
+//
+// Between 8 and 32 rows, in us: 24 sequences of 20 rows on up to 30K keys take
+// 446 by warps at d = 128 (their registers spill), 258 by CTAs; at d = 64 and
+// 16K keys 76 by warps, 116 by CTAs.  Beside larger entries 16 rows spill too:
+// 40 sequences of 1 to 40 new tokens on up to 8K keys take 170 with
+// kBesideRows 8, 396 with 16.
+//
+// Light: a batch with entries of more rows that all workers' warps take in a
+// few units each, in tiles of kBesideRows rows that read their keys several
+// times (from L2): 7 sequences on a prefix of 2000 keys take 15.2 us so and
+// 17.4 by CTAs, 16 sequences 17.5 and 18.1; at kLightUnits 16, 7 on 8000 keys
+// would take 23.0 and not 21.9.
 constexpr int kSmallWarps = 8;  // workers of a CTA
 constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
 constexpr int kSmallMinUnits = 3;
 constexpr int kSmallLead = 3;
+constexpr int kBesideRows = 8;
+constexpr int kLightUnits = 12, kLightRows = 128;
 constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
 constexpr int kLargeLead = 4;
 constexpr int kMaxEntries = 8192;
 
 inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
-  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead};
+  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead, 0};
 }
-inline __host__ __device__ PagedCut paged_cut_large(int G, int small_rows) {
-  return PagedCut{small_rows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
+// All entries in the small workers' tiles; too many units if one has more
+// rows than kLightRows, or a token more than a tile.
+inline __host__ __device__ PagedCut paged_cut_light(int G) {
+  return PagedCut{1, G <= kBesideRows ? kLightRows : 0, G <= kBesideRows ? kBesideRows / G : 1, kSmallKeyShift, kSmallLead,
+                  kLightUnits * kSmallWorkers + 1};
+}
+inline __host__ __device__ bool paged_is_light(long long units, int ctas) {
+  return units > 0 && units <= static_cast<long long>(kLightUnits) * kSmallWarps * ctas;
+}
+inline __host__ __device__ PagedCut paged_cut_large(int G) {
+  return PagedCut{kBesideRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead, 0};
 }
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
@@ -208,10 +233,10 @@ __host__ __device__ inline long long paged_most_own_rows(const PagedGeom& g) {
 __host__ __device__ inline long long paged_most_rows(const PagedGeom& g) {
   return g.NP > 0 ? static_cast<long long>(g.N) * g.G : paged_most_own_rows(g);
 }
-// Rows up to which entries are the small workers', for a batch of at most
-// `most` rows an entry, and beside the large ones for at most `own` own rows.
+// Whether a batch of at most `most` rows an entry may have large entries; if
+// not, the rows of the small workers' tiles.
 __host__ __device__ inline int paged_small_rows(long long most) { return most <= 8 ? 8 : most <= 16 ? 16 : kSmallRows; }
-__host__ __device__ inline int paged_beside_rows(long long own) { return own <= 8 ? 8 : 16; }
+__host__ __device__ inline bool paged_has_large(long long most, int d) { return most > (d == 64 ? kSmallRows : 16); }
 
 // One run of key tiles of one token tile and KV head, as a worker gets it and
 // as the fetching warp hands it to the others through shared memory.

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
     debug_bounds_fail(args.status, __LINE__, CP_TU_ID);
     return;
   }
-  PagedWalker walk(args);
+  PagedWalker<false> walk(args);
   const PagedCut cuts[1] = {paged_cut_small(args.g.G, ROWS)};
   // Workers of different SMs first, so that a short batch has the whole card.
   const auto role = [&](const long long (&)[1]) {
@@ -259,14 +259,16 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const PagedGeom& g = a.g;
   const long long most = paged_most_rows(g);
   int rc;
-  if (most > kSmallRows)
+  if (paged_has_large(most, D))
     rc = launch_paged_large(a, stream);
   else if (paged_small_rows(most) == 8)
     rc = launch_small<T, D, 8>(a, stream);
   else if (paged_small_rows(most) == 16)
     rc = launch_small<T, D, 16>(a, stream);
-  else
+  else if constexpr (D == 64)
     rc = launch_small<T, D, kSmallRows>(a, stream);
+  else
+    rc = CP_ERR_UNSUPPORTED;  // paged_has_large
   if (rc != CP_OK) return rc;
   const long long rows = static_cast<long long>(g.N) * g.Hq;
   const auto blocks = [](long long n) { return static_cast<unsigned>(n < kMergeBlocks ? n : kMergeBlocks); };

@@ -98,8 +98,7 @@ constexpr uint32_t kLaunchBytes =
     LargeSmem<D>::kBytes > SmallSmem<D>::kBytes ? LargeSmem<D>::kBytes : static_cast<uint32_t>(SmallSmem<D>::kBytes);
 static_assert(kLaunchBytes<128> <= 227 * 1024, "one CTA an SM");
 
-// BESIDE: entries of up to so many rows are the small workers'.
-template <typename T, int D, int BESIDE>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_large_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
@@ -123,11 +122,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
-  PagedWalker walk(args);
-  const PagedCut cuts[2] = {paged_cut_small(g.G, BESIDE), paged_cut_large(g.G, BESIDE)};
+  PagedWalker<true> walk(args);
+  const PagedCut cuts[3] = {paged_cut_small(g.G, kBesideRows), paged_cut_large(g.G), paged_cut_light(g.G)};
   int large = 0;  // CTAs that take the entries of many rows
-  const auto role = [&](const long long (&units)[2]) {
+  const auto role = [&](const long long (&units)[3]) {
     const int ctas = gridDim.x, b = blockIdx.x;
+    if (paged_is_light(units[2], ctas)) return PagedRole{2, warp * ctas + b, kSmallWarps * ctas, kSmallMinUnits, 0, kSmallRows};
     large = paged_large_ctas(units[0], units[1], ctas);
     return b < large ? PagedRole{1, b, large, 1, static_cast<int>(args.rows_small), kLargeRows}
                      : PagedRole{0, warp * (ctas - large) + b - large, kSmallWarps * (ctas - large), kSmallMinUnits, 0, kSmallRows};
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         small_init<D>(smem, warp);
       }
       __syncwarp();
-      small_worker<SmallRows<T, D, BESIDE>, D>(smem, warp, tm_k16, tm_v16, walk);
+      small_worker<SmallColumns<T, D>, D>(smem, warp, tm_k16, tm_v16, walk);
     }
     return;
   }
@@ -633,12 +633,12 @@ bool make_o_map(CUtensorMap* m, const PagedGeom& g, const void* base) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int D, int BESIDE>
+template <typename T, int D>
 int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const PagedGeom& g = a.g;
   static std::atomic<int> known[64];
   int sms = 0;
-  int rc = prepare_kernel(known, paged_large_kernel<T, D, BESIDE>, kLaunchBytes<D>, &sms);
+  int rc = prepare_kernel(known, paged_large_kernel<T, D>, kLaunchBytes<D>, &sms);
   if (rc != CP_OK) return rc;
   const int page = 1 << g.page_shift, box = page < BN ? page : BN;
   CUtensorMap mk, mv, mk16, mv16;
@@ -651,24 +651,17 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_part_map(&mp, a.part_o, g.d, a.rows_large_end) || (o_boxes && !make_o_map(&mo, g, a.o))) return CP_ERR_CUDA;
   if (!o_boxes) mo = mp;  // not used
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D, BESIDE>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, mp, mo,
+  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, mp, mo,
                 a, box, o_boxes ? 1 : 0);
-}
-
-template <typename T, int BESIDE>
-int launch_large_t(const PagedAttnArgs& a, cudaStream_t stream) {
-  if (a.g.d == 128) return launch_large_d<T, 128, BESIDE>(a, stream);
-  if (a.g.d == 64) return launch_large_d<T, 64, BESIDE>(a, stream);
-  return CP_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
 int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream) {
-  const bool few = paged_beside_rows(paged_most_own_rows(a.g)) == 8;
-  if (a.g.dtype == CP_DTYPE_BF16)
-    return few ? launch_large_t<__nv_bfloat16, 8>(a, stream) : launch_large_t<__nv_bfloat16, 16>(a, stream);
-  return few ? launch_large_t<__half, 8>(a, stream) : launch_large_t<__half, 16>(a, stream);
+  const bool bf16 = a.g.dtype == CP_DTYPE_BF16;
+  if (a.g.d == 128) return bf16 ? launch_large_d<__nv_bfloat16, 128>(a, stream) : launch_large_d<__half, 128>(a, stream);
+  if (a.g.d == 64) return bf16 ? launch_large_d<__nv_bfloat16, 64>(a, stream) : launch_large_d<__half, 64>(a, stream);
+  return CP_ERR_UNSUPPORTED;
 }
 
 }  // namespace cpattn

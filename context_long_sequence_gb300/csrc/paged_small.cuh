@@ -24,8 +24,8 @@ struct SmallSmem {
   // Segments known: those of the tiles in flight (a segment may be one tile)
   // and the end mark.
   static constexpr int kSegs = kStages + 1;
-  static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, two cuts
-  static constexpr int offBar = offSums + 2 * kMaxEntries / 32 * 8;
+  static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, three cuts
+  static constexpr int offBar = offSums + 3 * kMaxEntries / 32 * 8;
   static constexpr int offSeg = offBar + kSmallWarps * kStages * 8;
   static constexpr int offHeld = offSeg + kSmallWarps * kSegs * static_cast<int>(sizeof(PagedSegment));
   static constexpr int kBytes = offHeld + kSmallWarps * kStages * 4;  // held: whether the stage's page was fetched
@@ -387,9 +387,9 @@ using SmallRows = typename std::conditional<ROWS == 8, SmallColumns<T, D>, Small
 
 // The share of the block's warp `warp`, whose walk has begun and whose
 // barriers are set.
-template <typename Rows, int D>
+template <typename Rows, int D, typename Walk>
 __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                             PagedWalker& walk) {
+                                             Walk& walk) {
   using SM = SmallSmem<D>;
   constexpr int S = SM::kStages;
   constexpr uint32_t kAll = 0xffffffffu;

@@ -90,6 +90,16 @@ MORE = {
     "groups_2800": (dict(past=[0, 500], new=[300, 400], d=64, Hq=8, Hkv=4), {}),
     "tokens_4200": (dict(past=[0] * 14, new=[300] * 14, d=64, Hq=4, Hkv=2), {}),
     "forty_kv_heads": (dict(past=[0, 90], new=[150, 100], d=64, Hq=40, Hkv=40), {}),
+    # Few rows, light and not: by the small workers in several tiles, or by CTAs
+    # because a token has more than 8 rows or the keys are many.
+    "light_prefix": (dict(past=[3, 0, 40, 7, 300], new=[1, 2, 1, 5, 1], prefixes=[(3, 200), (2, 1000)], d=128, Hq=8, Hkv=2), {}),
+    "light_prefix_d64": (dict(past=[3] * 25, new=[1] * 25, prefixes=[(25, 300)], d=64, Hq=20, Hkv=4), {}),
+    "light_chunk": (dict(past=[50, 100], new=[30, 9], d=128, Hq=6, Hkv=2, dtype=FP), {}),
+    "light_but_one": (dict(past=[50, 100, 0], new=[1, 9, 40], d=128, Hq=8, Hkv=2), {}),
+    "drafts_group_9": (dict(past=[50, 100, 700], new=[2, 3, 1], d=128, Hq=18, Hkv=2), {}),
+    "prefix_group_16": (dict(past=[5, 0, 90], new=[1, 2, 1], prefixes=[(3, 500)], d=128, Hq=32, Hkv=2, dtype=FP), {}),
+    "prefix_group_12_d64": (dict(past=[5, 0, 90], new=[1, 2, 1], prefixes=[(3, 500)], d=64, Hq=24, Hkv=2), {}),
+    "chunk_long_few_rows": (dict(past=[60000], new=[20], d=64, Hq=8, Hkv=2, page_size=256), {}),
     "prefix_tokens": (dict(past=[0] * 6, new=[200] * 6, prefixes=[(4, 300)], first=1, d=64, Hq=8, Hkv=8), {}),
 }
 for page in (16, 32, 64, 128, 256):

@@ -231,6 +231,20 @@ def test_shares_cover_everything_once(cpa, seed):
             assert max(cost.values()) <= -(-(sum(cost.values()) + (lead + 1) * len(w)) // len(cost)) + 3 * lead + 4
 
 
+@pytest.mark.parametrize("Hq,new,prefix,light", [
+    (8, [1] * 7, 2000, True), (8, [1] * 32, 500, True), (8, [1] * 33, 500, False), (8, [1] * 7, 80000, False),
+    (18, [1] * 7, 2000, False), (8, [1] * 20 + [40], 0, False), (8, [20], 0, True)])
+def test_shares_of_light_batches(cpa, Hq, new, prefix, light):
+    """A batch with entries of more rows than the small workers' tiles is theirs
+    all the same when it is light: few rows, few units, 8 rows a token at most."""
+    start = np.concatenate([[0], np.cumsum(new)]).tolist()
+    kv = [n + 30 for n in new]
+    first, plen = ([0, len(new)], [prefix]) if prefix else (None, None)
+    plan, t = shares(cpa, start, kv, first, plen, Hq=Hq, Hkv=2, prefix_pages=8192)
+    check_shares(t, start, kv, first, plen, Hq, 2, plan.max_tokens)
+    assert (t[:, 0] == 0).all() == light
+
+
 def test_shares_of_a_million_keys(cpa):
     start, kv = [0, 1], [1 << 20]
     plan, t = shares(cpa, start, kv, Hq=32, Hkv=8, ps=64, pages=1 << 14)
