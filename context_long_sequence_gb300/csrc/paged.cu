@@ -195,7 +195,8 @@ int cp_paged_shares(const cp_paged_t* p, const cp_paged_batch_t* batch, int32_t 
   const PagedWorkspace w = paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0);
   const long long most = paged_most_rows(g);
   const bool both = paged_has_large(most, g.d);
-  PagedCut cuts[3] = {paged_cut_small(g.G, both ? kBesideRows : paged_small_rows(most)), paged_cut_large(g.G), paged_cut_light(g.G)};
+  PagedCut cuts[3] = {both ? paged_cut_beside(g.G, kCutBeside) : paged_cut_all(g.G, paged_small_rows(most)),
+                      paged_cut_large(g.G), paged_cut_beside(g.G, kCutLight)};
   long long units[3] = {0, 0, 0};
   for (int e = 0; e < g.B + g.NP; ++e)
     for (int c = 0; c < (both ? 3 : 1); ++c) units[c] += paged_head_units(g, cuts[c], paged_entry(g, e)) * g.Hkv;

@@ -84,21 +84,70 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
   return r;
 }
 
-// How the attention of a batch is cut into work.  A cut takes the entries
-// whose rows (tokens x query heads of a KV head) lie in [min_rows, max_rows],
-// cuts their tokens into tiles of tile_tokens and each tile's visible keys
-// into tiles of 2^key_shift.  One key tile of one token tile and KV head is a
-// unit, and the loading and writing of its rows a few more; units are numbered
-// entry by entry, KV head by KV head, token tile by token tile, and each of
-// the workers (warps or CTAs) takes an equal, contiguous share of the numbers.  A token tile whose units fall to several workers
-// has as many parts, merged afterwards by their log-sum-exp.  The cut depends
-// on the batch's lengths alone, so the result does too.
+// How the attention of a batch is cut into work.  A cut takes the entries of
+// its kind, cuts their tokens into tiles of tile_tokens and each tile's
+// visible keys into tiles of 2^key_shift.  One key tile of one token tile and
+// KV head is a unit, and the loading and writing of its rows a few more; units
+// are numbered entry by entry, KV head by KV head, token tile by token tile,
+// and each of the workers (warps or CTAs) takes an equal, contiguous share of
+// the numbers.  A token tile whose units fall to several workers has as many
+// parts, merged afterwards by their log-sum-exp.  The cut depends on the
+// batch's lengths alone, so the result does too.
+//
+// Two sorts of worker.  A warp (paged_small.cuh): 16 keys a tile, and 8, 16 or
+// (d = 64) 32 rows (tokens x query heads of a KV head), the fewest that hold a
+// batch's entries.  A CTA (paged_attn_large.cu): two blocks of up to 128 rows,
+// 128 keys a tile; in such a batch warps of 8 rows take some entries too.
+//
+// Between 8 and 32 rows, in us: 24 sequences of 20 rows on up to 30K keys take
+// 446 by warps at d = 128 (their registers spill), 258 by CTAs; at d = 64 and
+// 16K keys 76 by warps, 116 by CTAs.  Beside CTAs 16 rows spill too: 40
+// sequences of 1 to 40 new tokens on up to 8K keys take 170 with warps of 8
+// rows, 396 with 16.
+enum : int {
+  kCutAll = 0,     // warps, every entry
+  kCutBeside = 1,  // warps, the entries that paged_by_warps gives them
+  kCutLarge = 2,   // CTAs, the others
+  kCutLight = 3,   // warps, every entry of a batch that is light (paged_is_light)
+};
 struct PagedCut {
-  int min_rows, max_rows;
+  int kind;
   int tile_tokens, key_shift;  // tiles of 2^key_shift keys
   int lead;                    // units without keys that stand for a token tile's own cost
-  int above;                   // units of an entry of more than max_rows
 };
+
+constexpr int kSmallWarps = 8;  // workers of a CTA
+constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
+constexpr int kSmallMinUnits = 3;  // of a worker, at least
+constexpr int kSmallLead = 3;
+constexpr int kBesideRows = 8, kBesideMaxRows = 128, kBesideWeight = 12;
+constexpr int kLightUnits = 12;
+constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
+constexpr int kLargeLead = 4;
+constexpr int kMaxEntries = 8192;
+
+inline __host__ __device__ PagedCut paged_cut_all(int G, int rows) {
+  return PagedCut{kCutAll, rows / G, kSmallKeyShift, kSmallLead};
+}
+inline __host__ __device__ PagedCut paged_cut_beside(int G, int kind) {
+  return PagedCut{kind, G <= kBesideRows ? kBesideRows / G : 1, kSmallKeyShift, kSmallLead};
+}
+inline __host__ __device__ PagedCut paged_cut_large(int G) {
+  return PagedCut{kCutLarge, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
+}
+
+// Whether an entry is the warps' in a batch that CTAs work on too: one of up
+// to 8 rows, and one whose tiles of 8 rows, that read the keys once each, cost
+// less than a CTA's one tile: short ones.  (In us, at weights 0, 8, 12, 16: 420
+// sequences of 24 rows on a few keys 155, 43, 43, 43; 64 of 8 to 24 on 1000
+// beside a prefix 206, 207, 163, 163; 64 of 12 on 1000 to 4000 153, 153, 179, 213.)
+__host__ __device__ inline bool paged_by_warps(const PagedGeom& g, const PagedEntry& e) {
+  const long long rows = static_cast<long long>(e.n) * g.G;
+  if (rows <= kBesideRows) return true;
+  if (g.G > kBesideRows || rows > kBesideMaxRows) return false;
+  const long long warps = (rows + kBesideRows - 1) / kBesideRows * (((e.keys + 15) >> kSmallKeyShift) + kSmallLead);
+  return warps <= kBesideWeight * (((e.keys + 127) >> kLargeKeyShift) + kLargeLead);
+}
 
 // Units of token tile `rb` of entry `e`: `lead`, then the key tiles it sees;
 // none if it sees no key.
@@ -110,9 +159,12 @@ __host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEn
 
 // Units of entry `e` for one KV head.
 __host__ __device__ inline long long paged_head_units(const PagedGeom& g, const PagedCut& c, const PagedEntry& e) {
-  const long long rows = static_cast<long long>(e.n) * g.G;
-  if (e.n <= 0 || rows < c.min_rows) return 0;
-  if (rows > c.max_rows) return c.above;
+  if (e.n <= 0) return 0;
+  if (c.kind == kCutLight) {
+    if (g.G > kBesideRows || static_cast<long long>(e.n) * g.G > kBesideMaxRows) return kLightUnits * kSmallWorkers + 1;
+  } else if (c.kind != kCutAll && paged_by_warps(g, e) != (c.kind == kCutBeside)) {
+    return 0;
+  }
   if (e.n <= c.tile_tokens) return paged_tile_units(c, e, 0);
   const int tiles = (e.n + c.tile_tokens - 1) / c.tile_tokens;
   if (e.limit0 >= e.keys) return static_cast<long long>(tiles) * paged_tile_units(c, e, 0);  // all rows see all keys
@@ -148,52 +200,18 @@ struct PagedShares {
   }
 };
 
+// A batch is light if all its entries, of up to 128 rows, are a few units for
+// every warp in tiles of 8 rows: 7 sequences on a prefix of 2000 keys take 15.2
+// us so and 17.4 with CTAs, 16 sequences 17.5 and 18.1; at kLightUnits 16, 7 on
+// 8000 keys would take 23.0 and not 21.9.
+inline __host__ __device__ bool paged_is_light(long long units, int ctas) {
+  return units > 0 && units <= static_cast<long long>(kLightUnits) * kSmallWarps * ctas;
+}
+
 // Workers and slots.  A worker holds at most two incomplete token tiles: the
 // one its share begins in (its slot 2w) and the one its share ends in (slot
 // 2w + 1); a part that is complete but has a partner (own keys and a prefix)
 // goes to a home row of its own.
-//
-// Small: a warp (paged_small.cuh), 16 keys a tile; up to 8, 16 or (d = 64) 32
-// rows in a batch that has nothing larger, up to kBesideRows beside larger
-// entries; at least kSmallMinUnits units each.  Large: a CTA
-// (paged_attn_large.cu), two blocks of up to 128 rows, 128 keys a tile.
-//
-// Between 8 and 32 rows, in us: 24 sequences of 20 rows on up to 30K keys take
-// 446 by warps at d = 128 (their registers spill), 258 by CTAs; at d = 64 and
-// 16K keys 76 by warps, 116 by CTAs.  Beside larger entries 16 rows spill too:
-// 40 sequences of 1 to 40 new tokens on up to 8K keys take 170 with
-// kBesideRows 8, 396 with 16.
-//
-// Light: a batch with entries of more rows that all workers' warps take in a
-// few units each, in tiles of kBesideRows rows that read their keys several
-// times (from L2): 7 sequences on a prefix of 2000 keys take 15.2 us so and
-// 17.4 by CTAs, 16 sequences 17.5 and 18.1; at kLightUnits 16, 7 on 8000 keys
-// would take 23.0 and not 21.9.
-constexpr int kSmallWarps = 8;  // workers of a CTA
-constexpr int kSmallWorkers = 1216, kSmallRows = 32, kSmallKeyShift = 4;
-constexpr int kSmallMinUnits = 3;
-constexpr int kSmallLead = 3;
-constexpr int kBesideRows = 8;
-constexpr int kLightUnits = 12, kLightRows = 128;
-constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
-constexpr int kLargeLead = 4;
-constexpr int kMaxEntries = 8192;
-
-inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
-  return PagedCut{1, rows, G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead, 0};
-}
-// All entries in the small workers' tiles; too many units if one has more
-// rows than kLightRows, or a token more than a tile.
-inline __host__ __device__ PagedCut paged_cut_light(int G) {
-  return PagedCut{1, G <= kBesideRows ? kLightRows : 0, G <= kBesideRows ? kBesideRows / G : 1, kSmallKeyShift, kSmallLead,
-                  kLightUnits * kSmallWorkers + 1};
-}
-inline __host__ __device__ bool paged_is_light(long long units, int ctas) {
-  return units > 0 && units <= static_cast<long long>(kLightUnits) * kSmallWarps * ctas;
-}
-inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kBesideRows + 1, 0x7fffffff, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead, 0};
-}
 
 // Where a (token, KV head)'s parts over one entry are: G consecutive rows each.
 struct alignas(16) PagedParts {

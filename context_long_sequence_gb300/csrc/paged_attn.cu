@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
     return;
   }
   PagedWalker<false> walk(args);
-  const PagedCut cuts[1] = {paged_cut_small(args.g.G, ROWS)};
+  const PagedCut cuts[1] = {paged_cut_all(args.g.G, ROWS)};
   // Workers of different SMs first, so that a short batch has the whole card.
   const auto role = [&](const long long (&)[1]) {
     return PagedRole{0, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kSmallWarps * static_cast<int>(gridDim.x),

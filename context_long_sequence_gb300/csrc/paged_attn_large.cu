@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
   PagedWalker<true> walk(args);
-  const PagedCut cuts[3] = {paged_cut_small(g.G, kBesideRows), paged_cut_large(g.G), paged_cut_light(g.G)};
+  const PagedCut cuts[3] = {paged_cut_beside(g.G, kCutBeside), paged_cut_large(g.G), paged_cut_beside(g.G, kCutLight)};
   int large = 0;  // CTAs that take the entries of many rows
   const auto role = [&](const long long (&units)[3]) {
     const int ctas = gridDim.x, b = blockIdx.x;
