@@ -195,19 +195,23 @@ int cp_paged_shares(const cp_paged_t* p, const cp_paged_batch_t* batch, int32_t 
   const PagedWorkspace w = paged_workspace(d.max_tokens, d.Hq, d.Hkv, d.d, d.max_prefixes > 0);
   const long long most = paged_most_rows(g);
   const bool both = paged_has_large(most, g.d);
-  PagedCut cuts[3] = {both ? paged_cut_beside(g.G, kCutBeside) : paged_cut_all(g.G, paged_small_rows(most)),
-                      paged_cut_large(g.G), paged_cut_beside(g.G, kCutLight)};
-  long long units[3] = {0, 0, 0};
+  const PagedCut cuts[2] = {paged_cut_small(g.G, both ? kBesideRows : paged_small_rows(most)), paged_cut_large(g.G)};
+  // Units of an entry for one KV head, of the sum `which`.
+  const auto head_units = [&](const PagedEntry& e, int which) {
+    if (!both) return which == kUnitsBeside ? paged_entry_units(cuts[0], e) : 0;
+    long long x[kUnitSums];
+    paged_unit_sums(g, cuts, e, x, paged_entry_units);
+    return x[which];
+  };
+  long long units[kUnitSums] = {0, 0, 0};
   for (int e = 0; e < g.B + g.NP; ++e)
-    for (int c = 0; c < (both ? 3 : 1); ++c) units[c] += paged_head_units(g, cuts[c], paged_entry(g, e)) * g.Hkv;
-  if (paged_is_light(units[2], ctas)) {
-    cuts[0] = cuts[2];
-    units[0] = units[2];
-    units[1] = 0;
-  }
-  const int large = both ? paged_large_ctas(units[0], units[1], ctas) : 0;
+    for (int i = 0; i < kUnitSums; ++i) units[i] += head_units(paged_entry(g, e), i) * g.Hkv;
+  const bool light = both && paged_is_light(units[kUnitsLight], ctas);
+  const int large = both && !light ? paged_large_ctas(units[kUnitsBeside], units[kUnitsLarge], ctas) : 0;
   for (int c = 0; c < 2; ++c) {
-    const PagedShares shares(units[c], c ? large : kSmallWarps * (ctas - large), c ? 1 : kSmallMinUnits);
+    const int which = c == 0 && light ? kUnitsLight : c == 0 ? kUnitsBeside : kUnitsLarge;
+    if (c == 1 && light) break;
+    const PagedShares shares(units[which], c ? large : kSmallWarps * (ctas - large), c ? 1 : kSmallMinUnits);
     PagedPlace at;
     at.slots = c ? static_cast<int>(w.rows_small) : 0;
     at.slot_rows = c ? kLargeRows : kSmallRows;
@@ -225,7 +229,7 @@ int cp_paged_shares(const cp_paged_t* p, const cp_paged_batch_t* batch, int32_t 
       const long long end = shares.first(at.worker + 1);
       while (u < end) {
         const PagedEntry entry = paged_entry(g, e);
-        const long long hu = paged_head_units(g, cuts[c], entry);
+        const long long hu = head_units(entry, which);
         if (u >= before + hu * g.Hkv) {
           before += hu * g.Hkv;
           ++e;

@@ -63,29 +63,38 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ long long shfl64(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
-// Which share a warp takes up: cut number `cut`, as worker `worker` of at most
-// max_workers with at least min_units units each; its slots.
+// A barrier of the block's first `threads` threads.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Which share a warp takes up: of the units of sum `sum` under cut number
+// `cut`, as worker `worker` of at most max_workers with at least min_units
+// units each; its slots.
 struct PagedRole {
-  int cut, worker, max_workers, min_units, slots, slot_rows;
+  int sum, cut, worker, max_workers, min_units, slots, slot_rows;
 };
 
-__device__ __noinline__ inline long long paged_head_units_call(int n, int keys, int limit0, int G, PagedCut c) {
-  PagedGeom g;
-  g.G = G;
-  return paged_head_units(g, c, PagedEntry{0, n, keys, limit0, nullptr, false});
+__device__ __noinline__ inline long long paged_entry_units_call(int n, int keys, int limit0, PagedCut c) {
+  return paged_entry_units(c, PagedEntry{0, n, keys, limit0, nullptr, false});
 }
 
 // Walks a worker's units, one warp, 32 entries at a time, an entry a lane.
-// ONE_COPY: with a call to the entries' unit counts, which the walk has in
-// three places and for several cuts (a call costs a kernel of one cut more
-// than it saves: decode_1x1000 8.0 -> 8.2 us).
-// Every warp of a block totals the units and chooses; the one that fetches
-// goes on to walk.
-template <bool ONE_COPY>
+// Every warp that walks totals the units and chooses; a CTA's one that fetches
+// goes on to walk.  SUMS: 1, a batch for warps alone, or kUnitSums.
+//
+// Code that a CTA runs once comes from L2 line by line, the same lines for
+// all SMs at once, some 12 clocks an instruction: this is written to be short.
+// Of kUnitSums the entries' units are counted by a call, in one copy (for one
+// sum the call costs more than it saves: decode_1x1000 8.0 -> 8.2 us).
+template <int SUMS>
 struct PagedWalker {
+  static constexpr int kCuts = SUMS == 1 ? 1 : 2;
   const PagedAttnArgs& a;
   const PagedGeom& g;
+  const PagedCut (&cuts)[kCuts];
   PagedCut cut;
+  int sum = 0;                 // the role's
   PagedPlace place;
   int E;
   PagedShares shares;
@@ -97,29 +106,32 @@ struct PagedWalker {
   const int32_t* table;        // page table of the last segment's entry
   bool once;                   // no other token tile reads its keys
 
-  __device__ __forceinline__ explicit PagedWalker(const PagedAttnArgs& args)
-      : a(args), g(args.g), E(args.g.B + args.g.NP), shares(0, 1, 1) {}
+  __device__ __forceinline__ PagedWalker(const PagedAttnArgs& args, const PagedCut (&c)[kCuts])
+      : a(args), g(args.g), cuts(c), E(args.g.B + args.g.NP), shares(0, 1, 1) {}
 
-  __device__ __forceinline__ void load(int first) {
+  // The window from entry `first` on, and the units of the lane's entry.
+  __device__ __forceinline__ void load(int first, long long (&x)[SUMS]) {
     const int lane = threadIdx.x & 31;
     base = first;
     entry = PagedEntry{0, 0, 0, 0, nullptr, false};
     if (base + lane < E) entry = paged_entry(g, base + lane);
     if (entry.bad) debug_bounds_fail(a.status, __LINE__, kTuPagedAttn);
+    if constexpr (SUMS == 1)
+      x[0] = paged_entry_units(cuts[0], entry);
+    else
+      paged_unit_sums(g, cuts, entry, x, [](const PagedCut& c, const PagedEntry& e) {
+        return paged_entry_units_call(e.n, e.keys, e.limit0, c);
+      });
   }
-  __device__ __forceinline__ long long units_of(const PagedCut& c) const {
-    return ONE_COPY ? paged_head_units_call(entry.n, entry.keys, entry.limit0, g.G, c) : paged_head_units(g, c, entry);
+  __device__ __forceinline__ long long pick(const long long (&x)[SUMS]) const {
+    long long r = x[0];
+#pragma unroll
+    for (int i = 1; i < SUMS; ++i) r = sum == i ? x[i] : r;
+    return r;
   }
-  // Units of the window's entries under cut `c`.
-  __device__ __forceinline__ long long window_units(const PagedCut& c) const {
-    const long long x = units_of(c) * g.Hkv;  // below 2^48: two 24-bit sums of 32 each
-    const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x & 0xffffff));
-    const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(x >> 24));
-    return (static_cast<long long>(hi) << 24) + lo;
-  }
-  __device__ __forceinline__ void scan() {
+  __device__ __forceinline__ void scan(long long of_head) {
     const int lane = threadIdx.x & 31;
-    head_units = units_of(cut);
+    head_units = of_head;
     upto = head_units * g.Hkv;
 #pragma unroll 1
     for (int x = 1; x < 32; x <<= 1) {
@@ -128,49 +140,49 @@ struct PagedWalker {
     }
   }
 
-  // The worker's place among the units.  Called by the whole block: every
-  // warp totals the units under the N cuts (`sums`: N numbers in shared
-  // memory for each window of 32 entries), and choose(units) returns the
-  // PagedRole of the calling warp.  False: nothing for it.  `sums` is free
-  // once every warp has returned.
-  //
-  // Code that a CTA runs once comes from L2 line by line, the same lines for
-  // all SMs at once, some 15 clocks an instruction: this is written to be
-  // short, with one copy of load().
-  template <int N, typename F>
-  __device__ __forceinline__ bool start(long long* sums, const PagedCut (&cuts)[N], F&& choose) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // The worker's place among the units.  Called by the block's first `warps`
+  // warps: they total the units (`sums`: SUMS numbers in shared memory for
+  // each window of 32 entries), and choose(units) returns the PagedRole of the
+  // calling warp.  False: nothing for it.  `sums` is free once every warp has
+  // returned.
+  template <typename F>
+  __device__ __forceinline__ bool start(long long* sums, int warps, F&& choose) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int windows = (E + 31) / 32;
     const bool alone = windows == 1;
     place.covered0 = g.NP > 0 ? g.prefix_first[0] : 0;
     place.covered1 = g.NP > 0 ? g.prefix_first[g.NP] : 0;
-    long long units[N];
-    bool chosen = false, any = false;
+    long long x[SUMS], units[SUMS];
+    bool chosen = false;
     int w = alone ? 0 : warp;
 #pragma unroll 1
     while (true) {
-      if (w < windows) load(w * 32);
-      if (chosen) break;
       if (w < windows) {
+        load(w * 32, x);
+        if (chosen) break;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          units[i] = window_units(cuts[i]);
-          if (!alone && lane == 0) sums[w * N + i] = units[i];
+        for (int i = 0; i < SUMS; ++i) {
+          const long long y = x[i] * g.Hkv;  // below 2^48: two 24-bit sums of 32 each
+          const unsigned lo = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(y & 0xffffff));
+          const unsigned hi = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(y >> 24));
+          units[i] = (static_cast<long long>(hi) << 24) + lo;
+          if (!alone && lane == 0) sums[w * SUMS + i] = units[i];
         }
       }
       if (!alone) {
         w += warps;
         if (w < windows) continue;
-        __syncthreads();
+        named_barrier(1, warps * 32);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < SUMS; ++i) {
           units[i] = 0;
 #pragma unroll 1
-          for (int k = 0; k < windows; ++k) units[i] += sums[k * N + i];
+          for (int k = 0; k < windows; ++k) units[i] += sums[k * SUMS + i];
         }
       }
       const PagedRole r = choose(units);
-      cut = cuts[r.cut];
+      cut = cuts[kCuts == 1 ? 0 : r.cut];
+      sum = r.sum;
       place.worker = r.worker;
       place.slots = r.slots;
       place.slot_rows = r.slot_rows;
@@ -179,19 +191,18 @@ struct PagedWalker {
       place.B = g.B;
       place.G = g.G;
       place.Hq = g.Hq;
-      shares = PagedShares(units[r.cut], r.max_workers, r.min_units);
+      shares = PagedShares(pick(units), r.max_workers, r.min_units);
       before = 0;
-      any = r.worker < shares.workers;
-      if (!any) break;
+      if (r.worker >= shares.workers) return false;
       u = shares.first(r.worker);
       end = shares.first(r.worker + 1);
       if (alone) break;
 #pragma unroll 1
-      for (w = 0; w + 1 < windows && before + sums[w * N + r.cut] <= u; ++w) before += sums[w * N + r.cut];
+      for (w = 0; w + 1 < windows && before + sums[w * SUMS + sum] <= u; ++w) before += sums[w * SUMS + sum];
       chosen = true;
     }
-    if (any) scan();
-    return any;
+    scan(pick(x));
+    return true;
   }
 
   // The next segment (warp-uniform), nt == 0 behind the last.  The run that
@@ -206,8 +217,9 @@ struct PagedWalker {
           return s;
         }
         before += total;
-        load(base + 32);
-        scan();
+        long long x[SUMS];
+        load(base + 32, x);
+        scan(pick(x));
         total = shfl64(upto, 31);
       }
       long long rel = u - before;

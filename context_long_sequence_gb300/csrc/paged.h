@@ -84,9 +84,9 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
   return r;
 }
 
-// How the attention of a batch is cut into work.  A cut takes the entries of
-// its kind, cuts their tokens into tiles of tile_tokens and each tile's
-// visible keys into tiles of 2^key_shift.  One key tile of one token tile and
+// How the attention of a batch is cut into work.  A cut takes some of the
+// entries, cuts their tokens into tiles of tile_tokens and each tile's visible
+// keys into tiles of 2^key_shift.  One key tile of one token tile and
 // KV head is a unit, and the loading and writing of its rows a few more; units
 // are numbered entry by entry, KV head by KV head, token tile by token tile,
 // and each of the workers (warps or CTAs) takes an equal, contiguous share of
@@ -104,14 +104,7 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 // 16K keys 76 by warps, 116 by CTAs.  Beside CTAs 16 rows spill too: 40
 // sequences of 1 to 40 new tokens on up to 8K keys take 170 with warps of 8
 // rows, 396 with 16.
-enum : int {
-  kCutAll = 0,     // warps, every entry
-  kCutBeside = 1,  // warps, the entries that paged_by_warps gives them
-  kCutLarge = 2,   // CTAs, the others
-  kCutLight = 3,   // warps, every entry of a batch that is light (paged_is_light)
-};
 struct PagedCut {
-  int kind;
   int tile_tokens, key_shift;  // tiles of 2^key_shift keys
   int lead;                    // units without keys that stand for a token tile's own cost
 };
@@ -126,14 +119,12 @@ constexpr int kLargeWorkers = 152, kLargeRows = 256, kLargeKeyShift = 7;
 constexpr int kLargeLead = 4;
 constexpr int kMaxEntries = 8192;
 
-inline __host__ __device__ PagedCut paged_cut_all(int G, int rows) {
-  return PagedCut{kCutAll, rows / G, kSmallKeyShift, kSmallLead};
-}
-inline __host__ __device__ PagedCut paged_cut_beside(int G, int kind) {
-  return PagedCut{kind, G <= kBesideRows ? kBesideRows / G : 1, kSmallKeyShift, kSmallLead};
+// Warps of `rows` rows.
+inline __host__ __device__ PagedCut paged_cut_small(int G, int rows) {
+  return PagedCut{G <= rows ? rows / G : 1, kSmallKeyShift, kSmallLead};
 }
 inline __host__ __device__ PagedCut paged_cut_large(int G) {
-  return PagedCut{kCutLarge, 2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
+  return PagedCut{2 * (kLargeRows / 2 / G), kLargeKeyShift, kLargeLead};
 }
 
 // Whether an entry is the warps' in a batch that CTAs work on too: one of up
@@ -158,19 +149,30 @@ __host__ __device__ inline int paged_tile_units(const PagedCut& c, const PagedEn
 }
 
 // Units of entry `e` for one KV head.
-__host__ __device__ inline long long paged_head_units(const PagedGeom& g, const PagedCut& c, const PagedEntry& e) {
+__host__ __device__ inline long long paged_entry_units(const PagedCut& c, const PagedEntry& e) {
   if (e.n <= 0) return 0;
-  if (c.kind == kCutLight) {
-    if (g.G > kBesideRows || static_cast<long long>(e.n) * g.G > kBesideMaxRows) return kLightUnits * kSmallWorkers + 1;
-  } else if (c.kind != kCutAll && paged_by_warps(g, e) != (c.kind == kCutBeside)) {
-    return 0;
-  }
   if (e.n <= c.tile_tokens) return paged_tile_units(c, e, 0);
   const int tiles = (e.n + c.tile_tokens - 1) / c.tile_tokens;
   if (e.limit0 >= e.keys) return static_cast<long long>(tiles) * paged_tile_units(c, e, 0);  // all rows see all keys
   long long sum = 0;
   for (int rb = 0; rb < tiles; ++rb) sum += paged_tile_units(c, e, rb);
   return sum;
+}
+
+// The sums that decide how a batch with entries for CTAs is shared out: units
+// of the entries that the warps take beside CTAs, of the CTAs' entries, and of
+// all entries if the warps took them (too many where they cannot).  An entry's
+// for one KV head, under cuts[0] of the warps and cuts[1] of the CTAs.
+enum : int { kUnitsBeside = 0, kUnitsLarge = 1, kUnitsLight = 2, kUnitSums = 3 };
+template <typename F>
+__host__ __device__ inline void paged_unit_sums(const PagedGeom& g, const PagedCut (&cuts)[2], const PagedEntry& e,
+                                                long long (&units)[kUnitSums], F&& entry_units) {
+  const bool warps = paged_by_warps(g, e);
+  units[kUnitsLight] = kLightUnits * kSmallWorkers + 1;
+  if (warps || (g.G <= kBesideRows && static_cast<long long>(e.n) * g.G <= kBesideMaxRows))
+    units[kUnitsLight] = entry_units(cuts[0], e);
+  units[kUnitsBeside] = warps ? units[kUnitsLight] : 0;
+  units[kUnitsLarge] = warps ? 0 : entry_units(cuts[1], e);
 }
 
 // Quotient of numbers that nearly always fit in 32 bits: a 64-bit division

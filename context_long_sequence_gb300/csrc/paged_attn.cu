@@ -46,14 +46,14 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
     debug_bounds_fail(args.status, __LINE__, CP_TU_ID);
     return;
   }
-  PagedWalker<false> walk(args);
-  const PagedCut cuts[1] = {paged_cut_all(args.g.G, ROWS)};
+  const PagedCut cuts[1] = {paged_cut_small(args.g.G, ROWS)};
+  PagedWalker<1> walk(args, cuts);
   // Workers of different SMs first, so that a short batch has the whole card.
   const auto role = [&](const long long (&)[1]) {
-    return PagedRole{0, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kSmallWarps * static_cast<int>(gridDim.x),
+    return PagedRole{0, 0, warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), kSmallWarps * static_cast<int>(gridDim.x),
                      kSmallMinUnits, 0, kSmallRows};
   };
-  if (walk.start(reinterpret_cast<long long*>(smem + SM::offSums), cuts, role))
+  if (walk.start(reinterpret_cast<long long*>(smem + SM::offSums), kSmallWarps, role))
     small_worker<SmallRows<T, D, ROWS>, D>(smem, warp, tm_k, tm_v, walk);
 }
 

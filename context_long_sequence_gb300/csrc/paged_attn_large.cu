@@ -122,18 +122,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg);
-  PagedWalker<true> walk(args);
-  const PagedCut cuts[3] = {paged_cut_beside(g.G, kCutBeside), paged_cut_large(g.G), paged_cut_beside(g.G, kCutLight)};
+  const PagedCut cuts[2] = {paged_cut_small(g.G, kBesideRows), paged_cut_large(g.G)};
+  PagedWalker<kUnitSums> walk(args, cuts);
   int large = 0;  // CTAs that take the entries of many rows
-  const auto role = [&](const long long (&units)[3]) {
+  const auto role = [&](const long long (&units)[kUnitSums]) {
     const int ctas = gridDim.x, b = blockIdx.x;
-    if (paged_is_light(units[2], ctas)) return PagedRole{2, warp * ctas + b, kSmallWarps * ctas, kSmallMinUnits, 0, kSmallRows};
-    large = paged_large_ctas(units[0], units[1], ctas);
-    return b < large ? PagedRole{1, b, large, 1, static_cast<int>(args.rows_small), kLargeRows}
-                     : PagedRole{0, warp * (ctas - large) + b - large, kSmallWarps * (ctas - large), kSmallMinUnits, 0, kSmallRows};
+    const bool light = paged_is_light(units[kUnitsLight], ctas);
+    if (!light) large = paged_large_ctas(units[kUnitsBeside], units[kUnitsLarge], ctas);
+    return b < large ? PagedRole{kUnitsLarge, 1, b, large, 1, static_cast<int>(args.rows_small), kLargeRows}
+                     : PagedRole{light ? kUnitsLight : kUnitsBeside, 0, warp * (ctas - large) + b - large,
+                                 kSmallWarps * (ctas - large), kSmallMinUnits, 0, kSmallRows};
   };
   // The sums lie behind the small workers' stages, and where V will be for the large.
-  const bool any = walk.start(reinterpret_cast<long long*>(smem + SmallSmem<D>::offSums), cuts, role);
+  const bool any = walk.start(reinterpret_cast<long long*>(smem + SmallSmem<D>::offSums), kThreads / 32, role);
   if (static_cast<int>(blockIdx.x) >= large) {
     // Entries of few rows: a warp each, eight of the ten.
     if (warp < kSmallWarps && any) {
