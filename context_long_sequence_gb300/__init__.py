@@ -459,7 +459,12 @@ class PagedPlan:
         self.max_seqs, self.max_tokens, self.max_new = desc.max_seqs, desc.max_tokens, desc.max_new
         self.max_pages, self.max_prefixes, self.max_prefix_pages = desc.max_pages, desc.max_prefixes, desc.max_prefix_pages
         self.out_fp32 = bool(out_fp32)
+        self.lse_dtype = torch.float32
         self.o_dtype = torch.float32 if out_fp32 else dtype
+        self.page = (desc.page_size, desc.Hkv, desc.d, dtype)
+        # A decode step's calls take the host about as long as the GPU: torch's
+        # functions that they need are looked up once.
+        self._current = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     @property
     def handle(self):
@@ -494,7 +499,7 @@ class PagedCache:
         if k.dim() != 4 or k.shape != v.shape or strides[0] != strides[1] or k.dtype != v.dtype or k.device != v.device \
                 or k.stride(3) != 1:
             _refuse("PagedCache", "k and v are [pages][page_size][Hkv][d] tensors alike, the last dimension contiguous")
-        self.k, self.v, self.device = k, v, k.device
+        self.k, self.v, self.device, self._dev = k, v, k.device, k.get_device()
         self.page = (k.shape[1], k.shape[2], k.shape[3], k.dtype)
         self.c = cp_paged_cache_t(k.data_ptr(), v.data_ptr(), k.shape[0], *strides[0][:3])
         self.ref = ctypes.addressof(self.c)
@@ -509,7 +514,7 @@ class PagedBatch:
         import torch
         self.n_seqs, self.n_tokens = kv_len.shape[0], int(n_tokens)
         self.n_prefixes = 0 if prefix_len is None else prefix_len.shape[0]
-        self.device = q_start.device
+        self.device, self._dev = q_start.device, q_start.get_device()
         self.max_pages = page_table.shape[1] if page_table.dim() == 2 else -1
         self.max_prefix_pages = prefix_table.shape[1] if prefix_table is not None and prefix_table.dim() == 2 else 0
         want = [(q_start, (self.n_seqs + 1,)), (kv_len, (self.n_seqs,)), (page_table, (self.n_seqs, self.max_pages)),
@@ -534,31 +539,33 @@ class PagedBatch:
 def _paged_stream(where, plan, cache, batch, stream):
     """The checks that need the tensors' shapes, types and devices (the
     library sees addresses); the stream the call goes to."""
-    if cache.page != (plan.page_size, plan.Hkv, plan.d, plan.dtype):
-        _refuse(where, f"the cache's pages are {cache.page}, the plan's {(plan.page_size, plan.Hkv, plan.d, plan.dtype)}")
+    dev, (current, raw_stream) = cache._dev, plan._current
+    if cache.page == plan.page and batch.max_pages == plan.max_pages and batch._dev == dev and dev >= 0 and current() == dev \
+            and (not batch.n_prefixes or batch.max_prefix_pages == plan.max_prefix_pages):
+        return raw_stream(dev) if stream is None else _stream(stream)
+    if cache.page != plan.page:
+        _refuse(where, f"the cache's pages are {cache.page}, the plan's {plan.page}")
     if batch.max_pages != plan.max_pages or (batch.n_prefixes and batch.max_prefix_pages != plan.max_prefix_pages):
         _refuse(where, "the page tables' columns differ from the plan's")
-    if batch.device != cache.device:
+    if batch._dev != dev:
         _refuse(where, f"the batch is on {batch.device}, the cache on {cache.device}")
-    import torch
-    if cache.device.type != "cuda" or cache.device.index != torch._C._cuda_getDevice():
-        _refuse(where, f"the tensors are on {cache.device}, which is not the current device")
-    return _stream(stream)
+    _refuse(where, f"the tensors are on {cache.device}, which is not the current device")
 
 
-def _tokens(where, name, x, n, heads, plan, device):
-    """Address and token stride of a [n_tokens][heads][d] tensor."""
+def _tokens(where, name, x, n, heads, plan, dev):
+    """Address and token stride of a [n_tokens][heads][d] tensor on device
+    number `dev`."""
     s, d = x.stride(), plan.d
-    if x.shape != (n, heads, d) or x.dtype != plan.dtype or s[2] != 1 or (heads > 1 and s[1] != d) or x.device != device:
-        _refuse(where, f"{name} is [{n}][{heads}][{d}] {plan.dtype} with contiguous heads on {device}, got "
-                       f"{x.dtype} {tuple(x.shape)} with strides {s} on {x.device}")
-    return x.data_ptr(), s[0] if n > 1 else heads * d
+    if x.shape == (n, heads, d) and x.dtype is plan.dtype and s[2] == 1 and (s[1] == d or heads == 1) and x.get_device() == dev:
+        return x.data_ptr(), s[0] if n > 1 else heads * d
+    _refuse(where, f"{name} is [{n}][{heads}][{d}] {plan.dtype} with contiguous heads on cuda:{dev}, got "
+                   f"{x.dtype} {tuple(x.shape)} with strides {s} on {x.device}")
 
 
 def cp_cache_append(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, k, v, q_out=None, stream=None):
     where = "cp_cache_append"
     st = _paged_stream(where, plan, cache, batch, stream)
-    n, dev = batch.n_tokens, cache.device
+    n, dev = batch.n_tokens, cache._dev
     qa = oa = (None, 0)
     if q is not None:
         if q_out is None:
@@ -573,19 +580,18 @@ def cp_cache_append(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, k,
 
 
 def cp_attn_paged(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, o, lse, workspace=None, stream=None):
-    import torch
     where = "cp_attn_paged"
     st = _paged_stream(where, plan, cache, batch, stream)
-    n, dev = batch.n_tokens, cache.device
+    n, dev = batch.n_tokens, cache._dev
     qa = _tokens(where, "q", q, n, plan.Hq, plan, dev)
-    if o.shape != (n, plan.Hq, plan.d) or o.dtype != plan.o_dtype or not o.is_contiguous() or o.device != dev:
-        _refuse(where, f"o is a contiguous [{n}][{plan.Hq}][{plan.d}] {plan.o_dtype} on {dev}")
-    if lse.shape != (plan.Hq, n) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
-        _refuse(where, f"lse is a contiguous [{plan.Hq}][{n}] float32 on {dev}")
+    if o.shape != (n, plan.Hq, plan.d) or o.dtype != plan.o_dtype or not o.is_contiguous() or o.get_device() != dev:
+        _refuse(where, f"o is a contiguous [{n}][{plan.Hq}][{plan.d}] {plan.o_dtype} on cuda:{dev}")
+    if lse.shape != (plan.Hq, n) or lse.dtype is not plan.lse_dtype or not lse.is_contiguous() or lse.get_device() != dev:
+        _refuse(where, f"lse is a contiguous [{plan.Hq}][{n}] float32 on cuda:{dev}")
     wa = wn = 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            _refuse(where, f"the workspace is a contiguous tensor on {dev}")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(where, f"the workspace is a contiguous tensor on cuda:{dev}")
         wa, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), wa, wn, st)
     if rc != CP_OK:

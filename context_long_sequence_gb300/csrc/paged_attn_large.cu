@@ -115,6 +115,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::offMisc + 4);
   volatile uint32_t* mask = reinterpret_cast<volatile uint32_t*>(smem + SM::offMisc + 8);
+  if (threadIdx.x == kThreads - 32) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_k16);
+    tma_prefetch_desc(&tm_v16);
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (s0 & 1023) {  // the swizzle is a function of the address
@@ -138,11 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (static_cast<int>(blockIdx.x) >= large) {
     // Entries of few rows: a warp each, eight of the ten.
     if (warp < kSmallWarps && any) {
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_k16);
-        tma_prefetch_desc(&tm_v16);
-        small_init<D>(smem, warp);
-      }
+      if (lane == 0) small_init<D>(smem, warp);
       __syncwarp();
       small_worker<SmallColumns<T, D>, D>(smem, warp, tm_k16, tm_v16, walk);
     }
@@ -153,8 +155,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t box_all = (1u << (BN / box_rows)) - 1;
 
   if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
     mbar_init(bar(BAR_Q), 8);
     for (int i = 0; i < kTileBars; ++i) mbar_init(bar(BAR_T_FULL + i), 1);
     for (int i = 0; i < kSlots; ++i) mbar_init(bar(BAR_KV_EMPTY + i), 1);
