@@ -1,6 +1,6 @@
 // paged_attn_large.cu -- attention over the paged cache for batches with
-// entries of many rows: a prefix with the rows of all its sequences, or a sequence with a
-// chunk of new tokens.
+// entries of many rows: a prefix with the rows of all its sequences, or a
+// sequence with a chunk of new tokens.
 //
 // Rows are (token, query head of the KV head) pairs, token by token; a token
 // tile holds two blocks of up to 128 rows, whole tokens each, that share
@@ -18,12 +18,24 @@
 // out, and the runs' (O, LSE) are merged.  K and V come page by page.
 //
 // At 256 rows a 128-key tile is 256 flops a byte, the card's own balance:
-// fewer rows are bound by the cache's bytes, more by the tensor core.
+// fewer rows are bound by the cache's bytes, more by the tensor core.  A tile
+// of 256 rows takes 2750 clocks, 2165 of them the MMAs'.  Measured (32 query
+// heads on 8, d = 128): chunks of up to 2K tokens after up to 14K keys, 569
+// GFLOP in 382 us, 1.49 PFLOP/s (tensor pipe 66 % active; the rest is the
+// softmax's share of a tile and the change from one segment to the next); 64
+// sequences on a prefix of 32K keys, 274 MB and 35 GFLOP in 52 us of the
+// kernel's own 60 with the merge: the first tile's rows are done 11 us in (the
+// shares 3, the segment 2, Q, K and S 4, its exponentials 2, all of them code
+// that comes from L2 once), and tiles follow every 1.4 us.
+//
+// Rows leave through shared memory: as TMA boxes of 32 rows where they lie
+// together, else as lines of 128 bytes (256 sequences on prefixes 98.8 us with
+// lines alone, 95.3 with boxes).
 //
 // A batch's entries of few rows are taken by other CTAs of the same launch
-// (paged_small.cuh, eight workers a CTA), in proportion to their work: one
-// kernel bound by the tensor core and one by the cache's bytes share the card
-// better side by side than one after the other.
+// (paged_small.cuh, eight workers a CTA), in proportion to their work
+// (paged_large_ctas): work bound by the tensor core and work bound by the
+// cache's bytes share the card better side by side than one after the other.
 //
 // Warps (320 threads): 0 fetches, 1 issues the MMAs (and holds the TMEM),
 // 2..5 and 6..9 load Q, take the softmax and write the rows of block 0 and 1.

@@ -2,12 +2,19 @@
 // (a decode step, short drafts), by single warps.
 //
 // Bound by reading the cache: at 16 rows a key's 4 d bytes take 64 d flops.
-// A warp is a worker of its own: it fetches its 16-key tiles (TMA boxes,
-// 128-byte swizzle) into a ring of stages, multiplies with mma.sync (8 rows at
-// a time, where tcgen05 would waste 120 of 128) and writes its part.  Nothing is
-// shared between warps, so none waits for another, and the eight of an SM hide
-// each other's latencies; the many parts cost little to merge, a row of d
-// floats each for few rows.
+// A warp is a worker of its own: it fetches its 16-key tiles (one TMA box each
+// for K and V, 128-byte swizzle) into a ring of stages, multiplies with
+// mma.sync (8 rows at a time, where tcgen05 would waste 120 of 128) and writes
+// its part.  Nothing is shared between warps, so none waits for another, and
+// the eight of an SM hide each other's latencies; the many parts cost little
+// to merge, a row of d floats each for few rows.
+//
+// Measured (32 query heads on 8 of d = 128, keys of one step): 64 sequences of
+// up to 16K keys, 2.16 GB from DRAM in 324 us, 6.65 TB/s; a sequence of 2^20
+// keys 4.3 GB in 636 us, 6.75 TB/s.  An SM by itself reads 112 GB/s: 79 with a
+// copy for each 64 columns, 87 with one a tile and rows as the MMA's rows.
+// With few keys the time is latency: 1000 keys of one sequence, 7.5 us with
+// the merge, most of it instructions that come from L2 once.
 #pragma once
 #include <type_traits>
 
@@ -238,7 +245,10 @@ struct SmallColumns {
   }
 };
 
-// Up to 16 NB rows, as the MMAs' rows: S = Q K^T, O = P V.
+// Up to 16 NB rows, as the MMAs' rows: S = Q K^T, O = P V.  NB = 2 at d = 64
+// only: at d = 128 its registers spill (PagedCut).  24 sequences of 20 rows on
+// 16K keys, d = 64: 75.7 us (5.2 TB/s) with NB = 2, 122 with two tiles of NB =
+// 1, that read the keys twice.
 template <typename T, int D, int NB>
 struct SmallBlocks {
   static constexpr int kRows = 16 * NB;
