@@ -34,8 +34,7 @@ struct SmallSmem {
   static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, three cuts
   static constexpr int offBar = offSums + 3 * kMaxEntries / 32 * 8;
   static constexpr int offSeg = offBar + kSmallWarps * kStages * 8;
-  static constexpr int offHeld = offSeg + kSmallWarps * kSegs * static_cast<int>(sizeof(PagedSegment));
-  static constexpr int kBytes = offHeld + kSmallWarps * kStages * 4;  // held: whether the stage's page was fetched
+  static constexpr int kBytes = offSeg + kSmallWarps * kSegs * static_cast<int>(sizeof(PagedSegment));
 };
 
 template <typename T>
@@ -410,11 +409,11 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
   const PagedGeom& g = args.g;
   int32_t* status = args.status;
   PagedSegment* segs = reinterpret_cast<PagedSegment*>(smem + SM::offSeg) + warp * SM::kSegs;
-  volatile int* held = reinterpret_cast<volatile int*>(smem + SM::offHeld) + warp * S;
 
   // ---- Fetching, S tiles ahead of the computing.
   const uint64_t policy = read_once_policy();
-  int f_seg = 0, f_n = 0;              // segments walked, tiles fetched
+  int f_seg = 0, f_n = 0, f_st = 0;    // segments walked, tiles fetched, the next one's stage
+  uint32_t held = 0;                   // stages whose page was fetched
   int f_tile = 0, f_end = 0, f_h = 0;  // of the segment being fetched
   int f_pages = -1, f_next = -1;       // lane: page of tile (f_tile & ~31) + lane, and of the 32 after
   bool f_more = true;
@@ -438,12 +437,12 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
       f_pages = f_next;
       f_next = pages_of(f_tile + 32 + lane);
     }
-    const int page = __shfl_sync(kAll, f_pages, f_tile & 31), st = f_n % S;
+    const int page = __shfl_sync(kAll, f_pages, f_tile & 31);
     const bool there = page >= 0 && page < g.num_pages;
+    held = (held & ~(1u << f_st)) | (there ? 1u << f_st : 0u);
     if (lane == 0) {
-      const uint32_t full = full0 + 8u * st, dst = s0 + st * 2 * SM::kKV;
+      const uint32_t full = full0 + 8u * f_st, dst = s0 + f_st * 2 * SM::kKV;
       const int row = (f_tile * 16) & ((1 << g.page_shift) - 1);
-      held[st] = there;
       mbar_arrive_expect_tx(full, there ? 2 * SM::kKV : 0);
       if (CP_CHECK_DATA(there, status)) {
         tma_load_5d(dst, &tm_k, full, 0, row, 0, f_h, page, policy);
@@ -451,6 +450,7 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
       }
     }
     __syncwarp();
+    f_st = f_st + 1 == S ? 0 : f_st + 1;
     ++f_n;
     ++f_tile;
   };
@@ -460,7 +460,8 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
   // ---- Computing.
   const float sl2 = g.scale * 1.4426950408889634f;
   Rows rows(s0, s0 + SM::kKV, g.G);
-  int n = 0;
+  int n = 0, st = 0;    // tiles computed, the next one's stage
+  uint32_t phase = 0;
   bool ok = true;
 #pragma unroll 1
   for (int c_seg = 0; ok; ++c_seg) {
@@ -470,10 +471,10 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
     rows.begin(args, seg);
 #pragma unroll 1
     for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++n) {
-      const int st = n % S, key0 = tile * 16;
-      ok = __all_sync(kAll, mbar_wait_short(full0 + 8u * st, (n / S) & 1, nullptr, status));
+      const int key0 = tile * 16;
+      ok = __all_sync(kAll, mbar_wait_short(full0 + 8u * st, phase, nullptr, status));
       if (!ok) break;
-      const bool there = held[st], clean = there && key0 + 16 <= lim_all;
+      const bool there = (held >> st) & 1u, clean = there && key0 + 16 <= lim_all;
       uint32_t keep[2] = {kAll, kAll};
       if (!clean) {
         // What lies behind the last key may be anything, NaN included: 0 * NaN
@@ -484,6 +485,8 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
       }
       rows.tile(st * 2 * SM::kKV, key0, there, clean, keep, sl2);
       __syncwarp();  // the stage is read: the next tile may land on it
+      st = st + 1 == S ? 0 : st + 1;
+      phase ^= st == 0;
       fetch();
     }
     if (!ok) break;

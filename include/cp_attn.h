@@ -433,6 +433,7 @@ int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const
  *   q [n_tokens][Hq][d], tokens q_stride elements apart (a multiple of 8);
  *   o [n_tokens][Hq][d] out (fp32 if out_fp32), contiguous;
  *   lse [Hq][n_tokens] fp32 out (natural log); (0, -inf) for a row that sees no key.
+ * o, lse and the workspace overlap neither each other nor the inputs.
  * Keys behind a sequence's or a prefix's length are never part of the
  * result, whatever their page holds.  A key below kv_len that the causal mask
  * hides from some rows of its sequence must be finite.
