@@ -62,10 +62,12 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 // O = sum_p 2^(lse_p - m) O_p / sum_p 2^(lse_p - m) over a row's parts, its own
 // keys' first, then its prefix's, in key order; rows whose only part went
 // straight to the output are left alone.  What it reads is small and in L2, so
-// its time is latency: eight loads of 16 bytes a lane are in flight.
+// its time is latency: eight loads of 16 bytes a lane are in flight, or ten.
 //   kMergeBlock  a block per (token, query head), its warps share the parts:
 //                few rows, many parts (a decode of one sequence 9.7 us without,
-//                8.0 with; 7 sequences on a prefix 27.9 and 22.0).
+//                8.0 with; 20 sequences on a prefix of 30K keys, 640 rows, 39.8
+//                and 37.0).  Ten parts a warp at a time: 7 sequences on a
+//                prefix 13.7 us, 14.4 with eight, 13.9 with sixteen.
 //   kMergeHead   a warp per (token, query head), eight parts at a time (24
 //                drafts of 5 tokens 27.3 us without, 21.0 with; 64 sequences on
 //                a prefix 64.8 and 60.5).
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 enum MergeBy { kMergeBlock, kMergeHead, kMergeGroup, kMergeToken };
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBlocks = 152 * 12;  // at most; they loop
-constexpr long long kMergeBlockRows = 608;                         // (token, query head)s up to which BY is kMergeBlock,
+constexpr long long kMergeBlockRows = 1216;                        // (token, query head)s up to which BY is kMergeBlock,
 constexpr long long kMergeHeadGroups = 1216, kMergeGroups = 8192;  // (token, KV head)s: kMergeHead, kMergeGroup
 
 // Join the parts `a` (own keys) and `b` (prefix) of token t's query heads
@@ -86,7 +88,7 @@ constexpr long long kMergeHeadGroups = 1216, kMergeGroups = 8192;  // (token, KV
 template <typename T, int D, MergeBy BY>
 __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const PagedParts& a, const PagedParts& b, int t, int hk,
                                            int h0, int h1, float (*joint)[32][D / 32 + 2]) {
-  constexpr int E = D / 32, HB = BY >= kMergeGroup ? 4 : 1, PB = 8 / HB;  // heads and parts at a time
+  constexpr int E = D / 32, HB = BY >= kMergeGroup ? 4 : 1, PB = BY == kMergeBlock ? 10 : 8 / HB;  // heads and parts at a time
   constexpr int step = BY == kMergeBlock ? kMergeWarps : 1;               // between a warp's parts
   using Vec = typename std::conditional<E == 4, float4, float2>::type;
   const PagedGeom& g = args.g;
