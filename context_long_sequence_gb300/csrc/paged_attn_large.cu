@@ -24,7 +24,7 @@
 // GFLOP in 382 us, 1.49 PFLOP/s (tensor pipe 66 % active; the rest is the
 // softmax's share of a tile and the change from one segment to the next); 64
 // sequences on a prefix of 32K keys, 274 MB and 35 GFLOP in 52 us of the
-// kernel's own 60 with the merge: the first tile's rows are done 11 us in (the
+// kernel's own, 59 with the merge: the first tile's rows are done 11 us in (the
 // shares 3, the segment 2, Q, K and S 4, its exponentials 2, all of them code
 // that comes from L2 once), and tiles follow every 1.4 us.
 //
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (!any) return;  // the whole block
   const int block_tokens = cuts[1].tile_tokens / 2;
-  const uint32_t box_all = (1u << (BN / box_rows)) - 1;
+  const uint32_t box_all = 0xffffffffu >> (32 - 2 * NH * (BN / box_rows));  // every box of a tile held
 
   if (threadIdx.x == 0) {
     mbar_init(bar(BAR_Q), 8);
@@ -224,17 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++nt) {
         const int ahead = page_of(tile + 1);
         const int n = 2 * nt, slk = n % kSlots, slv = (n + 1) % kSlots;
-        ok = warp_all(mbar_wait(bar(BAR_KV_EMPTY + slk), ((n / kSlots) & 1) ^ 1, abort_flag, status) &&
-                      mbar_wait(bar(BAR_KV_EMPTY + slv), (((n + 1) / kSlots) & 1) ^ 1, abort_flag, status));
+        ok = warp_all(mbar_wait_short(bar(BAR_KV_EMPTY + slk), ((n / kSlots) & 1) ^ 1, abort_flag, status) &&
+                      mbar_wait_short(bar(BAR_KV_EMPTY + slv), (((n + 1) / kSlots) & 1) ^ 1, abort_flag, status));
         if (!ok) break;
         const uint32_t tb = bar(BAR_T_FULL + nt % kTileBars);
         bool load = page != -2;
         if (load && !CP_CHECK_DATA(page >= 0 && page < g.num_pages, status)) load = false;
         const uint32_t all = __ballot_sync(0xffffffffu, load);
         if (lane == 0) {
-          uint32_t held = 0;
-          for (int b = 0; b < boxes; ++b) held |= ((all >> (2 * NH * b)) & 1u) << b;
-          mask[nt % kTileBars] = held;
+          mask[nt % kTileBars] = all;  // 2 NH bits a box
           mbar_arrive_expect_tx(tb, __popc(all) * box_rows * 128);
         }
         __syncwarp();
@@ -378,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (held != box_all || key0 + BN > seg.keys) {
           // V rows behind the last key (or in a page that was not fetched) may
           // hold anything, NaN included; a zero weight does not remove a NaN.
-          if (!((held >> (row >> box_shift)) & 1u) || key0 + row >= seg.keys) {
+          if (!((held >> ((row >> box_shift) * 2 * NH)) & 1u) || key0 + row >= seg.keys) {
             const uint32_t v = sKV + ((2 * j + 1) % kSlots) * SM::kKV + row * 128;
 #pragma unroll 1
             for (int b = 0; b < 8 * NH; ++b) st_shared_v4(v + (b >> 3) * HALF_BYTES + (b & 7) * 16, 0u, 0u, 0u, 0u);
@@ -412,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!full) {
                 // Hidden keys become -inf in S.  Boxes are 16 keys or more:
                 // two bits cover 32 columns.
-                const uint32_t in0 = (held >> ((c * 32) >> box_shift)) & 1u, in1 = (held >> ((c * 32 + 16) >> box_shift)) & 1u;
+                const uint32_t in0 = (held >> (((c * 32) >> box_shift) * 2 * NH)) & 1u, in1 = (held >> (((c * 32 + 16) >> box_shift) * 2 * NH)) & 1u;
                 const int left = my_lim - key0 - c * 32;
                 const int n0 = in0 ? left : 0, n1 = in1 ? left : 0;
 #pragma unroll
