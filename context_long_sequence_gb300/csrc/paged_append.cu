@@ -11,7 +11,7 @@
 //
 // Bound by memory: every new row is read once and written once (16K tokens of
 // 32 + 2 x 8 heads of 128: 403 MB in 62.4 us, 6.45 TB/s), and for few tokens
-// by the launch (2.9 us in a graph).  A warp owns one token (or a share of its
+// by the launch (3.3 us in a graph).  A warp owns one token (or a share of its
 // heads): a lane holds 16 elements of a head, two 16-byte pieces that hold
 // both halves of eight pairs, so its eight sines and cosines serve every head
 // it visits; four groups of heads are loaded before the first is stored.
