@@ -31,7 +31,7 @@ struct SmallSmem {
   // Segments known: those of the tiles in flight (a segment may be one tile)
   // and the end mark.
   static constexpr int kSegs = kStages + 1;
-  static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, three cuts
+  static constexpr int offSums = kSmallWarps * kWarp;    // the walker's window sums, three a window
   static constexpr int offBar = offSums + 3 * kMaxEntries / 32 * 8;
   static constexpr int offSeg = offBar + kSmallWarps * kStages * 8;
   static constexpr int kBytes = offSeg + kSmallWarps * kSegs * static_cast<int>(sizeof(PagedSegment));
