@@ -81,8 +81,13 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   if (g.positions) {
     pos = g.positions[t];
   } else if (args.rope_dim > 0) {
-    const int p = warp_prefix_of(g, s);  // by the whole warp, the lanes behind rope_dim too
-    if (p >= 0) pos += g.prefix_len[p];
+    // Looked up by the whole warp, the lanes behind rope_dim too.  A bad prefix,
+    // or one whose rows this is not among, is none: as in the attention.
+    const int p = warp_prefix_of(g, s);
+    if (p >= 0) {
+      const PagedEntry pre = paged_entry(g, g.B + p);
+      if (CP_CHECK_DATA(!pre.bad, args.status) && t >= pre.t0 && t < pre.t0 + pre.n) pos += pre.keys;
+    }
   }
   if (rotated) {
 #pragma unroll

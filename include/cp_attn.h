@@ -347,6 +347,9 @@ int cp_merge_lse(int n_parts, int rows, int H, int d, const float *o_parts,
  * likewise (its sequences then attend to their own keys alone), and keys in a
  * page outside [0, num_pages) are neither read nor written and take no part
  * in the softmax; each is recorded as CP_ERR_DEVICE_BOUNDS (cp_get_status).
+ * cp_cache_append looks at a prefix where it places a rotation by it (rope_dim
+ * > 0, positions null); the tokens behind a bad one are placed by their own keys
+ * alone, as cp_attn_paged attends to them.
  * Rows behind q_start[n_seqs] (a padded batch) stay as they were; a batch
  * without sequences or rows is no work, whatever the tensors.
  * These arrays need only 4-byte alignment. */
@@ -401,7 +404,8 @@ typedef struct {
   const int32_t *prefix_len;   /* [n_prefixes] */
   const int32_t *prefix_table; /* [n_prefixes][max_prefix_pages] */
   const int32_t *positions;    /* [n_tokens] or null: where cp_cache_append's rotation places the token;
-                                  null => prefix_len + its place among the sequence's own keys */
+                                  null => prefix_len (0 without a prefix, or with a bad one) + its place among
+                                  the sequence's own keys */
 } cp_paged_batch_t;
 
 typedef struct cp_paged cp_paged_t; /* opaque; immutable after creation; usable from any stream */

@@ -1,0 +1,80 @@
+"""What the paged-cache operators make of the data they are given: prefixes
+and pages that are not there, and frequencies of every size at far positions."""
+import math
+import os
+import sys
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(__file__))
+
+pytestmark = pytest.mark.gpu
+
+import paged_ref  # noqa: E402
+from paged_ref import Batch, check_attention  # noqa: E402
+from test_gpu_paged import check_append, run_append  # noqa: E402
+from test_gpu_paged_use import ints, outputs  # noqa: E402
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def cpa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import context_long_sequence_gb300 as m
+    return m
+
+
+# prefix_first, prefix_len and the keys that a bad prefix leaves to each of
+# four sequences of a batch with prefixes of 77 and 500 keys.
+BAD_PREFIXES = {
+    "negative": ([0, 2, 3], [-7, 500], [0, 0, 500, 0]),
+    "too_long": ([0, 2, 3], [77, 10 ** 9], [77, 77, 0, 0]),
+    "longest_int": ([0, 2, 3], [2 ** 31 - 1, 500], [0, 0, 500, 0]),
+    "backwards": ([0, 3, 1], [77, 500], [77, 0, 0, 0]),       # 1 and 2 fall to a prefix of 3 .. 1
+    "behind_the_batch": ([0, 2, 9], [77, 500], [77, 77, 0, 0]),
+    "before_the_batch": ([-1, 2, 3], [77, 500], [0, 0, 500, 0]),
+}
+
+
+@pytest.mark.parametrize("name", list(BAD_PREFIXES))
+def test_append_beside_a_bad_prefix(cpa, name):
+    """The sequences of a bad prefix have their own keys alone, in the append
+    as in the attention: their tokens are turned by their own places, the
+    others' as ever, and both calls record it."""
+    first, plen, before = BAD_PREFIXES[name]
+    kw = dict(past=[2, 0, 9, 4], new=[1, 2, 1, 1], prefixes=[(2, 77), (1, 500)], d=64, Hq=4, Hkv=2)
+    b = Batch(seed=21, appended=False, **kw)
+    freqs = 10000.0 ** (-2.0 * np.arange(32) / 64)
+    plan = b.plan(cpa, rope_dim=64)
+    cache, _, q, k, v = b.to_gpu(cpa)
+    batch = cpa.PagedBatch(ints(b.start), ints(b.kv), ints(b.page_table), n_tokens=b.N, prefix_first=ints(first),
+                           prefix_len=ints(plen), prefix_table=ints(b.prefix_table))
+    q_out, (o, lse) = torch.full((b.N, 4, 64), float("nan"), dtype=BF, device="cuda"), outputs(plan, b.N)
+    cpa.cp_cache_append(plan, cache, batch, q, k, v, q_out)
+    rec = cpa.cp_get_status_detail()
+    assert rec[0] == cpa.CP_ERR_DEVICE_BOUNDS and rec[3] == 6
+    positions = np.concatenate([before[s] + b.past[s] + np.arange(b.new[s]) for s in range(4)])
+    check_append(b, q_out, cache, 64, False, freqs, positions)
+    cpa.cp_attn_paged(plan, cache, batch, q_out, o, lse, cpa.alloc_paged_workspace(plan))
+    rec = cpa.cp_get_status_detail()
+    assert rec[0] == cpa.CP_ERR_DEVICE_BOUNDS and rec[3] == 7
+    b.of = [-1 if n == 0 else [77, 500].index(n) for n in before]
+    ref = b.attention(q=q_out.cpu(), k_cache=cache.k.cpu(), v_cache=cache.v.cpu())
+    check_attention(o, lse, ref, BF, 64, b.N, name)
+
+
+def test_append_with_positions_asks_no_prefix(cpa):
+    """Tokens that are placed by the caller, or not turned, need no prefix."""
+    b = Batch(past=[2, 0], new=[1, 2], prefixes=[(2, 77)], d=64, Hq=4, Hkv=2, seed=22, appended=False)
+    b.plen = [-7]
+    freqs = 10000.0 ** (-2.0 * np.arange(32) / 64)
+    positions = np.array([5, 900, 901])
+    q_out, cache = run_append(cpa, b, positions=positions, rope_dim=64)
+    check_append(b, q_out, cache, 64, False, freqs, positions)
+    run_append(cpa, b, rope_dim=0)
+    assert cpa.cp_get_status_detail()[0] == 0
