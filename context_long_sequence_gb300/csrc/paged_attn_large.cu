@@ -216,9 +216,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++nseg;
       if (seg.nt == 0) break;
       const uint64_t policy = walk.once ? read_once_policy() : read_again_policy();
+      // Whether the lane has a box of the tile, and the page that it is in: any
+      // number, as it stands in the table.
+      auto wants = [&](int tile) { return mine && tile < seg.tile1 && tile * BN + box * box_rows < seg.keys; };
       auto page_of = [&](int tile) {
-        const int key = tile * BN + box * box_rows;
-        return mine && tile < seg.tile1 && key < seg.keys ? walk.table[key >> g.page_shift] : -2;
+        return wants(tile) ? walk.table[(tile * BN + box * box_rows) >> g.page_shift] : 0;
       };
       int page = page_of(seg.tile0);
       for (int tile = seg.tile0; tile < seg.tile1; ++tile, ++nt) {
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       mbar_wait_short(bar(BAR_KV_EMPTY + slv), (((n + 1) / kSlots) & 1) ^ 1, abort_flag, status));
         if (!ok) break;
         const uint32_t tb = bar(BAR_T_FULL + nt % kTileBars);
-        bool load = page != -2;
+        bool load = wants(tile);
         if (load && !CP_CHECK_DATA(page >= 0 && page < g.num_pages, status)) load = false;
         const uint32_t all = __ballot_sync(0xffffffffu, load);
         if (lane == 0) {

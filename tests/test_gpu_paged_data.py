@@ -78,3 +78,38 @@ def test_append_with_positions_asks_no_prefix(cpa):
     check_append(b, q_out, cache, 64, False, freqs, positions)
     run_append(cpa, b, rope_dim=0)
     assert cpa.cp_get_status_detail()[0] == 0
+
+
+WITHOUT_PAGES = {
+    "few_rows": dict(past=[200, 60], new=[1, 1], d=128, Hq=8, Hkv=2),
+    "many_rows": dict(past=[200, 60], new=[30, 1], d=64, Hq=8, Hkv=2),
+    "many_rows_d128": dict(past=[300, 9], new=[70, 5], d=128, Hq=8, Hkv=2, page_size=32),
+    "prefix": dict(past=[3, 4, 5], new=[1, 1, 1], prefixes=[(3, 200)], d=128, Hq=32, Hkv=2),
+}
+
+
+@pytest.mark.parametrize("page", [-1, -2, -3, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("name", list(WITHOUT_PAGES))
+def test_every_page_that_is_not_there_is_recorded(cpa, name, page):
+    """A page number outside the cache takes its keys out of the softmax and is
+    recorded, whatever the number."""
+    b = Batch(seed=23, **WITHOUT_PAGES[name])
+    table = b.prefix_table if b.plen else b.page_table
+    table[0][2] = page
+    plan = b.plan(cpa)
+    cache, batch, q, _, _ = b.to_gpu(cpa)
+    o, lse = outputs(plan, b.N)
+    cpa.cp_attn_paged(plan, cache, batch, q, o, lse, cpa.alloc_paged_workspace(plan))
+    rec = cpa.cp_get_status_detail()
+    assert rec[0] == cpa.CP_ERR_DEVICE_BOUNDS and rec[3] == 7
+    table[0][2] = 0
+    gone = range(2 * b.ps, 3 * b.ps)
+    keys = b.prefix_keys(0) if b.plen else b.keys_of(0)
+    left = [np.delete(x, gone, axis=0) for x in keys]
+    if b.plen:
+        b.prefix_keys = lambda p: left
+    else:
+        full, of = list(b.kv), Batch.keys_of
+        b.kv = [full[0] - b.ps] + full[1:]
+        b.keys_of = lambda s, *a: left if s == 0 else of(b, s, *a)
+    check_attention(o, lse, b.attention(), BF, b.d, b.N, name)
