@@ -95,6 +95,24 @@ int check_tokens(const void* p, int64_t stride, int heads, int d) {
   return aligned(p, 16) ? CP_OK : CP_ERR_ALIGNMENT;
 }
 
+// The fraction of a full circle in x >= 0 turns, in units of 2^-64.
+uint64_t fraction(double x) { return static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64)); }
+
+// f radians as a fraction of a full circle: f / 2 pi = high + low, high the
+// rounded product and low what it leaves out, with 1 / 2 pi to 110 bits.  Off
+// by at most 2^-63 for |f| up to 2^42 (two cuts at 2^-64; the constant and
+// low's rounding stay below |f| 2^-106); f / 2 pi in one double would be off by
+// 2^-54 times itself, which a position of 2^31 makes 10^-5 radians at f = 100.
+uint64_t turns_of(double f) {
+  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;
+  const double x = std::fabs(f);
+  const volatile double product = x * kHigh;  // rounded: never fused with what follows
+  const double high = product, low = std::fma(x, kLow, std::fma(x, kHigh, -high));
+  const uint64_t rest = fraction(std::fabs(low));
+  const uint64_t turns = fraction(high) + (low < 0 ? 0 - rest : rest);
+  return f < 0 ? 0 - turns : turns;
+}
+
 PagedGeom geom(const cp_paged& p, const cp_paged_cache_t& c, const cp_paged_batch_t& b) {
   const cp_paged_desc_t& d = p.desc;
   PagedGeom g;
@@ -161,12 +179,8 @@ int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
   p->desc.rope_freqs = nullptr;
   for (p->page_shift = 0; (1 << p->page_shift) < d.page_size;) ++p->page_shift;
   p->scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.d));
-  for (int j = 0; j < d.rope_dim / 2; ++j) {
-    const double f = d.rope_freqs ? d.rope_freqs[j] : std::pow(d.rope_base, -2.0 * j / d.rope_dim);
-    const double x = std::fabs(f) / 6.283185307179586476925;  // below 2^64 once its whole turns are off
-    const uint64_t turns = static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64));
-    p->turns[j] = f < 0 ? 0 - turns : turns;
-  }
+  for (int j = 0; j < d.rope_dim / 2; ++j)
+    p->turns[j] = turns_of(d.rope_freqs ? d.rope_freqs[j] : std::pow(d.rope_base, -2.0 * j / d.rope_dim));
   *out = p;
   return CP_OK;
 }

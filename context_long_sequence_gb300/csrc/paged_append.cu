@@ -5,9 +5,11 @@
 // theta = pos * f_j: (a cos - b sin, b cos + a sin).  An angle of a far
 // position needs more than fp32: at pos = 10^6, pos * f_0 has an fp32 step of
 // 0.06 rad.  The host therefore gives f_j / 2 pi as a 64-bit binary fraction
-// of a circle; pos * that, modulo 2^64, is the exact fraction of a turn (to
-// pos * 2^-56 turns), one integer product, whose upper 32 bits go to
-// sincospif as a number of half-turns in [-1, 1).
+// of a circle, good to 2^-63 for |f_j| up to 2^42 (turns_of in paged.cu).  pos *
+// that, modulo 2^64, is one integer product, good to pos * 2^-63 turns, 2^-32 at
+// the farthest position; its upper 32 bits, cut at 2^-32 turns and rounded to
+// fp32 (at most 2^-25 half-turns), go to sincospif as a number of half-turns in
+// [-1, 1).  rope_base's f_j is a double itself, off by 2^-53 of it.
 //
 // Bound by memory: every new row is read once and written once (16K tokens of
 // 32 + 2 x 8 heads of 128: 403 MB in 62.4 us, 6.45 TB/s), and for few tokens

@@ -113,3 +113,37 @@ def test_every_page_that_is_not_there_is_recorded(cpa, name, page):
         b.kv = [full[0] - b.ps] + full[1:]
         b.keys_of = lambda s, *a: left if s == 0 else of(b, s, *a)
     check_attention(o, lse, b.attention(), BF, b.d, b.N, name)
+
+
+# pi to 77 decimal places.
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494459230781640628620, 10 ** 77)
+
+
+@pytest.mark.parametrize("far", [1000, 1048575, 2 ** 31 - 40])
+def test_append_far_positions_of_any_frequency(cpa, far):
+    """Angles of frequencies from 1e-30 to 2^40 at far positions, against
+    fractions of a turn in whole numbers.  A pair's share of a turn is held to
+    2^-63 or better (two roundings of 2^-64 each), times the position less than
+    2^-32 of a turn; the bound is check_append's, whose largest part is the
+    conversion to fp32."""
+    b = Batch(past=[5, 100], new=[30, 2], d=128, Hq=4, Hkv=2, dtype=FP, seed=24, appended=False)
+    positions = far + np.arange(b.N)
+    freqs = np.concatenate([np.geomspace(1.0, 1e4, 30), -np.geomspace(1.0, 300.0, 20), np.geomspace(1e4, 2.0 ** 40, 9),
+                            [1e-30, -1e-30, 0.25, 0.5, 2 * math.pi]])
+    q_out, cache = run_append(cpa, b, positions=positions, rope_dim=128, rope_freqs=[float(f) for f in freqs])
+    turns = np.array([[float(Fraction(int(p)) * Fraction(float(f)) / (2 * PI) % 1) for f in freqs] for p in positions])
+    c, s = np.cos(2 * math.pi * turns), np.sin(2 * math.pi * turns)
+    u = paged_ref.HALF_STEP[FP]
+
+    def check(got, x, t):
+        a, z = x[:, :64], x[:, 64:]
+        ref = np.concatenate([a * c[t] - z * s[t], z * c[t] + a * s[t]], axis=1)
+        size = np.tile(np.abs(a) + np.abs(z), (1, 2))
+        err = np.abs(got.double().cpu().numpy() - ref)
+        bound = u * np.abs(ref) + 2.0 ** -21 * size + 2.0 ** -25
+        assert np.all(err <= bound), (t, (err / bound).max(), np.argwhere(err > bound)[:3].tolist())
+    for sq in range(2):
+        for i in range(b.new[sq]):
+            t, at = int(b.start[sq]) + i, b.past[sq] + i
+            check(q_out[t], b.q[t].double().numpy(), t)
+            check(cache.k[int(b.page_table[sq][at // 16]), at % 16], b.k[t].double().numpy(), t)
