@@ -17,9 +17,7 @@
 namespace cpattn {
 
 // File ids of the record.
-enum : int32_t {
-  kTuCpAttn = 1, kTuAttnFwd = 2, kTuAttnBwd = 3, kTuReshard = 4, kTuMerge = 5, kTuPagedAppend = 6, kTuPagedAttn = 7
-};
+enum : int32_t { kTuCpAttn = 1, kTuAttnFwd = 2, kTuAttnBwd = 3, kTuReshard = 4, kTuMerge = 5 };
 
 inline __device__ bool debug_bounds_fail(int32_t* status, int line, int file) {
   if (status && atomicCAS(status, 0, CP_ERR_DEVICE_BOUNDS) == 0) {
