@@ -66,6 +66,18 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 
 __device__ __forceinline__ long long shfl64(long long x, int lane) { return __shfl_sync(0xffffffffu, x, lane); }
 
+// Debug builds (debug.cuh): whether rows of the workspace, tokens and query
+// heads of the batch, and boxes of the cache are there.
+__device__ __forceinline__ bool part_rows_in(const PagedAttnArgs& a, long long row, int n) {
+  return row >= 0 && row + n <= static_cast<long long>(a.rows);
+}
+__device__ __forceinline__ bool token_in(const PagedGeom& g, long long token, int head) {
+  return token >= 0 && token < g.N && head >= 0 && head < g.Hq;
+}
+__device__ __forceinline__ bool cache_box_in(const PagedGeom& g, int row, int rows, int head, int page) {
+  return row >= 0 && row + rows <= 1 << g.page_shift && head >= 0 && head < g.Hkv && page >= 0 && page < g.num_pages;
+}
+
 // A barrier of the block's first `threads` threads.
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -245,7 +257,7 @@ struct PagedWalker {
       if (rec.count > 0) {
         PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
         for (int i = threadIdx.x & 31; i < s.nt; i += 32)
-          parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] =
+          if (CP_IN_BOUNDS(s.t0 >= 0 && s.t0 + i < a.max_tokens && s.h < g.Hkv, a.status)) parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] =
               PagedParts{rec.first + i * rec.first_step, rec.second + i * g.G, rec.count, rec.stride};
       }
       break;

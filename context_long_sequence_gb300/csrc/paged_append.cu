@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
         src = static_cast<const T*>(args.v) + t * args.v_stride + (h - g.Hq - g.Hkv) * D;
         dst[i] = static_cast<T*>(args.v_cache) + row + (h - g.Hq - g.Hkv) * g.head_stride;
       }
+      if (src && !CP_IN_BOUNDS(ea + 8 <= D && eb + 8 <= D && e.t0 + e.n <= g.N, args.status)) src = nullptr, dst[i] = nullptr;
       if (src) {
         a[i] = *reinterpret_cast<const uint4*>(src + ea);
         b[i] = *reinterpret_cast<const uint4*>(src + eb);

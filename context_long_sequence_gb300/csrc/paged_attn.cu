@@ -116,7 +116,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
 #pragma unroll
         for (int h = 0; h < HB; ++h) {
           lse[k][h] = -INFINITY;
-          if (i < n && sub + h < h1) {
+          if (i < n && sub + h < h1 && CP_IN_BOUNDS(part_rows_in(args, row + h, 1), args.status)) {
             lse[k][h] = args.part_lse[row + h];
             v[k][h] = *reinterpret_cast<const Vec*>(args.part_o + (row + h) * D + lane * E);
           }
@@ -172,6 +172,7 @@ __device__ __forceinline__ void join_parts(const PagedAttnArgs& args, const Page
       if (sub + h >= h1) continue;
       const float inv = sum[h] != 0.f ? __fdividef(1.f, sum[h]) : 0.f;
       const int head = hk * g.G + sub + h;
+      if (!CP_IN_BOUNDS(token_in(g, t, head), args.status)) continue;
       const long long at = (static_cast<long long>(t) * g.Hq + head) * D + lane * E;
       if (args.out_fp32) {
         float* dst = static_cast<float*>(args.o) + at;

@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         const int key = tile * BN + box * box_rows;
+        (void)CP_IN_BOUNDS(!load || cache_box_in(g, key & page_mask, box_rows, seg.h, page), status);
         if (load) tma_load_4d(dst0 + (kv ? slv : slk) * SM::kKV, map, tb, half * 64, key & page_mask, seg.h, page, policy);
         page = ahead;
       }
@@ -350,7 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < P; ++n) {
           const int r = n * (32 / P) + lane / P;
           const int i = __shfl_sync(0xffffffffu, tok, r), h = __shfl_sync(0xffffffffu, sub, r);
-          if (r < mine) cp_async16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), q0 + i * args.q_stride + h * D);
+          if (r < mine && CP_IN_BOUNDS(token_in(g, seg.t0 + first + i, seg.h * g.G + h), status))
+            cp_async16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), q0 + i * args.q_stride + h * D);
         }
         cp_async_wait_all();
         fence_proxy_async_smem();
@@ -578,10 +580,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (seg.mode == kRowsSlot)
-              tma_store_2d(&tm_part, stage, c * 32, seg.row + first * g.G + wq * 32);
-            else
-              tma_store_3d(&tm_o, stage, c * 64, seg.h * g.G, seg.t0 + first + wq * 32 / g.G);
+            const int slot_row = seg.row + first * g.G + wq * 32, token = seg.t0 + first + wq * 32 / g.G;
+            if (seg.mode == kRowsSlot) {
+              if (CP_IN_BOUNDS(slot_row >= args.rows_small && slot_row + 32 <= args.rows_large_end, status))
+                tma_store_2d(&tm_part, stage, c * 32, slot_row);
+            } else if (CP_IN_BOUNDS(token_in(g, token, seg.h * g.G) && token_in(g, token + 32 / g.G - 1, seg.h * g.G + g.G - 1), status)) {
+              tma_store_3d(&tm_o, stage, c * 64, seg.h * g.G, token);
+            }
             bulk_commit();
           }
           continue;
@@ -597,17 +602,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < 8; ++n) {
           const int r = n * 4 + (lane >> 3), p = lane & 7;
           const int line = __shfl_sync(0xffffffffu, my_line, r);
-          if (r < mine) *reinterpret_cast<uint4*>(base + static_cast<long long>(line) * row_bytes + c * 128 + p * 16) = y[n];
+          if (r < mine && CP_IN_BOUNDS(final_rows ? tile_row + line < static_cast<long long>(g.N) * g.Hq
+                                       : part_rows_in(args, seg.row + (seg.mode == kRowsHome ? tile_row : first * g.G) + line, 1), status))
+            *reinterpret_cast<uint4*>(base + static_cast<long long>(line) * row_bytes + c * 128 + p * 16) = y[n];
         }
         if (NH == 1) __syncwarp();  // one staging place; with two, the step between orders them
       }
       if (boxes && lane == 0) bulk_wait_read<0>();
-      if (row_valid) {
+      const long long my_row = seg.row + (seg.mode == kRowsHome ? tile_row + my_off : first * g.G + row);
+      if (row_valid && CP_IN_BOUNDS(token_in(g, seg.t0 + first + tok, seg.h * g.G + sub) &&
+                                        (final_rows || part_rows_in(args, my_row, 1)), status)) {
         const float lse2 = l != 0.f ? m + lg2_approx(l) - kBias : -INFINITY;
         if (final_rows)
           args.lse[static_cast<long long>(seg.h * g.G + sub) * g.N + seg.t0 + first + tok] = lse2 * 0.69314718055994531f;
         else
-          args.part_lse[seg.row + (seg.mode == kRowsHome ? tile_row + my_off : first * g.G + row)] = lse2;
+          args.part_lse[my_row] = lse2;
       }
       __syncwarp();      // the staging is read before the next segment's Q lands on it
       tc_fence_before();  // O was read before this warp's next arrival lets a PV overwrite it

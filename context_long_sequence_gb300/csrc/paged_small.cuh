@@ -151,10 +151,11 @@ struct SmallColumns {
     }
     const int i = of.token(r);
     const T* p = static_cast<const T*>(a.q) + (static_cast<long long>(seg.t0) + i) * a.q_stride + (seg.h * G + r - i * G) * D + c2;
+    const bool there = r < rows && CP_IN_BOUNDS(token_in(a.g, seg.t0 + i, seg.h * G + r - i * G), a.status);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      q[k][0] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
-      q[k][1] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
+      q[k][0] = there ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
+      q[k][1] = there ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
     }
@@ -229,6 +230,7 @@ struct SmallColumns {
       const float inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
       const int token = seg.t0 + i, head = seg.h * G + r - i * G;
       const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
+      if (!CP_IN_BOUNDS(token_in(a.g, token, head) && (seg.mode == kRowsFinal || part_rows_in(a, at, 1)), a.status)) continue;
       // Column 8 j + d0.
       if (seg.mode == kRowsFinal && !a.out_fp32) {
         T* dst = static_cast<T*>(a.o) + row * D + d0;
@@ -277,10 +279,11 @@ struct SmallBlocks {
         l[b][y] = 0.f;
         const T* p = static_cast<const T*>(a.q) + (static_cast<long long>(seg.t0) + i) * a.q_stride +
                      (seg.h * G + r - i * G) * D + 2 * (lane & 3);
+        const bool there = r < rows && CP_IN_BOUNDS(token_in(a.g, seg.t0 + i, seg.h * G + r - i * G), a.status);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          q[b][k][y] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
-          q[b][k][2 + y] = r < rows ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
+          q[b][k][y] = there ? *reinterpret_cast<const uint32_t*>(p + k * 16) : 0u;
+          q[b][k][2 + y] = there ? *reinterpret_cast<const uint32_t*>(p + k * 16 + 8) : 0u;
         }
       }
 #pragma unroll
@@ -374,6 +377,7 @@ struct SmallBlocks {
         const float inv = sum != 0.f ? __fdividef(1.f, sum) : 0.f;
         const int token = seg.t0 + i, head = seg.h * G + r - i * G;
         const long long row = static_cast<long long>(token) * a.g.Hq + head, at = seg.row + (seg.mode == kRowsHome ? row : r);
+        if (!CP_IN_BOUNDS(token_in(a.g, token, head) && (seg.mode == kRowsFinal || part_rows_in(a, at, 1)), a.status)) continue;
         if (seg.mode == kRowsFinal && !a.out_fp32) {
           T* dst = static_cast<T*>(a.o) + row * D + 2 * (lane & 3);
 #pragma unroll
@@ -445,6 +449,7 @@ __device__ __forceinline__ void small_worker(uint8_t* smem, int warp, const CUte
       const int row = (f_tile * 16) & ((1 << g.page_shift) - 1);
       mbar_arrive_expect_tx(full, there ? 2 * SM::kKV : 0);
       if (CP_CHECK_DATA(there, status)) {
+        (void)CP_IN_BOUNDS(cache_box_in(g, row, 16, f_h, page), status);
         tma_load_5d(dst, &tm_k, full, 0, row, 0, f_h, page, policy);
         tma_load_5d(dst + SM::kKV, &tm_v, full, 0, row, 0, f_h, page, policy);
       }
