@@ -31,6 +31,7 @@ struct NvtxRange {
 constexpr long long kMaxKeys = 1LL << 30;  // of one page table row; key indices and limits stay in 32 bits
 constexpr long long kMaxRows = 1LL << 30;  // of the workspace's home rows
 constexpr int64_t kMaxStride = 1LL << 36;  // elements; a tensor map takes strides below 2^40 bytes
+constexpr int64_t kMaxSpan = 1LL << 60;    // elements from the cache's first to its last; offsets stay in 64 bits
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -70,8 +71,8 @@ int check_cache(const cp_paged_desc_t& d, const cp_paged_cache_t& c) {
   int64_t span = d.d;
   for (int i = 0; i < 3; ++i) {
     if (n[o[i]] == 1) continue;
-    if (s[o[i]] < span) return CP_ERR_INVALID_ARG;
-    span = s[o[i]] * (n[o[i]] - 1) + span;
+    if (s[o[i]] < span || n[o[i]] - 1 > (kMaxSpan - span) / s[o[i]]) return CP_ERR_INVALID_ARG;
+    span += s[o[i]] * (n[o[i]] - 1);
   }
   return CP_OK;
 }

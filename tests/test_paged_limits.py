@@ -1,0 +1,27 @@
+"""Host-side refusals of the paged-cache ABI at the ends of its ranges (no GPU:
+the checks come before any use of the addresses)."""
+import ctypes
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(__file__))
+
+from test_paged_host import FAKE, c_args, cpa, make_plan  # noqa: E402, F401
+
+
+@pytest.mark.parametrize("cache", [
+    # Strides and counts whose span passes 2^63: (2^31 - 1) pages, 2^35 elements
+    # apart, under tokens that lie 2^35 + 8 apart, overlap.
+    dict(num_pages=2 ** 31 - 1, page_stride=1 << 35, token_stride=(1 << 35) + 8),
+    dict(num_pages=2 ** 31 - 1, page_stride=(1 << 36) - 8, token_stride=(1 << 36) - 8),
+    dict(num_pages=2 ** 31 - 1, page_stride=(1 << 36) - 8),
+])
+def test_cache_spans_that_overflow(cpa, cache):  # noqa: F811
+    plan = make_plan(cpa, rope_dim=128)
+    c, b = c_args(cpa, plan, cache)
+    L, A = cpa._L(), ctypes.addressof
+    assert L.cp_attn_paged(plan.handle, A(c), A(b), FAKE, 1024, FAKE, FAKE, FAKE, plan.workspace_size(), None) == -1
+    assert L.cp_cache_append(plan.handle, A(c), A(b), FAKE, 1024, FAKE, 256, FAKE, 256, FAKE, 1024, None) == -1
