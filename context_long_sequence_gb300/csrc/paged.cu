@@ -160,7 +160,7 @@ int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
   if (d.max_prefixes < 0 || d.max_prefix_pages < 0 || (d.max_prefixes > 0) != (d.max_prefix_pages > 0))
     return CP_ERR_INVALID_ARG;
   if ((d.causal | 1) != 1 || (d.out_fp32 | 1) != 1 || (d.rope_interleaved | 1) != 1) return CP_ERR_INVALID_ARG;
-  if (!(d.softmax_scale >= 0.f) || std::isinf(d.softmax_scale)) return CP_ERR_INVALID_ARG;
+  if (!(d.softmax_scale >= 0.f) || std::isinf(d.softmax_scale * 1.4426950408889634f)) return CP_ERR_INVALID_ARG;  // scores are in log2 units
   if (d.rope_dim < 0 || d.rope_dim > d.d) return CP_ERR_INVALID_ARG;
   if (static_cast<long long>(d.max_pages) * d.page_size >= kMaxKeys ||
       static_cast<long long>(d.max_prefix_pages) * d.page_size >= kMaxKeys ||

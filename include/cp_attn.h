@@ -373,7 +373,7 @@ typedef struct {
   int32_t causal;             /* 1: new token i of n sees the own keys j <= kv_len - n + i;
                                  0: every own key.  Prefixes are seen whole. */
   int32_t out_fp32;           /* 1: o is fp32, unrounded */
-  float softmax_scale;        /* 0 => 1/sqrt(d) */
+  float softmax_scale;        /* 0 => 1/sqrt(d); not negative, and finite times log2(e) */
   int32_t rope_dim;           /* elements of a head turned by cp_cache_append: 0 (none) or a multiple
                                  of 16 up to d, the first of the head */
   int32_t rope_interleaved;   /* 0: pair j is elements (j, j + rope_dim/2); 1: (2j, 2j + 1) */

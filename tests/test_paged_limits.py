@@ -25,3 +25,15 @@ def test_cache_spans_that_overflow(cpa, cache):  # noqa: F811
     L, A = cpa._L(), ctypes.addressof
     assert L.cp_attn_paged(plan.handle, A(c), A(b), FAKE, 1024, FAKE, FAKE, FAKE, plan.workspace_size(), None) == -1
     assert L.cp_cache_append(plan.handle, A(c), A(b), FAKE, 1024, FAKE, 256, FAKE, 256, FAKE, 1024, None) == -1
+
+
+@pytest.mark.parametrize("scale,ok", [(3e38, False), (2.4e38, False), (2.3e38, True), (1e-38, True)])
+def test_softmax_scale_stays_a_number_in_base_2(cpa, scale, ok):  # noqa: F811
+    """The kernels multiply by scale * log2(e) in fp32: one that is infinite
+    makes 0 * inf of a score of 0."""
+    if ok:
+        make_plan(cpa, softmax_scale=scale)
+        return
+    with pytest.raises(cpa.CPError) as e:
+        make_plan(cpa, softmax_scale=scale)
+    assert e.value.code == -1
