@@ -463,8 +463,9 @@ class PagedPlan:
         self.o_dtype = torch.float32 if out_fp32 else dtype
         self.page = (desc.page_size, desc.Hkv, desc.d, dtype)
         # A decode step's calls take the host about as long as the GPU: torch's
-        # functions that they need are looked up once.
-        self._current = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        # functions that they need are looked up once (a torch without CUDA has
+        # none; its tensors are refused before they would be called).
+        self._current = tuple(getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
 
     @property
     def handle(self):

@@ -37,3 +37,18 @@ def test_softmax_scale_stays_a_number_in_base_2(cpa, scale, ok):  # noqa: F811
     with pytest.raises(cpa.CPError) as e:
         make_plan(cpa, softmax_scale=scale)
     assert e.value.code == -1
+
+
+def test_plan_without_cuda_in_torch(cpa, monkeypatch):  # noqa: F811
+    """A plan holds no device memory and is made wherever the library loads; a
+    call on host tensors is refused there too."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    plan = make_plan(cpa)
+    assert plan.workspace_size() > 0
+    k = torch.zeros(10, 16, 2, 128, dtype=torch.bfloat16)
+    i32 = dict(dtype=torch.int32)
+    b = cpa.PagedBatch(torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(1, 100, **i32), n_tokens=1)
+    q = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
+    with pytest.raises(cpa.CPError, match="not the current device"):
+        cpa.cp_attn_paged(plan, cpa.PagedCache(k, k.clone()), b, q, q.clone(), torch.zeros(8, 1))
