@@ -8,7 +8,11 @@
 // sequences (attn_fwd.cu):
 //
 //   S_t = Q_t K^T        tcgen05.mma, operands in shared memory, S in TMEM
-//   online softmax       one thread per row; P_t packed back over S_t
+//   online softmax       one thread per row; P_t packed back over S_t, rounded
+//                        once to the cache's type (its sum is not): what is left
+//                        over as a second operand (split_weights in
+//                        paged_small.cuh) would make three products of two, and
+//                        the tensor core is the bound here
 //   O_t += P_t V         tcgen05.mma with A read from TMEM
 //
 // and the two row blocks ping-pong on the tensor core (issue order QK_0,

@@ -62,6 +62,22 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// A weight in two halves of the cache's type, p = hi + lo, for the product with
+// V (the sum is taken in fp32 before): what is left out is under 2^-16 of it in
+// bf16, 2^-22 in fp16, where one half leaves 2^-8 and 2^-11.  In us, one half
+// and two: 64 sequences of up to 16K keys at 4 query heads a KV head 319 and
+// 320, at 16 336 and 341 (d = 128), 194 and 181 (d = 64); one of 2^20 keys 620
+// and 624: the keys' bytes hide the second product.  At 32 rows (24 sequences of
+// 20 rows on 16K keys, d = 64) the products are the bound, 75 and 84, as they
+// are for CTAs, where the second would be a third of the MMAs: those round a
+// weight once, to half a step of the cache's type.
+template <typename T>
+__device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  hi = Elem<T>::pack(p0, p1);
+  const float2 h = Elem<T>::unpack(hi);
+  lo = Elem<T>::pack(p0 - h.x, p1 - h.y);
+}
+
 // The barriers of warp `warp`, by one lane.
 template <int D>
 __device__ __forceinline__ void small_init(uint8_t* smem, int warp) {
@@ -201,9 +217,13 @@ struct SmallColumns {
     for (int i = 0; i < 4; ++i) p[i] = ex2_approx(fmaf(x[i], sl2, Weight<T>::kBias - (m[i & 1] == -INFINITY ? 0.f : m[i & 1])));
     l[0] += p[0] + p[2];
     l[1] += p[1] + p[3];
-    // The weights are rounded to the cache's type for the product with V;
-    // their sum is not.
-    const uint32_t b0 = movmatrix_trans(Elem<T>::pack(p[0], p[1])), b1 = movmatrix_trans(Elem<T>::pack(p[2], p[3]));
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      split_weights<T>(p[2 * i], p[2 * i + 1], hi[i], lo[i]);
+      hi[i] = movmatrix_trans(hi[i]);
+      lo[i] = movmatrix_trans(lo[i]);
+    }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       uint32_t f[4];
@@ -214,7 +234,8 @@ struct SmallColumns {
         f[2] &= keep[1];
         f[3] &= keep[1];
       }
-      mma16816<T>(o[i], f, b0, b1);
+      mma16816<T>(o[i], f, hi[0], hi[1]);
+      mma16816<T>(o[i], f, lo[0], lo[1]);
     }
   }
 
@@ -310,7 +331,8 @@ struct SmallBlocks {
         mma16816<T>(c[b][k % CH][1], q[b][k], f[2], f[3]);
       }
     }
-    uint32_t pa[NB][4];
+    constexpr bool kTwo = NB == 1;  // halves of a weight (split_weights)
+    uint32_t hi[NB][4], lo[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float x[8];  // first row: 0, 1, 4, 5; second: 2, 3, 6, 7
@@ -343,7 +365,12 @@ struct SmallBlocks {
       l[b][0] += (p[0] + p[1]) + (p[4] + p[5]);
       l[b][1] += (p[2] + p[3]) + (p[6] + p[7]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pa[b][i] = Elem<T>::pack(p[2 * i], p[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (kTwo)
+          split_weights<T>(p[2 * i], p[2 * i + 1], hi[b][i], lo[b][i]);
+        else
+          hi[b][i] = Elem<T>::pack(p[2 * i], p[2 * i + 1]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -357,8 +384,12 @@ struct SmallBlocks {
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        mma16816<T>(o[b][2 * i], pa[b], f[0], f[1]);
-        mma16816<T>(o[b][2 * i + 1], pa[b], f[2], f[3]);
+        mma16816<T>(o[b][2 * i], hi[b], f[0], f[1]);
+        mma16816<T>(o[b][2 * i + 1], hi[b], f[2], f[3]);
+        if constexpr (kTwo) {
+          mma16816<T>(o[b][2 * i], lo[b], f[0], f[1]);
+          mma16816<T>(o[b][2 * i + 1], lo[b], f[2], f[3]);
+        }
       }
     }
   }

@@ -336,7 +336,7 @@ int cp_merge_lse(int n_parts, int rows, int H, int d, const float *o_parts,
  * A context-parallel cache: a rank that holds a share of a sequence's keys
  * runs cp_attn_paged on its share (out_fp32, causal = 0 for a share that
  * lies wholly in the past) and the ranks' (O, LSE) merge with cp_merge_lse,
- * whose layout they have.  causal = 0 also serves cross attention to an
+ * whose layout they have (it writes bf16, whatever the cache's type).  causal = 0 also serves cross attention to an
  * encoder's states held in the pages.
  *
  * The int32 arrays of a batch are read on the device while the kernels run,
@@ -372,7 +372,7 @@ typedef struct {
   int32_t max_prefix_pages;   /* columns of prefix_table (the same bound); 0 if max_prefixes is 0 */
   int32_t causal;             /* 1: new token i of n sees the own keys j <= kv_len - n + i;
                                  0: every own key.  Prefixes are seen whole. */
-  int32_t out_fp32;           /* 1: o is fp32, unrounded */
+  int32_t out_fp32;           /* 1: o is fp32, the normalised accumulator (cp_attn_paged says what is rounded on the way) */
   float softmax_scale;        /* 0 => 1/sqrt(d); not negative, and finite times log2(e) */
   int32_t rope_dim;           /* elements of a head turned by cp_cache_append: 0 (none) or a multiple
                                  of 16 up to d, the first of the head */
@@ -442,6 +442,12 @@ int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const
  * Keys behind a sequence's or a prefix's length are never part of the
  * result, whatever their page holds.  A key below kv_len that the causal mask
  * hides from some rows of its sequence must be finite.
+ * Scores, softmax sums, lse and the sums over keys are fp32.  A weight is a
+ * 16-bit operand of the product with V: rounded once to the cache's type (half
+ * a step, 2^-8 of it in bf16, 2^-11 in fp16) for entries of more than 16 rows
+ * (new tokens x query heads of a KV head; a prefix has the rows of all its
+ * sequences), in two halves (2^-16, 2^-22) for entries of up to 8 and, where no
+ * entry of the batch may have more than 16, of up to 16.
  * Deterministic: no atomics on results; the work is split by the batch's
  * lengths alone.
  * workspace: cp_paged_workspace_size() bytes. */

@@ -160,3 +160,34 @@ def test_ends_of_the_ranges(cpa, name):
     b.k_cache, b.v_cache = b.k_cache.double(), b.v_cache.double()  # once, not a sequence at a time
     check_attention(o, lse, b.attention(), b.dtype, b.d, n, name)
     assert torch.isnan(o[n:]).all() and torch.isnan(lse[:, n:]).all()
+
+
+FEW = {
+    "rows_4": dict(past=[47, 20, 300], new=[1] * 3, Hq=8, Hkv=2),
+    "rows_8_drafts": dict(past=[37, 20], new=[2, 1], Hq=8, Hkv=2),
+    "rows_16": dict(past=[47, 20], new=[1] * 2, Hq=32, Hkv=2),
+    "rows_14_drafts": dict(past=[35, 20], new=[2, 1], Hq=14, Hkv=2),
+    "light_prefix": dict(past=[3, 9, 20], new=[1] * 3, prefixes=[(3, 60)], Hq=32, Hkv=8),
+    "beside_ctas": dict(past=[33] * 300, new=[1] * 300, prefixes=[(1, 90), (40, 3000)], first=250, Hq=4, Hkv=1),
+}
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 128), (BF, 64), (FP, 64)], ids=["bf16-128", "fp16-128", "bf16-64", "fp16-64"])
+@pytest.mark.parametrize("name", list(FEW))
+def test_few_rows_keep_their_weights(cpa, name, dtype, d):
+    """Entries of up to 16 rows by single warps: a weight's two halves leave 2^-16
+    of it (bf16) or 2^-22 and 2^-34 of the largest (fp16, whose second half may be
+    a subnormal number), not the half step of the type.  Queries are small, so that
+    the scores' own error (d + 4) 2^-24 scale |q| |k| is; the sums of up to 24
+    products of 16 keys and of the parts add 2^-24 each, the merge's weights 2^-21."""
+    b = Batch(seed=81, dtype=dtype, d=d, **FEW[name])
+    b.qkv[:, :b.Hq] *= 0.05
+    o, lse = run_attention(cpa, b, out_fp32=True)
+    O, LSE, A, W = b.attention()
+    n = 250 if name == "beside_ctas" else b.N    # the others' prefix is the CTAs'
+    ds = (d + 4) * 2.0 ** -24 * W + 2.0 ** -21
+    left = 2.0 ** -16 if dtype == BF else 2.0 ** -22
+    most = 2.0 ** -34 * 400 * max(float(b.v_cache.nan_to_num().abs().max()), 1.0) if dtype == FP else 0.0
+    bound = 2.0 ** -24 * np.abs(O) + 1.02 * (left + 2 * ds[:, :, None] + 32 * 2.0 ** -24 + 2.0 ** -21) * A + most
+    err = np.abs(o.double().cpu().numpy() - O)
+    assert np.all(err[:n] <= bound[:n]), (name, (err[:n] / bound[:n]).max())
