@@ -305,9 +305,11 @@ struct Weight<__half> {
   static constexpr float kBias = 9.f, kSlack = 2.f, kSpecSum = 60000.f, kSpecMax = 6.5f;
 };
 
-// L2 policy of keys that are read once: first to go, so that a step's stream of
+// L2 policy of keys that are read once, and of all that warps read: first to go, so that a step's stream of
 // keys does not push out the queries, the parts and the kernels' own code (64
-// sequences on a prefix of 32K keys 74.8 -> 68.5 us).
+// sequences on a prefix of 32K keys 74.8 -> 68.5 us).  Warps beside CTAs have it
+// for short entries of up to 16 token tiles too, that read their keys again: a
+// policy by entry there took 256 sequences on prefixes from 93.5 to 95.9 us.
 __device__ __forceinline__ uint64_t read_once_policy() {
   uint64_t p;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -407,7 +409,7 @@ inline bool make_cache_map_whole(CUtensorMap* m, const PagedGeom& g, const void*
 // A launch that may begin while the kernel before it in the stream still
 // runs (it calls griddepcontrol.wait before it reads that kernel's results).
 template <typename... P, typename... A>
-int launch(void (*kernel)(P...), unsigned grid, int threads, int smem, bool overlap, cudaStream_t stream, A... args) {
+int launch(void (*kernel)(P...), unsigned grid, int threads, int smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -417,7 +419,7 @@ int launch(void (*kernel)(P...), unsigned grid, int threads, int smem, bool over
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? CP_OK : CP_ERR_CUDA;
 }
 

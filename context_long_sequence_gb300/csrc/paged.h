@@ -101,9 +101,16 @@ __host__ __device__ inline PagedEntry paged_entry(const PagedGeom& g, int e) {
 //
 // Between 8 and 32 rows, in us: 24 sequences of 20 rows on up to 30K keys take
 // 446 by warps at d = 128 (their registers spill), 258 by CTAs; at d = 64 and
-// 16K keys 76 by warps, 116 by CTAs.  Beside CTAs 16 rows spill too: 40
-// sequences of 1 to 40 new tokens on up to 8K keys take 170 with warps of 8
-// rows, 396 with 16.
+// 16K keys 75 by warps, 115 by CTAs.  Beside CTAs 16 rows spill in the loop over
+// the keys: 40 sequences of 1 to 40 new tokens on up to 8K keys take 170 with
+// warps of 8 rows, 396 with 16.  (With 8 the kernel of both stores 24 bytes a
+// thread at d = 128 and 36 at d = 64, by the compiler's account.)
+//
+// Which kernel a batch gets goes by the most rows that its plan's max_new and
+// the batch's n_tokens allow an entry, not by the lengths, which are on the
+// device: a plan with room to spare gets the kernel of both (64 sequences of up
+// to 16K keys 326 us by paged_small_kernel, 331 by paged_large_kernel's warps; 24
+// drafts of 5 tokens at d = 64 20.8 and 30.0, after 16K keys 75 and 115).
 struct PagedCut {
   int tile_tokens, key_shift;  // tiles of 2^key_shift keys
   int lead;                    // units without keys that stand for a token tile's own cost
@@ -130,8 +137,9 @@ inline __host__ __device__ PagedCut paged_cut_large(int G) {
 // Whether an entry is the warps' in a batch that CTAs work on too: one of up
 // to 8 rows, and one whose tiles of 8 rows, that read the keys once each, cost
 // less than a CTA's one tile: short ones.  (In us, at weights 0, 8, 12, 16: 420
-// sequences of 24 rows on a few keys 155, 43, 43, 43; 64 of 8 to 24 on 1000
-// beside a prefix 206, 207, 163, 163; 64 of 12 on 1000 to 4000 153, 153, 179, 213.)
+// sequences of 24 rows on up to 36 keys 149, 44, 44, 44; beside a prefix of 1000,
+// 64 of 8 to 24 rows on 1000 keys 90, 90, 79, 79, and 64 of 12 on 1000 to 4000
+// 139, 140, 178, 205.)
 __host__ __device__ inline bool paged_by_warps(const PagedGeom& g, const PagedEntry& e) {
   const long long rows = static_cast<long long>(e.n) * g.G;
   if (rows <= kBesideRows) return true;
@@ -203,9 +211,9 @@ struct PagedShares {
 };
 
 // A batch is light if all its entries, of up to 128 rows, are a few units for
-// every warp in tiles of 8 rows: 7 sequences on a prefix of 2000 keys take 15.2
-// us so and 17.4 with CTAs, 16 sequences 17.5 and 18.1; at kLightUnits 16, 7 on
-// 8000 keys would take 23.0 and not 21.9.
+// every warp in tiles of 8 rows: 7 sequences on a prefix of 2000 keys take 13.8
+// us so and 17.2 with CTAs, 16 sequences 16.9 and 17.8; at kLightUnits 16, 7 on
+// 8000 keys would take 22.2 and not 21.0.
 inline __host__ __device__ bool paged_is_light(long long units, int ctas) {
   return units > 0 && units <= static_cast<long long>(kLightUnits) * kSmallWarps * ctas;
 }
@@ -235,8 +243,8 @@ __host__ __device__ inline bool paged_parts_in(const PagedParts& p, int G, uint3
 // their units: one is 256 rows x 128 keys, some 2750 clocks on the tensor core
 // and the exponentials; one of few rows is 16 keys, about a twentieth of that
 // for a CTA's eight warps (112 GB/s).  (64 sequences on a prefix of 32K keys,
-// and 256 on two of 16K and 9K, in us at weights 12: 66.8, 109.8; 16: 62.6,
-// 105.4; 20: 60.7, 101.0; 24: 60.6, 105.5; 28: 65.0, 109.5.)
+// and 256 on two of 16K and 9K, in us at weights 12: 64.8, 106.5; 16: 60.5,
+// 99.4; 20: 59.0, 96.1; 22: 58.7, 91.4; 24: 59.8, 93.1; 28: 63.2, 100.3.)
 __host__ __device__ inline int paged_large_ctas(long long small, long long large, int ctas) {
   if (large == 0) return 0;
   if (small == 0) return ctas;
@@ -384,7 +392,8 @@ struct PagedAttnArgs {
 };
 
 int launch_paged_attn(const PagedAttnArgs& a, cudaStream_t stream);
-// For batches that may have entries of more than kSmallRows rows (paged_attn_large.cu).
+// For batches that may have entries of more rows than paged_small_kernel's tiles
+// (paged_has_large): 16 at d = 128, 32 at d = 64 (paged_attn_large.cu).
 int launch_paged_large(const PagedAttnArgs& a, cudaStream_t stream);
 
 // Device address of the status words on the current device (cp_attn.cu).

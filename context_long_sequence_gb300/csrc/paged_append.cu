@@ -146,7 +146,7 @@ int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const long long warps = static_cast<long long>(a.g.N) * units;
   const long long grid = (warps + kAppendWarps - 1) / kAppendWarps;
   if (grid > 0x7fffffffLL) return CP_ERR_UNSUPPORTED;
-  return launch(paged_append_kernel<T, D>, static_cast<unsigned>(grid), kAppendWarps * 32, 0, true, stream, a, units);
+  return launch(paged_append_kernel<T, D>, static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream, a, units);
 }
 
 }  // namespace

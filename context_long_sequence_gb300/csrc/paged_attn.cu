@@ -76,7 +76,11 @@ __global__ void __launch_bounds__(kSmallWarps * 32, 1)
 //                sequences on prefixes 105.8 us without, 99.1 with).
 //   kMergeToken  a warp per token, four heads x two parts at a time: prompts,
 //                whose rows have one part (and are left) or two (chunks of 2K
-//                tokens 412 us without, 392 with).
+//                tokens 412 us without, 392 with).  A decode batch that large
+//                joins every row, one KV head after another: on a prefix of 2000
+//                keys 1024 sequences of 8 KV heads take 94.0 us (kMergeGroup),
+//                1025 98.1; 256 of 32 heads of one query head each 56.6, 257
+//                86.7; 64 of 128 heads on 500 keys 50.2, 65 134.
 enum MergeBy { kMergeBlock, kMergeHead, kMergeGroup, kMergeToken };
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBlocks = 152 * 12;  // at most; they loop
@@ -259,7 +263,7 @@ int launch_small(const PagedAttnArgs& a, cudaStream_t stream) {
   CUtensorMap mk, mv;
   if (!make_cache_map_whole(&mk, a.g, a.k_cache, 16) || !make_cache_map_whole(&mv, a.g, a.v_cache, 16)) return CP_ERR_CUDA;
   const int ctas = sms < kSmallWorkers / kSmallWarps ? sms : kSmallWorkers / kSmallWarps;
-  return launch(paged_small_kernel<T, D, ROWS>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, true, stream, mk, mv, a);
+  return launch(paged_small_kernel<T, D, ROWS>, ctas, kSmallWarps * 32, SmallSmem<D>::kBytes, stream, mk, mv, a);
 }
 
 template <typename T, int D>
@@ -281,14 +285,14 @@ int launch_attn_d(const PagedAttnArgs& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(g.N) * g.Hq;
   const auto blocks = [](long long n) { return static_cast<unsigned>(n < kMergeBlocks ? n : kMergeBlocks); };
   if (rows <= kMergeBlockRows)
-    return launch(paged_merge_kernel<T, D, kMergeBlock>, blocks(rows), kMergeWarps * 32, 0, true, stream, a);
+    return launch(paged_merge_kernel<T, D, kMergeBlock>, blocks(rows), kMergeWarps * 32, 0, stream, a);
   const long long groups = static_cast<long long>(g.N) * g.Hkv;
   if (groups <= kMergeHeadGroups)
-    return launch(paged_merge_kernel<T, D, kMergeHead>, blocks((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
+    return launch(paged_merge_kernel<T, D, kMergeHead>, blocks((rows + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, stream, a);
   if (groups <= kMergeGroups)
-    return launch(paged_merge_kernel<T, D, kMergeGroup>, blocks((groups + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, true, stream, a);
+    return launch(paged_merge_kernel<T, D, kMergeGroup>, blocks((groups + kMergeWarps - 1) / kMergeWarps), kMergeWarps * 32, 0, stream, a);
   return launch(paged_merge_kernel<T, D, kMergeToken>, blocks((static_cast<long long>(g.N) + kMergeWarps - 1) / kMergeWarps),
-                kMergeWarps * 32, 0, true, stream, a);
+                kMergeWarps * 32, 0, stream, a);
 }
 
 }  // namespace

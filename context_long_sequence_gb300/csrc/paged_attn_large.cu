@@ -677,7 +677,7 @@ int launch_large_d(const PagedAttnArgs& a, cudaStream_t stream) {
   if (!make_part_map(&mp, a.part_o, g.d, a.rows_large_end) || (o_boxes && !make_o_map(&mo, g, a.o))) return CP_ERR_CUDA;
   if (!o_boxes) mo = mp;  // not used
   const int workers = sms < kLargeWorkers ? sms : kLargeWorkers;
-  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, true, stream, mk, mv, mk16, mv16, mp, mo,
+  return launch(paged_large_kernel<T, D>, workers, kThreads, kLaunchBytes<D>, stream, mk, mv, mk16, mv16, mp, mo,
                 a, box, o_boxes ? 1 : 0);
 }
 

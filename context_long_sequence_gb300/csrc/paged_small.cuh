@@ -13,7 +13,7 @@
 // up to 16K keys, 2.16 GB from DRAM in 324 us, 6.65 TB/s; a sequence of 2^20
 // keys 4.3 GB in 636 us, 6.75 TB/s.  An SM by itself reads 112 GB/s: 79 with a
 // copy for each 64 columns, 87 with one a tile and rows as the MMA's rows.
-// With few keys the time is latency: 1000 keys of one sequence, 7.5 us with
+// With few keys the time is latency: 1000 keys of one sequence, 8.1 us with
 // the merge, most of it instructions that come from L2 once.
 #pragma once
 #include <type_traits>

@@ -412,11 +412,19 @@ typedef struct {
 typedef struct cp_paged cp_paged_t; /* opaque; immutable after creation; usable from any stream */
 
 /* Validate `desc` and build the plan.  It holds no device memory and may be
- * used on any sm_103 device. */
+ * used on any sm_103 device.  One plan with room to spare serves every step; the
+ * kernels are chosen by its bounds, though, and a decode or draft step under a
+ * plan whose max_new is a prompt's takes up to 1.6 times as long as under one
+ * that fits (32 query heads on 8 of d = 128: 64 sequences of up to 16K keys 326
+ * and 331 us; 24 drafts of 5 tokens at d = 64 21 and 30, after 16K keys 75 and
+ * 115; 64 sequences of up to 1000 keys at 16 query heads a KV head 34 and 54).
+ * Plans are small: keep one for prompts and one for decode steps. */
 int cp_paged_create(const cp_paged_desc_t *desc, cp_paged_t **out);
 void cp_paged_destroy(cp_paged_t *plan);
 
-/* Bytes of device workspace cp_attn_paged needs for any batch of this plan.
+/* Bytes of device workspace cp_attn_paged needs for any batch of this plan:
+ * slots for the workers of a whole card, whatever the plan (80 MB at d = 128, 40
+ * at d = 64), and rows for max_tokens where it has prefixes.
  * Nothing in it has to be initialised or kept between calls; calls that may
  * run at the same time need one each. */
 int cp_paged_workspace_size(const cp_paged_t *plan, size_t *bytes);
@@ -426,7 +434,9 @@ int cp_paged_workspace_size(const cp_paged_t *plan, size_t *bytes);
  *   q [n_tokens][Hq][d], k, v [n_tokens][Hkv][d], q_out [n_tokens][Hq][d]; a token's
  *   heads are contiguous, tokens q_stride, k_stride, v_stride, q_out_stride
  *   elements apart (multiples of 8), so the three may lie side by side.
- * Sums in fp32, one rounding.  q may be null (q_out is then ignored); q_out
+ * Sums in fp32, one rounding.  A token whose key has no place (its page is not
+ * the cache's, its sequence is bad, or it would lie before the sequence's first
+ * key) is left out, its row of q_out too, and recorded.  q may be null (q_out is then ignored); q_out
  * may be q itself with the same stride and must not overlap the inputs
  * otherwise.  If two new tokens name the same row of a page, either may
  * remain. */
@@ -443,11 +453,14 @@ int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const
  * result, whatever their page holds.  A key below kv_len that the causal mask
  * hides from some rows of its sequence must be finite.
  * Scores, softmax sums, lse and the sums over keys are fp32.  A weight is a
- * 16-bit operand of the product with V: rounded once to the cache's type (half
- * a step, 2^-8 of it in bf16, 2^-11 in fp16) for entries of more than 16 rows
- * (new tokens x query heads of a KV head; a prefix has the rows of all its
- * sequences), in two halves (2^-16, 2^-22) for entries of up to 8 and, where no
- * entry of the batch may have more than 16, of up to 16.
+ * 16-bit operand of the product with V: in two halves (2^-16 of it left out in
+ * bf16, 2^-22 in fp16) where entries have few rows, else rounded once to the
+ * cache's type (half a step, 2^-8 and 2^-11).  An entry, a sequence's own keys or
+ * a prefix with all its sequences, has as many rows as new tokens x query heads
+ * of a KV head.  Two halves: every entry of a batch that may have at most 16
+ * rows an entry, by the bounds min(max_new, n_tokens) and, with prefixes,
+ * n_tokens; otherwise entries of up to 8 rows and short ones of up to 128,
+ * save in batches of up to 32 rows an entry at d = 64.
  * Deterministic: no atomics on results; the work is split by the batch's
  * lengths alone.
  * workspace: cp_paged_workspace_size() bytes. */
