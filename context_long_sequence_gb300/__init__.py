@@ -431,8 +431,9 @@ def _refuse(where: str, why: str):
 
 class PagedPlan:
     """Owns a cp_paged_t (cp_paged_create / cp_paged_destroy): the shapes and
-    bounds of serving steps over a paged cache.  ``dtype`` is torch.bfloat16
-    or torch.float16; ``rope_freqs`` (rope_dim/2 numbers) replaces
+    bounds of serving steps over a paged cache.  The kernels go by the bounds:
+    a plan for decode steps beside one for prompts is faster than one for
+    both.  ``dtype`` is torch.bfloat16 or torch.float16; ``rope_freqs`` (rope_dim/2 numbers) replaces
     ``rope_base``."""
 
     def __init__(self, Hq, Hkv, d, page_size, dtype, max_seqs, max_tokens, max_new, max_pages, max_prefixes=0,

@@ -305,9 +305,9 @@ struct Weight<__half> {
   static constexpr float kBias = 9.f, kSlack = 2.f, kSpecSum = 60000.f, kSpecMax = 6.5f;
 };
 
-// L2 policy of keys that are read once, and of all that warps read: first to go, so that a step's stream of
-// keys does not push out the queries, the parts and the kernels' own code (64
-// sequences on a prefix of 32K keys 74.8 -> 68.5 us).  Warps beside CTAs have it
+// L2 policy of keys that are read once, and of all that warps read: first to
+// go, so that a step's stream of keys does not push out the queries, the parts
+// and the kernels' own code (64 sequences on a prefix of 32K keys 74.8 -> 68.5 us).  Warps beside CTAs have it
 // for short entries of up to 16 token tiles too, that read their keys again: a
 // policy by entry there took 256 sequences on prefixes from 93.5 to 95.9 us.
 __device__ __forceinline__ uint64_t read_once_policy() {
