@@ -257,8 +257,9 @@ struct PagedWalker {
       if (rec.count > 0) {
         PagedParts* parts = a.parts + (prefix ? static_cast<size_t>(a.max_tokens) * g.Hkv : 0);
         for (int i = threadIdx.x & 31; i < s.nt; i += 32)
-          if (CP_IN_BOUNDS(s.t0 >= 0 && s.t0 + i < a.max_tokens && s.h < g.Hkv, a.status)) parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] =
-              PagedParts{rec.first + i * rec.first_step, rec.second + i * g.G, rec.count, rec.stride};
+          if (CP_IN_BOUNDS(s.t0 >= 0 && s.t0 + i < a.max_tokens && s.h < g.Hkv, a.status))
+            parts[static_cast<size_t>(s.t0 + i) * g.Hkv + s.h] =
+                PagedParts{rec.first + i * rec.first_step, rec.second + i * g.G, rec.count, rec.stride};
       }
       break;
     }
@@ -295,14 +296,17 @@ struct Elem<__half> {
 // bits down to 2^-23 of the largest, and a million keys below that are off by
 // at most 2^-14 of the sum, under fp16's own half step of 2^-11.
 // kSpecSum and kSpecMax bound weights taken before their maximum is known
-// (paged_attn_large.cu): a sum of weights, and one score over m.
+// (paged_attn_large.cu): a sum of weights, and one score over m.  kBelow: what
+// the first of a weight's two halves is the rounding of (paged_small.cuh).
 template <typename T>
 struct Weight {
   static constexpr float kBias = 0.f, kSlack = 8.f, kSpecSum = 65536.f, kSpecMax = 16.f;
+  static constexpr float kBelow = 1.f - 0x1p-8f - 0x1p-14f;
 };
 template <>
 struct Weight<__half> {
   static constexpr float kBias = 9.f, kSlack = 2.f, kSpecSum = 60000.f, kSpecMax = 6.5f;
+  static constexpr float kBelow = 1.f - 0x1p-11f - 0x1p-13f;
 };
 
 // L2 policy of keys that are read once, and of all that warps read: first to

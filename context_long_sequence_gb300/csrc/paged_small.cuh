@@ -63,8 +63,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 }
 
 // A weight in two halves of the cache's type, p = hi + lo, for the product with
-// V (the sum is taken in fp32 before): what is left out is under 2^-16 of it in
-// bf16, 2^-22 in fp16, where one half leaves 2^-8 and 2^-11.  In us, one half
+// V (the sum is taken in fp32 before): what is left out is under 1.02 2^-15 of it
+// in bf16, 1.13 2^-21 in fp16 (or 2^-25, 2^-34 of the largest weight), where one
+// half leaves 2^-8 and 2^-11.  hi is the rounding of a little less than p, so that
+// lo is positive where p is (down to 2^-12 in fp16): an infinite value in V stays what it is, which 0 and negative
+// halves would make a NaN.  With u the half step, hi = c p (1 + e), |e| <= u, and
+// c = 1 - u - s: s p <= lo <= (2 u + s) p, rounded to u of it.  In us, one half
 // and two: 64 sequences of up to 16K keys at 4 query heads a KV head 319 and
 // 320, at 16 336 and 341 (d = 128), 194 and 181 (d = 64); one of 2^20 keys 620
 // and 624: the keys' bytes hide the second product.  At 32 rows (24 sequences of
@@ -73,7 +77,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 // weight once, to half a step of the cache's type.
 template <typename T>
 __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  hi = Elem<T>::pack(p0, p1);
+  hi = Elem<T>::pack(p0 * Weight<T>::kBelow, p1 * Weight<T>::kBelow);
   const float2 h = Elem<T>::unpack(hi);
   lo = Elem<T>::pack(p0 - h.x, p1 - h.y);
 }

@@ -453,8 +453,8 @@ int cp_cache_append(const cp_paged_t *plan, const cp_paged_cache_t *cache, const
  * result, whatever their page holds.  A key below kv_len that the causal mask
  * hides from some rows of its sequence must be finite.
  * Scores, softmax sums, lse and the sums over keys are fp32.  A weight is a
- * 16-bit operand of the product with V: in two halves (2^-16 of it left out in
- * bf16, 2^-22 in fp16) where entries have few rows, else rounded once to the
+ * 16-bit operand of the product with V: in two halves (2^-15 of it left out in
+ * bf16, 2^-21 in fp16) where entries have few rows, else rounded once to the
  * cache's type (half a step, 2^-8 and 2^-11).  An entry, a sequence's own keys or
  * a prefix with all its sequences, has as many rows as new tokens x query heads
  * of a KV head.  Two halves: every entry of a batch that may have at most 16

@@ -175,9 +175,10 @@ FEW = {
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 128), (BF, 64), (FP, 64)], ids=["bf16-128", "fp16-128", "bf16-64", "fp16-64"])
 @pytest.mark.parametrize("name", list(FEW))
 def test_few_rows_keep_their_weights(cpa, name, dtype, d):
-    """Entries of up to 16 rows by single warps: a weight's two halves leave 2^-16
-    of it (bf16) or 2^-22 and 2^-34 of the largest (fp16, whose second half may be
-    a subnormal number), not the half step of the type.  Queries are small, so that
+    """Entries of up to 16 rows by single warps: a weight's two halves leave 2^-15
+    of it (bf16) or 2^-21 and 2^-34 of the largest (fp16, whose second half may be
+    a subnormal number), not the half step of the type: with u the half step, the
+    second is at most (2 u + s) of the weight, s 2^-14 or 2^-13, and rounded to u.  Queries are small, so that
     the scores' own error (d + 4) 2^-24 scale |q| |k| is; the sums of up to 24
     products of 16 keys and of the parts add 2^-24 each, the merge's weights 2^-21."""
     b = Batch(seed=81, dtype=dtype, d=d, **FEW[name])
@@ -186,8 +187,38 @@ def test_few_rows_keep_their_weights(cpa, name, dtype, d):
     O, LSE, A, W = b.attention()
     n = 250 if name == "beside_ctas" else b.N    # the others' prefix is the CTAs'
     ds = (d + 4) * 2.0 ** -24 * W + 2.0 ** -21
-    left = 2.0 ** -16 if dtype == BF else 2.0 ** -22
+    left = (2.0 ** -7 + 2.0 ** -14) * 2.0 ** -8 if dtype == BF else (2.0 ** -10 + 2.0 ** -13) * 2.0 ** -11
     most = 2.0 ** -34 * 400 * max(float(b.v_cache.nan_to_num().abs().max()), 1.0) if dtype == FP else 0.0
     bound = 2.0 ** -24 * np.abs(O) + 1.02 * (left + 2 * ds[:, :, None] + 32 * 2.0 ** -24 + 2.0 ** -21) * A + most
     err = np.abs(o.double().cpu().numpy() - O)
     assert np.all(err[:n] <= bound[:n]), (name, (err[:n] / bound[:n]).max())
+
+
+INFINITE = {
+    "rows_4": (dict(past=[47, 300], new=[1, 1], Hq=8, Hkv=2), 5),
+    "rows_16": (dict(past=[47, 20], new=[1, 1], Hq=32, Hkv=2), 5),
+    "rows_20": (dict(past=[47, 20], new=[5, 1], Hq=8, Hkv=2), 5),
+    "many_rows": (dict(past=[300, 20], new=[60, 1], Hq=8, Hkv=2), 140),
+    "only_key": (dict(past=[0, 20], new=[1, 1], Hq=8, Hkv=2), 0),
+}
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (FP, 128), (BF, 64), (FP, 64)], ids=["bf16-128", "fp16-128", "bf16-64", "fp16-64"])
+@pytest.mark.parametrize("name", list(INFINITE))
+def test_a_seen_infinity_in_v_stays_one(cpa, name, dtype, d):
+    """A weight times an infinite value is that infinity, as in the formula: the
+    columns that hold it, and no others, are infinite in every row that sees it."""
+    kw, at = INFINITE[name]
+    b = Batch(seed=91, dtype=dtype, d=d, **kw)
+    page, row = int(b.page_table[0][at // 16]), at % 16
+    b.v_cache[page, row, :, 3], b.v_cache[page, row, :, d - 1] = float("inf"), float("-inf")
+    n = int(b.start[1])
+    O, LSE, A, W = b.attention()
+    assert np.isposinf(O[:n, :, 3]).all() and np.isneginf(O[:n, :, d - 1]).all()
+    o, lse = run_attention(cpa, b)
+    got = o.double().cpu().numpy()
+    assert np.array_equal(np.isposinf(got), np.isposinf(O)) and np.array_equal(np.isneginf(got), np.isneginf(O))
+    o[:n, :, 3], o[:n, :, d - 1] = 0, 0
+    for x in (O, A):
+        x[:n, :, 3], x[:n, :, d - 1] = 0, 0
+    check_attention(o, lse, (O, LSE, A, W), dtype, d, b.N, name)
