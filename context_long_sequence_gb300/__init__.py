@@ -46,9 +46,12 @@ CP_OP_BWD_RANK_STATS = 2
 
 
 CP_RESHARD_MAX_JOBS = 8
-CP_PAGED_VERSION = 1
+CP_PAGED_VERSION = 2
 CP_DTYPE_BF16 = 0
 CP_DTYPE_FP16 = 1
+CP_DTYPE_FP32 = 2
+CP_ROPE_VERSION = 1
+CP_ROPE_MAX_JOBS = 8
 
 
 class cp_reshard_job_t(ctypes.Structure):
@@ -93,6 +96,44 @@ class cp_paged_desc_t(ctypes.Structure):
         ("rope_interleaved", ctypes.c_int32),
         ("rope_base", ctypes.c_double),
         ("rope_freqs", ctypes.POINTER(ctypes.c_double)),
+        ("rope_axes", ctypes.c_int32),
+        ("rope_axis", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class cp_rope_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("version", "d", "rope_dim", "rope_interleaved")] + [
+        ("rope_base", ctypes.c_double),
+        ("rope_freqs", ctypes.POINTER(ctypes.c_double)),
+        ("rope_axes", ctypes.c_int32),
+        ("rope_axis", ctypes.POINTER(ctypes.c_int32)),
+    ]
+
+
+class cp_rope_job_t(ctypes.Structure):
+    _fields_ = [
+        ("inp", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("heads", ctypes.c_int32),
+        ("in_stride", ctypes.c_int64),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class cp_verify_t(ctypes.Structure):
+    _fields_ = [
+        ("vocab", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("p", ctypes.c_void_p),
+        ("p_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p),
+        ("accept_u", ctypes.c_void_p),
+        ("sample_u", ctypes.c_void_p),
+        ("accepted", ctypes.c_void_p),
+        ("out_tokens", ctypes.c_void_p),
+        ("kv_len_out", ctypes.c_void_p),
     ]
 
 
@@ -166,6 +207,11 @@ def _L():
                                     ctypes.POINTER(ctypes.c_int64)]
     lib.cp_cache_append.argtypes = [_vp, _vp, _vp] + [_vp, ctypes.c_int64] * 4 + [_vp]
     lib.cp_attn_paged.argtypes = [_vp, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.cp_rope_create.argtypes = [ctypes.POINTER(cp_rope_desc_t), ctypes.POINTER(_vp)]
+    lib.cp_rope_destroy.argtypes = [_vp]
+    lib.cp_rope_destroy.restype = None
+    lib.cp_rope.argtypes = [_vp, ctypes.c_int32, _vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp]
+    lib.cp_verify_drafts.argtypes = [_vp, _vp, _vp, _vp]
     lib.cp_debug_build.argtypes = []
     lib.cp_measure_rates.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
     lib.cp_measure_barrier_check.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
@@ -180,6 +226,7 @@ EXPORTED = ["cp_plan_create", "cp_plan_destroy", "cp_index_map", "cp_workspace_s
             "cp_attn_fwd", "cp_attn_fwd_local", "cp_attn_fwd_rank", "cp_attn_fwd_noalloc", "cp_attn_bwd",
             "cp_attn_fwd_step", "cp_attn_bwd_delta", "cp_attn_bwd_step",
             "cp_paged_create", "cp_paged_destroy", "cp_paged_workspace_size", "cp_paged_shares", "cp_cache_append", "cp_attn_paged",
+            "cp_verify_drafts", "cp_rope_create", "cp_rope_destroy", "cp_rope",
             "cp_merge_lse", "cp_get_status", "cp_get_status_detail", "cp_debug_build", "cp_strerror",
             "cp_selftest_wait_timeout", "cp_selftest_bounds", "cp_tile_classes", "cp_measure_rates", "cp_measure_barrier_check"]
 
@@ -429,16 +476,35 @@ def _refuse(where: str, why: str):
     raise e
 
 
+def _rope_pairs(where, rope_dim, rope_freqs, rope_axes, rope_axis):
+    """rope_freqs and rope_axis as C arrays (or None), with as many entries as pairs."""
+    out = []
+    for name, x, t in (("rope_freqs", rope_freqs, ctypes.c_double), ("rope_axis", rope_axis, ctypes.c_int32)):
+        if x is not None:
+            if len(x) != int(rope_dim) // 2:
+                _refuse(where, f"{len(x)} {name} for rope_dim {rope_dim}")
+            x = (t * max(1, len(x)))(*[float(y) if t is ctypes.c_double else int(y) for y in x])
+        out.append(x)
+    if int(rope_axes) > 1 and int(rope_dim) > 0 and rope_axis is None:
+        _refuse(where, f"{rope_axes} rope_axes need rope_axis")
+    return out
+
+
+def _cast(array, t):
+    return None if array is None else ctypes.cast(array, ctypes.POINTER(t))
+
+
 class PagedPlan:
     """Owns a cp_paged_t (cp_paged_create / cp_paged_destroy): the shapes and
     bounds of serving steps over a paged cache.  The kernels go by the bounds:
     a plan for decode steps beside one for prompts is faster than one for
     both.  ``dtype`` is torch.bfloat16 or torch.float16; ``rope_freqs`` (rope_dim/2 numbers) replaces
-    ``rope_base``."""
+    ``rope_base``; ``rope_axes`` > 1: positions of several axes, pair j's that of
+    ``rope_axis[j]``."""
 
     def __init__(self, Hq, Hkv, d, page_size, dtype, max_seqs, max_tokens, max_new, max_pages, max_prefixes=0,
                  max_prefix_pages=0, causal=True, out_fp32=False, softmax_scale=0.0, rope_dim=0, rope_interleaved=False,
-                 rope_base=10000.0, rope_freqs=None):
+                 rope_base=10000.0, rope_freqs=None, rope_axes=1, rope_axis=None):
         import torch
         self._h = None
         codes = {torch.bfloat16: CP_DTYPE_BF16, torch.float16: CP_DTYPE_FP16}
@@ -448,17 +514,15 @@ class PagedPlan:
                                int(max_tokens), int(max_new), int(max_pages), int(max_prefixes), int(max_prefix_pages),
                                1 if causal else 0, 1 if out_fp32 else 0, float(softmax_scale), int(rope_dim),
                                1 if rope_interleaved else 0, float(rope_base), None)
-        if rope_freqs is not None:
-            if len(rope_freqs) != int(rope_dim) // 2:
-                _refuse("cp_paged_create", f"{len(rope_freqs)} rope_freqs for rope_dim {rope_dim}")
-            freqs = (ctypes.c_double * max(1, len(rope_freqs)))(*[float(x) for x in rope_freqs])
-            desc.rope_freqs = ctypes.cast(freqs, ctypes.POINTER(ctypes.c_double))
+        freqs, axis = _rope_pairs("cp_paged_create", rope_dim, rope_freqs, rope_axes, rope_axis)
+        desc.rope_freqs, desc.rope_axes, desc.rope_axis = _cast(freqs, ctypes.c_double), int(rope_axes), _cast(axis, ctypes.c_int32)
         h = _vp()
         _check(_L().cp_paged_create(ctypes.byref(desc), ctypes.byref(h)), "cp_paged_create")
         self._h = h
         self.Hq, self.Hkv, self.d, self.page_size, self.dtype = desc.Hq, desc.Hkv, desc.d, desc.page_size, dtype
         self.max_seqs, self.max_tokens, self.max_new = desc.max_seqs, desc.max_tokens, desc.max_new
         self.max_pages, self.max_prefixes, self.max_prefix_pages = desc.max_pages, desc.max_prefixes, desc.max_prefix_pages
+        self.rope_axes = int(rope_axes)
         self.out_fp32 = bool(out_fp32)
         self.lse_dtype = torch.float32
         self.o_dtype = torch.float32 if out_fp32 else dtype
@@ -509,7 +573,8 @@ class PagedCache:
 
 class PagedBatch:
     """A step's batch, as cp_paged_batch_t: int32 tensors on the cache's
-    device, kept alive here and read by the kernels when they run."""
+    device, kept alive here and read by the kernels when they run.
+    ``positions``: [n_tokens], or [rope_axes][n_tokens] under a plan of several axes."""
 
     def __init__(self, q_start, kv_len, page_table, n_tokens, prefix_first=None, prefix_len=None, prefix_table=None,
                  positions=None):
@@ -519,8 +584,10 @@ class PagedBatch:
         self.device, self._dev = q_start.device, q_start.get_device()
         self.max_pages = page_table.shape[1] if page_table.dim() == 2 else -1
         self.max_prefix_pages = prefix_table.shape[1] if prefix_table is not None and prefix_table.dim() == 2 else 0
+        # Axes of the positions; 0: none are given, which serves every plan.
+        self.axes = 0 if positions is None else positions.shape[0] if positions.dim() == 2 else 1
         want = [(q_start, (self.n_seqs + 1,)), (kv_len, (self.n_seqs,)), (page_table, (self.n_seqs, self.max_pages)),
-                (positions, (self.n_tokens,))]
+                (positions, (self.n_tokens,) if self.axes == 1 and positions.dim() == 1 else (self.axes, self.n_tokens))]
         given = [x is not None for x in (prefix_first, prefix_len, prefix_table)]
         if any(given) and not all(given):
             _refuse("PagedBatch", "prefix_first, prefix_len and prefix_table come together")
@@ -567,6 +634,8 @@ def _tokens(where, name, x, n, heads, plan, dev):
 def cp_cache_append(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, k, v, q_out=None, stream=None):
     where = "cp_cache_append"
     st = _paged_stream(where, plan, cache, batch, stream)
+    if batch.axes and batch.axes != plan.rope_axes:
+        _refuse(where, f"the batch's positions have {batch.axes} axes, the plan {plan.rope_axes}")
     n, dev = batch.n_tokens, cache._dev
     qa = oa = (None, 0)
     if q is not None:
@@ -596,6 +665,116 @@ def cp_attn_paged(plan: PagedPlan, cache: PagedCache, batch: PagedBatch, q, o, l
             _refuse(where, f"the workspace is a contiguous tensor on cuda:{dev}")
         wa, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     rc = _L().cp_attn_paged(plan._h, cache.ref, batch.ref, *qa, o.data_ptr(), lse.data_ptr(), wa, wn, st)
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+_DTYPES = {}
+
+
+def _dtype_code(x):
+    """CP_DTYPE_* of a tensor, or None."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: CP_DTYPE_BF16, torch.float16: CP_DTYPE_FP16, torch.float32: CP_DTYPE_FP32})
+    return _DTYPES.get(x.dtype)
+
+
+def _current_stream(where, dev, stream):
+    """The stream of a call on device number `dev`, which has to be the current one."""
+    import torch
+    if dev < 0 or not torch.cuda.is_available() or torch._C._cuda_getDevice() != dev:
+        _refuse(where, f"the tensors are on device {dev}, which is not the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def cp_verify_drafts(plan: PagedPlan, batch: PagedBatch, tokens, p, q, accept_u, sample_u, accepted, out_tokens, kv_len_out=None,
+                     stream=None):
+    """p, q: [n_tokens][vocab] of one type (q may be None); tokens, out_tokens:
+    int32 [n_tokens]; accept_u: float32 [n_tokens]; sample_u: float32 [n_seqs];
+    accepted, kv_len_out: int32 [n_seqs]."""
+    import torch
+    where, dev, B, N = "cp_verify_drafts", batch._dev, batch.n_seqs, batch.n_tokens
+    i32, f32 = torch.int32, torch.float32
+    for name, x, n, t in (("tokens", tokens, N, i32), ("accept_u", accept_u, N, f32), ("sample_u", sample_u, B, f32),
+                          ("accepted", accepted, B, i32), ("out_tokens", out_tokens, N, i32), ("kv_len_out", kv_len_out, B, i32)):
+        if x is None and name == "kv_len_out":
+            continue
+        if x.dtype is not t or x.shape != (n,) or not x.is_contiguous() or x.get_device() != dev:
+            _refuse(where, f"{name} is a contiguous [{n}] {t} on device {dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    code = _dtype_code(p)
+    for x in (p, q):
+        if x is not None and (code is None or x.dtype is not p.dtype or x.dim() != 2 or x.shape[0] != N or x.shape[1] != p.shape[1]
+                              or (x.stride(1) != 1 and x.shape[1] > 1) or x.get_device() != dev):
+            _refuse(where, f"p and q are [{N}][vocab] bfloat16, float16 or float32 alike with contiguous rows on device {dev}, got "
+                           f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+    V = p.shape[1]
+    many = N > 1  # the stride of a dimension of one element says nothing
+    v = cp_verify_t(V, code, p.data_ptr(), p.stride(0) if many else V, None if q is None else q.data_ptr(),
+                    0 if q is None else q.stride(0) if many else V, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
+                    accepted.data_ptr(), out_tokens.data_ptr(), None if kv_len_out is None else kv_len_out.data_ptr())
+    rc = _L().cp_verify_drafts(plan._h, batch.ref, ctypes.addressof(v), _current_stream(where, dev, stream))
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+class RopePlan:
+    """Owns a cp_rope_t (cp_rope_create / cp_rope_destroy): which pairs of a
+    head turn how fast, by which axis of the positions."""
+
+    def __init__(self, d, rope_dim, rope_axes=1, rope_axis=None, rope_interleaved=False, rope_base=10000.0, rope_freqs=None):
+        self._h = None
+        freqs, axis = _rope_pairs("cp_rope_create", rope_dim, rope_freqs, rope_axes, rope_axis)
+        desc = cp_rope_desc_t(CP_ROPE_VERSION, int(d), int(rope_dim), 1 if rope_interleaved else 0, float(rope_base),
+                              _cast(freqs, ctypes.c_double), int(rope_axes), _cast(axis, ctypes.c_int32))
+        h = _vp()
+        _check(_L().cp_rope_create(ctypes.byref(desc), ctypes.byref(h)), "cp_rope_create")
+        self._h = h
+        self.d, self.rope_dim, self.rope_axes = desc.d, desc.rope_dim, desc.rope_axes
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if self._h is not None:
+            _L().cp_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def cp_rope(plan: RopePlan, positions, xs, outs, inverse=False, stream=None):
+    """xs, outs: up to 8 tensors [tokens][heads][d] each (queries and keys, say);
+    positions: int32 [rope_axes][tokens], or [tokens] with one axis."""
+    import torch
+    where, d, axes = "cp_rope", plan.d, plan.rope_axes
+    n, dev = positions.shape[-1], positions.get_device()
+    if not 1 <= len(xs) <= CP_ROPE_MAX_JOBS or len(xs) != len(outs):
+        _refuse(where, f"{len(xs)} inputs and {len(outs)} outputs; 1 to {CP_ROPE_MAX_JOBS} of both are wanted")
+    jobs = (cp_rope_job_t * len(xs))()
+    for job, x, o in zip(jobs, xs, outs):
+        a, b = x.stride(), o.stride()
+        if x.dim() != 3 or o.shape != x.shape or x.shape[0] != n or x.shape[2] != d or a[2] != 1 or b[2] != 1 \
+                or (x.shape[1] > 1 and (a[1] != d or b[1] != d)) or x.dtype != xs[0].dtype or o.dtype != outs[0].dtype \
+                or x.get_device() != dev or o.get_device() != dev:
+            _refuse(where, f"tensors [{n}][heads][{d}] with contiguous heads, inputs of one type and outputs of one, on device {dev} "
+                           f"are wanted, got {x.dtype} {tuple(x.shape)} {a} on {x.device} and {o.dtype} {tuple(o.shape)} {b} on {o.device}")
+        row = x.shape[1] * d
+        job.inp, job.out, job.heads = x.data_ptr(), o.data_ptr(), x.shape[1]
+        job.in_stride, job.out_stride = (a[0], b[0]) if n > 1 else (row, row)
+    if positions.shape != (axes, n) and (axes > 1 or positions.dim() != 1) or not positions.is_contiguous() \
+            or positions.dtype != torch.int32:
+        _refuse(where, f"positions are contiguous int32 [{axes}][{n}], got {positions.dtype} {tuple(positions.shape)}")
+    ti, to = _dtype_code(xs[0]), _dtype_code(outs[0])
+    if ti is None or to is None:
+        _refuse(where, f"{xs[0].dtype} to {outs[0].dtype}: bfloat16, float16 and float32 are served")
+    st = _current_stream(where, dev, stream)
+    rc = _L().cp_rope(plan._h, n, positions.data_ptr(), len(xs), jobs, ti, to, 1 if inverse else 0, st)
     if rc != CP_OK:
         _check(rc, where)
 

@@ -3,13 +3,19 @@
 // and cp_attn_paged.  Host code only; the kernels live in paged_append.cu and
 // paged_attn.cu.
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <cmath>
+#include <cstddef>
+#include <cstring>
 #include <new>
 
+#include "host.h"
 #include "paged.h"
 
+using cpattn::aligned;
+using cpattn::check_arch;
+using cpattn::kMaxStride;
+using cpattn::NvtxRange;
 using cpattn::PagedGeom;
 
 struct cp_paged {
@@ -17,40 +23,48 @@ struct cp_paged {
   int page_shift;
   float scale;
   uint64_t turns[cpattn::kMaxRopePairs];  // of a full circle per position, 64-bit fraction
+  uint8_t axis[cpattn::kMaxRopePairs];    // of the positions, per pair
 };
+
+namespace cpattn {
+
+// The fraction of a full circle in x >= 0 turns, in units of 2^-64.
+static uint64_t fraction(double x) { return static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64)); }
+
+// f radians as a fraction of a full circle: f / 2 pi = high + low, high the
+// rounded product and low what it leaves out, with 1 / 2 pi to 110 bits.  Off
+// by at most 2^-63 for |f| up to 2^42 (two cuts at 2^-64; the constant and
+// low's rounding stay below |f| 2^-106); f / 2 pi in one double would be off by
+// 2^-54 times itself, which a position of 2^31 makes 10^-5 radians at f = 100.
+uint64_t turns_of(double f) {
+  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;
+  const double x = std::fabs(f);
+  const volatile double product = x * kHigh;  // rounded: never fused with what follows
+  const double high = product, low = std::fma(x, kLow, std::fma(x, kHigh, -high));
+  const uint64_t rest = fraction(std::fabs(low));
+  const uint64_t turns = fraction(high) + (low < 0 ? 0 - rest : rest);
+  return f < 0 ? 0 - turns : turns;
+}
+
+int rope_pairs(int rope_dim, double base, const double* freqs, int axes, const int32_t* axis_of, uint64_t* turns, uint8_t* axis) {
+  if (axes < 1 || axes > kMaxRopeAxes || (axes > 1 && !axis_of)) return CP_ERR_INVALID_ARG;
+  if (!freqs && !(base > 0 && std::isfinite(base))) return CP_ERR_INVALID_ARG;
+  for (int j = 0; j < rope_dim / 2; ++j) {
+    const int a = axes > 1 ? axis_of[j] : 0;
+    if (a < 0 || a >= axes || (freqs && !std::isfinite(freqs[j]))) return CP_ERR_INVALID_ARG;
+    axis[j] = static_cast<uint8_t>(a);
+    turns[j] = turns_of(freqs ? freqs[j] : std::pow(base, -2.0 * j / rope_dim));
+  }
+  return CP_OK;
+}
+
+}  // namespace cpattn
 
 namespace {
 
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 constexpr long long kMaxKeys = 1LL << 30;  // of one page table row; key indices and limits stay in 32 bits
 constexpr long long kMaxRows = 1LL << 30;  // of the workspace's home rows
-constexpr int64_t kMaxStride = 1LL << 36;  // elements; a tensor map takes strides below 2^40 bytes
 constexpr int64_t kMaxSpan = 1LL << 60;    // elements from the cache's first to its last; offsets stay in 64 bits
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// The kernels are built for sm_103 alone; asked once per device.
-int check_arch() {
-  static int known[64];  // 0 unknown, 1 sm_103, -1 other; racing calls store the same value
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
-  int k = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
-  if (k == 0) {
-    int major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-      return CP_ERR_CUDA;
-    k = major == 10 && minor == 3 ? 1 : -1;
-    __atomic_store_n(&known[dev], k, __ATOMIC_RELAXED);
-  }
-  return k > 0 ? CP_OK : CP_ERR_ARCH;
-}
 
 int check_cache(const cp_paged_desc_t& d, const cp_paged_cache_t& c) {
   if (!c.k || !c.v || c.num_pages <= 0) return CP_ERR_INVALID_ARG;
@@ -96,24 +110,6 @@ int check_tokens(const void* p, int64_t stride, int heads, int d) {
   return aligned(p, 16) ? CP_OK : CP_ERR_ALIGNMENT;
 }
 
-// The fraction of a full circle in x >= 0 turns, in units of 2^-64.
-uint64_t fraction(double x) { return static_cast<uint64_t>(std::ldexp(x - std::floor(x), 64)); }
-
-// f radians as a fraction of a full circle: f / 2 pi = high + low, high the
-// rounded product and low what it leaves out, with 1 / 2 pi to 110 bits.  Off
-// by at most 2^-63 for |f| up to 2^42 (two cuts at 2^-64; the constant and
-// low's rounding stay below |f| 2^-106); f / 2 pi in one double would be off by
-// 2^-54 times itself, which a position of 2^31 makes 10^-5 radians at f = 100.
-uint64_t turns_of(double f) {
-  constexpr double kHigh = 0.15915494309189535, kLow = -9.839338337591243e-18;
-  const double x = std::fabs(f);
-  const volatile double product = x * kHigh;  // rounded: never fused with what follows
-  const double high = product, low = std::fma(x, kLow, std::fma(x, kHigh, -high));
-  const uint64_t rest = fraction(std::fabs(low));
-  const uint64_t turns = fraction(high) + (low < 0 ? 0 - rest : rest);
-  return f < 0 ? 0 - turns : turns;
-}
-
 PagedGeom geom(const cp_paged& p, const cp_paged_cache_t& c, const cp_paged_batch_t& b) {
   const cp_paged_desc_t& d = p.desc;
   PagedGeom g;
@@ -147,12 +143,22 @@ PagedGeom geom(const cp_paged& p, const cp_paged_cache_t& c, const cp_paged_batc
 
 }  // namespace
 
+namespace cpattn {
+
+int paged_max_new(const cp_paged_t* plan, const cp_paged_batch_t& batch) {
+  const int rc = check_batch(plan->desc, batch);
+  return rc == CP_OK ? plan->desc.max_new : rc;
+}
+
+}  // namespace cpattn
+
 extern "C" {
 
 int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
-  if (!desc || !out) return CP_ERR_INVALID_ARG;
-  const cp_paged_desc_t& d = *desc;
-  if (d.version != CP_PAGED_VERSION) return CP_ERR_INVALID_ARG;
+  if (!desc || !out || desc->version < 1 || desc->version > CP_PAGED_VERSION) return CP_ERR_INVALID_ARG;
+  cp_paged_desc_t d = {};  // a version 1 description ends before the axes
+  std::memcpy(&d, desc, desc->version == 1 ? offsetof(cp_paged_desc_t, rope_axes) : sizeof d);
+  if (d.rope_axes == 0) d.rope_axes = 1;
   if (d.dtype != CP_DTYPE_BF16 && d.dtype != CP_DTYPE_FP16) return CP_ERR_INVALID_ARG;
   if (d.Hq <= 0 || d.Hkv <= 0 || d.Hq % d.Hkv) return CP_ERR_INVALID_ARG;
   if (d.page_size <= 0 || d.max_seqs <= 0 || d.max_tokens <= 0 || d.max_new <= 0 || d.max_pages <= 0)
@@ -170,18 +176,21 @@ int cp_paged_create(const cp_paged_desc_t* desc, cp_paged_t** out) {
   if (d.d != 64 && d.d != 128) return CP_ERR_UNSUPPORTED;
   if (d.page_size < 16 || d.page_size > 65536 || (d.page_size & (d.page_size - 1))) return CP_ERR_UNSUPPORTED;
   if (d.Hq / d.Hkv > 128 || d.rope_dim % 16) return CP_ERR_UNSUPPORTED;
-  if (d.rope_dim > 0 && !d.rope_freqs && !(d.rope_base > 0 && std::isfinite(d.rope_base))) return CP_ERR_INVALID_ARG;
-  if (d.rope_dim > 0 && d.rope_freqs)
-    for (int j = 0; j < d.rope_dim / 2; ++j)
-      if (!std::isfinite(d.rope_freqs[j])) return CP_ERR_INVALID_ARG;
+  if (d.rope_axes < 1 || d.rope_axes > cpattn::kMaxRopeAxes) return CP_ERR_INVALID_ARG;
   cp_paged* p = new (std::nothrow) cp_paged();
   if (!p) return CP_ERR_CUDA;
+  if (d.rope_dim > 0) {
+    const int rc = cpattn::rope_pairs(d.rope_dim, d.rope_base, d.rope_freqs, d.rope_axes, d.rope_axis, p->turns, p->axis);
+    if (rc != CP_OK) {
+      delete p;
+      return rc;
+    }
+  }
   p->desc = d;
   p->desc.rope_freqs = nullptr;
+  p->desc.rope_axis = nullptr;
   for (p->page_shift = 0; (1 << p->page_shift) < d.page_size;) ++p->page_shift;
   p->scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.d));
-  for (int j = 0; j < d.rope_dim / 2; ++j)
-    p->turns[j] = turns_of(d.rope_freqs ? d.rope_freqs[j] : std::pow(d.rope_base, -2.0 * j / d.rope_dim));
   *out = p;
   return CP_OK;
 }
@@ -298,7 +307,8 @@ int cp_cache_append(const cp_paged_t* p, const cp_paged_cache_t* cache, const cp
   a.q_out_stride = q_out_stride;
   a.rope_dim = d.rope_dim;
   a.interleaved = d.rope_interleaved;
-  for (int j = 0; j < cpattn::kMaxRopePairs; ++j) a.turns[j] = p->turns[j];
+  a.axes = d.rope_axes;
+  for (int j = 0; j < cpattn::kMaxRopePairs; ++j) a.turns[j] = p->turns[j], a.axis[j] = p->axis[j];
   a.status = cpattn::device_status_ptr();
   if (!a.status) return CP_ERR_CUDA;
   NvtxRange range("cp_cache_append");

@@ -14,7 +14,7 @@
 namespace cpattn {
 
 // File ids of the status record, after those in debug.cuh.
-enum : int32_t { kTuPagedAppend = 6, kTuPagedAttn = 7 };
+enum : int32_t { kTuPagedAppend = 6, kTuPagedAttn = 7, kTuRope = 8, kTuVerify = 9, kTuPages = 10 };
 
 // The batch arrays and page numbers are data that no host check has seen;
 // these checks are therefore in every build, unlike CP_IN_BOUNDS.
@@ -76,6 +76,13 @@ __device__ __forceinline__ bool token_in(const PagedGeom& g, long long token, in
 }
 __device__ __forceinline__ bool cache_box_in(const PagedGeom& g, int row, int rows, int head, int page) {
   return row >= 0 && row + rows <= 1 << g.page_shift && head >= 0 && head < g.Hkv && page >= 0 && page < g.num_pages;
+}
+
+// Sine and cosine of pos * turns / 2^64 of a full circle (paged_append.cu says
+// to what they are good).
+__device__ __forceinline__ void sincos_turns(int pos, uint64_t turns, float* s, float* c) {
+  const uint64_t x = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+  sincospif(static_cast<float>(static_cast<int32_t>(x >> 32)) * 4.656612873077393e-10f, s, c);  // 2^-31
 }
 
 // A barrier of the block's first `threads` threads.

@@ -11,6 +11,7 @@
 namespace cpattn {
 
 constexpr int kMaxRopePairs = 64;  // rope_dim <= d <= 128
+constexpr int kMaxRopeAxes = 4;
 
 // Plan and batch, passed to the kernels by value.  The int32 arrays are the
 // caller's device arrays; nothing in them is trusted: every row, page and
@@ -366,8 +367,10 @@ struct AppendArgs {
   void* v_cache;
   int64_t q_stride, k_stride, v_stride, q_out_stride;  // between tokens, in elements
   int rope_dim, interleaved;
-  // Pair j turns by pos * turns[j] / 2^64 of a full circle.
+  int axes;                // of the positions: [axes][N]
+  // Pair j turns by pos * turns[j] / 2^64 of a full circle, pos that of axis[j].
   uint64_t turns[kMaxRopePairs];
+  uint8_t axis[kMaxRopePairs];
   int32_t* status;
 };
 

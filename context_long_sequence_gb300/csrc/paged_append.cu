@@ -52,7 +52,7 @@ __device__ __forceinline__ void turn(uint4& a, uint4& b, const float (&c)[8], co
 
 // Warp `unit` of `units` of a token visits every units-th group of heads; a
 // group is 512 elements, 32 lanes of 16.
-template <typename T, int D>
+template <typename T, int D, bool AXES>
 __global__ void __launch_bounds__(kAppendWarps * 32)
     paged_append_kernel(const __grid_constant__ AppendArgs args, int units) {
   constexpr int LPH = D / 16;       // lanes per head
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   float c[8], sn[8];
   int pos = at;
   if (g.positions) {
-    pos = g.positions[t];
+    if constexpr (!AXES) pos = g.positions[t];
   } else if (args.rope_dim > 0) {
     // Looked up by the whole warp, the lanes behind rope_dim too.  A bad prefix,
     // or one whose rows this is not among, is none: as in the attention.
@@ -94,8 +94,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   if (rotated) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * args.turns[8 * j + i];
-      sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f, &sn[i], &c[i]);  // 2^-31
+      if constexpr (AXES) {
+        if (g.positions) pos = g.positions[static_cast<size_t>(args.axis[8 * j + i]) * g.N + t];
+      }
+      sincos_turns(pos, args.turns[8 * j + i], &sn[i], &c[i]);
     }
   }
   const int heads = g.Hq + 2 * g.Hkv, groups = (heads + HPG - 1) / HPG;
@@ -136,8 +138,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
   }
 }
 
-template <typename T, int D>
-int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
+template <typename T, int D, bool AXES>
+int launch_append_axes(const AppendArgs& a, cudaStream_t stream) {
   const int groups = (a.g.Hq + 2 * a.g.Hkv + 512 / D - 1) / (512 / D);
   // Few tokens: a warp for each group of heads, for latency.  Many: a warp
   // takes more of its token's heads, as one set of sines serves them all.
@@ -146,7 +148,13 @@ int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const long long warps = static_cast<long long>(a.g.N) * units;
   const long long grid = (warps + kAppendWarps - 1) / kAppendWarps;
   if (grid > 0x7fffffffLL) return CP_ERR_UNSUPPORTED;
-  return launch(paged_append_kernel<T, D>, static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream, a, units);
+  return launch(paged_append_kernel<T, D, AXES>, static_cast<unsigned>(grid), kAppendWarps * 32, 0, stream, a, units);
+}
+
+// A plan of several axes looks its positions up pair by pair.
+template <typename T, int D>
+int launch_append_d(const AppendArgs& a, cudaStream_t stream) {
+  return a.axes > 1 ? launch_append_axes<T, D, true>(a, stream) : launch_append_axes<T, D, false>(a, stream);
 }
 
 }  // namespace

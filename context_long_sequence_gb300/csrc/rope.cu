@@ -1,0 +1,257 @@
+// rope.cu -- rotary positions of whole sequences, with one position or
+// several (time, height, width) a token: C ABI and kernel of cp_rope.
+//
+// Pair j of a head turns by theta = pos[axis(j)][t] * f_j: (a, b) ->
+// (a cos - b sin, b cos + a sin); the gradient of that is the turn by -theta.
+// Angles are paged_append.cu's: 64-bit fractions of a circle, good at every
+// position.  The rotation is in fp32 with one rounding at the end.
+//
+// Bound by memory: each value is read once and written once.  As in the
+// append a warp owns a token (or a share of its heads), a lane 16 elements of
+// a head in two pieces that hold both halves of eight pairs, so that its eight
+// sines and cosines serve every head it visits, queries and keys alike.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <new>
+
+#define CP_TU_ID ::cpattn::kTuRope
+#include "host.h"
+#include "paged.cuh"
+
+struct cp_rope_plan {
+  cp_rope_desc_t desc;
+  uint64_t turns[128];
+  uint8_t axis[128];
+};
+
+namespace cpattn {
+namespace {
+
+constexpr int kRopeMaxDim = 256;
+constexpr int kRopeWarps = 4;
+constexpr int kRopeFillWarps = 152 * 32;  // warps that keep the memory busy
+
+struct RopeJob {
+  const void* in;
+  void* out;
+  int64_t in_stride, out_stride;
+  int first;  // its first head among those of all jobs
+};
+
+struct RopeArgs {
+  int n, d, rope_dim, interleaved, inverse, heads, jobs;
+  const int32_t* positions;  // [axes][n]
+  RopeJob job[CP_ROPE_MAX_JOBS];
+  uint64_t turns[kRopeMaxDim / 2];
+  uint8_t axis[kRopeMaxDim / 2];
+  int32_t* status;
+};
+
+// Eight elements as they lie in memory.
+template <typename T>
+struct Piece {
+  uint4 r[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r[i];
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(r);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = Elem<T>::unpack(w[i]);
+        x[2 * i] = u.x;
+        x[2 * i + 1] = u.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(r);
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = Elem<T>::pack(x[2 * i], x[2 * i + 1]);
+    }
+  }
+};
+
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeArgs args, unsigned units) {
+  constexpr int kAhead = sizeof(TI) == 2 ? 4 : 2;  // groups of heads whose loads are in flight together
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+  const unsigned t = w / units, unit = w - t * units;
+  if (t >= static_cast<unsigned>(args.n)) return;
+  const int lph = args.d / 16, hpg = 32 / lph;  // lanes per head, heads per group
+  const int sub = lane / lph, j = lane - sub * lph;
+  if (sub >= hpg) return;
+  const bool rotated = j < args.rope_dim / 16, halves = rotated && !args.interleaved;
+  const int ea = halves ? 8 * j : 16 * j;  // first elements of the lane's two pieces
+  const int eb = halves ? args.rope_dim / 2 + 8 * j : 16 * j + 8;
+  float c[8], sn[8];
+  if (rotated) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int pos = args.positions[static_cast<size_t>(args.axis[8 * j + i]) * args.n + t];
+      sincos_turns(pos, args.turns[8 * j + i], &sn[i], &c[i]);
+      if (args.inverse) sn[i] = -sn[i];
+    }
+  }
+  const int groups = (args.heads + hpg - 1) / hpg;
+  for (int g0 = unit; g0 < groups; g0 += kAhead * units) {
+    Piece<TI> a[kAhead], b[kAhead];
+    TO* dst[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = (g0 + i * static_cast<int>(units)) * hpg + sub;
+      dst[i] = nullptr;
+      if (h >= args.heads || !CP_IN_BOUNDS(ea + 8 <= args.d && eb + 8 <= args.d, args.status)) continue;
+      int k = 0;
+#pragma unroll
+      for (int x = 1; x < CP_ROPE_MAX_JOBS; ++x) k += x < args.jobs && h >= args.job[x].first;
+      const RopeJob& job = args.job[k];
+      const int64_t at = static_cast<int64_t>(h - job.first) * args.d;
+      const TI* src = static_cast<const TI*>(job.in) + t * job.in_stride + at;
+      dst[i] = static_cast<TO*>(job.out) + t * job.out_stride + at;
+      a[i].load(src + ea);
+      b[i].load(src + eb);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!dst[i]) continue;
+      float x[8], y[8];
+      a[i].get(x);
+      b[i].get(y);
+      if (halves) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = x[e], v = y[e];
+          x[e] = u * c[e] - v * sn[e];
+          y[e] = v * c[e] + u * sn[e];
+        }
+      } else if (rotated) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = x[2 * e], v = x[2 * e + 1], p = y[2 * e], q = y[2 * e + 1];
+          x[2 * e] = u * c[e] - v * sn[e];
+          x[2 * e + 1] = v * c[e] + u * sn[e];
+          y[2 * e] = p * c[4 + e] - q * sn[4 + e];
+          y[2 * e + 1] = q * c[4 + e] + p * sn[4 + e];
+        }
+      }
+      Piece<TO> o;
+      o.set(x);
+      o.store(dst[i] + ea);
+      o.set(y);
+      o.store(dst[i] + eb);
+    }
+  }
+}
+
+template <typename TI, typename TO>
+int launch_rope(const RopeArgs& a, cudaStream_t stream) {
+  const int hpg = 32 / (a.d / 16), groups = (a.heads + hpg - 1) / hpg;
+  // Few tokens: a warp for each group of heads, for latency.  Many: a warp
+  // takes more of its token's heads, as one set of sines serves them all.
+  int units = (kRopeFillWarps + a.n - 1) / a.n;
+  units = units < 1 ? 1 : units > groups ? groups : units;
+  const long long warps = static_cast<long long>(a.n) * units;  // below 2^31 + kRopeFillWarps + n
+  const long long grid = (warps + kRopeWarps - 1) / kRopeWarps;
+  return launch(rope_kernel<TI, TO>, static_cast<unsigned>(grid), kRopeWarps * 32, 0, stream, a, static_cast<unsigned>(units));
+}
+
+template <typename TI>
+int launch_rope_from(const RopeArgs& a, int out_dtype, cudaStream_t stream) {
+  if (out_dtype == CP_DTYPE_FP32) return launch_rope<TI, float>(a, stream);
+  if constexpr (std::is_same<TI, float>::value) {
+    return out_dtype == CP_DTYPE_BF16 ? launch_rope<TI, __nv_bfloat16>(a, stream) : launch_rope<TI, __half>(a, stream);
+  } else {
+    return launch_rope<TI, TI>(a, stream);
+  }
+}
+
+}  // namespace
+}  // namespace cpattn
+
+using namespace cpattn;
+
+extern "C" {
+
+int cp_rope_create(const cp_rope_desc_t* desc, cp_rope_t** out) {
+  if (!desc || !out || desc->version != CP_ROPE_VERSION) return CP_ERR_INVALID_ARG;
+  const cp_rope_desc_t& d = *desc;
+  if (d.d <= 0 || d.rope_dim <= 0 || d.rope_dim > d.d || (d.rope_interleaved | 1) != 1) return CP_ERR_INVALID_ARG;
+  if (d.d % 16 || d.d > kRopeMaxDim || d.rope_dim % 16) return CP_ERR_UNSUPPORTED;
+  cp_rope_plan* r = new (std::nothrow) cp_rope_plan();
+  if (!r) return CP_ERR_CUDA;
+  const int rc = rope_pairs(d.rope_dim, d.rope_base, d.rope_freqs, d.rope_axes, d.rope_axis, r->turns, r->axis);
+  if (rc != CP_OK) {
+    delete r;
+    return rc;
+  }
+  r->desc = d;
+  r->desc.rope_freqs = nullptr;
+  r->desc.rope_axis = nullptr;
+  *out = r;
+  return CP_OK;
+}
+
+void cp_rope_destroy(cp_rope_t* r) { delete r; }
+
+int cp_rope(const cp_rope_t* r, int32_t n_tokens, const int32_t* positions, int32_t n_jobs, const cp_rope_job_t* jobs, int32_t in_dtype,
+            int32_t out_dtype, int32_t inverse, cudaStream_t stream) {
+  if (!r || n_tokens < 0 || n_jobs < 1 || n_jobs > CP_ROPE_MAX_JOBS || !jobs || (inverse | 1) != 1) return CP_ERR_INVALID_ARG;
+  if (in_dtype < CP_DTYPE_BF16 || in_dtype > CP_DTYPE_FP32 || out_dtype < CP_DTYPE_BF16 || out_dtype > CP_DTYPE_FP32)
+    return CP_ERR_INVALID_ARG;
+  if (in_dtype != out_dtype && in_dtype != CP_DTYPE_FP32 && out_dtype != CP_DTYPE_FP32) return CP_ERR_UNSUPPORTED;
+  const cp_rope_desc_t& d = r->desc;
+  const int64_t in_unit = in_dtype == CP_DTYPE_FP32 ? 4 : 8, out_unit = out_dtype == CP_DTYPE_FP32 ? 4 : 8;  // of 16 bytes
+  RopeArgs a = {};
+  for (int i = 0; i < n_jobs; ++i) {
+    const cp_rope_job_t& j = jobs[i];
+    if (j.heads <= 0 || j.heads > 65536) return CP_ERR_INVALID_ARG;
+    const int64_t row = static_cast<int64_t>(j.heads) * d.d;
+    if (j.in_stride < row || j.in_stride >= kMaxStride || j.in_stride % in_unit || j.out_stride < row || j.out_stride >= kMaxStride ||
+        j.out_stride % out_unit)
+      return CP_ERR_INVALID_ARG;
+    if (n_tokens > 0 && (!j.in || !j.out)) return CP_ERR_INVALID_ARG;
+    if (!aligned(j.in, 16) || !aligned(j.out, 16)) return CP_ERR_ALIGNMENT;
+    if (j.in && j.in == j.out && (j.in_stride != j.out_stride || in_dtype != out_dtype)) return CP_ERR_INVALID_ARG;
+    a.job[i] = RopeJob{j.in, j.out, j.in_stride, j.out_stride, a.heads};
+    a.heads += j.heads;
+  }
+  if (n_tokens == 0) return CP_OK;
+  if (!positions) return CP_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return CP_ERR_ALIGNMENT;
+  const int rc = check_arch();
+  if (rc != CP_OK) return rc;
+  a.n = n_tokens;
+  a.d = d.d;
+  a.rope_dim = d.rope_dim;
+  a.interleaved = d.rope_interleaved;
+  a.inverse = inverse;
+  a.jobs = n_jobs;
+  a.positions = positions;
+  for (int j = 0; j < d.rope_dim / 2; ++j) a.turns[j] = r->turns[j], a.axis[j] = r->axis[j];
+  a.status = device_status_ptr();
+  if (!a.status) return CP_ERR_CUDA;
+  NvtxRange range("cp_rope");
+  return in_dtype == CP_DTYPE_FP32   ? launch_rope_from<float>(a, out_dtype, stream)
+         : in_dtype == CP_DTYPE_BF16 ? launch_rope_from<__nv_bfloat16>(a, out_dtype, stream)
+                                     : launch_rope_from<__half>(a, out_dtype, stream);
+}
+
+}  // extern "C"

@@ -353,13 +353,14 @@ int cp_merge_lse(int n_parts, int rows, int H, int d, const float *o_parts,
  * Rows behind q_start[n_seqs] (a padded batch) stay as they were; a batch
  * without sequences or rows is no work, whatever the tensors.
  * These arrays need only 4-byte alignment. */
-#define CP_PAGED_VERSION 1
+#define CP_PAGED_VERSION 2
 #define CP_DTYPE_BF16 0
 #define CP_DTYPE_FP16 1
+#define CP_DTYPE_FP32 2      /* cp_rope and cp_verify_drafts */
 
 /* Plan description (host struct; copied by cp_paged_create). */
 typedef struct {
-  int32_t version;            /* CP_PAGED_VERSION */
+  int32_t version;            /* CP_PAGED_VERSION; 1: the description ends before rope_axes */
   int32_t dtype;              /* CP_DTYPE_*: q, k, v, the cache, and o unless out_fp32 */
   int32_t Hq, Hkv;            /* query heads, KV heads; Hkv divides Hq, Hq/Hkv <= 128 */
   int32_t d;                  /* head dimension: 64 or 128 */
@@ -380,6 +381,9 @@ typedef struct {
   double rope_base;           /* pair j turns by pos * rope_base^(-2j/rope_dim) radians, */
   const double *rope_freqs;   /* or, if not null, by pos * rope_freqs[j] (host, rope_dim/2 entries; copied): finite;
                                  of numbers up to 2^42 the angle is good to 2^-22 radians at every position */
+  int32_t rope_axes;          /* positions of a token: 1 (or 0), .. 4, e.g. time, height and width */
+  const int32_t *rope_axis;   /* host, rope_dim/2 entries (copied): the axis, 0 .. rope_axes - 1, whose position
+                                 turns the pair; not read with one axis */
 } cp_paged_desc_t;
 
 /* The cache (host struct, read during the call).  Element x of head h of
@@ -404,8 +408,8 @@ typedef struct {
   const int32_t *prefix_first; /* [n_prefixes + 1], ascending */
   const int32_t *prefix_len;   /* [n_prefixes] */
   const int32_t *prefix_table; /* [n_prefixes][max_prefix_pages] */
-  const int32_t *positions;    /* [n_tokens] or null: where cp_cache_append's rotation places the token;
-                                  null => prefix_len (0 without a prefix, or with a bad one) + its place among
+  const int32_t *positions;    /* [rope_axes][n_tokens] or null: where cp_cache_append's rotation places the token;
+                                  null => on every axis prefix_len (0 without a prefix, or with a bad one) + its place among
                                   the sequence's own keys */
 } cp_paged_batch_t;
 
@@ -482,6 +486,88 @@ int cp_attn_paged(const cp_paged_t *plan, const cp_paged_cache_t *cache, const c
  * with capacity 0 to ask for the count.  Host only. */
 int cp_paged_shares(const cp_paged_t *plan, const cp_paged_batch_t *host_batch, int32_t ctas,
                     int32_t *host_rows, int64_t capacity, int64_t *n_rows);
+
+/* Verification of a step's drafts against the target's probabilities, from
+ * given random numbers (host struct of device arrays).  Sequence s has the
+ * batch's new tokens t0 = q_start[s] .. t0 + n - 1: the last token that is
+ * settled and n - 1 drafts behind it (n = 1: none, the step of a single token).
+ * Row t0 + i of p holds the target's probabilities of the token behind token
+ * t0 + i, the same row of q those that the draft there was drawn from.
+ * Numbers need not add up to 1; those that are negative, NaN, or (in p)
+ * infinite count as 0.  A row's sum must be finite in fp32. */
+typedef struct {
+  int32_t vocab;              /* 1 .. 2^30 */
+  int32_t dtype;              /* CP_DTYPE_*: p and q */
+  const void *p;              /* [n_tokens][vocab], rows p_stride elements apart (any alignment of rows) */
+  int64_t p_stride;
+  const void *q;              /* the same, or null: drafts that are certain (q = 1 at the draft, 0 elsewhere) */
+  int64_t q_stride;
+  const int32_t *tokens;      /* [n_tokens]: draft i + 1 of sequence s is tokens[t0 + i + 1] */
+  const float *accept_u;      /* [n_tokens], in [0, 1): row t0 + i's decides on the draft behind it */
+  const float *sample_u;      /* [n_seqs], in [0, 1) (less counts as 0, more as the largest): draws the last token */
+  int32_t *accepted;          /* [n_seqs] out: drafts accepted, 0 .. n - 1 */
+  int32_t *out_tokens;        /* [n_tokens] out: row t0 + i holds the token that now follows token t0 + i: the accepted
+                                 drafts, the token drawn behind them, and -1 in the rows after */
+  int32_t *kv_len_out;        /* [n_seqs] out or null: kv_len less the drafts that were not accepted */
+} cp_verify_t;
+
+/* Draft x in row i is accepted while accept_u q_i(x) < p_i(x); a draft outside
+ * the vocabulary is not, and is recorded.  At the first row a whose draft is not accepted the next token
+ * is drawn from w = max(p_a - q_a, 0) (from p_a itself if that is 0 throughout); if
+ * all are, from w = p_a of the last row.  It is the least k with w_0 + .. + w_k >
+ * sample_u (w_0 + .. + w_vocab-1); -1 if the row has no weight at all.  Products and
+ * differences are exact, sums good to 2^-40, so that the same numbers give the
+ * same tokens whatever the batch.  A sequence without new tokens has accepted 0
+ * and its kv_len.  Bad entries of q_start are skipped (their outputs stay as they
+ * were) and recorded, rows behind q_start[n_seqs] are not touched.  The
+ * outputs overlap neither each other nor the inputs, save that kv_len_out may be
+ * the batch's kv_len.  The plan gives the batch's bounds (max_seqs,
+ * max_tokens, max_new); its page tables and positions are not read. */
+int cp_verify_drafts(const cp_paged_t *plan, const cp_paged_batch_t *batch, const cp_verify_t *verify, cudaStream_t stream);
+
+/* ---- Rotary positions of whole sequences ------------------------------------
+ * (no counterpart in the pages.)  Turns queries and keys before cp_attn_fwd,
+ * and, inversely, their gradients after cp_attn_bwd.  Pair j of every head of
+ * token t turns by theta = positions[rope_axis[j]][t] * f_j, (a, b) -> (a cos
+ * theta - b sin theta, b cos theta + a sin theta): one axis, or several for
+ * images and video.  cp_cache_append does the same on the way into a cache. */
+#define CP_ROPE_VERSION 1
+#define CP_ROPE_MAX_JOBS 8
+
+/* The pairs (host struct; copied by cp_rope_create). */
+typedef struct {
+  int32_t version;            /* CP_ROPE_VERSION */
+  int32_t d;                  /* head dimension: a multiple of 16 up to 256 */
+  int32_t rope_dim;           /* elements of a head that are turned, the first of the head: a multiple of 16 up to d */
+  int32_t rope_interleaved;   /* 0: pair j is elements (j, j + rope_dim/2); 1: (2j, 2j + 1) */
+  double rope_base;           /* f_j = rope_base^(-2j/rope_dim), */
+  const double *rope_freqs;   /* or, if not null, rope_freqs[j] (host, rope_dim/2 entries): finite */
+  int32_t rope_axes;          /* 1 .. 4 */
+  const int32_t *rope_axis;   /* host, rope_dim/2 entries, each 0 .. rope_axes - 1; not read with one axis */
+} cp_rope_desc_t;
+
+/* One tensor of a call: [n_tokens][heads][d], a token's heads contiguous,
+ * tokens in_stride and out_stride elements apart (multiples of 16 bytes). */
+typedef struct {
+  const void *in;
+  void *out;                  /* may be `in` itself, of the same type and stride; else overlaps no input */
+  int32_t heads;              /* 1 .. 65536 */
+  int64_t in_stride, out_stride;
+} cp_rope_job_t;
+
+typedef struct cp_rope_plan cp_rope_t; /* opaque; immutable after creation; no device memory; usable from any stream */
+int cp_rope_create(const cp_rope_desc_t *desc, cp_rope_t **out);
+void cp_rope_destroy(cp_rope_t *rope);
+
+/* Turn n_jobs (1 .. CP_ROPE_MAX_JOBS) tensors in one launch, by theta or, with
+ * inverse = 1, by -theta: the gradient of the former.  positions: device int32
+ * [rope_axes][n_tokens], any numbers (4-byte alignment).  in_dtype, out_dtype:
+ * CP_DTYPE_*, of all tensors; alike, or one of them fp32 (gradients come from
+ * cp_attn_bwd in fp32).  fp32 arithmetic, one rounding to the output's type;
+ * elements behind rope_dim are copied.  The angles are as exact as
+ * cp_paged_desc_t says. */
+int cp_rope(const cp_rope_t *rope, int32_t n_tokens, const int32_t *positions, int32_t n_jobs, const cp_rope_job_t *jobs,
+            int32_t in_dtype, int32_t out_dtype, int32_t inverse, cudaStream_t stream);
 
 /* Debug table of the forward's tile classes (no counterpart in the pages: it
  * exposes which work the kernel skips).  For every work item of the plan's
@@ -587,7 +673,8 @@ int cp_get_status(cudaStream_t stream, int32_t *dev_code);
  * CP_ERR_DEVICE_BOUNDS, which only debug builds record (file ids: 1 the C-ABI
  * layer, 2 the forward kernel, 3 the backward kernels, 4 reshard and
  * gather, 5 merge) except where the data of a paged batch leave their bounds,
- * which every build records (6 cp_cache_append, 7 cp_attn_paged); otherwise 0.
+ * which every build records (6 cp_cache_append, 7 cp_attn_paged, 9 cp_verify_drafts,
+ * 10 the cp_pages_ calls; 8, cp_rope, in debug builds); otherwise 0.
  * Reads and clears all four words.
  *
  * Debug builds (compiled with -DCP_DEBUG, the library libcpattn_debug.so)
