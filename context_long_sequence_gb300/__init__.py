@@ -52,6 +52,8 @@ CP_DTYPE_FP16 = 1
 CP_DTYPE_FP32 = 2
 CP_ROPE_VERSION = 1
 CP_ROPE_MAX_JOBS = 8
+CP_PAGES_MAX_TABLES = 4
+CP_PAGES_MAX_CACHES = 128
 
 
 class cp_reshard_job_t(ctypes.Structure):
@@ -117,6 +119,25 @@ class cp_rope_job_t(ctypes.Structure):
         ("heads", ctypes.c_int32),
         ("in_stride", ctypes.c_int64),
         ("out_stride", ctypes.c_int64),
+    ]
+
+
+class cp_page_table_t(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int32),
+        ("columns", ctypes.c_int32),
+        ("pages", ctypes.c_void_p),
+        ("held", ctypes.c_void_p),
+    ]
+
+
+class cp_page_moves_t(ctypes.Structure):
+    _fields_ = [
+        ("capacity", ctypes.c_int32),
+        ("count", ctypes.c_void_p),
+        ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p),
     ]
 
 
@@ -212,6 +233,11 @@ def _L():
     lib.cp_rope_destroy.restype = None
     lib.cp_rope.argtypes = [_vp, ctypes.c_int32, _vp, ctypes.c_int32, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp]
     lib.cp_verify_drafts.argtypes = [_vp, _vp, _vp, _vp]
+    lib.cp_pages_resize.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp]
+    lib.cp_pages_fork.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.cp_pages_workspace_size.argtypes = [ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]
+    lib.cp_pages_compact.argtypes = [_vp, ctypes.c_int32, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.cp_pages_copy.argtypes = [_vp, ctypes.c_int32, _vp, _vp, _vp, _vp]
     lib.cp_debug_build.argtypes = []
     lib.cp_measure_rates.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
     lib.cp_measure_barrier_check.argtypes = [ctypes.POINTER(ctypes.c_double), _vp]
@@ -226,6 +252,7 @@ EXPORTED = ["cp_plan_create", "cp_plan_destroy", "cp_index_map", "cp_workspace_s
             "cp_attn_fwd", "cp_attn_fwd_local", "cp_attn_fwd_rank", "cp_attn_fwd_noalloc", "cp_attn_bwd",
             "cp_attn_fwd_step", "cp_attn_bwd_delta", "cp_attn_bwd_step",
             "cp_paged_create", "cp_paged_destroy", "cp_paged_workspace_size", "cp_paged_shares", "cp_cache_append", "cp_attn_paged",
+            "cp_pages_resize", "cp_pages_fork", "cp_pages_workspace_size", "cp_pages_compact", "cp_pages_copy",
             "cp_verify_drafts", "cp_rope_create", "cp_rope_destroy", "cp_rope",
             "cp_merge_lse", "cp_get_status", "cp_get_status_detail", "cp_debug_build", "cp_strerror",
             "cp_selftest_wait_timeout", "cp_selftest_bounds", "cp_tile_classes", "cp_measure_rates", "cp_measure_barrier_check"]
@@ -714,6 +741,138 @@ def cp_verify_drafts(plan: PagedPlan, batch: PagedBatch, tokens, p, q, accept_u,
                     0 if q is None else q.stride(0) if many else V, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
                     accepted.data_ptr(), out_tokens.data_ptr(), None if kv_len_out is None else kv_len_out.data_ptr())
     rc = _L().cp_verify_drafts(plan._h, batch.ref, ctypes.addressof(v), _current_stream(where, dev, stream))
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def _int_array(where, name, x, shape, dev):
+    """Address of a contiguous int32 tensor of this shape on device number `dev`."""
+    import torch
+    if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
+        _refuse(where, f"{name} is a contiguous int32 {list(shape)} on device {dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    return x.data_ptr()
+
+
+class PageTable:
+    """Rows of page numbers and how many of them each row holds, as
+    cp_page_table_t: int32 tensors pages [rows][columns] and held [rows]."""
+
+    def __init__(self, pages, held):
+        if pages.dim() != 2:
+            _refuse("PageTable", f"pages is [rows][columns], got {tuple(pages.shape)}")
+        self.pages, self.held, self._dev = pages, held, pages.get_device()
+        self.shape = (pages.shape[0], pages.shape[1])
+        self.c = cp_page_table_t(*self.shape, _int_array("PageTable", "pages", pages, self.shape, self._dev),
+                                 _int_array("PageTable", "held", held, self.shape[:1], self._dev))
+        self.ref = ctypes.addressof(self.c)
+
+
+class PageMoves:
+    """A list of page copies, as cp_page_moves_t: int32 tensors count [1], src,
+    dst and tokens [capacity].  ``PageMoves(capacity)`` makes an empty one for
+    cp_pages_fork and cp_pages_compact to write; with src, dst and tokens it is the caller's own
+    list (of all of them, unless count says fewer)."""
+
+    def __init__(self, capacity=None, src=None, dst=None, tokens=None, count=None, device="cuda"):
+        import torch
+        where = "PageMoves"
+        if src is None:
+            if capacity is None or int(capacity) < 0 or dst is not None or tokens is not None or count is not None:
+                _refuse(where, "a capacity, or src, dst and tokens, are wanted")
+            src, dst, tokens = torch.zeros(3, int(capacity), dtype=torch.int32, device=device)
+            count = torch.zeros(1, dtype=torch.int32, device=device)
+        elif dst is None or tokens is None:
+            _refuse(where, "src, dst and tokens come together")
+        n, dev = src.numel() if capacity is None else int(capacity), src.get_device()
+        if count is None:
+            count = torch.full((1,), n, dtype=torch.int32, device=src.device)
+        self.count, self.src, self.dst, self.tokens, self.capacity, self._dev = count, src, dst, tokens, n, dev
+        self.c = cp_page_moves_t(n, _int_array(where, "count", count, (1,), dev), *(
+            _int_array(where, name, x, (n,), dev) for name, x in (("src", src), ("dst", dst), ("tokens", tokens))))
+        self.ref = ctypes.addressof(self.c)
+
+
+def _page_refs(where, refs, *others):
+    """The checks that all calls on refs share: num_pages, address."""
+    import torch
+    dev = refs.get_device()
+    if refs.dtype is not torch.int32 or refs.dim() != 1 or not refs.is_contiguous():
+        _refuse(where, f"refs is a contiguous int32 [pages], got {refs.dtype} {tuple(refs.shape)}")
+    for x in others:
+        if x._dev != dev:
+            _refuse(where, f"refs is on {refs.device}, a table or the moves on device {x._dev}")
+    return refs.shape[0], refs.data_ptr(), dev
+
+
+def cp_pages_resize(plan: PagedPlan, refs, table: PageTable, tokens, served, stream=None):
+    """Row r of `table` comes to hold the pages of tokens[r] tokens (0: it is freed; -1: it is left alone)."""
+    where = "cp_pages_resize"
+    n, address, dev = _page_refs(where, refs, table)
+    rows = table.shape[:1]
+    ta, sa = _int_array(where, "tokens", tokens, rows, dev), _int_array(where, "served", served, rows, dev)
+    rc = _L().cp_pages_resize(plan._h, n, address, table.ref, ta, sa, _current_stream(where, dev, stream))
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def cp_pages_fork(plan: PagedPlan, refs, src: PageTable, dst: PageTable, parent, tokens, moves: PageMoves, served, stream=None):
+    """Row r of `dst` becomes a copy of the first tokens[r] tokens of row
+    parent[r] (-1: none) of `src`; `moves` gets the copies to run with cp_pages_copy."""
+    where = "cp_pages_fork"
+    n, address, dev = _page_refs(where, refs, src, dst, moves)
+    rows = dst.shape[:1]
+    pa, ta = _int_array(where, "parent", parent, rows, dev), _int_array(where, "tokens", tokens, rows, dev)
+    sa = _int_array(where, "served", served, rows, dev)
+    rc = _L().cp_pages_fork(plan._h, n, address, src.ref, dst.ref, pa, ta, moves.ref, sa, _current_stream(where, dev, stream))
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def cp_pages_workspace_size(num_pages) -> int:
+    n = ctypes.c_size_t()
+    _check(_L().cp_pages_workspace_size(int(num_pages), ctypes.byref(n)), "cp_pages_workspace_size")
+    return n.value
+
+
+def alloc_pages_workspace(num_pages, device="cuda"):
+    """A device byte buffer of cp_pages_workspace_size() bytes."""
+    import torch
+    return torch.empty(cp_pages_workspace_size(num_pages), dtype=torch.uint8, device=device)
+
+
+def cp_pages_compact(plan: PagedPlan, refs, tables, moves: PageMoves, workspace, refs_out=None, tables_out=None, used=None, stream=None):
+    """The held pages become the first ones; tables and refs in place unless
+    refs_out and tables_out (PageTables alike) are given.  `moves` gets the copies to run."""
+    where = "cp_pages_compact"
+    n, address, dev = _page_refs(where, refs, moves, *tables)
+    tables_out = tables if tables_out is None else tables_out
+    out = refs if refs_out is None else refs_out
+    oa = _int_array(where, "refs_out", out, refs.shape, dev)
+    if not 1 <= len(tables) <= CP_PAGES_MAX_TABLES or len(tables) != len(tables_out) \
+            or any(o._dev != dev or o.shape != t.shape for t, o in zip(tables, tables_out)):
+        _refuse(where, f"1 to {CP_PAGES_MAX_TABLES} tables, and as many outputs alike")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(where, f"the workspace is a contiguous tensor on device {dev}")
+    ua = None if used is None else _int_array(where, "used", used, (1,), dev)
+    a = (cp_page_table_t * len(tables))(*[t.c for t in tables])
+    b = (cp_page_table_t * len(tables))(*[t.c for t in tables_out])
+    rc = _L().cp_pages_compact(plan._h, n, address, oa, len(tables), a, b, moves.ref, ua, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _current_stream(where, dev, stream))
+    if rc != CP_OK:
+        _check(rc, where)
+
+
+def cp_pages_copy(plan: PagedPlan, src, dst, moves: PageMoves, stream=None):
+    """The moves over the caches (lists of PagedCache, one a layer): from src[i] to dst[i]."""
+    where, dev = "cp_pages_copy", moves._dev
+    if not 1 <= len(src) <= CP_PAGES_MAX_CACHES or len(src) != len(dst):
+        _refuse(where, f"{len(src)} and {len(dst)} caches; 1 to {CP_PAGES_MAX_CACHES} of both are wanted")
+    for c in (*src, *dst):
+        if c.page != plan.page or c._dev != dev:
+            _refuse(where, f"a cache's pages are {c.page} on {c.device}, the plan's {plan.page} and the moves on device {dev}")
+    a = (cp_paged_cache_t * len(src))(*[c.c for c in src])
+    b = a if dst is src else (cp_paged_cache_t * len(dst))(*[c.c for c in dst])
+    rc = _L().cp_pages_copy(plan._h, len(src), a, b, moves.ref, _current_stream(where, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 

@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libcpattn.so")
 LIB_DEBUG = os.path.join(PKG, "libcpattn_debug.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["cp_attn.cu", "attn_fwd.cu", "attn_bwd.cu", "reshard.cu", "merge.cu", "paged.cu", "paged_append.cu",
-           "paged_attn.cu", "paged_attn_large.cu", "rope.cu", "verify.cu"]
+           "paged_attn.cu", "paged_attn_large.cu", "rope.cu", "verify.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

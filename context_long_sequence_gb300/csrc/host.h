@@ -48,5 +48,9 @@ int rope_pairs(int rope_dim, double base, const double* freqs, int axes, const i
 // What a plan and a batch say to calls that have files of their own (paged.cu):
 // the plan's max_new, or a CP_ERR_* code if the batch leaves its bounds.
 int paged_max_new(const cp_paged_t* plan, const cp_paged_batch_t& batch);
+// log2 of its page size; the heads and dimension of its pages; what is wrong with a cache.
+int paged_page_shift(const cp_paged_t* plan);
+void paged_rows(const cp_paged_t* plan, int* Hkv, int* d);
+int paged_check_cache(const cp_paged_t* plan, const cp_paged_cache_t& cache);
 
 }  // namespace cpattn

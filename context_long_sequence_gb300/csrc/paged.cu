@@ -150,6 +150,15 @@ int paged_max_new(const cp_paged_t* plan, const cp_paged_batch_t& batch) {
   return rc == CP_OK ? plan->desc.max_new : rc;
 }
 
+int paged_page_shift(const cp_paged_t* plan) { return plan->page_shift; }
+
+void paged_rows(const cp_paged_t* plan, int* Hkv, int* d) {
+  *Hkv = plan->desc.Hkv;
+  *d = plan->desc.d;
+}
+
+int paged_check_cache(const cp_paged_t* plan, const cp_paged_cache_t& cache) { return check_cache(plan->desc, cache); }
+
 }  // namespace cpattn
 
 extern "C" {

@@ -525,6 +525,83 @@ typedef struct {
  * max_tokens, max_new); its page tables and positions are not read. */
 int cp_verify_drafts(const cp_paged_t *plan, const cp_paged_batch_t *batch, const cp_verify_t *verify, cudaStream_t stream);
 
+/* ---- The pages of a cache ---------------------------------------------------
+ * Who holds which page is kept on the device, so that captured steps follow it:
+ *   refs [num_pages]: how many table entries hold the page; 0: it is free;
+ *   tables: rows of page numbers, and how many of a row it holds.  A table can
+ *   be a batch's page_table (a row a sequence) or its prefix_table; several
+ *   tables may share one refs.
+ * A free page has no owner and no order: a call that takes pages takes the free
+ * ones of the lowest numbers, rows in order.  The same state and request give the
+ * same pages.  Page numbers, counts and requests are data, and not trusted: what
+ * leaves its bounds is skipped and recorded (CP_ERR_DEVICE_BOUNDS).  refs is
+ * 16-byte aligned, the other arrays 4-byte; none overlaps another, unless
+ * said.  Calls on one refs run one after another. */
+#define CP_PAGES_MAX_TABLES 4
+#define CP_PAGES_MAX_CACHES 128
+
+/* Host struct of device arrays. */
+typedef struct {
+  int32_t rows;               /* 1 .. 8192 */
+  int32_t columns;            /* entries of a row (columns * page_size < 2^30) */
+  int32_t *pages;             /* [rows][columns]; entries behind held mean nothing */
+  int32_t *held;              /* [rows]: pages that the row holds */
+} cp_page_table_t;
+
+/* A list of copies (host struct of device arrays): the first tokens[i] tokens of page src[i]
+ * go to page dst[i], for i below *count.  Written by cp_pages_fork and
+ * cp_pages_compact, or by the caller. */
+typedef struct {
+  int32_t capacity;           /* entries of src, dst and tokens */
+  int32_t *count;             /* [1] */
+  int32_t *src, *dst, *tokens;
+} cp_page_moves_t;
+
+/* Row r of the table comes to hold the pages of tokens[r] tokens, for each r:
+ * pages behind them are let go (all, with 0: that is how a sequence is freed),
+ * missing ones taken; -1 leaves a row alone.  Pages let go in this call can be
+ * taken in it.  Rows are served in order; a row whose pages have run out, and those
+ * behind it that want more, keep what they have.  served [rows] out: 1, or 0 for a row that did
+ * not get its pages or whose data are bad (those are left as they were).  Entries that a
+ * row lets go become -1. */
+int cp_pages_resize(const cp_paged_t *plan, int32_t num_pages, int32_t *refs, const cp_page_table_t *table,
+                    const int32_t *tokens, int32_t *served, cudaStream_t stream);
+
+/* Row r of dst, which holds nothing, becomes a copy of the first tokens[r] tokens of
+ * row parent[r] of src, for each r with parent[r] >= 0: whole pages are shared (one more
+ * holder each), a last page that is not full is a page of its own, whose
+ * copy is added to moves (capacity >= dst's rows).  src and dst may be one table; a
+ * prefix is made, or taken over, by forking between the two tables.  served
+ * as above, 1 for rows without a parent; pages are given to rows in order as long as they last.
+ * moves is overwritten; run it with cp_pages_copy before the children's pages are used. */
+int cp_pages_fork(const cp_paged_t *plan, int32_t num_pages, int32_t *refs, const cp_page_table_t *src,
+                  const cp_page_table_t *dst, const int32_t *parent, const int32_t *tokens,
+                  const cp_page_moves_t *moves, int32_t *served, cudaStream_t stream);
+
+/* The held pages become pages 0 .. used - 1: those above move to the free ones
+ * below, both in ascending order.  Written: refs_out (may be refs), each
+ * table's pages under their new numbers (tables_out[i].pages, which may be tables[i].pages; the same rows and
+ * columns, its held is not read; entries behind held stay as they were), moves
+ * (capacity >= num_pages / 2; whole pages; run it with cp_pages_copy from the
+ * cache to itself) and used [1] (or null).  Every table that holds pages of refs has to be given, up to
+ * CP_PAGES_MAX_TABLES of them.
+ * workspace: cp_pages_workspace_size(num_pages) bytes, 16-byte aligned; nothing in it is kept between calls. */
+int cp_pages_workspace_size(int32_t num_pages, size_t *bytes);
+int cp_pages_compact(const cp_paged_t *plan, int32_t num_pages, const int32_t *refs, int32_t *refs_out,
+                     int32_t n_tables, const cp_page_table_t *tables, const cp_page_table_t *tables_out,
+                     const cp_page_moves_t *moves, int32_t *used, void *workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/* Run a list of moves over n_caches pairs of caches (the layers of a model; 1 ..
+ * CP_PAGES_MAX_CACHES), K and V: from src[i] to dst[i], which may be one cache or two, of any
+ * layouts.  The sources are alike in strides and number of pages, and so are the
+ * destinations.  A page is the destination of one move only, and of none if
+ * it is another's source in the same cache; where a list breaks that, the
+ * destination may hold either, or parts of both.  Moves with a page or count out of
+ * bounds are skipped and recorded. */
+int cp_pages_copy(const cp_paged_t *plan, int32_t n_caches, const cp_paged_cache_t *src, const cp_paged_cache_t *dst,
+                  const cp_page_moves_t *moves, cudaStream_t stream);
+
 /* ---- Rotary positions of whole sequences ------------------------------------
  * (no counterpart in the pages.)  Turns queries and keys before cp_attn_fwd,
  * and, inversely, their gradients after cp_attn_bwd.  Pair j of every head of
