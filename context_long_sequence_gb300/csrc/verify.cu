@@ -440,8 +440,10 @@ int cp_verify_drafts(const cp_paged_t* plan, const cp_paged_batch_t* batch, cons
   if (v.dtype < CP_DTYPE_BF16 || v.dtype > CP_DTYPE_FP32) return CP_ERR_INVALID_ARG;
   if (v.vocab <= 0 || v.vocab > 1 << 30 || v.p_stride < v.vocab || v.p_stride >= kMaxStride) return CP_ERR_INVALID_ARG;
   if (v.q && (v.q_stride < v.vocab || v.q_stride >= kMaxStride)) return CP_ERR_INVALID_ARG;
-  if (batch->n_seqs == 0 || batch->n_tokens == 0) return CP_OK;
-  if (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.accepted || !v.out_tokens) return CP_ERR_INVALID_ARG;
+  if (batch->n_seqs == 0) return CP_OK;
+  if (!batch->q_start || !batch->kv_len || !v.accepted) return CP_ERR_INVALID_ARG;
+  // Without rows every sequence has none, which its outputs say.
+  if (batch->n_tokens > 0 && (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.out_tokens)) return CP_ERR_INVALID_ARG;
   if (!aligned(v.p, 16) || !aligned(v.q, 16)) return CP_ERR_ALIGNMENT;
   const void* arrays[] = {v.tokens, v.accept_u, v.sample_u, v.accepted, v.out_tokens, v.kv_len_out};
   for (const void* x : arrays)
