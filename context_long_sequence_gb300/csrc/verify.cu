@@ -12,19 +12,27 @@
 // Exactness.  Which k comes out hangs on sums over the whole vocabulary: with
 // sums good to e, one in about 1 / (2 V e) draws lands beside a border and comes
 // out differently: with fp32 sums (1e-7) of V = 10^5 numbers, one in 50.  So
-// differences and sums are kept in pairs of fp32 numbers whose sum is the
-// value (exact sum and difference of two floats: Knuth, Dekker), some 2^-46 of
-// it off, and a warp's totals in fp64 from there on: one in 10^8.  fp64 for
-// each element would be bound by the fp64 units (2 a clock and SM): two such
-// operations of 128K elements of 64 rows take 30 us, the pairs' 11 of fp32 5.
+// differences and sums are kept as pairs of fp32 numbers whose sum is the
+// value (exact sum and difference of two floats: Knuth, Dekker), good to some 2^-44:
+// one in 10^8.  In fp64 each element would cost two operations of units that
+// do two a clock and SM (128K elements of 64 rows: 27 us an operation).  From a
+// warp's totals on, the search counts in whole numbers, the row's sum being some 2^60.
 //
 // Bound by memory (each sequence's one row of p, and of q where it counts, is
 // read once) and, for few sequences, by a chain of dependent loads: lengths,
 // tokens, their probabilities, the row.  A cluster of up to 16 CTAs shares a
 // row, each warp a stretch of it, so that one sequence uses 16 SMs; the warps' totals
-// are exchanged through distributed shared memory; the CTA in whose stretch the
-// border lies reads it again, from L2, and looks closer.
+// are exchanged through distributed shared memory; the warp in whose stretch the
+// border lies looks closer, at its lanes' sums and then at one lane's elements.
+//
+// In a graph: one sequence of 5 drafts, V = 100003, 7.2 us (a third of it the
+// row's sums, the rest the chain); 64 sequences, 49 MB, 18.7 us; 256 without q, 26 MB of bf16,
+// 16.3 us (9 instructions an element and 1.3 elements for one that is there:
+// a warp's stretch is cut to whole slots).  CTAs of 128 or 512 threads, or
+// fewer on an SM, were slower (7.9 and 8.4; 21.5 and 19.3; 23.2 us).
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #define CP_TU_ID ::cpattn::kTuVerify
 #include "host.h"
@@ -33,8 +41,10 @@
 namespace cpattn {
 namespace {
 
-constexpr int kVerifyThreads = 512, kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyMaxCluster = 16;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyMaxCluster = 16, kVerifyResident = 4;  // CTAs of an SM
+constexpr int kVerifySums = kVerifyMaxCluster * kVerifyWarps;
+constexpr int kVerifySlots = 8;
 
 struct VerifyArgs {
   int B, N, V, max_new;
@@ -55,171 +65,240 @@ struct VerifyArgs {
 // A weight: finite and above zero, else zero.
 __device__ __forceinline__ float weight(float x) { return x > 0.f && x < INFINITY ? x : 0.f; }
 
-// The sum hi + lo of many numbers, exactly but for the rounding of lo.
+// The number hi + lo.
 struct Pair {
   float hi = 0.f, lo = 0.f;
+  // += x + rest, exactly but for the rounding of lo (Knuth's sum of two numbers).
   __device__ __forceinline__ void add(float x, float rest) {
     const float s = __fadd_rn(hi, x), b = __fadd_rn(s, -hi);
     const float e = __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(x, -b));
     hi = s;
     lo = __fadd_rn(lo, __fadd_rn(e, rest));
   }
-  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
-};
-
-template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-  return static_cast<float>(x);
-}
-
-// The numbers of 16 bytes.
-template <typename T>
-struct Granule {
-  static constexpr int kN = 16 / sizeof(T);
-  float x[kN];
-  __device__ __forceinline__ void from(const uint4& r) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        x[i] = __uint_as_float(w[i]);
-      } else {
-        const float2 u = Elem<T>::unpack(w[i]);
-        x[2 * i] = u.x;
-        x[2 * i + 1] = u.y;
-      }
-    }
+  // += x >= 0 where hi >= 0: the sum's rounding from the larger of the two (Dekker).
+  __device__ __forceinline__ void add(float x) {
+    const float s = __fadd_rn(hi, x);
+    lo = __fadd_rn(lo, __fadd_rn(fminf(hi, x), -__fadd_rn(s, -fmaxf(hi, x))));
+    hi = s;
   }
 };
 
-// A row of weights, in granules of 16 aligned bytes of p: granule g holds the
-// elements g * kN - skew .. + kN - 1, as far as they are in [0, V).
+// Numbers of a row in units of which its sum, about `sum`, is 2^60 to 2^61.
+struct Units {
+  float a = 0.f, b = 0.f;  // their product: 2^187 over the sum's power of two, with the exponent's bias
+  __device__ __forceinline__ void set(float sum) {
+    const int e = max(static_cast<int>(__float_as_uint(sum) >> 23), 1), k = 187 - e;
+    a = __uint_as_float((127 + k / 2) << 23);
+    b = __uint_as_float((127 + k - k / 2) << 23);
+  }
+  // At least 1 where there is anything.
+  __device__ __forceinline__ long long of(float hi, float lo) const {
+    const long long x = __float2ll_rn(hi * a * b) + __float2ll_rn(lo * a * b);
+    return hi > 0.f && x < 1 ? 1 : x;
+  }
+};
+
+// Code that a CTA runs once comes from L2 line by line, some 12 clocks an
+// instruction, and an fp64 operation takes a warp 64 clocks: from here on the code is
+// in loops and one copy, and counts in whole numbers.
+
+// The sum over the warp's lanes.
+__device__ __forceinline__ Pair warp_sum(Pair v) {
+#pragma unroll 1
+  for (int x = 16; x > 0; x >>= 1) v.add(__shfl_xor_sync(0xffffffffu, v.hi, x), __shfl_xor_sync(0xffffffffu, v.lo, x));
+  return v;
+}
+
+// The same of whole numbers of up to 61 bits, 27 of them at a time.
+__device__ __forceinline__ long long warp_sum(long long v) {
+  constexpr unsigned kMask = (1u << 27) - 1;
+  const unsigned a = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v) & kMask);
+  const unsigned b = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 27) & kMask);
+  const unsigned c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(v >> 54));
+  return a + (static_cast<long long>(b) << 27) + (static_cast<long long>(c) << 54);
+}
+
+struct Found {
+  int lane;
+  long long before, end;
+};
+
+// Of the lanes, each with a share `own` behind `before` and those of the lanes below it,
+// the first that ends above the border and has any weight, or else the last with
+// any; -1 without any.  What lies before that lane's share, and behind the last lane's.
+__device__ __noinline__ Found find_lane(long long own, long long before, long long border) {
+  const int lane = threadIdx.x & 31;
+  long long upto = own;
+#pragma unroll 1
+  for (int x = 1; x < 32; x <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, x);
+    if (lane >= x) upto += y;
+  }
+  upto += before;
+  const unsigned some = __ballot_sync(0xffffffffu, own > 0), above = __ballot_sync(0xffffffffu, own > 0 && upto > border);
+  const int who = above ? __ffs(above) - 1 : some ? 31 - __clz(some) : -1;
+  return Found{who, __shfl_sync(0xffffffffu, upto - own, max(who, 0)), __shfl_sync(0xffffffffu, upto, 31)};
+}
+
+// A row of weights w = max(p - q, 0), or p where there is no q; with draft x >= 0
+// and no q, max(p - 1, 0) there.
 template <typename T>
 struct Row {
-  static constexpr int kN = Granule<T>::kN;
+  static constexpr int kN = 16 / sizeof(T);  // elements of a granule, 16 aligned bytes of p
   const T* p;
-  const T* q;   // null: no second row
-  int V, skew, granules;
-  int x;        // with no second row: the rejected draft, which loses 1; else -1
-  bool alike;   // q's granules are aligned where p's are
+  const T* q;
+  int x, V, skew;  // granule g begins at element g * kN - skew
+  bool alike;      // q's granules are aligned where p's are
 
-  __device__ __forceinline__ void set(const T* p_row, const T* q_row, int vocab, int draft) {
-    p = p_row;
-    q = q_row;
-    V = vocab;
-    x = draft;
+  __device__ __forceinline__ Row(const T* p_row, const T* q_row, int vocab, int draft) : p(p_row), q(q_row), x(draft), V(vocab) {
     skew = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     alike = !q || ((reinterpret_cast<uintptr_t>(q) ^ reinterpret_cast<uintptr_t>(p)) & 15) == 0;
-    granules = static_cast<int>((static_cast<long long>(V) + skew + kN - 1) / kN);
   }
-  __device__ __forceinline__ void none() {
-    p = q = nullptr;
-    V = skew = granules = 0;
-    x = -1;
-    alike = true;
+  __device__ __forceinline__ int granules() const { return static_cast<int>((static_cast<long long>(V) + skew + kN - 1) / kN); }
+  // First element of granule g, within the row.
+  __device__ __forceinline__ int element(int g) const {
+    const long long e = static_cast<long long>(g) * kN - skew;
+    return static_cast<int>(e < 0 ? 0 : e > V ? V : e);
   }
-  __device__ __forceinline__ int first(int g) const { return g * kN - skew; }
-  __device__ __forceinline__ bool whole(int g) const { return alike && g > 0 && g < granules - 1; }
-  __device__ __forceinline__ void load_whole(int g, uint4& a, uint4& b) const {
-    a = *reinterpret_cast<const uint4*>(p + first(g));
-    if (q) b = *reinterpret_cast<const uint4*>(q + first(g));
-  }
-  // The granule's numbers one by one: at the row's ends, and where p and q are
-  // not aligned alike.
-  __device__ __forceinline__ void load_edge(int g, Granule<T>& a, Granule<T>& b) const {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int e = first(g) + i;
-      const bool in = e >= 0 && e < V;
-      a.x[i] = in ? to_float(p[e]) : 0.f;
-      b.x[i] = in && q ? to_float(q[e]) : 0.f;
-    }
-  }
-  // Weight of element e, of which p and q are given: d + rest exactly.
-  __device__ __forceinline__ void diff(int e, float of_p, float of_q, float& d, float& rest) const {
-    const float u = weight(of_p), v = e == x ? 1.f : of_q > 0.f ? of_q : 0.f;
+  // w = d + rest exactly: where u >= v >= 0 the difference's rounding is a float
+  // (Dekker).  u: p, or 0 where that is negative or NaN.
+  static __device__ __forceinline__ void diff(float u, float of_q, float& d, float& rest) {
+    const float v = fminf(fmaxf(of_q, 0.f), u);
     d = __fadd_rn(u, -v);
-    rest = __fadd_rn(__fadd_rn(u, -d), -v);  // exact where u >= v >= 0
-    if (!(u > v)) d = rest = 0.f;
+    rest = __fadd_rn(__fadd_rn(u, -d), -v);
   }
-  __device__ __forceinline__ void add(int g, const Granule<T>& a, const Granule<T>& b, Pair& sum) const {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      float d, rest;
-      diff(first(g) + i, a.x[i], b.x[i], d, rest);
-      sum.add(d, rest);
-    }
-  }
-  __device__ __forceinline__ void weight_of(int e, float& d, float& rest) const {
-    diff(e, to_float(p[e]), q ? to_float(q[e]) : 0.f, d, rest);
+  __device__ __forceinline__ void element_weight(int e, float& d, float& rest) const {
+    diff(weight(static_cast<float>(p[e])), q ? static_cast<float>(q[e]) : e == x ? 1.f : 0.f, d, rest);
   }
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-  return v;
-}
-
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// The double at the address of `local` in the shared memory of CTA `rank`.
-__device__ __forceinline__ double ld_cluster(const double* local, unsigned rank) {
-  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-  uint32_t remote;
-  double v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(remote) : "memory");
-  return v;
-}
-
-// Totals of granules [g0, g1) of the row, lane by lane.
 template <typename T>
-__device__ __forceinline__ double sum_granules(const Row<T>& row, int g0, int g1) {
-  constexpr int kAhead = 4;
-  const int lane = threadIdx.x & 31;
-  Pair sum;
-  for (int g = g0 + lane; g < g1; g += 32 * kAhead) {
-    uint4 a[kAhead], b[kAhead];
+__device__ __forceinline__ void unpack(const uint4& r, float (&x)[16 / sizeof(T)]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      a[i] = b[i] = make_uint4(0, 0, 0, 0);
-      if (g + 32 * i < g1 && row.whole(g + 32 * i)) row.load_whole(g + 32 * i, a[i], b[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int at = g + 32 * i;
-      if (at >= g1) break;
-      Granule<T> u, v;
-      u.from(a[i]);
-      v.from(b[i]);
-      if (!row.whole(at)) row.load_edge(at, u, v);
-      row.add(at, u, v, sum);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 u = Elem<T>::unpack(w[i]);
+      x[2 * i] = u.x;
+      x[2 * i + 1] = u.y;
     }
   }
-  return sum.value();
+}
+
+// A warp's sum of granules [g0, g1) of the row, in up to kVerifySlots slots of
+// 32 lanes x run granules: each lane takes `run` neighbours of a slot, four at a time, whose
+// sum it leaves in `slots`.  So the search finds its way down to one lane's
+// granules without reading the row again.  An infinite element makes the sum
+// infinite or NaN, unless it is taken one by one.
+template <typename T>
+__device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, int run, float2 (*slots)[32]) {
+  constexpr int kN = Row<T>::kN, kAhead = 4;
+  const int lane = threadIdx.x & 31;
+  Pair sum;
+  const uint4* p = reinterpret_cast<const uint4*>(row.p - row.skew);
+  const uint4* q = row.q ? reinterpret_cast<const uint4*>(row.q - row.skew) : nullptr;
+  // Granules that are vectors: not the row's first and last where they are not
+  // whole, nor the one of the draft that loses 1, and none where p and q are not
+  // aligned alike.
+  const int v0 = row.alike ? row.skew > 0 : INT_MAX, v1 = row.granules() - ((row.V + row.skew) % kN > 0);
+  const int gx = !q && row.x >= 0 ? (row.x + row.skew) / kN : -1;
+#pragma unroll 1
+  for (int slot = 0; g0 + slot * 32 * run < g1; ++slot) {
+    const int first = g0 + (slot * 32 + lane) * run, end = min(first + run, g1);
+    Pair parts[4];  // independent chains of sums
+#pragma unroll 1
+    for (int g = first; g < end; g += kAhead) {
+      uint4 x[kAhead], y[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        x[i] = y[i] = make_uint4(0, 0, 0, 0);
+        if (g + i < end && g + i >= v0 && g + i < v1 && g + i != gx) {
+          x[i] = p[g + i];
+          if (q) y[i] = q[g + i];
+        }
+      }
+      // Two at a time, in one copy of the code.  fmaxf: neither negative nor NaN.
+#pragma unroll 1
+      for (int half = 0; half < kAhead; half += 2) {
+        if (q) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float u[kN], v[kN];
+            unpack<T>(x[i], u);
+            unpack<T>(y[i], v);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+              float d, rest;
+              Row<T>::diff(fmaxf(u[e], 0.f), v[e], d, rest);
+              parts[e % 4].add(d);
+              parts[e % 4].lo = __fadd_rn(parts[e % 4].lo, rest);
+            }
+            y[i] = y[i + 2];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float u[kN];
+            unpack<T>(x[i], u);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) parts[e % 4].add(fmaxf(u[e], 0.f));
+          }
+        }
+        x[0] = x[2];
+        x[1] = x[3];
+      }
+      if (g < v0 || min(g + kAhead, end) > v1 || static_cast<unsigned>(gx - g) < kAhead) {  // some are not vectors
+#pragma unroll 1
+        for (int k = g; k < min(g + kAhead, end); ++k) {
+          if (k >= v0 && k < v1 && k != gx) continue;
+#pragma unroll 1
+          for (int e = row.element(k), e1 = row.element(k + 1); e < e1; ++e) {
+            float d, rest;
+            row.element_weight(e, d, rest);
+            parts[0].add(d, rest);
+          }
+        }
+      }
+    }
+    parts[0].add(parts[1].hi, parts[1].lo);
+    parts[2].add(parts[3].hi, parts[3].lo);
+    parts[0].add(parts[2].hi, parts[2].lo);
+    slots[slot][lane] = make_float2(parts[0].hi, parts[0].lo);
+    sum.add(parts[0].hi, parts[0].lo);
+  }
+  return warp_sum(sum);
+}
+
+__device__ __forceinline__ int cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// v to the address of `local` in the shared memory of CTA `rank`.
+__device__ __forceinline__ void st_cluster(float2* local, int rank, float x, float y) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(x), "f"(y) : "memory");
 }
 
 // One cluster a sequence.
 template <typename T>
-__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int cluster) {
-  constexpr int kEach = kVerifyMaxCluster * kVerifyWarps / 32;
-  __shared__ double totals[kVerifyWarps + 1];                 // this CTA's warps', read by the cluster; whether there is a residual
-  __shared__ double sums[kVerifyMaxCluster * kVerifyWarps];   // all warps'
-  __shared__ double close[kVerifyWarps];
-  __shared__ double found_total, found_before;
-  __shared__ int found_accepted, found_warp;
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel(const __grid_constant__ VerifyArgs a, int cluster) {
+  __shared__ float2 sums[3][kVerifySums + 1];  // all warps', for each turn; behind them whether there is a residual
+  __shared__ float2 slots[kVerifyWarps][kVerifySlots][32];
+  __shared__ int found_accepted;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(cluster_rank()), s = blockIdx.x / cluster;
+  const int rank = cluster_rank(), s = blockIdx.x / cluster;
+  cluster_arrive();  // waited for before the first store to another CTA, which has begun then
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = a.q_start[s], t1 = a.q_start[s + 1], n = t1 - t0;
+  const float of_all = a.sample_u[s];
   // Every CTA goes through the same cluster barriers, whatever it finds in the arrays.
   const bool good = CP_CHECK_DATA(t0 >= 0 && t1 >= t0 && t1 <= a.N && n <= a.max_new, a.status);
   const T* p = static_cast<const T*>(a.p);
@@ -227,19 +306,21 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
   // Drafts accepted: 32 at a time, by every CTA's first warp.
   if (warp == 0) {
     int accepted = good ? max(n - 1, 0) : 0;
+#pragma unroll 1
     for (int i0 = 0; good && i0 < n - 1; i0 += 32) {
       const int i = i0 + lane;
       bool ok = true;
       if (i < n - 1) {
         const int x = a.tokens[t0 + i + 1];
+        const float u = a.accept_u[t0 + i];
         ok = CP_CHECK_DATA(x >= 0 && x < a.V, a.status);
         if (ok) {
-          const float px = weight(to_float(p[(t0 + i) * a.p_stride + x]));
+          const float px = weight(static_cast<float>(p[(t0 + i) * a.p_stride + x]));
           float qx = 1.f;
-          if (q) qx = to_float(q[(t0 + i) * a.q_stride + x]);
+          if (q) qx = static_cast<float>(q[(t0 + i) * a.q_stride + x]);
           if (!(qx > 0.f)) qx = 0.f;
           // A product of two floats is exact in fp64.
-          ok = static_cast<double>(a.accept_u[t0 + i]) * static_cast<double>(qx) < static_cast<double>(px);
+          ok = static_cast<double>(u) * static_cast<double>(qx) < static_cast<double>(px);
         }
       }
       const unsigned no = __ballot_sync(0xffffffffu, !ok);
@@ -254,71 +335,57 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
   const int accepted = found_accepted;
   const bool live = good && n > 0, rejected = live && accepted < n - 1;
   const int64_t t = static_cast<int64_t>(t0) + accepted;
-  Row<T> row;
-  row.none();
-  if (live && CP_IN_BOUNDS(t < a.N, a.status))
-    row.set(p + t * a.p_stride, rejected && q ? q + t * a.q_stride : nullptr, a.V, rejected && !q ? a.tokens[t + 1] : -1);
-  const int warps = cluster * kVerifyWarps;
-  int per = 0;
-  for (int turn = 0; turn < 2; ++turn) {
-    // A stretch of whole granules for each warp of the cluster, a multiple of 32 where there are enough.
-    per = (row.granules + warps - 1) / warps;
-    if (per > 32) per = (per + 31) & ~31;
-    const int w = rank * kVerifyWarps + warp;
-    const int g0 = min(w * per, row.granules), g1 = min(g0 + per, row.granules);
-    const double v = warp_sum(sum_granules(row, g0, g1));
-    if (lane == 0) totals[warp] = v;
-    if (threadIdx.x == 0) totals[kVerifyWarps] = rejected ? 1 : 0;
-    cluster_sync_all();
-    if (static_cast<int>(threadIdx.x) < warps) sums[threadIdx.x] = ld_cluster(&totals[threadIdx.x % kVerifyWarps], threadIdx.x / kVerifyWarps);
-    const bool again = turn == 0 && ld_cluster(&totals[kVerifyWarps], 0) != 0;
-    cluster_sync_all();  // no CTA leaves, or writes its totals again, before all have read them
-    if (warp == 0) {
-      // Running sums of up to 256 numbers, eight to a lane; the first with any
-      // weight of its own that ends above the border, or else (rounding) the last with any.
-      double x[kEach], own = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        x[i] = lane * kEach + i < warps ? sums[lane * kEach + i] : 0.0;
-        own += x[i];
-      }
-      double upto = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
-      }
-      double at = __shfl_up_sync(0xffffffffu, upto, 1);
-      if (lane == 0) at = 0;
-      const double total = __shfl_sync(0xffffffffu, upto, 31);
-      const float r = live ? a.sample_u[s] : 0.f;
-      const double border = total * static_cast<double>(r >= 0.f ? fminf(r, 0x1.fffffep-1f) : 0.f);
-      int which = -1, any = -1;
-      double which_before = 0, any_before = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const double end = at + x[i];
-        if (x[i] > 0) {
-          any = lane * kEach + i;
-          any_before = at;
-          if (which < 0 && end > border) which = any, which_before = at;
-        }
-        at = end;
-      }
-      const unsigned above = __ballot_sync(0xffffffffu, which >= 0), some = __ballot_sync(0xffffffffu, any >= 0);
-      if (lane == 0) found_total = total, found_warp = -1;
-      __syncwarp();
-      if (above ? lane == __ffs(above) - 1 : some && lane == 31 - __clz(some)) {
-        found_warp = above ? which : any;
-        found_before = above ? which_before : any_before;
-        found_total = total;
-      }
+  const bool there = live && CP_IN_BOUNDS(t < a.N, a.status);
+  Row<T> row(there ? p + t * a.p_stride : nullptr, there && rejected && q ? q + t * a.q_stride : nullptr, there ? a.V : 0,
+             there && rejected && !q ? a.tokens[t + 1] : -1);
+  // A stretch of granules for each warp of the cluster.
+  const int warps = cluster * kVerifyWarps, granules = row.granules(), w = rank * kVerifyWarps + warp;
+  const int per = (granules + warps - 1) / warps, run = (per + 128 * kVerifySlots - 1) / (128 * kVerifySlots) * 4;
+  const int g0 = min(w * per, granules), g1 = min(g0 + per, granules);
+  Units units;
+  long long before = 0, total = 0, border = 0;
+  Pair v;
+  bool clean = false, plain = false;
+#pragma unroll 1
+  for (int turn = 0;; ++turn) {
+    v = sum_granules<T>(row, g0, g1, run, slots[warp]);
+    if (turn == 0) cluster_wait();
+    if (lane < cluster) {
+      st_cluster(&sums[turn][w], lane, v.hi, v.lo);
+      if (w == 0) st_cluster(&sums[turn][kVerifySums], lane, rejected ? 1.f : 0.f, 0.f);
     }
-    __syncthreads();
-    // Nothing left of p: no residual (the rows are not what they should be), so p itself.
-    if (found_total > 0 || !again) break;
-    if (live) row.set(row.p, nullptr, a.V, -1);
-    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+    // Every warp: what lies before its stretch, and in all.
+    float about = 0.f;
+#pragma unroll 1
+    for (int k = lane; k < warps; k += 32) about += sums[turn][k].x;
+#pragma unroll 1
+    for (int x = 16; x > 0; x >>= 1) about += __shfl_xor_sync(0xffffffffu, about, x);
+    if (about > 0.f && about < INFINITY) {
+      units.set(about);
+#pragma unroll 1
+      for (int k = lane; k < warps; k += 32) {
+        const long long x = units.of(sums[turn][k].x, sums[turn][k].y);
+        total += x;
+        if (k < w) before += x;
+      }
+      before = warp_sum(before);
+      total = warp_sum(total);
+      break;
+    }
+    // Seldom, and the same for all warps of the cluster, who decide it by what they have exchanged.
+    if (turn == 2) break;
+    if (about != 0.f) {  // infinite elements: again, one by one, without them
+      if (clean) break;  // a sum that is infinite all the same: outside what the call allows
+      clean = true;
+      row.alike = false;
+    } else {  // nothing is left of p (the rows are not what they should be): p itself
+      if (sums[0][kVerifySums].x == 0.f || plain) break;
+      plain = true;
+      row.q = nullptr;
+      row.x = -1;
+    }
   }
   if (!live) {
     if (good && rank == 0 && threadIdx.x == 0) {
@@ -327,75 +394,44 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const __grid_
     }
     return;
   }
-  const int mine = found_warp;
-  if (mine >= 0 && mine / kVerifyWarps == rank) {
-    // This CTA's warps share that stretch, then one of them its lanes.
-    const float r = a.sample_u[s];
-    const double border = found_total * static_cast<double>(r >= 0.f ? fminf(r, 0x1.fffffep-1f) : 0.f);
-    const int g0 = min(mine * per, row.granules), g1 = min(g0 + per, row.granules);
-    const int part = (g1 - g0 + kVerifyWarps - 1) / kVerifyWarps;
-    const int c0 = min(g0 + warp * part, g1), c1 = min(c0 + part, g1);
-    const double v = warp_sum(sum_granules(row, c0, c1));
-    if (lane == 0) close[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-      // The part that holds the border; rounding apart, there is one.  Else the last with any weight.
-      int k = -1;
-      double before = 0, at = found_before;
-      for (int i = 0; i < kVerifyWarps; ++i) {
-        const double end = at + close[i];
-        if (close[i] > 0) {
-          k = i;
-          before = at;
-          if (end > border) break;
-        }
-        at = end;
-      }
-      if (k >= 0) {
-        const int d0 = min(g0 + k * part, g1), d1 = min(d0 + part, g1);
-        const int each = (d1 - d0 + 31) / 32;
-        const int e0 = min(d0 + lane * each, d1), e1 = min(e0 + each, d1);
-        Pair lane_sum;
-        Granule<T> u, w;
-        for (int g = e0; g < e1; ++g) {
-          row.load_edge(g, u, w);
-          row.add(g, u, w, lane_sum);
-        }
-        const double own = lane_sum.value();
-        double upto = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, upto, o);
-          if (lane >= o) upto += y;
-        }
-        const unsigned above = __ballot_sync(0xffffffffu, own > 0 && before + upto > border);
-        const unsigned any = __ballot_sync(0xffffffffu, own > 0);
-        if (any && lane == (above ? __ffs(above) - 1 : 31 - __clz(any))) {
-          double sum = before + (upto - own);
-          int token = -1;
-          for (int e = max(row.first(e0), 0), end = min(row.first(e1), a.V); e < end; ++e) {
-            float d, rest;
-            row.weight_of(e, d, rest);
-            if (!(d > 0.f)) continue;
-            token = e;
-            sum += static_cast<double>(d) + static_cast<double>(rest);
-            if (sum > border) break;
-          }
-          a.out_tokens[t] = token;
-        }
-      }
-    }
-  } else if (mine < 0 && rank == 0 && threadIdx.x == 0) {
-    a.out_tokens[t] = -1;
-  }
   if (rank == 0 && warp == kVerifyWarps - 1) {
     for (int i = lane; i < n; i += 32)
       if (i != accepted) a.out_tokens[t0 + i] = i < accepted ? a.tokens[t0 + i + 1] : -1;
     if (lane == 0) {
       a.accepted[s] = accepted;
       if (a.kv_out) a.kv_out[s] = a.kv_len[s] - (n - 1 - accepted);
+      if (total == 0) a.out_tokens[t] = -1;
     }
   }
+  // r of the total, cut to a whole number, which no sum of whole numbers can tell from it.
+  unsigned long long r = 0;
+  if (of_all > 0.f) r = __float2ull_rz(fminf(of_all, 0x1.fffffep-1f) * 0x1p64f);
+  border = static_cast<long long>(__umul64hi(static_cast<unsigned long long>(total), r));
+  // One warp's stretch holds it, whose slots' lanes are searched, then a lane's elements.
+  // Their sums are rounded otherwise than the stretch's: where none ends above the border, it is the last with any weight.
+  if (before > border || border >= before + units.of(v.hi, v.lo)) return;
+  int e0 = 0, e1 = 0, token = -1;
+  long long at = before, lane_at = before;
+#pragma unroll 1
+  for (int slot = 0; g0 + slot * 32 * run < g1 && at <= border; ++slot) {
+    const Found f = find_lane(units.of(slots[warp][slot][lane].x, slots[warp][slot][lane].y), at, border);
+    at = f.end;
+    if (f.lane < 0) continue;
+    const int g = g0 + (slot * 32 + f.lane) * run;
+    e0 = row.element(g);
+    e1 = row.element(min(g + run, g1));
+    lane_at = f.before;
+  }
+  at = lane_at;
+#pragma unroll 1
+  for (; e0 < e1 && at <= border; e0 += 32) {
+    float d = 0.f, rest = 0.f;
+    if (e0 + lane < e1) row.element_weight(e0 + lane, d, rest);
+    const Found f = find_lane(units.of(d, rest), at, border);
+    at = f.end;
+    if (f.lane >= 0) token = e0 + f.lane;
+  }
+  if (lane == 0) a.out_tokens[t] = token;
 }
 
 template <typename T>
@@ -407,9 +443,9 @@ int launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return CP_ERR_CUDA;
     known[dev].store(1, std::memory_order_release);
   }
-  // As many CTAs a sequence as fill the card twice, none with less than 512 granules of 16 bytes.
+  // As many CTAs a sequence as the card holds at once, none with less than 512 elements.
   int cluster = 1;
-  while (cluster < kVerifyMaxCluster && a.B * cluster < 2 * 152 && a.V / cluster > 1024) cluster *= 2;
+  while (cluster < kVerifyMaxCluster && a.B * cluster * 2 <= kVerifyResident * 152 && a.V / cluster > 1024) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * cluster);
   cfg.blockDim = dim3(kVerifyThreads);
