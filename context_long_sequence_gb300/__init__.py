@@ -710,7 +710,7 @@ def _dtype_code(x):
 def _current_stream(where, dev, stream):
     """The stream of a call on device number `dev`, which has to be the current one."""
     import torch
-    if dev < 0 or not torch.cuda.is_available() or torch._C._cuda_getDevice() != dev:
+    if dev < 0 or torch._C._cuda_getDevice() != dev:
         _refuse(where, f"the tensors are on device {dev}, which is not the current CUDA device")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 

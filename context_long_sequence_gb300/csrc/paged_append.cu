@@ -27,7 +27,7 @@
 namespace cpattn {
 namespace {
 
-constexpr int kAppendWarps = 4;
+constexpr int kAppendWarps = 2;
 constexpr int kAhead = 4;            // groups of heads whose loads are in flight together
 constexpr int kFillWarps = 152 * 32;  // warps that keep the memory busy
 

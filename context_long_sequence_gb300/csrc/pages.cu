@@ -12,8 +12,11 @@
 // The three calls that change tables are bound by latency: a few dependent
 // loads and a count of refs (4 bytes a page).  Each is one cluster of CTAs, so that its
 // steps are separated by the cluster's hardware barrier, not by launches, and
-// their counts are exchanged through distributed shared memory.  The copies are bound
-// by memory.
+// their counts are exchanged through distributed shared memory.  refs is cut into
+// up to 2048 chunks, dealt out among the warps in turn, as the free pages of the lowest numbers lie together;
+// their finders only list them, and all threads of the CTA place them in the
+// tables (in one stretch a warp, and placed where they are found, 30K pages of a million took 57 us).
+// The copies are bound by memory.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -28,19 +31,43 @@ namespace {
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxTableRows = kMaxEntries;
-constexpr int kRowsPerThread = kMaxTableRows / kThreads;
+constexpr int kChunks = 2048;  // of refs
+constexpr int kList = 16384;   // pages that a call places at a time
+constexpr int kQueue = 1024;
+constexpr int kFirstPart = 65536;
 
-__device__ __forceinline__ unsigned cluster_rank() {
+// Shared memory of a CTA.
+struct PagesShared {
+  int start[kMaxTableRows + 1];  // pages that the rows before take
+  int warp_sums[kWarps];
+  int free_before[kChunks + 1];  // free pages in the chunks before
+  int counts[kChunks];           // free pages of this CTA's chunks: number i is chunk i * cluster + rank
+  int moved;
+  int queued, queue[kQueue];     // rows with many pages to let go
+  int listed;
+  int2 list[kList + 256];        // free pages that this CTA has found, and how many lie before each
+};
+extern __shared__ __align__(16) unsigned char pages_shared[];
+
+__device__ __forceinline__ int cluster_rank() {
   unsigned r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
+  return static_cast<int>(r);
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 // All threads of the cluster; what they wrote before, to global memory too, is
 // seen after (read past L1 where this kernel itself has written).
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void cluster_barrier(int cluster) {
+  if (cluster == 1) {
+    __syncthreads();
+  } else {
+    cluster_arrive();
+    cluster_wait();
+  }
 }
-__device__ __forceinline__ int ld_cluster(const int* local, unsigned rank) {
+// What is at the address of `local` in the shared memory of CTA `rank`; v to it.
+__device__ __forceinline__ int ld_cluster(const int* local, int rank) {
   const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
   uint32_t remote;
   int v;
@@ -48,21 +75,17 @@ __device__ __forceinline__ int ld_cluster(const int* local, unsigned rank) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
   return v;
 }
+__device__ __forceinline__ void st_cluster(int* local, int rank, int v) {
+  const uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(rank));
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(remote), "r"(v) : "memory");
+}
 
 struct Table {
   int rows, columns;
   int32_t* pages;
   int32_t* held;
-};
-
-// Each warp of the cluster counts its own stretch of refs, a multiple of 128 pages.
-struct Stretch {
-  int lo, hi;
-  __device__ __forceinline__ Stretch(int pages, int warp, int warps) {
-    const int per = ((pages + warps - 1) / warps + 127) & ~127;
-    lo = static_cast<int>(min(static_cast<long long>(warp) * per, static_cast<long long>(pages)));
-    hi = static_cast<int>(min(static_cast<long long>(lo) + per, static_cast<long long>(pages)));
-  }
 };
 
 // refs of four pages; -1 behind the last.
@@ -78,96 +101,158 @@ __device__ __forceinline__ unsigned free_bits(const int4& v) {
   return (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
 }
 
-// Free pages of the warp's stretch.
-__device__ __forceinline__ int count_free(const int32_t* refs, const Stretch& s, int pages) {
-  constexpr int kAhead = 4;
-  const int lane = threadIdx.x & 31;
-  int n = 0;
-  for (int p = s.lo; p < s.hi; p += 128 * kAhead) {
-    int4 v[kAhead];
+// refs in chunks of a multiple of 128 pages; warp `gw` of the cluster has every warps-th.
+// It goes through a chunk 128 pages at a time, four to a lane.
+struct Chunks {
+  const int32_t* refs;
+  int pages, size, count, gw, warps;
+  unsigned long long mask;  // the lane's free pages in the first 16 such times
+  __device__ __forceinline__ Chunks(const int32_t* r, int n, int warp, int all) : refs(r), pages(n), gw(warp), warps(all), mask(0) {
+    const int most = all == kWarps ? kWarps : kChunks;  // one CTA: a chunk a warp
+    size = ((n + most - 1) / most + 127) & ~127;
+    count = (n + size - 1) / size;
+  }
+  // Leaves the free pages of all chunks before each in sh.free_before (the last
+  // entry: all).  All threads of the cluster; has a barrier of it, and arrives
+  // at another, which no CTA may leave without (leave).  A CTA runs this once and its code
+  // comes from L2, some 12 clocks an instruction: it is written to be short.
+  __device__ __forceinline__ void count_free(PagesShared& sh, int cluster) {
+    constexpr int kAhead = 4;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int time = 0, sum = 0;
+    int load_chunk = gw, load_at = 4 * lane, chunk = gw, at = 0;  // the next to load and to count
+#pragma unroll 1
+    while (chunk < count) {
+      int4 v[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int at = p + 128 * i + 4 * lane;
-      v[i] = p + 128 * i < s.hi ? load_refs(refs, at, pages) : make_int4(-1, -1, -1, -1);
+      for (int i = 0; i < kAhead; ++i) {
+        const long long p = static_cast<long long>(load_chunk) * size + load_at;
+        v[i] = make_int4(-1, -1, -1, -1);
+        if (load_chunk < count && p + 4 <= pages) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + p));
+        load_at += 128;
+        if (load_at >= size) load_at = 4 * lane, load_chunk += warps;
+      }
+      unsigned all = 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) all |= free_bits(v[i]) << 4 * i;
+#pragma unroll 1
+      for (int i = 0; i < kAhead && chunk < count; ++i, ++time) {
+        unsigned bits = all & 15u;
+        all >>= 4;
+        const int p = chunk * size + at + 4 * lane;
+        if (p < pages && p + 4 > pages) bits = free_bits(load_refs(refs, p, pages));
+        if (time < 16) mask |= static_cast<unsigned long long>(bits) << 4 * time;
+        sum += __popc(bits);
+        at += 128;
+        if (at >= size) {
+          sum = __reduce_add_sync(0xffffffffu, sum);
+          if (lane == 0) sh.counts[chunk / cluster] = sum;
+          sum = at = 0;
+          chunk += warps;
+        }
+      }
     }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) n += __popc(free_bits(v[i]));
-  }
-  return __reduce_add_sync(0xffffffffu, n);
-}
-
-// f(page, free pages before it) for the free pages of the warp's stretch, of
-// which `before` lie before it, as long as fewer than `most` do.
-template <typename F>
-__device__ __forceinline__ void each_free(const int32_t* refs, const Stretch& s, int pages, int before, int most, F&& f) {
-  const int lane = threadIdx.x & 31;
-  const unsigned lower = (1u << lane) - 1;
-  for (int p = s.lo; p < s.hi && before < most; p += 128) {
-    const int at = p + 4 * lane;
-    const unsigned bits = free_bits(load_refs(refs, at, pages));
-    int mine = before, all = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned b = __ballot_sync(0xffffffffu, bits >> i & 1);
-      mine += __popc(b & lower);
-      all += __popc(b);
+    cluster_barrier(cluster);
+    const int blocks = ((count + cluster - 1) / cluster + 31) / 32;  // of a CTA's chunks
+#pragma unroll 1
+    for (int b = warp; b < blocks * cluster; b += kWarps) {
+      const int from = b / blocks, i = (b - from * blocks) * 32 + lane, c = i * cluster + from;
+      if (c < count) sh.free_before[c] = cluster == 1 ? sh.counts[i] : ld_cluster(&sh.counts[i], from);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (bits >> i & 1) f(at + i, mine++);
-    before += all;
+    if (cluster > 1) cluster_arrive();
+    __syncthreads();
+    // Running sums, two chunks to a thread.
+    const int c = 2 * threadIdx.x, x = c < count ? sh.free_before[c] : 0, y = c + 1 < count ? sh.free_before[c + 1] : 0;
+    int upto = x + y;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += z;
+    }
+    if (lane == 31) sh.warp_sums[warp] = upto;
+    __syncthreads();
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sums[lane] : 0) + upto - x - y;
+    if (c <= count) sh.free_before[c] = before;
+    if (c + 1 <= count) sh.free_before[c + 1] = before + x;
+    if (c + 2 == count) sh.free_before[count] = before + x + y;
+    __syncthreads();
   }
+  // Behind it no CTA reads this one's shared memory.
+  __device__ __forceinline__ void leave(int cluster) const {
+    if (cluster > 1) cluster_wait();
+  }
+  // Free pages of four of the lane, from page p on of the warp's time number `time`.
+  __device__ __forceinline__ unsigned bits(int p, int time) const {
+    return time < 16 ? static_cast<unsigned>(mask >> 4 * time) & 15u : free_bits(load_refs(refs, p + 4 * (threadIdx.x & 31), pages));
+  }
+  // f(first page, the lane's free bits of it and the three behind, free pages before the first, of all lanes)
+  // for the warp's runs of 128 pages that have free ones numbered base .. end - 1.
+  template <typename F>
+  __device__ __forceinline__ void each_run(const PagesShared& sh, int base, int end, F&& f) const {
+    const unsigned lower = (1u << (threadIdx.x & 31)) - 1;
+    int time = 0;
+#pragma unroll 1
+    for (int chunk = gw; chunk < count; chunk += warps) {
+      int before = sh.free_before[chunk];
+      if (before >= end) break;
+      if (sh.free_before[chunk + 1] <= base) {
+        time += size / 128;
+        continue;
+      }
+#pragma unroll 1
+      for (int at = 0; at < size; at += 128, ++time) {
+        const int p = chunk * size + at;
+        const unsigned b = bits(p, time);
+        int mine = before, all = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned ones = __ballot_sync(0xffffffffu, b >> i & 1);
+          mine += __popc(ones & lower);
+          all += __popc(ones);
+        }
+        if (before + all > base && before < end) f(p + 4 * (threadIdx.x & 31), b, mine, all);
+        before += all;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ int add_up(int a, int b) {  // of numbers from 0 on, no further than INT_MAX
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), static_cast<unsigned>(INT_MAX)));
 }
 
-// Sums over the cluster of one number a warp: the sum of the warps before this
-// one, and of all.  Two cluster barriers.
-__device__ __forceinline__ int cluster_scan(int mine, int cluster, int* warp_sums, int* cta_sum, int* all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) warp_sums[warp] = mine;
-  __syncthreads();
-  const int x = warp_sums[lane];
-  if (threadIdx.x == 0) *cta_sum = 0;
-  __syncthreads();
-  const int here = __reduce_add_sync(0xffffffffu, x);
-  const int before_here = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-  if (threadIdx.x == 0) *cta_sum = here;
-  cluster_barrier();
-  const unsigned rank = cluster_rank();
-  const int other = lane < cluster ? ld_cluster(cta_sum, lane) : 0;
-  *all = __reduce_add_sync(0xffffffffu, other);
-  const int before = before_here + __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? other : 0);
-  cluster_barrier();
-  return before;
-}
-
-// start[r] = need(0) + .. + need(r - 1), cut off at INT_MAX, for 0 <= r <= rows.
+// start[r] = need(0) + .. + need(r - 1), no further than INT_MAX, for 0 <= r <= rows.
 template <typename F>
-__device__ __forceinline__ void scan_rows(int rows, int* start, long long* warp_totals, F&& need) {
+__device__ __forceinline__ void scan_rows(PagesShared& sh, int* start, int rows, F&& need) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int each = (rows + kThreads - 1) / kThreads, r0 = threadIdx.x * each;
-  int x[kRowsPerThread];
-  long long sum = 0;
-#pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
-    x[i] = i < each && r0 + i < rows ? need(r0 + i) : 0;
-    sum += x[i];
+  const int each = (rows + kThreads - 1) / kThreads, r0 = min(static_cast<int>(threadIdx.x) * each, rows), r1 = min(r0 + each, rows);
+  int sum = 0;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    start[r] = need(r);
+    sum = add_up(sum, start[r]);
   }
-  long long upto = sum;
-#pragma unroll
+  int upto = sum;
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto = add_up(upto, y);
   }
-  if (lane == 31) warp_totals[warp] = upto;
+  int at = __shfl_up_sync(0xffffffffu, upto, 1);
+  if (lane == 0) at = 0;
+  if (lane == 31) sh.warp_sums[warp] = upto;
   __syncthreads();
-  long long at = upto - sum;
-  for (int w = 0; w < warp; ++w) at += warp_totals[w];
-#pragma unroll
-  for (int i = 0; i < kRowsPerThread; ++i) {
-    if (i < each && r0 + i < rows) start[r0 + i] = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
-    at += x[i];
+  int before = lane < warp ? sh.warp_sums[lane] : 0;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) before = add_up(before, __shfl_xor_sync(0xffffffffu, before, o));
+  at = add_up(before, at);
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    const int x = start[r];
+    start[r] = at;
+    at = add_up(at, x);
   }
-  if (threadIdx.x == kThreads - 1) start[rows] = static_cast<int>(min(at, static_cast<long long>(INT_MAX)));
+  if (threadIdx.x == kThreads - 1) start[rows] = at;
   __syncthreads();
 }
 
@@ -179,6 +264,60 @@ __device__ __forceinline__ int row_of(const int* start, int rows, int k) {
     if (start[m] <= k) lo = m; else hi = m - 1;
   }
   return lo;
+}
+
+// place(page, k, free) for the k-th free page, k < need as far as there are any;
+// returns how many are free, or fewer, but then `need`.  All threads of the cluster.
+template <typename F>
+__device__ __forceinline__ int take_pages(PagesShared& sh, const int32_t* refs, int pages, int need, int cluster, F&& place) {
+  const int lane = threadIdx.x & 31, rank = cluster_rank();
+  if (threadIdx.x == 0) sh.listed = 0;
+  // Of a large pool the first part is mostly enough.
+  int part = pages > kFirstPart ? max(kFirstPart, pages / 8) : pages;
+#pragma unroll 1
+  while (true) {
+    Chunks chunks(refs, part, (threadIdx.x >> 5) * cluster + rank, cluster * kWarps);
+    chunks.count_free(sh, cluster);
+    const int free_pages = sh.free_before[chunks.count], given = min(need, free_pages);
+    if (free_pages < need && part < pages) {
+      part = pages;
+      chunks.leave(cluster);
+      __syncthreads();
+      continue;
+    }
+    // As many at a time as this CTA's list holds; of the cluster's, mostly all.
+    int mine = cluster == 1 ? given : 0;
+    for (int i = lane; i * cluster + rank < chunks.count && cluster > 1; i += 32)
+      if (sh.free_before[i * cluster + rank] < given) mine += sh.counts[i];
+    if (cluster > 1) mine = __reduce_add_sync(0xffffffffu, mine);
+    const int window = mine <= kList ? given : kList;
+#pragma unroll 1
+    for (int base = 0; base < given; base += window) {
+      const int end = given - base < window ? given : base + window;
+      chunks.each_run(sh, base, end, [&](int page, unsigned bits, int k, int all) {
+        int to = 0;
+        if (lane == 0) to = atomicAdd(&sh.listed, all);
+        to = __shfl_sync(0xffffffffu, to, 0) + k - __shfl_sync(0xffffffffu, k, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (bits >> i & 1) {
+            // The run's free pages have places side by side; those outside the window
+            // leave theirs empty, in a first and a last run.
+            sh.list[to] = make_int2(k >= base && k < end ? page + i : -1, k);
+            ++to, ++k;
+          }
+      });
+      __syncthreads();
+      const int listed = sh.listed;
+      for (int i = threadIdx.x; i < listed; i += kThreads)
+        if (sh.list[i].x >= 0) place(sh.list[i].x, sh.list[i].y, free_pages);
+      __syncthreads();
+      if (threadIdx.x == 0) sh.listed = 0;
+      __syncthreads();
+    }
+    chunks.leave(cluster);
+    return free_pages;
+  }
 }
 
 struct ResizeArgs {
@@ -198,52 +337,73 @@ __device__ __forceinline__ int wanted(const ResizeArgs& a, int r, int held) {
   return held < 0 || held > a.table.columns || want > a.table.columns ? -2 : want;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_resize_kernel(const __grid_constant__ ResizeArgs a, int cluster) {
-  __shared__ int start[kMaxTableRows + 1];
-  __shared__ long long warp_totals[kWarps];
-  __shared__ int warp_sums[kWarps], cta_sum;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(cluster_rank()), gw = rank * kWarps + warp, warps = cluster * kWarps;
+__device__ __forceinline__ void let_go(const ResizeArgs& a, int r, int c) {
+  if (!CP_CHECK_DATA(c >= 0 && c < a.table.columns, a.status)) return;
+  int32_t* entry = a.table.pages + static_cast<size_t>(r) * a.table.columns + c;
+  const int page = *entry;
+  *entry = -1;
+  if (!CP_CHECK_DATA(page >= 0 && page < a.num_pages, a.status)) return;
+  if (!CP_CHECK_DATA(atomicSub(a.refs + page, 1) > 0, a.status)) atomicAdd(a.refs + page, 1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) pages_resize_kernel(const __grid_constant__ ResizeArgs a, int cluster) {
+  constexpr int kFew = 4;  // pages that a row's thread lets go itself
+  PagesShared& sh = *reinterpret_cast<PagesShared*>(pages_shared);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = cluster_rank();
   const int rows = a.table.rows;
+  if (cluster > 1) cluster_arrive();
+  if (threadIdx.x == 0) sh.queued = 0;
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  scan_rows(rows, start, warp_totals, [&](int r) {
+  // Every CTA counts what all rows take; each lets go of the pages of its share of them.
+  scan_rows(sh, sh.start, rows, [&](int r) {
     const int held = a.table.held[r], want = wanted(a, r, held);
-    if (want == -2 && rank == 0) debug_bounds_fail(a.status, __LINE__, CP_TU_ID);
+    if (r % cluster == rank) {
+      if (want == -2) debug_bounds_fail(a.status, __LINE__, CP_TU_ID);
+      if (want >= 0 && want < held) {
+        int k = kQueue;
+        if (held - want > kFew) k = atomicAdd(&sh.queued, 1);
+        if (k < kQueue) {
+          sh.queue[k] = r;
+        } else {
+          for (int c = want; c < held; ++c) let_go(a, r, c);
+        }
+      }
+    }
     return want >= 0 ? max(want - held, 0) : 0;
   });
-  // Pages behind those that a row should hold are let go.
-  for (int r = gw; r < rows; r += warps) {
-    const int held = a.table.held[r], want = wanted(a, r, held);
-    if (want < 0 || !CP_IN_BOUNDS(held <= a.table.columns, a.status)) continue;  // wanted() has looked at held
-    int32_t* pages = a.table.pages + static_cast<size_t>(r) * a.table.columns;
-    for (int c = want + lane; c < held; c += 32) {
-      const int page = pages[c];
-      pages[c] = -1;
-      if (!CP_CHECK_DATA(page >= 0 && page < a.num_pages, a.status)) continue;
-      if (!CP_CHECK_DATA(atomicSub(a.refs + page, 1) > 0, a.status)) atomicAdd(a.refs + page, 1);
+  const int queued = min(sh.queued, kQueue);
+  if (queued > 0) {
+    // Pages of rows with many, shared out to all threads.
+    int* first = sh.free_before;
+    scan_rows(sh, first, queued, [&](int i) {
+      const int r = sh.queue[i], held = a.table.held[r];
+      return max(held - max(wanted(a, r, held), 0), 0);
+    });
+#pragma unroll 1
+    for (int k = threadIdx.x; k < first[queued]; k += kThreads) {
+      const int i = row_of(first, queued, k), r = sh.queue[i];
+      let_go(a, r, a.table.held[r] - 1 - (k - first[i]));
     }
   }
-  const int need = start[rows];
-  cluster_barrier();
+  const int need = sh.start[rows];
+  if (cluster > 1) cluster_wait();
+  cluster_barrier(cluster);
   int free_pages = 0;
-  if (need > 0) {
-    const Stretch s(a.num_pages, gw, warps);
-    const int before = cluster_scan(count_free(a.refs, s, a.num_pages), cluster, warp_sums, &cta_sum, &free_pages);
-    each_free(a.refs, s, a.num_pages, before, min(need, free_pages), [&](int page, int k) {
-      if (k >= need) return;
-      const int r = row_of(start, rows, k);
-      if (start[r + 1] > free_pages) return;  // served in order, as long as pages last
+  if (need > 0)
+    free_pages = take_pages(sh, a.refs, a.num_pages, need, cluster, [&](int page, int k, int free) {
+      const int r = row_of(sh.start, rows, k);
+      if (sh.start[r + 1] > free) return;  // served in order, as long as pages last
       const int want = static_cast<int>((static_cast<long long>(a.tokens[r]) + (1 << a.page_shift) - 1) >> a.page_shift);
-      const int c = want - (start[r + 1] - k);
+      const int c = want - (sh.start[r + 1] - k);
       if (!CP_CHECK_DATA(c >= 0 && c < a.table.columns, a.status)) return;  // only where the arrays change under the kernel
       a.refs[page] = 1;
       a.table.pages[static_cast<size_t>(r) * a.table.columns + c] = page;
     });
-  }
   for (int r = rank * kThreads + threadIdx.x; r < rows; r += cluster * kThreads) {
     const int want = wanted(a, r, a.table.held[r]);
-    const bool ok = want != -2 && (start[r + 1] == start[r] || start[r + 1] <= free_pages);
+    const bool ok = want != -2 && (sh.start[r + 1] == sh.start[r] || sh.start[r + 1] <= free_pages);
     if (ok && want >= 0) a.table.held[r] = want;
     a.served[r] = ok;
   }
@@ -272,46 +432,44 @@ __device__ __forceinline__ int is_child(const ForkArgs& a, int r) {
   return held >= want && held <= a.src.columns && want <= a.dst.columns ? 1 : -1;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_constant__ ForkArgs a, int cluster) {
-  __shared__ int start[kMaxTableRows + 1];
+__global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_constant__ ForkArgs a, int cluster) {
   __shared__ int8_t child[kMaxTableRows];
-  __shared__ long long warp_totals[kWarps];
-  __shared__ int warp_sums[kWarps], cta_sum;
+  PagesShared& sh = *reinterpret_cast<PagesShared*>(pages_shared);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(cluster_rank()), gw = rank * kWarps + warp, warps = cluster * kWarps;
+  const int rank = cluster_rank(), gw = rank * kWarps + warp, warps = cluster * kWarps;
   const int rows = a.dst.rows, rest = (1 << a.page_shift) - 1;
+  if (cluster > 1) cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
-  scan_rows(rows, start, warp_totals, [&](int r) {
+  scan_rows(sh, sh.start, rows, [&](int r) {
     const int c = is_child(a, r);
     child[r] = static_cast<int8_t>(c);
     if (c < 0 && rank == 0) debug_bounds_fail(a.status, __LINE__, CP_TU_ID);
     return c > 0 && (a.tokens[r] & rest) ? 1 : 0;
   });
-  const int need = start[rows];
-  // Every row's data have been read by the whole cluster behind the scan's barriers.
-  const Stretch s(a.num_pages, gw, warps);
-  int free_pages;
-  const int before = cluster_scan(need > 0 ? count_free(a.refs, s, a.num_pages) : 0, cluster, warp_sums, &cta_sum, &free_pages);
-  const int given = min(need, free_pages);
-  each_free(a.refs, s, a.num_pages, before, given, [&](int page, int k) {
-    if (k >= given) return;
-    const int r = row_of(start, rows, k);  // its part page
-    const int t = a.tokens[r], full = t >> a.page_shift, parent = a.parent[r];
-    if (!CP_CHECK_DATA(parent >= 0 && parent < a.src.rows && full < a.dst.columns && full < a.src.columns, a.status)) return;  // as above
-    a.refs[page] = 1;
-    a.dst.pages[static_cast<size_t>(r) * a.dst.columns + full] = page;
-    a.move_src[k] = a.src.pages[static_cast<size_t>(parent) * a.src.columns + full];
-    a.move_dst[k] = page;
-    a.move_tokens[k] = t & rest;
-  });
-  if (rank == 0 && threadIdx.x == 0) *a.count = given;
+  const int need = sh.start[rows];
+  if (cluster > 1) cluster_wait();
+  cluster_barrier(cluster);  // every row's data have been read
+  int free_pages = 0;
+  if (need > 0)
+    free_pages = take_pages(sh, a.refs, a.num_pages, need, cluster, [&](int page, int k, int) {
+      const int r = row_of(sh.start, rows, k);  // its part page
+      const int t = a.tokens[r], full = t >> a.page_shift, parent = a.parent[r];
+      // Only where the arrays change under the kernel.
+      if (!CP_CHECK_DATA(parent >= 0 && parent < a.src.rows && full < a.dst.columns && full < a.src.columns, a.status)) return;
+      a.refs[page] = 1;
+      a.dst.pages[static_cast<size_t>(r) * a.dst.columns + full] = page;
+      a.move_src[k] = a.src.pages[static_cast<size_t>(parent) * a.src.columns + full];
+      a.move_dst[k] = page;
+      a.move_tokens[k] = t & rest;
+    });
+  if (rank == 0 && threadIdx.x == 0) *a.count = min(need, free_pages);
   for (int r = gw; r < rows; r += warps) {
-    const bool ok = child[r] >= 0 && (start[r + 1] == start[r] || start[r + 1] <= free_pages);
+    const bool ok = child[r] >= 0 && (sh.start[r + 1] == sh.start[r] || sh.start[r + 1] <= free_pages);
     if (lane == 0) a.served[r] = ok;
     if (!ok || child[r] == 0) continue;
     const int full = a.tokens[r] >> a.page_shift, parent = a.parent[r];
-    if (!CP_CHECK_DATA(full <= a.dst.columns && full <= a.src.columns && parent >= 0 && parent < a.src.rows, a.status)) continue;
+    if (!CP_CHECK_DATA(full <= a.dst.columns && full <= a.src.columns && parent >= 0 && parent < a.src.rows, a.status)) continue;  // as above
     const int32_t* from = a.src.pages + static_cast<size_t>(parent) * a.src.columns;
     int32_t* to = a.dst.pages + static_cast<size_t>(r) * a.dst.columns;
     for (int c = lane; c < full; c += 32) {
@@ -320,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) pages_fork_kernel(const __grid_const
       if (there) atomicAdd(a.refs + page, 1);
       to[c] = there ? page : -1;
     }
-    if (lane == 0) a.dst.held[r] = full + (start[r + 1] - start[r]);
+    if (lane == 0) a.dst.held[r] = full + (sh.start[r + 1] - sh.start[r]);
   }
 }
 
@@ -339,61 +497,70 @@ struct CompactArgs {
   int32_t* status;
 };
 
-__global__ void __launch_bounds__(kThreads) pages_compact_kernel(const __grid_constant__ CompactArgs a, int cluster) {
-  __shared__ int warp_sums[kWarps], cta_sum, moved_here;
+__global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid_constant__ CompactArgs a, int cluster) {
+  PagesShared& sh = *reinterpret_cast<PagesShared*>(pages_shared);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(cluster_rank()), gw = rank * kWarps + warp, warps = cluster * kWarps;
+  const int rank = cluster_rank(), gw = warp * cluster + rank, warps = cluster * kWarps;
   const int P = a.num_pages;
+  if (cluster > 1) cluster_arrive();
   pdl_wait();
   pdl_launch_dependents();
-  const Stretch s(P, gw, warps);
-  int free_pages;
-  const int before = cluster_scan(count_free(a.refs, s, P), cluster, warp_sums, &cta_sum, &free_pages);
+  Chunks chunks(a.refs, P, gw, warps);
+  if (cluster > 1) cluster_wait();
+  chunks.count_free(sh, cluster);
+  chunks.leave(cluster);
   // Held pages from number `used` on move to the free ones below it, which are
-  // as many: `moves`, the free pages before number `used`, known to the warp of that stretch.
-  const int used = P - free_pages;
-  const int per = ((P + warps - 1) / warps + 127) & ~127;
-  const int owner = used / per;  // P / per at most, that is, perhaps behind the last warp
-  if (gw == owner) {
-    int n = before;
-    each_free(a.refs, s, P, before, INT_MAX, [&](int page, int) { n += page < used; });
-    n = before + __reduce_add_sync(0xffffffffu, n - before);
-    if (lane == 0) moved_here = n;
+  // as many: `moves`, the free pages before number `used`, counted by the warp of that chunk.
+  const int used = P - sh.free_before[chunks.count], chunk_of_used = used / chunks.size;
+  if (used < P && chunk_of_used % warps == gw) {
+    int n = 0;
+    for (int p = chunk_of_used * chunks.size; p < used; p += 128) {
+      const unsigned bits = free_bits(load_refs(a.refs, p + 4 * lane, P));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += (bits >> i & 1) && p + 4 * lane + i < used;
+    }
+    n = sh.free_before[chunk_of_used] + __reduce_add_sync(0xffffffffu, n);
+    if (cluster == 1) sh.moved = n;
+    else if (lane < cluster) st_cluster(&sh.moved, lane, n);
   }
-  cluster_barrier();
-  const int moves = used < P ? ld_cluster(&moved_here, owner / kWarps) : 0;
+  cluster_barrier(cluster);
+  const int moves = used < P ? sh.moved : 0;
   // Free pages below `used` in order, held ones from there on in order.
   const unsigned lower = (1u << lane) - 1;
-  int n = before;
-  for (int p = s.lo; p < s.hi; p += 128) {
-    const int at = p + 4 * lane;
-    const int4 v = load_refs(a.refs, at, P);
-    const unsigned bits = free_bits(v);
-    int mine = n;
+#pragma unroll 1
+  for (int chunk = gw; chunk < chunks.count; chunk += warps) {
+    int n = sh.free_before[chunk];
+#pragma unroll 1
+    for (int p = chunk * chunks.size; p < min((chunk + 1) * chunks.size, P); p += 128) {
+      const int at = p + 4 * lane;
+      const int4 v = load_refs(a.refs, at, P);
+      const unsigned bits = free_bits(v);
+      int rank_of = n;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned b = __ballot_sync(0xffffffffu, bits >> i & 1);
-      mine += __popc(b & lower);
-      n += __popc(b);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int page = at + i, held = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-      if (page >= P) break;
-      const bool free_page = bits >> i & 1;
-      if (a.refs_out != a.refs) a.refs_out[page] = page < used ? held : 0;
-      if (page < used && free_page) {
-        if (CP_CHECK_DATA(mine < P / 2, a.status)) a.move_dst[mine] = page;
-      } else if (page >= used) {
-        a.to[page] = -1;
-        // page - mine held ones lie before it, used - moves of them below `used`.
-        const int k = page - mine - (used - moves);
-        if (!free_page && CP_CHECK_DATA(k >= 0 && k < P / 2, a.status)) a.move_src[k] = page;
+      for (int i = 0; i < 4; ++i) {
+        const unsigned b = __ballot_sync(0xffffffffu, bits >> i & 1);
+        rank_of += __popc(b & lower);
+        n += __popc(b);
       }
-      mine += free_page;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int page = at + i, held = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+        if (page >= P) break;
+        const bool free_page = bits >> i & 1;
+        if (a.refs_out != a.refs) a.refs_out[page] = page < used ? held : 0;
+        if (page < used && free_page) {
+          if (CP_CHECK_DATA(rank_of < P / 2, a.status)) a.move_dst[rank_of] = page;
+        } else if (page >= used) {
+          a.to[page] = -1;
+          // page - rank_of held ones lie before it, used - moves of them below `used`.
+          const int k = page - rank_of - (used - moves);
+          if (!free_page && CP_CHECK_DATA(k >= 0 && k < P / 2, a.status)) a.move_src[k] = page;
+        }
+        rank_of += free_page;
+      }
     }
   }
-  cluster_barrier();
+  cluster_barrier(cluster);
   for (int i = rank * kThreads + threadIdx.x; i < min(moves, P / 2); i += cluster * kThreads) {
     const int src = __ldcg(a.move_src + i), dst = __ldcg(a.move_dst + i);
     // These and the checks above fail only where refs changes under the kernel.
@@ -522,10 +689,10 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
   }
 }
 
-// CTAs of a call that looks at `pages` counts and `rows` rows.
-int cluster_for(int pages, int rows) {
+// CTAs of a call that looks at `pages` counts and `rows` rows, of which a CTA does `each` well.
+int cluster_for(int pages, int rows, int each) {
   int c = 1;
-  while (c < kMaxCluster && (pages > 8192 * c || rows > 256 * c)) c *= 2;
+  while (c < kMaxCluster && (pages > 32768 * c || rows > each * c)) c *= 2;
   return c;
 }
 
@@ -534,12 +701,15 @@ int launch_cluster(std::atomic<int> (&known)[64], K kernel, const A& a, int clus
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CP_ERR_CUDA;
   if (!known[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return CP_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(PagesShared)) != cudaSuccess)
+      return CP_ERR_CUDA;
     known[dev].store(1, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = sizeof(PagesShared);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -596,7 +766,7 @@ int cp_pages_resize(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, co
   if (!a.status) return CP_ERR_CUDA;
   NvtxRange range("cp_pages_resize");
   static std::atomic<int> known[64];
-  return launch_cluster(known, pages_resize_kernel, a, cluster_for(num_pages, table->rows), stream);
+  return launch_cluster(known, pages_resize_kernel, a, cluster_for(num_pages, table->rows, 1024), stream);
 }
 
 int cp_pages_fork(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, const cp_page_table_t* src, const cp_page_table_t* dst,
@@ -627,7 +797,7 @@ int cp_pages_fork(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, cons
   if (!a.status) return CP_ERR_CUDA;
   NvtxRange range("cp_pages_fork");
   static std::atomic<int> known[64];
-  return launch_cluster(known, pages_fork_kernel, a, cluster_for(num_pages, dst->rows), stream);
+  return launch_cluster(known, pages_fork_kernel, a, cluster_for(num_pages, dst->rows, 64), stream);
 }
 
 int cp_pages_workspace_size(int32_t num_pages, size_t* bytes) {
@@ -683,7 +853,7 @@ int cp_pages_compact(const cp_paged_t* plan, int32_t num_pages, const int32_t* r
   b.status = a.status;
   NvtxRange range("cp_pages_compact");
   static std::atomic<int> known[64];
-  rc = launch_cluster(known, pages_compact_kernel, a, cluster_for(num_pages, 0), stream);
+  rc = launch_cluster(known, pages_compact_kernel, a, cluster_for(num_pages, 0, 1), stream);
   if (rc != CP_OK) return rc;
   const unsigned grid = static_cast<unsigned>(chunks < 152 * 8 ? chunks : 152 * 8);
   return launch(pages_rename_kernel, grid, kRenameThreads, 0, stream, b);

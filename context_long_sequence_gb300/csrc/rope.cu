@@ -7,9 +7,10 @@
 // position.  The rotation is in fp32 with one rounding at the end.
 //
 // Bound by memory: each value is read once and written once.  As in the
-// append a warp owns a token (or a share of its heads), a lane 16 elements of
-// a head in two pieces that hold both halves of eight pairs, so that its eight
-// sines and cosines serve every head it visits, queries and keys alike.
+// append a warp owns a token (or a share of its heads), a lane two pieces of 16 bytes of
+// a head that hold both halves of eight pairs (four in fp32), so that its
+// sines and cosines serve every head it visits, queries and keys alike.  The
+// warp's lanes compute a pair each and hand them on through shared memory.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -29,7 +30,7 @@ namespace cpattn {
 namespace {
 
 constexpr int kRopeMaxDim = 256;
-constexpr int kRopeWarps = 4;
+constexpr int kRopeWarps = 2;
 constexpr int kRopeFillWarps = 152 * 32;  // warps that keep the memory busy
 
 struct RopeJob {
@@ -40,7 +41,7 @@ struct RopeJob {
 };
 
 struct RopeArgs {
-  int n, d, rope_dim, interleaved, inverse, heads, jobs;
+  int n, d, rope_dim, interleaved, inverse, heads, jobs, axes;
   const int32_t* positions;  // [axes][n]
   RopeJob job[CP_ROPE_MAX_JOBS];
   uint64_t turns[kRopeMaxDim / 2];
@@ -48,77 +49,76 @@ struct RopeArgs {
   int32_t* status;
 };
 
-// Eight elements as they lie in memory.
-template <typename T>
+// N elements as they lie in memory, 8 or 16 bytes at a time.
+template <typename T, int N>
 struct Piece {
-  uint4 r[sizeof(T) / 2];
+  static constexpr int kBytes = N * static_cast<int>(sizeof(T));
+  using Vector = typename std::conditional<kBytes % 16 == 0, uint4, uint2>::type;
+  static constexpr int kVectors = kBytes / static_cast<int>(sizeof(Vector));
+  Vector r[kVectors];
   __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < kVectors; ++i) r[i] = reinterpret_cast<const Vector*>(p)[i];
   }
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r[i];
+    for (int i = 0; i < kVectors; ++i) reinterpret_cast<Vector*>(p)[i] = r[i];
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  __device__ __forceinline__ void get(float (&x)[N]) const {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(r);
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < N; ++i) x[i] = __uint_as_float(w[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < N / 2; ++i) {
         const float2 u = Elem<T>::unpack(w[i]);
         x[2 * i] = u.x;
         x[2 * i + 1] = u.y;
       }
     }
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
+  __device__ __forceinline__ void set(const float (&x)[N]) {
     uint32_t* w = reinterpret_cast<uint32_t*>(r);
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(x[i]);
+      for (int i = 0; i < N; ++i) w[i] = __float_as_uint(x[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = Elem<T>::pack(x[2 * i], x[2 * i + 1]);
+      for (int i = 0; i < N / 2; ++i) w[i] = Elem<T>::pack(x[2 * i], x[2 * i + 1]);
     }
   }
 };
 
+// Elements of a lane's piece of a head: 16 bytes.
+template <typename TI>
+constexpr __host__ __device__ int rope_piece() {
+  return 16 / static_cast<int>(sizeof(TI));
+}
+
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeArgs args, unsigned units) {
-  constexpr int kAhead = sizeof(TI) == 2 ? 4 : 2;  // groups of heads whose loads are in flight together
+  constexpr int N = rope_piece<TI>();
+  constexpr int kAhead = 2;  // groups of heads whose loads are in flight together
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
   const unsigned t = w / units, unit = w - t * units;
   if (t >= static_cast<unsigned>(args.n)) return;
-  const int lph = args.d / 16, hpg = 32 / lph;  // lanes per head, heads per group
+  const int lph = args.d / (2 * N), hpg = 32 / lph;  // lanes per head, heads per group
   const int sub = lane / lph, j = lane - sub * lph;
-  if (sub >= hpg) return;
-  const bool rotated = j < args.rope_dim / 16, halves = rotated && !args.interleaved;
-  const int ea = halves ? 8 * j : 16 * j;  // first elements of the lane's two pieces
-  const int eb = halves ? args.rope_dim / 2 + 8 * j : 16 * j + 8;
-  float c[8], sn[8];
-  if (rotated) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pos = args.positions[static_cast<size_t>(args.axis[8 * j + i]) * args.n + t];
-      sincos_turns(pos, args.turns[8 * j + i], &sn[i], &c[i]);
-      if (args.inverse) sn[i] = -sn[i];
-    }
-  }
-  const int groups = (args.heads + hpg - 1) / hpg;
-  for (int g0 = unit; g0 < groups; g0 += kAhead * units) {
-    Piece<TI> a[kAhead], b[kAhead];
-    TO* dst[kAhead];
+  const bool rotated = j < args.rope_dim / (2 * N), halves = rotated && !args.interleaved;
+  const int ea = halves ? N * j : 2 * N * j;  // first elements of the lane's two pieces
+  const int eb = halves ? args.rope_dim / 2 + N * j : 2 * N * j + N;
+  Piece<TI, N> a[kAhead], b[kAhead];
+  TO* dst[kAhead];
+  const auto load = [&](int g0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int h = (g0 + i * static_cast<int>(units)) * hpg + sub;
       dst[i] = nullptr;
-      if (h >= args.heads || !CP_IN_BOUNDS(ea + 8 <= args.d && eb + 8 <= args.d, args.status)) continue;
+      if (sub >= hpg || h >= args.heads || !CP_IN_BOUNDS(ea + N <= args.d && eb + N <= args.d, args.status)) continue;
       int k = 0;
 #pragma unroll
       for (int x = 1; x < CP_ROPE_MAX_JOBS; ++x) k += x < args.jobs && h >= args.job[x].first;
@@ -129,41 +129,70 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
       a[i].load(src + ea);
       b[i].load(src + eb);
     }
+  };
+  load(unit);  // on their way while the angles are computed
+  __shared__ __align__(16) float2 turned[kRopeWarps][kRopeMaxDim / 2];  // cosine, sine
+  float2* mine = turned[threadIdx.x >> 5];
+  const int of_lane = lane < args.axes ? args.positions[static_cast<size_t>(lane) * args.n + t] : 0;
+#pragma unroll 1
+  for (int i = 0; i < args.rope_dim / 2; i += 32) {
+    const int pair = min(i + lane, args.rope_dim / 2 - 1);
+    float c, sn;
+    sincos_turns(__shfl_sync(0xffffffffu, of_lane, args.axis[pair]), args.turns[pair], &sn, &c);
+    mine[pair] = make_float2(c, args.inverse ? -sn : sn);  // the last one's lanes agree
+  }
+  __syncwarp();
+  float c[N], sn[N];
+  if (rotated) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(mine + N * j)[i];
+      c[2 * i] = v.x;
+      sn[2 * i] = v.y;
+      c[2 * i + 1] = v.z;
+      sn[2 * i + 1] = v.w;
+    }
+  }
+  const int groups = (args.heads + hpg - 1) / hpg;
+  for (int g0 = unit;;) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (!dst[i]) continue;
-      float x[8], y[8];
+      float x[N], y[N];
       a[i].get(x);
       b[i].get(y);
       if (halves) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
           const float u = x[e], v = y[e];
           x[e] = u * c[e] - v * sn[e];
           y[e] = v * c[e] + u * sn[e];
         }
       } else if (rotated) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < N / 2; ++e) {
           const float u = x[2 * e], v = x[2 * e + 1], p = y[2 * e], q = y[2 * e + 1];
           x[2 * e] = u * c[e] - v * sn[e];
           x[2 * e + 1] = v * c[e] + u * sn[e];
-          y[2 * e] = p * c[4 + e] - q * sn[4 + e];
-          y[2 * e + 1] = q * c[4 + e] + p * sn[4 + e];
+          y[2 * e] = p * c[N / 2 + e] - q * sn[N / 2 + e];
+          y[2 * e + 1] = q * c[N / 2 + e] + p * sn[N / 2 + e];
         }
       }
-      Piece<TO> o;
+      Piece<TO, N> o;
       o.set(x);
       o.store(dst[i] + ea);
       o.set(y);
       o.store(dst[i] + eb);
     }
+    g0 += kAhead * static_cast<int>(units);
+    if (g0 >= groups) break;
+    load(g0);
   }
 }
 
 template <typename TI, typename TO>
 int launch_rope(const RopeArgs& a, cudaStream_t stream) {
-  const int hpg = 32 / (a.d / 16), groups = (a.heads + hpg - 1) / hpg;
+  const int hpg = 32 / (a.d / (2 * rope_piece<TI>())), groups = (a.heads + hpg - 1) / hpg;
   // Few tokens: a warp for each group of heads, for latency.  Many: a warp
   // takes more of its token's heads, as one set of sines serves them all.
   int units = (kRopeFillWarps + a.n - 1) / a.n;
@@ -244,6 +273,7 @@ int cp_rope(const cp_rope_t* r, int32_t n_tokens, const int32_t* positions, int3
   a.interleaved = d.rope_interleaved;
   a.inverse = inverse;
   a.jobs = n_jobs;
+  a.axes = d.rope_axes;
   a.positions = positions;
   for (int j = 0; j < d.rope_dim / 2; ++j) a.turns[j] = r->turns[j], a.axis[j] = r->axis[j];
   a.status = device_status_ptr();
