@@ -521,6 +521,12 @@ def _cast(array, t):
     return None if array is None else ctypes.cast(array, ctypes.POINTER(t))
 
 
+def _current_functions():
+    """torch's functions for the current device and its stream, and torch.int32."""
+    import torch
+    return tuple(getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream")), torch.int32
+
+
 class PagedPlan:
     """Owns a cp_paged_t (cp_paged_create / cp_paged_destroy): the shapes and
     bounds of serving steps over a paged cache.  The kernels go by the bounds:
@@ -557,7 +563,7 @@ class PagedPlan:
         # A decode step's calls take the host about as long as the GPU: torch's
         # functions that they need are looked up once (a torch without CUDA has
         # none; its tensors are refused before they would be called).
-        self._current = tuple(getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+        self._current, self._i32 = _current_functions()
 
     @property
     def handle(self):
@@ -707,12 +713,12 @@ def _dtype_code(x):
     return _DTYPES.get(x.dtype)
 
 
-def _current_stream(where, dev, stream):
+def _current_stream(where, plan, dev, stream):
     """The stream of a call on device number `dev`, which has to be the current one."""
-    import torch
-    if dev < 0 or torch._C._cuda_getDevice() != dev:
+    current, raw_stream = plan._current
+    if dev < 0 or current() != dev:
         _refuse(where, f"the tensors are on device {dev}, which is not the current CUDA device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return raw_stream(dev) if stream is None else _stream(stream)
 
 
 def cp_verify_drafts(plan: PagedPlan, batch: PagedBatch, tokens, p, q, accept_u, sample_u, accepted, out_tokens, kv_len_out=None,
@@ -720,35 +726,35 @@ def cp_verify_drafts(plan: PagedPlan, batch: PagedBatch, tokens, p, q, accept_u,
     """p, q: [n_tokens][vocab] of one type (q may be None); tokens, out_tokens:
     int32 [n_tokens]; accept_u: float32 [n_tokens]; sample_u: float32 [n_seqs];
     accepted, kv_len_out: int32 [n_seqs]."""
-    import torch
     where, dev, B, N = "cp_verify_drafts", batch._dev, batch.n_seqs, batch.n_tokens
-    i32, f32 = torch.int32, torch.float32
+    i32, f32 = plan._i32, plan.lse_dtype
     for name, x, n, t in (("tokens", tokens, N, i32), ("accept_u", accept_u, N, f32), ("sample_u", sample_u, B, f32),
                           ("accepted", accepted, B, i32), ("out_tokens", out_tokens, N, i32), ("kv_len_out", kv_len_out, B, i32)):
         if x is None and name == "kv_len_out":
             continue
         if x.dtype is not t or x.shape != (n,) or not x.is_contiguous() or x.get_device() != dev:
             _refuse(where, f"{name} is a contiguous [{n}] {t} on device {dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    code = _dtype_code(p)
+    code, shape = _dtype_code(p), p.shape
     for x in (p, q):
-        if x is not None and (code is None or x.dtype is not p.dtype or x.dim() != 2 or x.shape[0] != N or x.shape[1] != p.shape[1]
-                              or (x.stride(1) != 1 and x.shape[1] > 1) or x.get_device() != dev):
+        if x is not None and (code is None or x.dtype is not p.dtype or len(shape) != 2 or x.shape != shape or shape[0] != N
+                              or (x.stride(1) != 1 and shape[1] > 1) or x.get_device() != dev):
             _refuse(where, f"p and q are [{N}][vocab] bfloat16, float16 or float32 alike with contiguous rows on device {dev}, got "
                            f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
-    V = p.shape[1]
+    V = shape[1]
     many = N > 1  # the stride of a dimension of one element says nothing
     v = cp_verify_t(V, code, p.data_ptr(), p.stride(0) if many else V, None if q is None else q.data_ptr(),
                     0 if q is None else q.stride(0) if many else V, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
                     accepted.data_ptr(), out_tokens.data_ptr(), None if kv_len_out is None else kv_len_out.data_ptr())
-    rc = _L().cp_verify_drafts(plan._h, batch.ref, ctypes.addressof(v), _current_stream(where, dev, stream))
+    rc = _L().cp_verify_drafts(plan._h, batch.ref, ctypes.addressof(v), _current_stream(where, plan, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 
 
-def _int_array(where, name, x, shape, dev):
+def _int_array(where, name, x, shape, dev, i32=None):
     """Address of a contiguous int32 tensor of this shape on device number `dev`."""
-    import torch
-    if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
+    if i32 is None:
+        i32 = _current_functions()[1]
+    if x.dtype is not i32 or x.shape != shape or not x.is_contiguous() or x.get_device() != dev:
         _refuse(where, f"{name} is a contiguous int32 {list(shape)} on device {dev}, got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
@@ -792,25 +798,24 @@ class PageMoves:
         self.ref = ctypes.addressof(self.c)
 
 
-def _page_refs(where, refs, *others):
-    """The checks that all calls on refs share: num_pages, address."""
-    import torch
-    dev = refs.get_device()
-    if refs.dtype is not torch.int32 or refs.dim() != 1 or not refs.is_contiguous():
+def _page_refs(where, plan, refs, *others):
+    """The checks that all calls on refs share: num_pages, address, device number."""
+    dev, shape = refs.get_device(), refs.shape
+    if refs.dtype is not plan._i32 or len(shape) != 1 or not refs.is_contiguous():
         _refuse(where, f"refs is a contiguous int32 [pages], got {refs.dtype} {tuple(refs.shape)}")
     for x in others:
         if x._dev != dev:
             _refuse(where, f"refs is on {refs.device}, a table or the moves on device {x._dev}")
-    return refs.shape[0], refs.data_ptr(), dev
+    return shape[0], refs.data_ptr(), dev
 
 
 def cp_pages_resize(plan: PagedPlan, refs, table: PageTable, tokens, served, stream=None):
     """Row r of `table` comes to hold the pages of tokens[r] tokens (0: it is freed; -1: it is left alone)."""
-    where = "cp_pages_resize"
-    n, address, dev = _page_refs(where, refs, table)
+    where, i32 = "cp_pages_resize", plan._i32
+    n, address, dev = _page_refs(where, plan, refs, table)
     rows = table.shape[:1]
-    ta, sa = _int_array(where, "tokens", tokens, rows, dev), _int_array(where, "served", served, rows, dev)
-    rc = _L().cp_pages_resize(plan._h, n, address, table.ref, ta, sa, _current_stream(where, dev, stream))
+    ta, sa = _int_array(where, "tokens", tokens, rows, dev, i32), _int_array(where, "served", served, rows, dev, i32)
+    rc = _L().cp_pages_resize(plan._h, n, address, table.ref, ta, sa, _current_stream(where, plan, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 
@@ -818,12 +823,12 @@ def cp_pages_resize(plan: PagedPlan, refs, table: PageTable, tokens, served, str
 def cp_pages_fork(plan: PagedPlan, refs, src: PageTable, dst: PageTable, parent, tokens, moves: PageMoves, served, stream=None):
     """Row r of `dst` becomes a copy of the first tokens[r] tokens of row
     parent[r] (-1: none) of `src`; `moves` gets the copies to run with cp_pages_copy."""
-    where = "cp_pages_fork"
-    n, address, dev = _page_refs(where, refs, src, dst, moves)
+    where, i32 = "cp_pages_fork", plan._i32
+    n, address, dev = _page_refs(where, plan, refs, src, dst, moves)
     rows = dst.shape[:1]
-    pa, ta = _int_array(where, "parent", parent, rows, dev), _int_array(where, "tokens", tokens, rows, dev)
-    sa = _int_array(where, "served", served, rows, dev)
-    rc = _L().cp_pages_fork(plan._h, n, address, src.ref, dst.ref, pa, ta, moves.ref, sa, _current_stream(where, dev, stream))
+    pa, ta = _int_array(where, "parent", parent, rows, dev, i32), _int_array(where, "tokens", tokens, rows, dev, i32)
+    sa = _int_array(where, "served", served, rows, dev, i32)
+    rc = _L().cp_pages_fork(plan._h, n, address, src.ref, dst.ref, pa, ta, moves.ref, sa, _current_stream(where, plan, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 
@@ -844,7 +849,7 @@ def cp_pages_compact(plan: PagedPlan, refs, tables, moves: PageMoves, workspace,
     """The held pages become the first ones; tables and refs in place unless
     refs_out and tables_out (PageTables alike) are given.  `moves` gets the copies to run."""
     where = "cp_pages_compact"
-    n, address, dev = _page_refs(where, refs, moves, *tables)
+    n, address, dev = _page_refs(where, plan, refs, moves, *tables)
     tables_out = tables if tables_out is None else tables_out
     out = refs if refs_out is None else refs_out
     oa = _int_array(where, "refs_out", out, refs.shape, dev)
@@ -857,7 +862,7 @@ def cp_pages_compact(plan: PagedPlan, refs, tables, moves: PageMoves, workspace,
     a = (cp_page_table_t * len(tables))(*[t.c for t in tables])
     b = (cp_page_table_t * len(tables))(*[t.c for t in tables_out])
     rc = _L().cp_pages_compact(plan._h, n, address, oa, len(tables), a, b, moves.ref, ua, workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _current_stream(where, dev, stream))
+                               workspace.numel() * workspace.element_size(), _current_stream(where, plan, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 
@@ -872,7 +877,7 @@ def cp_pages_copy(plan: PagedPlan, src, dst, moves: PageMoves, stream=None):
             _refuse(where, f"a cache's pages are {c.page} on {c.device}, the plan's {plan.page} and the moves on device {dev}")
     a = (cp_paged_cache_t * len(src))(*[c.c for c in src])
     b = a if dst is src else (cp_paged_cache_t * len(dst))(*[c.c for c in dst])
-    rc = _L().cp_pages_copy(plan._h, len(src), a, b, moves.ref, _current_stream(where, dev, stream))
+    rc = _L().cp_pages_copy(plan._h, len(src), a, b, moves.ref, _current_stream(where, plan, dev, stream))
     if rc != CP_OK:
         _check(rc, where)
 
@@ -890,6 +895,7 @@ class RopePlan:
         _check(_L().cp_rope_create(ctypes.byref(desc), ctypes.byref(h)), "cp_rope_create")
         self._h = h
         self.d, self.rope_dim, self.rope_axes = desc.d, desc.rope_dim, desc.rope_axes
+        self._current, self._i32 = _current_functions()
 
     @property
     def handle(self):
@@ -910,7 +916,6 @@ class RopePlan:
 def cp_rope(plan: RopePlan, positions, xs, outs, inverse=False, stream=None):
     """xs, outs: up to 8 tensors [tokens][heads][d] each (queries and keys, say);
     positions: int32 [rope_axes][tokens], or [tokens] with one axis."""
-    import torch
     where, d, axes = "cp_rope", plan.d, plan.rope_axes
     n, dev = positions.shape[-1], positions.get_device()
     if not 1 <= len(xs) <= CP_ROPE_MAX_JOBS or len(xs) != len(outs):
@@ -927,12 +932,12 @@ def cp_rope(plan: RopePlan, positions, xs, outs, inverse=False, stream=None):
         job.inp, job.out, job.heads = x.data_ptr(), o.data_ptr(), x.shape[1]
         job.in_stride, job.out_stride = (a[0], b[0]) if n > 1 else (row, row)
     if positions.shape != (axes, n) and (axes > 1 or positions.dim() != 1) or not positions.is_contiguous() \
-            or positions.dtype != torch.int32:
+            or positions.dtype is not plan._i32:
         _refuse(where, f"positions are contiguous int32 [{axes}][{n}], got {positions.dtype} {tuple(positions.shape)}")
     ti, to = _dtype_code(xs[0]), _dtype_code(outs[0])
     if ti is None or to is None:
         _refuse(where, f"{xs[0].dtype} to {outs[0].dtype}: bfloat16, float16 and float32 are served")
-    st = _current_stream(where, dev, stream)
+    st = _current_stream(where, plan, dev, stream)
     rc = _L().cp_rope(plan._h, n, positions.data_ptr(), len(xs), jobs, ti, to, 1 if inverse else 0, st)
     if rc != CP_OK:
         _check(rc, where)

@@ -766,7 +766,7 @@ int cp_pages_resize(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, co
   if (!a.status) return CP_ERR_CUDA;
   NvtxRange range("cp_pages_resize");
   static std::atomic<int> known[64];
-  return launch_cluster(known, pages_resize_kernel, a, cluster_for(num_pages, table->rows, 1024), stream);
+  return launch_cluster(known, pages_resize_kernel, a, cluster_for(num_pages, table->rows, 256), stream);
 }
 
 int cp_pages_fork(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, const cp_page_table_t* src, const cp_page_table_t* dst,
@@ -910,7 +910,7 @@ int cp_pages_copy(const cp_paged_t* plan, int32_t n_caches, const cp_paged_cache
   if (pieces > 1 << 30) return CP_ERR_UNSUPPORTED;
   a.parts = static_cast<int>((pieces + kCopyPart - 1) / kCopyPart);
   const long long units = 2LL * n_caches * a.parts * moves->capacity;  // at most; the moves' count is on the device
-  const unsigned grid = static_cast<unsigned>(units < 152 * 8 ? units : 152 * 8);
+  const unsigned grid = static_cast<unsigned>(units < 152 * 20 ? units : 152 * 20);
   NvtxRange range("cp_pages_copy");
   return launch(pages_copy_kernel, grid, kCopyThreads, 0, stream, a);
 }

@@ -187,6 +187,9 @@ __device__ __forceinline__ void unpack(const uint4& r, float (&x)[16 / sizeof(T)
   }
 }
 
+// Granules of a lane in a slot with `left` of them: no more than run, an even number.
+__device__ __forceinline__ int slot_run(int left, int run) { return min(run, (left + 63) / 64 * 2); }
+
 // A warp's sum of granules [g0, g1) of the row, in up to kVerifySlots slots of
 // 32 lanes x run granules: each lane takes `run` neighbours of a slot, four at a time, whose
 // sum it leaves in `slots`.  So the search finds its way down to one lane's
@@ -206,22 +209,25 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
   const int gx = !q && row.x >= 0 ? (row.x + row.skew) / kN : -1;
 #pragma unroll 1
   for (int slot = 0; g0 + slot * 32 * run < g1; ++slot) {
-    const int first = g0 + (slot * 32 + lane) * run, end = min(first + run, g1);
-    Pair parts[4];  // independent chains of sums
+    const int base = g0 + slot * 32 * run, mine = slot_run(g1 - base, run);
+    const int first = base + lane * mine, end = min(first + mine, g1);
+    const int lo = max(first, v0);
+    const unsigned vectors = static_cast<unsigned>(max(min(end, v1) - lo, 0));
+    Pair parts[2];  // independent chains of sums
 #pragma unroll 1
     for (int g = first; g < end; g += kAhead) {
       uint4 x[kAhead], y[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        if (g + i < end && g + i >= v0 && g + i < v1 && g + i != gx) {
+        if (static_cast<unsigned>(g + i - lo) < vectors && g + i != gx) {
           x[i] = p[g + i];
           if (q) y[i] = q[g + i];
         }
       }
       // Two at a time, in one copy of the code.  fmaxf: neither negative nor NaN.
 #pragma unroll 1
-      for (int half = 0; half < kAhead; half += 2) {
+      for (int half = 0; half < min(kAhead, mine - (g - first)); half += 2) {
         if (q) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -232,8 +238,8 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
             for (int e = 0; e < kN; ++e) {
               float d, rest;
               Row<T>::diff(fmaxf(u[e], 0.f), v[e], d, rest);
-              parts[e % 4].add(d);
-              parts[e % 4].lo = __fadd_rn(parts[e % 4].lo, rest);
+              parts[e % 2].add(d);
+              parts[e % 2].lo = __fadd_rn(parts[e % 2].lo, rest);
             }
             y[i] = y[i + 2];
           }
@@ -243,7 +249,7 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
             float u[kN];
             unpack<T>(x[i], u);
 #pragma unroll
-            for (int e = 0; e < kN; ++e) parts[e % 4].add(fmaxf(u[e], 0.f));
+            for (int e = 0; e < kN; ++e) parts[e % 2].add(fmaxf(u[e], 0.f));
           }
         }
         x[0] = x[2];
@@ -252,7 +258,7 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
       if (g < v0 || min(g + kAhead, end) > v1 || static_cast<unsigned>(gx - g) < kAhead) {  // some are not vectors
 #pragma unroll 1
         for (int k = g; k < min(g + kAhead, end); ++k) {
-          if (k >= v0 && k < v1 && k != gx) continue;
+          if (static_cast<unsigned>(k - lo) < vectors && k != gx) continue;
 #pragma unroll 1
           for (int e = row.element(k), e1 = row.element(k + 1); e < e1; ++e) {
             float d, rest;
@@ -263,8 +269,6 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
       }
     }
     parts[0].add(parts[1].hi, parts[1].lo);
-    parts[2].add(parts[3].hi, parts[3].lo);
-    parts[0].add(parts[2].hi, parts[2].lo);
     slots[slot][lane] = make_float2(parts[0].hi, parts[0].lo);
     sum.add(parts[0].hi, parts[0].lo);
   }
@@ -417,9 +421,9 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel
     const Found f = find_lane(units.of(slots[warp][slot][lane].x, slots[warp][slot][lane].y), at, border);
     at = f.end;
     if (f.lane < 0) continue;
-    const int g = g0 + (slot * 32 + f.lane) * run;
+    const int of_slot = g0 + slot * 32 * run, of_lane = slot_run(g1 - of_slot, run), g = of_slot + f.lane * of_lane;
     e0 = row.element(g);
-    e1 = row.element(min(g + run, g1));
+    e1 = row.element(min(g + of_lane, g1));
     lane_at = f.before;
   }
   at = lane_at;
