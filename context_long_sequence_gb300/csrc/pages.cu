@@ -291,8 +291,10 @@ __device__ __forceinline__ int take_pages(PagesShared& sh, const int32_t* refs, 
       if (sh.free_before[i * cluster + rank] < given) mine += sh.counts[i];
     if (cluster > 1) mine = __reduce_add_sync(0xffffffffu, mine);
     const int window = mine <= kList ? given : kList;
+    // From the highest on: a chunk that is looked at again then lacks only pages
+    // behind those that are counted.
 #pragma unroll 1
-    for (int base = 0; base < given; base += window) {
+    for (int base = given > 0 ? (given - 1) / window * window : -1; base >= 0; base -= window) {
       const int end = given - base < window ? given : base + window;
       chunks.each_run(sh, base, end, [&](int page, unsigned bits, int k, int all) {
         int to = 0;
@@ -734,7 +736,8 @@ int check_table(const cp_page_table_t* t, int page_shift) {
   return aligned(t->pages, 4) && aligned(t->held, 4) ? CP_OK : CP_ERR_ALIGNMENT;
 }
 int check_moves(const cp_page_moves_t* m, int least) {
-  if (!m || m->capacity < least || !m->count || !m->src || !m->dst || !m->tokens) return CP_ERR_INVALID_ARG;
+  if (!m || m->capacity < 0 || m->capacity < least || !m->count) return CP_ERR_INVALID_ARG;
+  if (m->capacity > 0 && (!m->src || !m->dst || !m->tokens)) return CP_ERR_INVALID_ARG;
   return aligned(m->count, 4) && aligned(m->src, 4) && aligned(m->dst, 4) && aligned(m->tokens, 4) ? CP_OK : CP_ERR_ALIGNMENT;
 }
 Table table_of(const cp_page_table_t& t) { return Table{t.rows, t.columns, t.pages, t.held}; }
@@ -753,7 +756,7 @@ int cp_pages_resize(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, co
   a.page_shift = paged_page_shift(plan);
   int rc = check_refs(num_pages, refs);
   if (rc == CP_OK) rc = check_table(table, a.page_shift);
-  if (rc == CP_OK && (!tokens || !served)) rc = CP_ERR_INVALID_ARG;
+  if (rc == CP_OK && (!tokens || !served || served == tokens || served == table->held || tokens == table->held)) rc = CP_ERR_INVALID_ARG;
   if (rc == CP_OK && (!aligned(tokens, 4) || !aligned(served, 4))) rc = CP_ERR_ALIGNMENT;
   if (rc == CP_OK) rc = check_arch();
   if (rc != CP_OK) return rc;
@@ -778,7 +781,9 @@ int cp_pages_fork(const cp_paged_t* plan, int32_t num_pages, int32_t* refs, cons
   if (rc == CP_OK) rc = check_table(src, a.page_shift);
   if (rc == CP_OK) rc = check_table(dst, a.page_shift);
   if (rc == CP_OK) rc = check_moves(moves, dst->rows);
-  if (rc == CP_OK && (!parent || !tokens || !served)) rc = CP_ERR_INVALID_ARG;
+  if (rc == CP_OK && (!parent || !tokens || !served || served == parent || served == tokens || served == src->held || served == dst->held ||
+                      parent == dst->held || tokens == dst->held))
+    rc = CP_ERR_INVALID_ARG;
   if (rc == CP_OK && (!aligned(parent, 4) || !aligned(tokens, 4) || !aligned(served, 4))) rc = CP_ERR_ALIGNMENT;
   if (rc == CP_OK) rc = check_arch();
   if (rc != CP_OK) return rc;

@@ -290,6 +290,9 @@ __device__ __forceinline__ void st_cluster(float2* local, int rank, float x, flo
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(x), "f"(y) : "memory");
 }
 
+// A draft's place in a row; -1: none.
+__device__ __forceinline__ int draft_at(int x, int V) { return x >= 0 && x < V ? x : -1; }
+
 // One cluster a sequence.
 template <typename T>
 __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel(const __grid_constant__ VerifyArgs a, int cluster) {
@@ -341,7 +344,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel
   const int64_t t = static_cast<int64_t>(t0) + accepted;
   const bool there = live && CP_IN_BOUNDS(t < a.N, a.status);
   Row<T> row(there ? p + t * a.p_stride : nullptr, there && rejected && q ? q + t * a.q_stride : nullptr, there ? a.V : 0,
-             there && rejected && !q ? a.tokens[t + 1] : -1);
+             there && rejected && !q ? draft_at(a.tokens[t + 1], a.V) : -1);
   // A stretch of granules for each warp of the cluster.
   const int warps = cluster * kVerifyWarps, granules = row.granules(), w = rank * kVerifyWarps + warp;
   const int per = (granules + warps - 1) / warps, run = (per + 128 * kVerifySlots - 1) / (128 * kVerifySlots) * 4;
@@ -484,7 +487,9 @@ int cp_verify_drafts(const cp_paged_t* plan, const cp_paged_batch_t* batch, cons
   if (!batch->q_start || !batch->kv_len || !v.accepted) return CP_ERR_INVALID_ARG;
   // Without rows every sequence has none, which its outputs say.
   if (batch->n_tokens > 0 && (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.out_tokens)) return CP_ERR_INVALID_ARG;
-  if (!aligned(v.p, 16) || !aligned(v.q, 16)) return CP_ERR_ALIGNMENT;
+  if (v.out_tokens == v.tokens || v.accepted == v.kv_len_out || v.accepted == batch->kv_len) return CP_ERR_INVALID_ARG;
+  const uintptr_t element = v.dtype == CP_DTYPE_FP32 ? 4 : 2;
+  if (!aligned(v.p, element) || !aligned(v.q, element)) return CP_ERR_ALIGNMENT;
   const void* arrays[] = {v.tokens, v.accept_u, v.sample_u, v.accepted, v.out_tokens, v.kv_len_out};
   for (const void* x : arrays)
     if (!aligned(x, 4)) return CP_ERR_ALIGNMENT;

@@ -498,7 +498,7 @@ int cp_paged_shares(const cp_paged_t *plan, const cp_paged_batch_t *host_batch, 
 typedef struct {
   int32_t vocab;              /* 1 .. 2^30 */
   int32_t dtype;              /* CP_DTYPE_*: p and q */
-  const void *p;              /* [n_tokens][vocab], rows p_stride elements apart (any alignment of rows) */
+  const void *p;              /* [n_tokens][vocab], rows p_stride elements apart; an element's alignment is enough */
   int64_t p_stride;
   const void *q;              /* the same, or null: drafts that are certain (q = 1 at the draft, 0 elsewhere) */
   int64_t q_stride;
@@ -519,9 +519,10 @@ typedef struct {
  * differences are exact, sums good to 2^-40, so that the same numbers give the
  * same tokens whatever the batch.  A sequence without new tokens has accepted 0
  * and its kv_len.  Bad entries of q_start are skipped (their outputs stay as they
- * were) and recorded, rows behind q_start[n_seqs] are not touched.  The
- * outputs overlap neither each other nor the inputs, save that kv_len_out may be
- * the batch's kv_len.  The plan gives the batch's bounds (max_seqs,
+ * were) and recorded, rows behind q_start[n_seqs] are not touched.  The arrays
+ * need 4-byte alignment.  The outputs overlap neither each other nor the inputs
+ * (CP_ERR_INVALID_ARG where their addresses are the same), save that kv_len_out
+ * may be the batch's kv_len.  The plan gives the batch's bounds (max_seqs,
  * max_tokens, max_new); its page tables and positions are not read. */
 int cp_verify_drafts(const cp_paged_t *plan, const cp_paged_batch_t *batch, const cp_verify_t *verify, cudaStream_t stream);
 
@@ -585,7 +586,8 @@ int cp_pages_fork(const cp_paged_t *plan, int32_t num_pages, int32_t *refs, cons
  * (capacity >= num_pages / 2; whole pages; run it with cp_pages_copy from the
  * cache to itself) and used [1] (or null).  Every table that holds pages of refs has to be given, up to
  * CP_PAGES_MAX_TABLES of them.
- * workspace: cp_pages_workspace_size(num_pages) bytes, 16-byte aligned; nothing in it is kept between calls. */
+ * workspace: cp_pages_workspace_size(num_pages) bytes, 16-byte aligned; nothing
+ * in it is kept between calls; calls that may run at the same time, captured ones too, need one each. */
 int cp_pages_workspace_size(int32_t num_pages, size_t *bytes);
 int cp_pages_compact(const cp_paged_t *plan, int32_t num_pages, const int32_t *refs, int32_t *refs_out,
                      int32_t n_tables, const cp_page_table_t *tables, const cp_page_table_t *tables_out,

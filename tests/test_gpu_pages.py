@@ -132,6 +132,28 @@ def test_pages_in_turn(cpa, name):
     assert set(np.unique(b.pool.refs)) <= {0, 2} and max(used) > 0
 
 
+def test_a_pool_that_is_looked_at_in_parts(cpa):
+    """More than a million pages, most of them taken in one call (a CTA lists 16K at a
+    time and looks at refs again), then again among those that are held."""
+    b = Both(cpa, (1 << 21) + 77, 16, (300, 6000), seed=5, taken=0.3)
+    rng = b.rng
+    b.resize(rng.integers(60000, 70000, 300))
+    b.resize(np.where(rng.random(300) < 0.5, 0, -1))
+    assert 0 in b.resize(rng.integers(90000, 96000, 300))
+    b.compact()
+
+
+def test_no_moves(cpa):
+    """A pool of one page, lists without room: nothing moves."""
+    b = Both(cpa, 1, 16, (1, 1))
+    b.moves = cpa.PageMoves(0)
+    b.resize([16])
+    b.compact()
+    k = torch.zeros(1, 16, 2, 64, dtype=BF, device="cuda")
+    cache = cpa.PagedCache(k, k.clone())
+    cpa.cp_pages_copy(b.plan, [cache], [cache], b.moves)
+
+
 def test_lengths_of_a_row(cpa):
     b = Both(cpa, 50, 16, (2, 10))
     for t in (0, 1, 15, 16, 17, 160, 159, 145, 144, 16, 1, 0, 160, 0):

@@ -95,6 +95,19 @@ def test_verify_strides(cpa, p, q, dtype):
     Drafts([4, 5, 3, 1, 6, 2, 4], 999, dtype, seed=p + q).check(cpa, p=p, q=q)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_verify_rows_of_a_larger_tensor(cpa, dtype):
+    """p and q begin anywhere: an element's alignment is enough."""
+    d = Drafts([4, 5, 3], 517, dtype, seed=19)
+    for skip, (i, j) in ((1, (3, 0)), (2, (5, 7)), (0, (1, 1))):
+        views = []
+        for x, k in ((d.p, i), (d.q, j)):
+            buf = torch.full((d.N + skip, 541), float("nan"), dtype=dtype, device="cuda")
+            views.append(buf[skip:, k:k + 517])
+            views[-1].copy_(x)
+        d.check(cpa, p=views[0], q=views[1])
+
+
 def test_verify_does_not_hang_on_the_batch(cpa):
     """A sequence alone (16 CTAs) gives what it gives among 300 (one)."""
     d = Drafts([3] * 300, 20011, seed=3)

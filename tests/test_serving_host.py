@@ -125,7 +125,7 @@ def test_verify_refusals(cpa):  # noqa: F811
 
     def call(batch=None, **kw):
         _, b = c_args(cpa, plan, None, batch)
-        v = cpa.cp_verify_t(1000, 2, FAKE, 1000, FAKE, 1000, *[FAKE] * 6)
+        v = cpa.cp_verify_t(1000, 2, FAKE, 1000, FAKE, 1000, *[FAKE + 4096 * i for i in range(1, 7)])
         for k, x in kw.items():
             setattr(v, k, x)
         return L.cp_verify_drafts(plan.handle, A(b), A(v), None)
@@ -133,10 +133,11 @@ def test_verify_refusals(cpa):  # noqa: F811
         assert call(**{name: None}) == -1, name
     for name in ("tokens", "accept_u", "sample_u", "accepted", "out_tokens", "kv_len_out"):
         assert call(**{name: FAKE + 2}) == -3, name
-    assert call(p=FAKE + 4) == -3 and call(q=FAKE + 8) == -3
+    assert call(p=FAKE + 2) == -3 and call(q=FAKE + 6) == -3 and call(dtype=0, p=FAKE + 1) == -3 and call(dtype=1, q=FAKE + 3) == -3
     assert call(vocab=0) == -1 and call(vocab=(1 << 30) + 1) == -1 and call(dtype=3) == -1 and call(dtype=-1) == -1
     assert call(p_stride=999) == -1 and call(q_stride=999) == -1 and call(p_stride=1 << 36) == -1
     assert call(batch=dict(n_seqs=5)) == -1 and call(batch=dict(n_tokens=65)) == -1 and call(batch=dict(q_start=None)) == -1
+    assert call(out_tokens=FAKE + 4096) == -1 and call(kv_len_out=FAKE + 4096 * 4) == -1 and call(accepted=FAKE + 64) == -1
     assert call(batch=dict(n_seqs=0), p=None) == 0
     assert call(batch=dict(n_tokens=0), accepted=None) == -1 and call(batch=dict(n_tokens=0, q_start=None)) == -1
     assert L.cp_verify_drafts(None, None, None, None) == -1
@@ -177,13 +178,14 @@ BAD_REFS = [(0, FAKE, -1), (-5, FAKE, -1), ((1 << 30) + 1, FAKE, -1), (100, None
 
 def test_resize_refusals(cpa):  # noqa: F811
     plan, L = make_plan(cpa), cpa._L()
-    call = lambda t, n=100, refs=FAKE, tokens=FAKE, served=FAKE: L.cp_pages_resize(plan.handle, n, refs, A(t), tokens, served, None)  # noqa: E731
+    call = lambda t, n=100, refs=FAKE, tokens=FAKE + 64, served=FAKE + 128: L.cp_pages_resize(plan.handle, n, refs, A(t), tokens, served, None)  # noqa: E731
     for kw, code in BAD_TABLES:
         assert call(structs(cpa, kw)[0]) == code, kw
     t, _ = structs(cpa)
     for n, refs, code in BAD_REFS:
         assert call(t, n, refs) == code
     assert call(t, tokens=None) == -1 and call(t, served=None) == -1 and call(t, tokens=FAKE + 2) == -3
+    assert call(t, served=FAKE + 64) == -1 and call(t, tokens=FAKE + 4096) == -1 and call(t, served=FAKE + 4096) == -1
     assert L.cp_pages_resize(None, 100, FAKE, A(t), FAKE, FAKE, None) == -1
     assert L.cp_pages_resize(plan.handle, 100, FAKE, None, FAKE, FAKE, None) == -1
 
@@ -191,7 +193,7 @@ def test_resize_refusals(cpa):  # noqa: F811
 def test_fork_refusals(cpa):  # noqa: F811
     plan, L = make_plan(cpa), cpa._L()
 
-    def call(src=None, dst=None, moves=None, n=100, refs=FAKE, parent=FAKE, tokens=FAKE, served=FAKE):
+    def call(src=None, dst=None, moves=None, n=100, refs=FAKE, parent=FAKE + 64, tokens=FAKE + 128, served=FAKE + 192):
         (s, m), (d, _) = structs(cpa, src, moves), structs(cpa, dst)
         return L.cp_pages_fork(plan.handle, n, refs, A(s), A(d), parent, tokens, A(m), served, None)
     for kw, code in BAD_TABLES:
@@ -201,6 +203,7 @@ def test_fork_refusals(cpa):  # noqa: F811
     for n, refs, code in BAD_REFS:
         assert call(n=n, refs=refs) == code
     assert call(parent=None) == -1 and call(tokens=None) == -1 and call(served=None) == -1 and call(parent=FAKE + 1) == -3
+    assert call(served=FAKE + 64) == -1 and call(served=FAKE + 128) == -1 and call(served=FAKE + 4096) == -1 and call(parent=FAKE + 4096) == -1
 
 
 def test_compact_refusals(cpa):  # noqa: F811
