@@ -25,11 +25,12 @@
 // are exchanged through distributed shared memory; the warp in whose stretch the
 // border lies looks closer, at its lanes' sums and then at one lane's elements.
 //
-// In a graph: one sequence of 5 drafts, V = 100003, 7.2 us (a third of it the
-// row's sums, the rest the chain); 64 sequences, 49 MB, 18.7 us; 256 without q, 26 MB of bf16,
-// 16.3 us (9 instructions an element and 1.3 elements for one that is there:
-// a warp's stretch is cut to whole slots).  CTAs of 128 or 512 threads, or
-// fewer on an SM, were slower (7.9 and 8.4; 21.5 and 19.3; 23.2 us).
+// In a graph: one sequence of 5 drafts, V = 100003, 7.3 us (a third of it the
+// row's sums, the rest the chain); 64 sequences, 49 MB, 16.9 us; 256 without q,
+// 26 MB of bf16, 15.1 us: there the instructions count, 11 an element (20 a
+// pair in fp32) and 550 a warp.  CTAs of 128 or 512 threads, or 3 or 5 on an
+// SM, were slower (5: 7.6, 20.8, 19.1), and so were granules on their way through shared
+// memory by asynchronous copies (27.7 and 23.2).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -44,7 +45,9 @@ namespace {
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxCluster = 16, kVerifyResident = 4;  // CTAs of an SM
 constexpr int kVerifySums = kVerifyMaxCluster * kVerifyWarps;
-constexpr int kVerifySlots = 8;
+constexpr int kVerifySlots = 4;
+constexpr int kVerifyAhead = 2;                 // granules of a lane in a step
+constexpr int kVerifyStep = 32 * kVerifyAhead;  // and of a warp
 
 struct VerifyArgs {
   int B, N, V, max_new;
@@ -187,17 +190,20 @@ __device__ __forceinline__ void unpack(const uint4& r, float (&x)[16 / sizeof(T)
   }
 }
 
-// Granules of a lane in a slot with `left` of them: no more than run, an even number.
-__device__ __forceinline__ int slot_run(int left, int run) { return min(run, (left + 63) / 64 * 2); }
+// How the lanes of a warp share granules: in each step of a slot of `steps` a lane
+// takes those number lane * lane_step + step * step_size + i * next, i < kVerifyAhead.
+struct Share {
+  int steps, lane_step, step_size, next;
+};
+// Neighbouring lanes take neighbours, as the memory likes it, or a lane takes neighbours.
+__device__ __forceinline__ Share by_granule(int steps) { return Share{steps, 1, kVerifyStep, 32}; }
+__device__ __forceinline__ Share by_lane(int steps) { return Share{steps, kVerifyAhead * steps, kVerifyAhead, 1}; }
 
-// A warp's sum of granules [g0, g1) of the row, in up to kVerifySlots slots of
-// 32 lanes x run granules: each lane takes `run` neighbours of a slot, four at a time, whose
-// sum it leaves in `slots`.  So the search finds its way down to one lane's
-// granules without reading the row again.  An infinite element makes the sum
-// infinite or NaN, unless it is taken one by one.
+// The lane's sum of granules [g0, g1) of the row; of each slot its sum goes to `slots`.
+// An infinite element makes the sum infinite or NaN, unless it is taken one by one.
 template <typename T>
-__device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, int run, float2 (*slots)[32]) {
-  constexpr int kN = Row<T>::kN, kAhead = 4;
+__device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, const Share& share, float2 (*slots)[32]) {
+  constexpr int kN = Row<T>::kN, kAhead = kVerifyAhead;
   const int lane = threadIdx.x & 31;
   Pair sum;
   const uint4* p = reinterpret_cast<const uint4*>(row.p - row.skew);
@@ -205,74 +211,78 @@ __device__ __forceinline__ Pair sum_granules(const Row<T>& row, int g0, int g1, 
   // Granules that are vectors: not the row's first and last where they are not
   // whole, nor the one of the draft that loses 1, and none where p and q are not
   // aligned alike.
-  const int v0 = row.alike ? row.skew > 0 : INT_MAX, v1 = row.granules() - ((row.V + row.skew) % kN > 0);
+  const int v0 = max(g0, row.alike ? row.skew > 0 : INT_MAX), v1 = min(g1, row.granules() - ((row.V + row.skew) % kN > 0));
+  const unsigned vectors = static_cast<unsigned>(max(v1 - v0, 0));
   const int gx = !q && row.x >= 0 ? (row.x + row.skew) / kN : -1;
+  const int size = share.steps * kVerifyStep;
+  int number = 0;
 #pragma unroll 1
-  for (int slot = 0; g0 + slot * 32 * run < g1; ++slot) {
-    const int base = g0 + slot * 32 * run, mine = slot_run(g1 - base, run);
-    const int first = base + lane * mine, end = min(first + mine, g1);
-    const int lo = max(first, v0);
-    const unsigned vectors = static_cast<unsigned>(max(min(end, v1) - lo, 0));
-    Pair parts[2];  // independent chains of sums
+  for (int slot = g0; slot < g1; slot += size) {
+    Pair part;
+    const int slot_end = min(slot + size, g1);
+    int g = slot + lane * share.lane_step;
 #pragma unroll 1
-    for (int g = first; g < end; g += kAhead) {
+    for (int step = 0; step < share.steps; ++step, g += share.step_size) {
       uint4 x[kAhead], y[kAhead];
+      bool whole = true;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        x[i] = y[i] = make_uint4(0, 0, 0, 0);
-        if (static_cast<unsigned>(g + i - lo) < vectors && g + i != gx) {
-          x[i] = p[g + i];
-          if (q) y[i] = q[g + i];
+      for (int i = 0; i < kAhead; ++i) whole &= static_cast<unsigned>(g + i * share.next - v0) < vectors && g + i * share.next != gx;
+      const bool all = __all_sync(0xffffffffu, whole);
+      if (all) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          x[i] = p[g + i * share.next];
+          if (q) y[i] = q[g + i * share.next];
         }
-      }
-      // Two at a time, in one copy of the code.  fmaxf: neither negative nor NaN.
+      } else {
+        if (!__any_sync(0xffffffffu, g < slot_end)) break;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int at = g + i * share.next;
+          x[i] = y[i] = make_uint4(0, 0, 0, 0);
+          if (at >= slot_end) continue;
+          if (static_cast<unsigned>(at - v0) < vectors && at != gx) {
+            x[i] = p[at];
+            if (q) y[i] = q[at];
+          } else {  // not a vector
 #pragma unroll 1
-      for (int half = 0; half < min(kAhead, mine - (g - first)); half += 2) {
-        if (q) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float u[kN], v[kN];
-            unpack<T>(x[i], u);
-            unpack<T>(y[i], v);
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
+            for (int e = row.element(at), end = row.element(at + 1); e < end; ++e) {
               float d, rest;
-              Row<T>::diff(fmaxf(u[e], 0.f), v[e], d, rest);
-              parts[e % 2].add(d);
-              parts[e % 2].lo = __fadd_rn(parts[e % 2].lo, rest);
+              row.element_weight(e, d, rest);
+              part.add(d, rest);
             }
-            y[i] = y[i + 2];
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float u[kN];
-            unpack<T>(x[i], u);
-#pragma unroll
-            for (int e = 0; e < kN; ++e) parts[e % 2].add(fmaxf(u[e], 0.f));
           }
         }
-        x[0] = x[2];
-        x[1] = x[3];
       }
-      if (g < v0 || min(g + kAhead, end) > v1 || static_cast<unsigned>(gx - g) < kAhead) {  // some are not vectors
-#pragma unroll 1
-        for (int k = g; k < min(g + kAhead, end); ++k) {
-          if (static_cast<unsigned>(k - lo) < vectors && k != gx) continue;
-#pragma unroll 1
-          for (int e = row.element(k), e1 = row.element(k + 1); e < e1; ++e) {
+      // fmaxf: neither negative nor NaN.
+      if (q) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float u[kN], v[kN];
+          unpack<T>(x[i], u);
+          unpack<T>(y[i], v);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) {
             float d, rest;
-            row.element_weight(e, d, rest);
-            parts[0].add(d, rest);
+            Row<T>::diff(fmaxf(u[e], 0.f), v[e], d, rest);
+            part.add(d);
+            part.lo = __fadd_rn(part.lo, rest);
           }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          float u[kN];
+          unpack<T>(x[i], u);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) part.add(fmaxf(u[e], 0.f));
         }
       }
     }
-    parts[0].add(parts[1].hi, parts[1].lo);
-    slots[slot][lane] = make_float2(parts[0].hi, parts[0].lo);
-    sum.add(parts[0].hi, parts[0].lo);
+    slots[number++][lane] = make_float2(part.hi, part.lo);
+    sum.add(part.hi, part.lo);
   }
-  return warp_sum(sum);
+  return sum;
 }
 
 __device__ __forceinline__ int cluster_rank() {
@@ -345,17 +355,23 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel
   const bool there = live && CP_IN_BOUNDS(t < a.N, a.status);
   Row<T> row(there ? p + t * a.p_stride : nullptr, there && rejected && q ? q + t * a.q_stride : nullptr, there ? a.V : 0,
              there && rejected && !q ? draft_at(a.tokens[t + 1], a.V) : -1);
-  // A stretch of granules for each warp of the cluster.
+  // A stretch of granules for each warp of the cluster, in slots of `steps` steps.
   const int warps = cluster * kVerifyWarps, granules = row.granules(), w = rank * kVerifyWarps + warp;
-  const int per = (granules + warps - 1) / warps, run = (per + 128 * kVerifySlots - 1) / (128 * kVerifySlots) * 4;
-  const int g0 = min(w * per, granules), g1 = min(g0 + per, granules);
+  const int per = (granules + warps - 1) / warps, steps = (per + kVerifySlots * kVerifyStep - 1) / (kVerifySlots * kVerifyStep);
+  const int size = steps * kVerifyStep;
+  int g0 = min(w * per, granules), g1 = min(g0 + per, granules);
+  Share share = by_granule(steps);
   Units units;
-  long long before = 0, total = 0, border = 0;
+  long long at = 0, border = 0;
   Pair v;
-  bool clean = false, plain = false;
+  bool clean = false, plain = false, found = false;
+  // First every warp its stretch, in one turn and seldom more; then the warp that
+  // has found the border in its stretch one slot of that: in one copy of the code.
 #pragma unroll 1
   for (int turn = 0;; ++turn) {
-    v = sum_granules<T>(row, g0, g1, run, slots[warp]);
+    v = sum_granules<T>(row, g0, g1, share, slots[warp]);
+    if (found) break;
+    v = warp_sum(v);
     if (turn == 0) cluster_wait();
     if (lane < cluster) {
       st_cluster(&sums[turn][w], lane, v.hi, v.lo);
@@ -369,72 +385,73 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel
     for (int k = lane; k < warps; k += 32) about += sums[turn][k].x;
 #pragma unroll 1
     for (int x = 16; x > 0; x >>= 1) about += __shfl_xor_sync(0xffffffffu, about, x);
+    long long total = 0;
     if (about > 0.f && about < INFINITY) {
       units.set(about);
 #pragma unroll 1
       for (int k = lane; k < warps; k += 32) {
         const long long x = units.of(sums[turn][k].x, sums[turn][k].y);
         total += x;
-        if (k < w) before += x;
+        if (k < w) at += x;
       }
-      before = warp_sum(before);
+      at = warp_sum(at);
       total = warp_sum(total);
-      break;
+    } else if (turn < 2 && (about != 0.f ? !clean : !plain && sums[0][kVerifySums].x != 0.f)) {
+      // Seldom, and the same for all warps of the cluster, who decide it by what
+      // they have exchanged.  Infinite elements: again, one by one, without them.
+      // Nothing left of p (the rows are not what they should be): p itself.
+      if (about != 0.f) {
+        clean = true;
+        row.alike = false;
+      } else {
+        plain = true;
+        row.q = nullptr;
+        row.x = -1;
+      }
+      continue;
     }
-    // Seldom, and the same for all warps of the cluster, who decide it by what they have exchanged.
-    if (turn == 2) break;
-    if (about != 0.f) {  // infinite elements: again, one by one, without them
-      if (clean) break;  // a sum that is infinite all the same: outside what the call allows
-      clean = true;
-      row.alike = false;
-    } else {  // nothing is left of p (the rows are not what they should be): p itself
-      if (sums[0][kVerifySums].x == 0.f || plain) break;
-      plain = true;
-      row.q = nullptr;
-      row.x = -1;
+    if (rank == 0 && warp == kVerifyWarps - 1 && good) {
+      for (int i = lane; i < n; i += 32)
+        if (i != accepted) a.out_tokens[t0 + i] = i < accepted ? a.tokens[t0 + i + 1] : -1;
+      if (lane == 0) {
+        a.accepted[s] = accepted;
+        if (a.kv_out) a.kv_out[s] = a.kv_len[s] - max(n - 1 - accepted, 0);
+        if (live && total == 0) a.out_tokens[t] = -1;
+      }
     }
-  }
-  if (!live) {
-    if (good && rank == 0 && threadIdx.x == 0) {
-      a.accepted[s] = 0;
-      if (a.kv_out) a.kv_out[s] = a.kv_len[s];
-    }
-    return;
-  }
-  if (rank == 0 && warp == kVerifyWarps - 1) {
-    for (int i = lane; i < n; i += 32)
-      if (i != accepted) a.out_tokens[t0 + i] = i < accepted ? a.tokens[t0 + i + 1] : -1;
-    if (lane == 0) {
-      a.accepted[s] = accepted;
-      if (a.kv_out) a.kv_out[s] = a.kv_len[s] - (n - 1 - accepted);
-      if (total == 0) a.out_tokens[t] = -1;
-    }
-  }
-  // r of the total, cut to a whole number, which no sum of whole numbers can tell from it.
-  unsigned long long r = 0;
-  if (of_all > 0.f) r = __float2ull_rz(fminf(of_all, 0x1.fffffep-1f) * 0x1p64f);
-  border = static_cast<long long>(__umul64hi(static_cast<unsigned long long>(total), r));
-  // One warp's stretch holds it, whose slots' lanes are searched, then a lane's elements.
-  // Their sums are rounded otherwise than the stretch's: where none ends above the border, it is the last with any weight.
-  if (before > border || border >= before + units.of(v.hi, v.lo)) return;
-  int e0 = 0, e1 = 0, token = -1;
-  long long at = before, lane_at = before;
+    // r of the total, cut to a whole number, which no sum of whole numbers can tell from it.
+    unsigned long long r = 0;
+    if (of_all > 0.f) r = __float2ull_rz(fminf(of_all, 0x1.fffffep-1f) * 0x1p64f);
+    border = static_cast<long long>(__umul64hi(static_cast<unsigned long long>(total), r));
+    if (!live || at > border || border >= at + units.of(v.hi, v.lo)) return;
+    // This warp's stretch holds it: which of its slots.  Their sums are rounded
+    // otherwise than the stretch's: where none ends above the border, it is the last with any weight.
+    int slot = -1;
+    long long before = at;
 #pragma unroll 1
-  for (int slot = 0; g0 + slot * 32 * run < g1 && at <= border; ++slot) {
-    const Found f = find_lane(units.of(slots[warp][slot][lane].x, slots[warp][slot][lane].y), at, border);
-    at = f.end;
-    if (f.lane < 0) continue;
-    const int of_slot = g0 + slot * 32 * run, of_lane = slot_run(g1 - of_slot, run), g = of_slot + f.lane * of_lane;
-    e0 = row.element(g);
-    e1 = row.element(min(g + of_lane, g1));
-    lane_at = f.before;
+    for (int k = 0; g0 + k * size < g1 && at <= border; ++k) {
+      const long long x = warp_sum(units.of(slots[warp][k][lane].x, slots[warp][k][lane].y));
+      if (x > 0) slot = k, before = at;
+      at += x;
+    }
+    if (slot < 0) return;  // not so: the stretch has weight
+    at = before;
+    g0 += slot * size;
+    g1 = min(g0 + size, g1);
+    share = by_lane(steps);
+    found = true;
   }
-  at = lane_at;
+  // Which lane's part of the slot, and which of its elements.
+  Found f = find_lane(units.of(v.hi, v.lo), at, border);
+  if (f.lane < 0) return;
+  const int part = steps * kVerifyAhead, e1 = row.element(min(g0 + (f.lane + 1) * part, g1));
+  int token = -1;
+  at = f.before;
 #pragma unroll 1
-  for (; e0 < e1 && at <= border; e0 += 32) {
+  for (int e0 = row.element(g0 + f.lane * part); e0 < e1 && at <= border; e0 += 32) {
     float d = 0.f, rest = 0.f;
     if (e0 + lane < e1) row.element_weight(e0 + lane, d, rest);
-    const Found f = find_lane(units.of(d, rest), at, border);
+    f = find_lane(units.of(d, rest), at, border);
     at = f.end;
     if (f.lane >= 0) token = e0 + f.lane;
   }
@@ -487,7 +504,7 @@ int cp_verify_drafts(const cp_paged_t* plan, const cp_paged_batch_t* batch, cons
   if (!batch->q_start || !batch->kv_len || !v.accepted) return CP_ERR_INVALID_ARG;
   // Without rows every sequence has none, which its outputs say.
   if (batch->n_tokens > 0 && (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.out_tokens)) return CP_ERR_INVALID_ARG;
-  if (v.out_tokens == v.tokens || v.accepted == v.kv_len_out || v.accepted == batch->kv_len) return CP_ERR_INVALID_ARG;
+  if ((v.out_tokens && v.out_tokens == v.tokens) || v.accepted == v.kv_len_out || v.accepted == batch->kv_len) return CP_ERR_INVALID_ARG;
   const uintptr_t element = v.dtype == CP_DTYPE_FP32 ? 4 : 2;
   if (!aligned(v.p, element) || !aligned(v.q, element)) return CP_ERR_ALIGNMENT;
   const void* arrays[] = {v.tokens, v.accept_u, v.sample_u, v.accepted, v.out_tokens, v.kv_len_out};
