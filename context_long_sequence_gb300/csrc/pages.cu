@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxTableRows = kMaxEntries;
-constexpr int kChunks = 2048;  // of refs
+constexpr int kChunks = 2 * kThreads;  // of refs, at most
 constexpr int kList = 16384;   // pages that a call places at a time
 constexpr int kQueue = 1024;
 constexpr int kFirstPart = 65536;
@@ -42,7 +42,7 @@ struct PagesShared {
   int warp_sums[kWarps];
   int free_before[kChunks + 1];  // free pages in the chunks before
   int counts[kChunks];           // free pages of this CTA's chunks: number i is chunk i * cluster + rank
-  int moved;
+  int moved, need;               // what one CTA has found and tells the others
   int queued, queue[kQueue];     // rows with many pages to let go
   int listed;
   int2 list[kList + 256];        // free pages that this CTA has found, and how many lie before each
@@ -256,6 +256,20 @@ __device__ __forceinline__ void scan_rows(PagesShared& sh, int* start, int rows,
   __syncthreads();
 }
 
+// The first CTA's number of pages to take, for all: with it they go through the
+// same barriers, even if the arrays should change under the kernel.  Waits for the
+// cluster's CTAs to have begun, and ends with a barrier of it.
+__device__ __forceinline__ int agree_on_need(PagesShared& sh, int need, int cluster) {
+  if (cluster > 1) {
+    cluster_wait();
+    if (cluster_rank() == 0 && static_cast<int>(threadIdx.x) < cluster) st_cluster(&sh.need, threadIdx.x, need);
+    cluster_barrier(cluster);
+    return sh.need;
+  }
+  __syncthreads();
+  return need;
+}
+
 // The row that item k falls to: the last with start[r] <= k.
 __device__ __forceinline__ int row_of(const int* start, int rows, int k) {
   int lo = 0, hi = rows - 1;
@@ -305,12 +319,12 @@ __device__ __forceinline__ int take_pages(PagesShared& sh, const int32_t* refs, 
           if (bits >> i & 1) {
             // The run's free pages have places side by side; those outside the window
             // leave theirs empty, in a first and a last run.
-            sh.list[to] = make_int2(k >= base && k < end ? page + i : -1, k);
+            if (to < kList + 256) sh.list[to] = make_int2(k >= base && k < end ? page + i : -1, k);
             ++to, ++k;
           }
       });
       __syncthreads();
-      const int listed = sh.listed;
+      const int listed = min(sh.listed, kList + 256);  // more only where refs changes under the kernel
       for (int i = threadIdx.x; i < listed; i += kThreads)
         if (sh.list[i].x >= 0) place(sh.list[i].x, sh.list[i].y, free_pages);
       __syncthreads();
@@ -389,9 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_resize_kernel(const __grid_
       let_go(a, r, a.table.held[r] - 1 - (k - first[i]));
     }
   }
-  const int need = sh.start[rows];
-  if (cluster > 1) cluster_wait();
-  cluster_barrier(cluster);
+  const int need = agree_on_need(sh, sh.start[rows], cluster);  // behind it all has been let go
   int free_pages = 0;
   if (need > 0)
     free_pages = take_pages(sh, a.refs, a.num_pages, need, cluster, [&](int page, int k, int free) {
@@ -404,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_resize_kernel(const __grid_
       a.table.pages[static_cast<size_t>(r) * a.table.columns + c] = page;
     });
   for (int r = rank * kThreads + threadIdx.x; r < rows; r += cluster * kThreads) {
-    const int want = wanted(a, r, a.table.held[r]);
-    const bool ok = want != -2 && (sh.start[r + 1] == sh.start[r] || sh.start[r + 1] <= free_pages);
+    const int held = a.table.held[r], want = wanted(a, r, held);
+    const bool ok = want != -2 && (want <= held || sh.start[r + 1] <= free_pages);
     if (ok && want >= 0) a.table.held[r] = want;
     a.served[r] = ok;
   }
@@ -449,9 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
     if (c < 0 && rank == 0) debug_bounds_fail(a.status, __LINE__, CP_TU_ID);
     return c > 0 && (a.tokens[r] & rest) ? 1 : 0;
   });
-  const int need = sh.start[rows];
-  if (cluster > 1) cluster_wait();
-  cluster_barrier(cluster);  // every row's data have been read
+  const int need = agree_on_need(sh, sh.start[rows], cluster);  // behind it every row's data have been read
   int free_pages = 0;
   if (need > 0)
     free_pages = take_pages(sh, a.refs, a.num_pages, need, cluster, [&](int page, int k, int) {

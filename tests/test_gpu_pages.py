@@ -143,6 +143,31 @@ def test_a_pool_that_is_looked_at_in_parts(cpa):
     b.compact()
 
 
+def test_tables_beyond_32_bits(cpa):
+    """8192 rows of 300000 pages: requests for more than 2^31 pages in all are not
+    served, and the last rows' entries lie behind entry 2^31."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    rows, columns, pages = 8192, 300000, 1000
+    plan = plan_of(cpa, 16)
+    table = cpa.PageTable(torch.full((rows, columns), -1, dtype=torch.int32, device="cuda"), ints(np.zeros(rows)))
+    refs, served = ints(np.zeros(pages)), ints(np.full(rows, -7))
+    cpa.cp_pages_resize(plan, refs, table, ints(np.full(rows, columns * 16)), served)
+    assert not served.any() and not table.held.any() and not refs.any()
+    tokens = np.full(rows, -1)
+    tokens[[0, 8000, 8191]] = 20, 100, 33
+    cpa.cp_pages_resize(plan, refs, table, ints(tokens), served)
+    assert served.all() and table.pages[0, :3].tolist() == [0, 1, -1] and table.pages[8000, :8].tolist() == [2, 3, 4, 5, 6, 7, 8, -1]
+    parent, moves = np.full(rows, -1), cpa.PageMoves(rows)
+    parent[8190] = 8191
+    cpa.cp_pages_fork(plan, refs, table, table, ints(parent), ints(np.where(parent >= 0, 33, 0)), moves, served)
+    assert served.all() and table.pages[8190, :4].tolist() == [9, 10, 12, -1] and moves.src[0].item() == 11
+    cpa.cp_pages_resize(plan, refs, table, ints(np.where(np.arange(rows) == 8000, 0, -1)), served)
+    used = ints([0])
+    cpa.cp_pages_compact(plan, refs, [table], moves, cpa.alloc_pages_workspace(pages), used=used)
+    assert used.item() == 6 and table.pages[8191, :3].tolist() == [2, 3, 4] and table.pages[8190, :3].tolist() == [2, 3, 5]
+
+
 def test_no_moves(cpa):
     """A pool of one page, lists without room: nothing moves."""
     b = Both(cpa, 1, 16, (1, 1))
