@@ -9,14 +9,20 @@
 // hang neither on the order of threads nor on the calls' history, and counts
 // are changed by integer atomics alone.
 //
-// The three calls that change tables are bound by latency: a few dependent
-// loads and a count of refs (4 bytes a page).  Each is one cluster of CTAs, so that its
-// steps are separated by the cluster's hardware barrier, not by launches, and
-// their counts are exchanged through distributed shared memory.  refs is cut into
-// up to 2048 chunks, dealt out among the warps in turn, as the free pages of the lowest numbers lie together;
-// their finders only list them, and all threads of the CTA place them in the
-// tables (in one stretch a warp, and placed where they are found, 30K pages of a million took 57 us).
-// The copies are bound by memory.
+// The three calls that change tables are bound by latency: dependent loads, code
+// that runs once, and a count of refs (4 bytes a page).  Each is one cluster of
+// CTAs, so that its steps are separated by the cluster's hardware barrier, not by
+// launches, and their counts are exchanged through distributed shared memory.
+// refs is cut into up to 2048 chunks, dealt out among the warps in turn, as the
+// free pages of the lowest numbers lie together; their finders only list them,
+// and all threads of the CTA place them in the tables (in one stretch a warp, and placed where
+// they are found, 30K pages of a million took 57 us).  In a graph: 64 rows and
+// 16K pages 5.3 us a call, 4096 rows and a million pages 11.0, of which letting
+// go and taking 20K pages.
+//
+// The copies are bound by memory: 1.0 GB of pages of 262 KB in 296 us (0.98 of
+// the copy's rate, in 20 blocks of 2048 16-byte pieces an SM; 8 an SM 307, as
+// the last ones end far apart).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -34,7 +40,6 @@ constexpr int kMaxTableRows = kMaxEntries;
 constexpr int kChunks = 2 * kThreads;  // of refs, at most
 constexpr int kList = 16384;   // pages that a call places at a time
 constexpr int kQueue = 1024;
-constexpr int kFirstPart = 65536;
 
 // Shared memory of a CTA.
 struct PagesShared {
@@ -106,29 +111,53 @@ __device__ __forceinline__ unsigned free_bits(const int4& v) {
 struct Chunks {
   const int32_t* refs;
   int pages, size, count, gw, warps;
+  int counted;              // chunks that have been counted
+  int chunk, time;          // the next that this warp counts, and how many times 128 pages lie before
   unsigned long long mask;  // the lane's free pages in the first 16 such times
-  __device__ __forceinline__ Chunks(const int32_t* r, int n, int warp, int all) : refs(r), pages(n), gw(warp), warps(all), mask(0) {
+  __device__ __forceinline__ Chunks(const int32_t* r, int n, int warp, int all)
+      : refs(r), pages(n), gw(warp), warps(all), counted(0), chunk(warp), time(0), mask(0) {
     const int most = all == kWarps ? kWarps : kChunks;  // one CTA: a chunk a warp
     size = ((n + most - 1) / most + 127) & ~127;
     count = (n + size - 1) / size;
   }
-  // Leaves the free pages of all chunks before each in sh.free_before (the last
-  // entry: all).  All threads of the cluster; has a barrier of it, and arrives
-  // at another, which no CTA may leave without (leave).  A CTA runs this once and its code
-  // comes from L2, some 12 clocks an instruction: it is written to be short.
-  __device__ __forceinline__ void count_free(PagesShared& sh, int cluster) {
+  // Counts the chunks up to number `to`: leaves the free pages of all before each in
+  // sh.free_before (and behind the last).  All threads of the cluster; has a barrier of it, and arrives
+  // at another, which no CTA may leave or count on without (leave).  A CTA runs
+  // this once and its code comes from L2, some 12 clocks an instruction: it is written to be short.
+  __device__ __forceinline__ void count_free(PagesShared& sh, int cluster, int to) {
     constexpr int kAhead = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int time = 0, sum = 0;
-    int load_chunk = gw, load_at = 4 * lane, chunk = gw, at = 0;  // the next to load and to count
+    int sum = 0, at = 0;
+    // Whole chunks of four times, as large pools have them.
 #pragma unroll 1
-    while (chunk < count) {
+    while (size % (128 * kAhead) == 0 && chunk < to && (chunk + 1LL) * size <= pages) {
+      const int4* from = reinterpret_cast<const int4*>(refs + static_cast<size_t>(chunk) * size + at) + lane;
+      int4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v[i] = __ldcg(from + 32 * i);
+      unsigned bits = 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) bits |= free_bits(v[i]) << 4 * i;
+      if (time < 16) mask |= static_cast<unsigned long long>(bits) << 4 * time;
+      time += kAhead;
+      sum += __popc(bits);
+      at += 128 * kAhead;
+      if (at >= size) {
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) sh.counts[chunk / cluster] = sum;
+        sum = at = 0;
+        chunk += warps;
+      }
+    }
+    int load_chunk = chunk, load_at = 4 * lane;  // the next to load
+#pragma unroll 1
+    while (chunk < to) {
       int4 v[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const long long p = static_cast<long long>(load_chunk) * size + load_at;
         v[i] = make_int4(-1, -1, -1, -1);
-        if (load_chunk < count && p + 4 <= pages) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + p));
+        if (load_chunk < to && p + 4 <= pages) v[i] = __ldcg(reinterpret_cast<const int4*>(refs + p));
         load_at += 128;
         if (load_at >= size) load_at = 4 * lane, load_chunk += warps;
       }
@@ -136,7 +165,7 @@ struct Chunks {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) all |= free_bits(v[i]) << 4 * i;
 #pragma unroll 1
-      for (int i = 0; i < kAhead && chunk < count; ++i, ++time) {
+      for (int i = 0; i < kAhead && chunk < to; ++i, ++time) {
         unsigned bits = all & 15u;
         all >>= 4;
         const int p = chunk * size + at + 4 * lane;
@@ -153,16 +182,19 @@ struct Chunks {
       }
     }
     cluster_barrier(cluster);
-    const int blocks = ((count + cluster - 1) / cluster + 31) / 32;  // of a CTA's chunks
+    // Of each CTA's chunks, those from number `counted` on.
+    const int i0 = counted / cluster, blocks = ((to + cluster - 1) / cluster - i0 + 31) / 32;
 #pragma unroll 1
     for (int b = warp; b < blocks * cluster; b += kWarps) {
-      const int from = b / blocks, i = (b - from * blocks) * 32 + lane, c = i * cluster + from;
-      if (c < count) sh.free_before[c] = cluster == 1 ? sh.counts[i] : ld_cluster(&sh.counts[i], from);
+      const int from = b / blocks, i = i0 + (b - from * blocks) * 32 + lane, c = i * cluster + from;
+      if (c >= counted && c < to) sh.free_before[c + 1] = cluster == 1 ? sh.counts[i] : ld_cluster(&sh.counts[i], from);
     }
     if (cluster > 1) cluster_arrive();
+    if (counted == 0 && threadIdx.x == 0) sh.free_before[0] = 0;
     __syncthreads();
     // Running sums, two chunks to a thread.
-    const int c = 2 * threadIdx.x, x = c < count ? sh.free_before[c] : 0, y = c + 1 < count ? sh.free_before[c + 1] : 0;
+    const int c = counted + 2 * threadIdx.x, x = c < to ? sh.free_before[c + 1] : 0, y = c + 1 < to ? sh.free_before[c + 2] : 0;
+    const int base = sh.free_before[counted];
     int upto = x + y;
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,10 +203,10 @@ struct Chunks {
     }
     if (lane == 31) sh.warp_sums[warp] = upto;
     __syncthreads();
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sums[lane] : 0) + upto - x - y;
-    if (c <= count) sh.free_before[c] = before;
-    if (c + 1 <= count) sh.free_before[c + 1] = before + x;
-    if (c + 2 == count) sh.free_before[count] = before + x + y;
+    const int behind = base + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sums[lane] : 0) + upto;
+    if (c < to) sh.free_before[c + 1] = behind - y;
+    if (c + 1 < to) sh.free_before[c + 2] = behind;
+    counted = to;
     __syncthreads();
   }
   // Behind it no CTA reads this one's shared memory.
@@ -192,7 +224,7 @@ struct Chunks {
     const unsigned lower = (1u << (threadIdx.x & 31)) - 1;
     int time = 0;
 #pragma unroll 1
-    for (int chunk = gw; chunk < count; chunk += warps) {
+    for (int chunk = gw; chunk < counted; chunk += warps) {
       int before = sh.free_before[chunk];
       if (before >= end) break;
       if (sh.free_before[chunk + 1] <= base) {
@@ -286,54 +318,49 @@ template <typename F>
 __device__ __forceinline__ int take_pages(PagesShared& sh, const int32_t* refs, int pages, int need, int cluster, F&& place) {
   const int lane = threadIdx.x & 31, rank = cluster_rank();
   if (threadIdx.x == 0) sh.listed = 0;
-  // Of a large pool the first part is mostly enough.
-  int part = pages > kFirstPart ? max(kFirstPart, pages / 8) : pages;
-#pragma unroll 1
-  while (true) {
-    Chunks chunks(refs, part, (threadIdx.x >> 5) * cluster + rank, cluster * kWarps);
-    chunks.count_free(sh, cluster);
-    const int free_pages = sh.free_before[chunks.count], given = min(need, free_pages);
-    if (free_pages < need && part < pages) {
-      part = pages;
-      chunks.leave(cluster);
-      __syncthreads();
-      continue;
-    }
-    // As many at a time as this CTA's list holds; of the cluster's, mostly all.
-    int mine = cluster == 1 ? given : 0;
-    for (int i = lane; i * cluster + rank < chunks.count && cluster > 1; i += 32)
-      if (sh.free_before[i * cluster + rank] < given) mine += sh.counts[i];
-    if (cluster > 1) mine = __reduce_add_sync(0xffffffffu, mine);
-    const int window = mine <= kList ? given : kList;
-    // From the highest on: a chunk that is looked at again then lacks only pages
-    // behind those that are counted.
-#pragma unroll 1
-    for (int base = given > 0 ? (given - 1) / window * window : -1; base >= 0; base -= window) {
-      const int end = given - base < window ? given : base + window;
-      chunks.each_run(sh, base, end, [&](int page, unsigned bits, int k, int all) {
-        int to = 0;
-        if (lane == 0) to = atomicAdd(&sh.listed, all);
-        to = __shfl_sync(0xffffffffu, to, 0) + k - __shfl_sync(0xffffffffu, k, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (bits >> i & 1) {
-            // The run's free pages have places side by side; those outside the window
-            // leave theirs empty, in a first and a last run.
-            if (to < kList + 256) sh.list[to] = make_int2(k >= base && k < end ? page + i : -1, k);
-            ++to, ++k;
-          }
-      });
-      __syncthreads();
-      const int listed = min(sh.listed, kList + 256);  // more only where refs changes under the kernel
-      for (int i = threadIdx.x; i < listed; i += kThreads)
-        if (sh.list[i].x >= 0) place(sh.list[i].x, sh.list[i].y, free_pages);
-      __syncthreads();
-      if (threadIdx.x == 0) sh.listed = 0;
-      __syncthreads();
-    }
+  // First a chunk a warp, which in a large pool may be enough, then the rest.
+  Chunks chunks(refs, pages, (threadIdx.x >> 5) * cluster + rank, cluster * kWarps);
+  chunks.count_free(sh, cluster, min(chunks.count, chunks.warps));
+  if (sh.free_before[chunks.counted] < need && chunks.counted < chunks.count) {
     chunks.leave(cluster);
-    return free_pages;
+    __syncthreads();
+    chunks.count_free(sh, cluster, chunks.count);
   }
+  const int free_pages = sh.free_before[chunks.counted], given = min(need, free_pages);
+  // As many at a time as this CTA's list holds; of the cluster's, mostly all.
+  int mine = cluster == 1 ? given : 0;
+  for (int i = lane; i * cluster + rank < chunks.counted && cluster > 1; i += 32)
+    if (sh.free_before[i * cluster + rank] < given) mine += sh.counts[i];
+  if (cluster > 1) mine = __reduce_add_sync(0xffffffffu, mine);
+  const int window = mine <= kList ? given : kList;
+  // From the highest on: a chunk that is looked at again then lacks only pages
+  // behind those that are counted.
+#pragma unroll 1
+  for (int base = given > 0 ? (given - 1) / window * window : -1; base >= 0; base -= window) {
+    const int end = given - base < window ? given : base + window;
+    chunks.each_run(sh, base, end, [&](int page, unsigned bits, int k, int all) {
+      int to = 0;
+      if (lane == 0) to = atomicAdd(&sh.listed, all);
+      to = __shfl_sync(0xffffffffu, to, 0) + k - __shfl_sync(0xffffffffu, k, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (bits >> i & 1) {
+          // The run's free pages have places side by side; those outside the window
+          // leave theirs empty, in a first and a last run.
+          if (to < kList + 256) sh.list[to] = make_int2(k >= base && k < end ? page + i : -1, k);
+          ++to, ++k;
+        }
+    });
+    __syncthreads();
+    const int listed = min(sh.listed, kList + 256);  // more only where refs changes under the kernel
+    for (int i = threadIdx.x; i < listed; i += kThreads)
+      if (sh.list[i].x >= 0) place(sh.list[i].x, sh.list[i].y, free_pages);
+    __syncthreads();
+    if (threadIdx.x == 0) sh.listed = 0;
+    __syncthreads();
+  }
+  chunks.leave(cluster);
+  return free_pages;
 }
 
 struct ResizeArgs {
@@ -519,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
   pdl_launch_dependents();
   Chunks chunks(a.refs, P, gw, warps);
   if (cluster > 1) cluster_wait();
-  chunks.count_free(sh, cluster);
+  chunks.count_free(sh, cluster, chunks.count);
   chunks.leave(cluster);
   // Held pages from number `used` on move to the free ones below it, which are
   // as many: `moves`, the free pages before number `used`, counted by the warp of that chunk.
-  const int used = P - sh.free_before[chunks.count], chunk_of_used = used / chunks.size;
+  const int used = P - sh.free_before[chunks.counted], chunk_of_used = used / chunks.size;
   if (used < P && chunk_of_used % warps == gw) {
     int n = 0;
     for (int p = chunk_of_used * chunks.size; p < used; p += 128) {
