@@ -20,9 +20,9 @@
 // 16K pages 5.3 us a call, 4096 rows and a million pages 11.0, of which letting
 // go and taking 20K pages.
 //
-// The copies are bound by memory: 1.0 GB of pages of 262 KB in 296 us (0.98 of
-// the copy's rate, in 20 blocks of 2048 16-byte pieces an SM; 8 an SM 307, as
-// the last ones end far apart).
+// The copies are bound by memory: a compaction that moves 1.0 GB in pages of 131
+// KB takes 313 us in all (0.98 of a copy's rate), in 20 blocks of 2048 pieces of
+// 16 bytes an SM; in 8 an SM, of which some end late, 324.
 #include <cuda_runtime.h>
 
 #include <climits>
