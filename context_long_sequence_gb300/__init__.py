@@ -920,17 +920,16 @@ def cp_rope(plan: RopePlan, positions, xs, outs, inverse=False, stream=None):
     n, dev = positions.shape[-1], positions.get_device()
     if not 1 <= len(xs) <= CP_ROPE_MAX_JOBS or len(xs) != len(outs):
         _refuse(where, f"{len(xs)} inputs and {len(outs)} outputs; 1 to {CP_ROPE_MAX_JOBS} of both are wanted")
-    jobs = (cp_rope_job_t * len(xs))()
-    for job, x, o in zip(jobs, xs, outs):
-        a, b = x.stride(), o.stride()
-        if x.dim() != 3 or o.shape != x.shape or x.shape[0] != n or x.shape[2] != d or a[2] != 1 or b[2] != 1 \
-                or (x.shape[1] > 1 and (a[1] != d or b[1] != d)) or x.dtype != xs[0].dtype or o.dtype != outs[0].dtype \
+    jobs, ti, to = [], xs[0].dtype, outs[0].dtype
+    for x, o in zip(xs, outs):
+        shape, a, b = x.shape, x.stride(), o.stride()
+        if len(shape) != 3 or o.shape != shape or shape[0] != n or shape[2] != d or a[2] != 1 or b[2] != 1 \
+                or (shape[1] > 1 and (a[1] != d or b[1] != d)) or x.dtype is not ti or o.dtype is not to \
                 or x.get_device() != dev or o.get_device() != dev:
             _refuse(where, f"tensors [{n}][heads][{d}] with contiguous heads, inputs of one type and outputs of one, on device {dev} "
                            f"are wanted, got {x.dtype} {tuple(x.shape)} {a} on {x.device} and {o.dtype} {tuple(o.shape)} {b} on {o.device}")
-        row = x.shape[1] * d
-        job.inp, job.out, job.heads = x.data_ptr(), o.data_ptr(), x.shape[1]
-        job.in_stride, job.out_stride = (a[0], b[0]) if n > 1 else (row, row)
+        row = shape[1] * d
+        jobs.append((x.data_ptr(), o.data_ptr(), shape[1], a[0] if n > 1 else row, b[0] if n > 1 else row))
     if positions.shape != (axes, n) and (axes > 1 or positions.dim() != 1) or not positions.is_contiguous() \
             or positions.dtype is not plan._i32:
         _refuse(where, f"positions are contiguous int32 [{axes}][{n}], got {positions.dtype} {tuple(positions.shape)}")
@@ -938,7 +937,7 @@ def cp_rope(plan: RopePlan, positions, xs, outs, inverse=False, stream=None):
     if ti is None or to is None:
         _refuse(where, f"{xs[0].dtype} to {outs[0].dtype}: bfloat16, float16 and float32 are served")
     st = _current_stream(where, plan, dev, stream)
-    rc = _L().cp_rope(plan._h, n, positions.data_ptr(), len(xs), jobs, ti, to, 1 if inverse else 0, st)
+    rc = _L().cp_rope(plan._h, n, positions.data_ptr(), len(jobs), (cp_rope_job_t * len(jobs))(*jobs), ti, to, 1 if inverse else 0, st)
     if rc != CP_OK:
         _check(rc, where)
 
