@@ -30,8 +30,8 @@
 // 26 MB of bf16, 15.1 us: there the instructions count, 11 an element (20 a
 // pair in fp32) and 550 a warp.  CTAs of 128 or 512 threads, or 3 or 5 on an
 // SM, were slower (5: 7.6, 20.8, 19.1), and so were granules on their way through shared
-// memory by asynchronous copies (27.7 and 23.2); the next step's granules held in registers
-// gained nothing.
+// memory by asynchronous copies (27.7 and 23.2); the next step's granules held in registers,
+// packed additions and a prefetch of the stretch into L2 gained nothing (the last: 7.4, 19.5, 15.3).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -471,7 +471,7 @@ int launch_verify(const VerifyArgs& a, cudaStream_t stream) {
   // As many CTAs a sequence as the card holds at once, none with less than 2048
   // elements; 16 only for up to 8 sequences, as so many that have to start
   // together wait for one another (V = 128000, 8 and 16 CTAs: 2 sequences 8.8 and 7.4 us, 8
-  // 8.9 and 8.5, 16 9.7 and 9.8, 32 12.3 and 16.8; V = 32000: 2 6.0 and 5.9, 8 6.0 and 6.6).
+  // 8.9 and 8.5, 16 9.7 and 9.8, 32 12.3 and 16.8; V = 32000: 1 5.8 and 5.9, 8 6.0 and 6.6).
   int cluster = 1;
   while (a.B * cluster * 2 <= kVerifyResident * 152 && a.V / cluster > 4096 && cluster < (a.B <= 8 ? kVerifyMaxCluster : 8)) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
