@@ -81,8 +81,17 @@ class DistComm:
             self.abort(f"{kind} on process {self.rank} at step {step}")
             raise TransportError(kind, self.rank, step, peer, str(e)[:200]) from e
 
-    def check_abort(self, step: int):
-        if self.store.check([ABORT_KEY]):
+    def check_abort(self, step: int, begun: bool = False):
+        """Raises another process's abort.  Without the store: an error, but
+        not in a ring that has begun, as the process that keeps the store may
+        have all its chunks and be gone; this one's waits have limits of their own."""
+        try:
+            aborted = self.store.check([ABORT_KEY])
+        except Exception as e:
+            if begun:
+                return
+            raise TransportError("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
+        if aborted:
             raise TransportError("peer_abort", self.rank, step, -1, self.store.get(ABORT_KEY).decode())
 
     def abort(self, why: str):
@@ -112,7 +121,7 @@ class LocalComm:
     def wait(self, handle, step, peer):
         return None
 
-    def check_abort(self, step):
+    def check_abort(self, step, begun=False):
         return None
 
     def abort(self, why):
@@ -180,7 +189,7 @@ def ring_forward(comm, kernels, place: RingPlacement, q, kv, o_out, lse_out):
     spare = tuple(kernels.empty_like(t) for t in kv[0])
     parts = [[kernels.partial_buffers(q[i][u], R) for u in range(U)] for i in range(Rl)]
     for s in range(R):
-        comm.check_abort(s)
+        comm.check_abort(s, s > 0)
         handles = _post(comm, place, hold[-1], spare, s, TAG_KV) if s < R - 1 else None
         for i in range(Rl):
             for u in range(U):
@@ -215,7 +224,7 @@ def ring_backward(comm, kernels, place: RingPlacement, q, kv, o, lse, do, dq_out
     ghold = [tuple(kernels.grad_buffer(t) for t in kv[0]) for _ in range(Rl)]
     gspare = tuple(kernels.grad_buffer(t) for t in kv[0])
     for s in range(R):
-        comm.check_abort(s)
+        comm.check_abort(s, s > 0)
         handles = _post(comm, place, hold[-1], spare, s, TAG_KV) if s < R - 1 else None
         for i in range(Rl):
             for u in range(U):
