@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyResident) verify_kernel
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = a.q_start[s], t1 = a.q_start[s + 1], n = t1 - t0;
-  const float of_all = a.sample_u[s];
+  const float of_all = a.N > 0 ? a.sample_u[s] : 0.f;  // without rows the array may be null
   // Every CTA goes through the same cluster barriers, whatever it finds in the arrays.
   const bool good = CP_CHECK_DATA(t0 >= 0 && t1 >= t0 && t1 <= a.N && n <= a.max_new, a.status);
   const T* p = static_cast<const T*>(a.p);
@@ -510,7 +510,7 @@ int cp_verify_drafts(const cp_paged_t* plan, const cp_paged_batch_t* batch, cons
   if (v.q && (v.q_stride < v.vocab || v.q_stride >= kMaxStride)) return CP_ERR_INVALID_ARG;
   if (batch->n_seqs == 0) return CP_OK;
   if (!batch->q_start || !batch->kv_len || !v.accepted) return CP_ERR_INVALID_ARG;
-  // Without rows every sequence has none, which its outputs say.
+  // Without rows every sequence has none, which its outputs say; the kernel reads none of these then.
   if (batch->n_tokens > 0 && (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.out_tokens)) return CP_ERR_INVALID_ARG;
   if ((v.out_tokens && v.out_tokens == v.tokens) || v.accepted == v.kv_len_out || v.accepted == batch->kv_len) return CP_ERR_INVALID_ARG;
   const uintptr_t element = v.dtype == CP_DTYPE_FP32 ? 4 : 2;

@@ -518,7 +518,8 @@ typedef struct {
  * sample_u (w_0 + .. + w_vocab-1); -1 if the row has no weight at all.  Products and
  * differences are exact, sums good to 2^-40, so that the same numbers give the
  * same tokens whatever the batch.  A sequence without new tokens has accepted 0
- * and its kv_len.  Bad entries of q_start are skipped (their outputs stay as they
+ * and its kv_len; in a batch without rows (n_tokens 0) every sequence is one, and the
+ * arrays of the rows, sample_u and out_tokens may be null.  Bad entries of q_start are skipped (their outputs stay as they
  * were) and recorded, rows behind q_start[n_seqs] are not touched.  The arrays
  * need 4-byte alignment.  The outputs overlap neither each other nor the inputs
  * (CP_ERR_INVALID_ARG where their addresses are the same), save that kv_len_out
