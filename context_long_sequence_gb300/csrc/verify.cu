@@ -110,10 +110,14 @@ struct Units {
 // instruction, and an fp64 operation takes a warp 64 clocks: from here on the code is
 // in loops and one copy, and counts in whole numbers.
 
-// The sum over the warp's lanes.
+// The sum over the warp's lanes, the same bits in all of them: hi is, as the sum of two
+// numbers does not hang on their order; lo + (e + rest) does, by a rounding, and the
+// search wants each stretch's share to be one number for every lane and CTA (of
+// equal stretches up to all of the borders between them had no owner, or two).
 __device__ __forceinline__ Pair warp_sum(Pair v) {
 #pragma unroll 1
   for (int x = 16; x > 0; x >>= 1) v.add(__shfl_xor_sync(0xffffffffu, v.hi, x), __shfl_xor_sync(0xffffffffu, v.lo, x));
+  v.lo = __shfl_sync(0xffffffffu, v.lo, 0);
   return v;
 }
 
