@@ -516,7 +516,16 @@ int cp_verify_drafts(const cp_paged_t* plan, const cp_paged_batch_t* batch, cons
   if (!batch->q_start || !batch->kv_len || !v.accepted) return CP_ERR_INVALID_ARG;
   // Without rows every sequence has none, which its outputs say; the kernel reads none of these then.
   if (batch->n_tokens > 0 && (!v.p || !v.tokens || !v.accept_u || !v.sample_u || !v.out_tokens)) return CP_ERR_INVALID_ARG;
-  if ((v.out_tokens && v.out_tokens == v.tokens) || v.accepted == v.kv_len_out || v.accepted == batch->kv_len) return CP_ERR_INVALID_ARG;
+  // No output is another array, save that kv_len_out may be kv_len.  Without rows theirs are not touched.
+  const void* in[] = {batch->q_start, batch->kv_len, v.tokens, v.accept_u, v.sample_u, v.p, v.q};
+  const void* out[] = {v.accepted, v.kv_len_out, v.out_tokens};
+  const int ins = batch->n_tokens > 0 ? 7 : 2, outs = batch->n_tokens > 0 ? 3 : 2;
+  for (int i = 0; i < outs; ++i) {
+    for (int k = 0; k < ins; ++k)
+      if (out[i] && out[i] == in[k] && !(i == 1 && k == 1)) return CP_ERR_INVALID_ARG;
+    for (int k = 0; k < i; ++k)
+      if (out[i] && out[i] == out[k]) return CP_ERR_INVALID_ARG;
+  }
   const uintptr_t element = v.dtype == CP_DTYPE_FP32 ? 4 : 2;
   if (!aligned(v.p, element) || !aligned(v.q, element)) return CP_ERR_ALIGNMENT;
   const void* arrays[] = {v.tokens, v.accept_u, v.sample_u, v.accepted, v.out_tokens, v.kv_len_out};
