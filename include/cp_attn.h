@@ -516,8 +516,10 @@ typedef struct {
  * is drawn from w = max(p_a - q_a, 0) (from p_a itself if that is 0 throughout); if
  * all are, from w = p_a of the last row.  It is the least k with w_0 + .. + w_k >
  * sample_u (w_0 + .. + w_vocab-1); -1 if the row has no weight at all.  Products and
- * differences are exact, sums good to 2^-40, so that the same numbers give the
- * same tokens whatever the batch.  A sequence without new tokens has accepted 0
+ * differences are exact, sums good to 2^-40.  How a row is summed hangs on the number of
+ * sequences: the same numbers give the same tokens in another batch, but for a draw
+ * that lies within that rounding of a border between two tokens (about one in 10^8
+ * at a vocabulary of 10^5).  A sequence without new tokens has accepted 0
  * and its kv_len; in a batch without rows (n_tokens 0) every sequence is one, and the
  * arrays of the rows, sample_u and out_tokens may be null.  Bad entries of q_start are skipped (their outputs stay as they
  * were) and recorded, rows behind q_start[n_seqs] are not touched.  The arrays
