@@ -555,7 +555,7 @@ class PagedPlan:
         self.Hq, self.Hkv, self.d, self.page_size, self.dtype = desc.Hq, desc.Hkv, desc.d, desc.page_size, dtype
         self.max_seqs, self.max_tokens, self.max_new = desc.max_seqs, desc.max_tokens, desc.max_new
         self.max_pages, self.max_prefixes, self.max_prefix_pages = desc.max_pages, desc.max_prefixes, desc.max_prefix_pages
-        self.rope_axes = int(rope_axes)
+        self.rope_axes = max(1, int(rope_axes))  # 0: one, as without a word of them
         self.out_fp32 = bool(out_fp32)
         self.lse_dtype = torch.float32
         self.o_dtype = torch.float32 if out_fp32 else dtype
