@@ -54,10 +54,20 @@ class TransportError(RuntimeError):
         super().__init__(f"ring transport {kind} on process {rank} at step {step} (peer {peer}): {detail}")
 
 
+def _connection_lost(e: Exception) -> bool:
+    import torch.distributed as dist
+    return isinstance(e, (dist.DistNetworkError, ConnectionError)) or \
+        any(x in str(e) for x in ("Connection reset", "Connection was likely closed", "Broken pipe"))
+
+
 class DistComm:
     """Point-to-point over an initialised torch.distributed process group,
     with a bounded wait on every transfer and an abort flag in the group's
-    store that every process checks before each step."""
+    store that every process checks before each step, as long as there is
+    the store: the process that keeps it may have all its chunks, and end,
+    while others have several steps to go."""
+
+    lost = ""  # since when, and how, the connection to the store is gone
 
     def __init__(self, timeout_s: float = 60.0):
         import torch.distributed as dist
@@ -79,15 +89,19 @@ class DistComm:
         except Exception as e:  # the backend's timeout or a failed peer
             kind = "timeout" if "imed out" in str(e) or "imeout" in str(e) else "error"
             self.abort(f"{kind} on process {self.rank} at step {step}")
-            raise TransportError(kind, self.rank, step, peer, str(e)[:200]) from e
+            raise TransportError(kind, self.rank, step, peer, str(e)[:200] + (f" ({self.lost})" if self.lost else "")) from e
 
     def check_abort(self, step: int, begun: bool = False):
-        """Raises another process's abort.  Without the store: an error, but
-        not in a ring that has begun, as the process that keeps the store may
-        have all its chunks and be gone; this one's waits have limits of their own."""
+        """Raises another process's abort.  Where the connection to the store is
+        lost: an error, or with `begun` nothing, as the waits have limits of
+        their own; `lost` keeps it for them to name.  Every other failure of
+        the store may hide an abort and is an error."""
         try:
             aborted = self.store.check([ABORT_KEY])
         except Exception as e:
+            if not _connection_lost(e):
+                raise TransportError("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
+            self.lost = self.lost or f"the group's store was lost at step {step}: {str(e)[:100]}"
             if begun:
                 return
             raise TransportError("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
