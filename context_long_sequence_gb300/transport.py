@@ -106,7 +106,11 @@ class DistComm:
                 return
             raise TransportError("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
         if aborted:
-            raise TransportError("peer_abort", self.rank, step, -1, self.store.get(ABORT_KEY).decode())
+            try:
+                why = self.store.get(ABORT_KEY).decode()
+            except Exception as e:
+                why = f"its reason could not be read: {str(e)[:200]}"
+            raise TransportError("peer_abort", self.rank, step, -1, why)
 
     def abort(self, why: str):
         try:

@@ -172,3 +172,11 @@ def test_the_keeper_of_the_store_may_end_steps_before_another():
             p.kill()
     assert ended and all(status == "ok" for status, _ in got.values()), got
     assert "at step 2" in got[2][1], got
+
+
+@pytest.mark.parametrize("error", LOST + OTHER, ids=lambda e: type(e).__name__)
+def test_abort_counts_without_its_reason(error):
+    """The store may go between the check and the reading of the reason."""
+    with pytest.raises(tr.TransportError) as e:
+        comm_of(Store(9, get_error=error)).check_abort(1)
+    assert e.value.kind == "peer_abort" and e.value.step == 1
