@@ -54,6 +54,10 @@ class TransportError(RuntimeError):
         super().__init__(f"ring transport {kind} on process {rank} at step {step} (peer {peer}): {detail}")
 
 
+class StoreLost(TransportError):
+    """The connection to the group's store is gone (kind 'error')."""
+
+
 def _connection_lost(e: Exception) -> bool:
     import torch.distributed as dist
     return isinstance(e, (dist.DistNetworkError, ConnectionError)) or \
@@ -93,7 +97,7 @@ class DistComm:
 
     def check_abort(self, step: int, begun: bool = False):
         """Raises another process's abort.  Where the connection to the store is
-        lost: an error, or with `begun` nothing, as the waits have limits of
+        lost: StoreLost, or with `begun` nothing, as the waits have limits of
         their own; `lost` keeps it for them to name.  Every other failure of
         the store may hide an abort and is an error."""
         try:
@@ -104,7 +108,7 @@ class DistComm:
             self.lost = self.lost or f"the group's store was lost at step {step}: {str(e)[:100]}"
             if begun:
                 return
-            raise TransportError("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
+            raise StoreLost("error", self.rank, step, -1, f"the group's store: {str(e)[:200]}") from e
         if aborted:
             try:
                 why = self.store.get(ABORT_KEY).decode()
@@ -163,6 +167,15 @@ class RingPlacement:
         self.prev = (self.rank - 1) % self.world
 
 
+def _check_abort(comm, step: int):
+    """Before each step.  A ring that has begun goes on without the store."""
+    try:
+        comm.check_abort(step)
+    except StoreLost:
+        if step == 0:
+            raise
+
+
 def _post(comm, place: RingPlacement, last, spare, step: int, tag_kind: int):
     """Send the tensors of `last` (the chunk of this process's last ring
     rank) to the next process and receive the previous process's into
@@ -207,7 +220,7 @@ def ring_forward(comm, kernels, place: RingPlacement, q, kv, o_out, lse_out):
     spare = tuple(kernels.empty_like(t) for t in kv[0])
     parts = [[kernels.partial_buffers(q[i][u], R) for u in range(U)] for i in range(Rl)]
     for s in range(R):
-        comm.check_abort(s, s > 0)
+        _check_abort(comm, s)
         handles = _post(comm, place, hold[-1], spare, s, TAG_KV) if s < R - 1 else None
         for i in range(Rl):
             for u in range(U):
@@ -242,7 +255,7 @@ def ring_backward(comm, kernels, place: RingPlacement, q, kv, o, lse, do, dq_out
     ghold = [tuple(kernels.grad_buffer(t) for t in kv[0]) for _ in range(Rl)]
     gspare = tuple(kernels.grad_buffer(t) for t in kv[0])
     for s in range(R):
-        comm.check_abort(s, s > 0)
+        _check_abort(comm, s)
         handles = _post(comm, place, hold[-1], spare, s, TAG_KV) if s < R - 1 else None
         for i in range(Rl):
             for u in range(U):

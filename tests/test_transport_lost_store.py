@@ -180,3 +180,15 @@ def test_abort_counts_without_its_reason(error):
     with pytest.raises(tr.TransportError) as e:
         comm_of(Store(9, get_error=error)).check_abort(1)
     assert e.value.kind == "peer_abort" and e.value.step == 1
+
+
+@pytest.mark.parametrize("way", ["forward", "backward"])
+@pytest.mark.parametrize("lasts", [1, 2, 9])
+def test_a_communicator_that_takes_the_step_alone(way, lasts):
+    """check_abort(step), as a user's own communicator has it."""
+    class Own(Comm):
+        def check_abort(self, step):
+            super().check_abort(step)
+    ring(way, Own(Store(lasts, LOST[0])))
+    with pytest.raises(tr.TransportError):
+        ring(way, Own(Store(0, LOST[0])))
