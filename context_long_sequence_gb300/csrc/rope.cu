@@ -216,8 +216,8 @@ int launch_rope(const RopeArgs& a, cudaStream_t stream) {
   const int hpg = 32 / (a.d / (2 * rope_piece<TI>())), groups = (a.heads + hpg - 1) / hpg;
   // Few tokens: a warp for each group of heads, for latency.  Many: a warp
   // takes more of its token's heads, as one set of sines serves them all.
-  int units = (kRopeFillWarps + a.n - 1) / a.n;
-  units = units < 1 ? 1 : units > groups ? groups : units;
+  const long long fill = (kRopeFillWarps + a.n - 1LL) / a.n;  // n itself may be 2^31 - 1
+  const int units = static_cast<int>(fill > groups ? groups : fill);
   const long long warps = static_cast<long long>(a.n) * units;  // below 2^31 + kRopeFillWarps + n
   const long long grid = (warps + kRopeWarps - 1) / kRopeWarps;
   return launch(rope_kernel<TI, TO>, static_cast<unsigned>(grid), kRopeWarps * 32, 0, stream, a, static_cast<unsigned>(units));
