@@ -216,7 +216,7 @@ int launch_rope(const RopeArgs& a, cudaStream_t stream) {
   const int hpg = 32 / (a.d / (2 * rope_piece<TI>())), groups = (a.heads + hpg - 1) / hpg;
   // Few tokens: a warp for each group of heads, for latency.  Many: a warp
   // takes more of its token's heads, as one set of sines serves them all.
-  const long long fill = (kRopeFillWarps + a.n - 1LL) / a.n;  // n itself may be 2^31 - 1
+  const long long fill = (static_cast<long long>(a.n) + kRopeFillWarps - 1) / a.n;  // n itself may be 2^31 - 1
   const int units = static_cast<int>(fill > groups ? groups : fill);
   const long long warps = static_cast<long long>(a.n) * units;  // below 2^31 + kRopeFillWarps + n
   const long long grid = (warps + kRopeWarps - 1) / kRopeWarps;
