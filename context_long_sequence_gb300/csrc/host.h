@@ -1,5 +1,5 @@
-// host.h -- what the C-ABI files share on the host: argument checks, the
-// architecture check, NVTX ranges.
+// host.h -- what the C-ABI files of the paged cache and of the calls around its
+// attention share on the host: argument checks, the architecture check, NVTX ranges.
 #pragma once
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>

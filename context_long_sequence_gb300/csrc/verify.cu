@@ -26,15 +26,17 @@
 // border lies looks closer, at its lanes' sums and then at one lane's elements.
 //
 // In a graph: one sequence of 5 drafts, V = 100003, 7.3 us (a third of it the
-// row's sums, the rest the chain); 64 sequences, 49 MB, 16.9 us; 256 without q,
-// 26 MB of bf16, 15.1 us: 0.9 to the accepted drafts, 6 for the row (4.7 on SMs with two
+// row's sums, the rest the chain); 64 sequences, 49 MB, 17.0 us; 256 without q,
+// 26 MB of bf16, 14.9 us: 0.9 to the accepted drafts, 6 for the row (4.7 on SMs with two
 // CTAs, 6.6 with four), 1.5 for the exchange, 2.9 for the search behind it, and
-// the launch.  400 rows of 128000 in bf16, one CTA each, take 44 us: the issue slots
-// half used, half of the warps' time spent on loads.  What was tried on these and not kept:
+// the launch.  Where each row has one CTA, the time is that of a CTA on its way
+// through the row, whatever runs beside it: V = 128000 in bf16, 305 rows 40 us, 400
+// 42, 608 43 (152 SMs of four CTAs), 700 74; 304 rows, two CTAs each, 25.  At 400 the issue slots
+// are half used, and half of the warps' time is spent on loads.  What was tried on these and not kept:
 // CTAs of 128 or 512 threads, or 3 or 5 on an SM (5: 7.6, 20.8, 19.1); granules
 // through shared memory by asynchronous copies (27.7 and 23.2); a prefetch of the stretch
 // into L2 (7.4, 19.5, 15.3); the next step's granules in registers, or without q
-// four of p at a time (7.6, 18.1, 16.0; 400 rows 42); sums in packed additions (7.4, 17.1, 15.6)
+// four of p at a time (7.6, 18.1, 16.0; 400 rows 44 to 42); sums in packed additions (7.4, 17.1, 15.6)
 // or above a power of two that spares the minimum and maximum (7.5, 16.9, 16.0).
 #include <cuda_runtime.h>
 
